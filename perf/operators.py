@@ -232,13 +232,14 @@ def _own(s):
     new = lambda n: torch.empty(n, device="cuda")  # noqa: E731
     if c["op"] == "logprob":
         logp, lse, ent = new(rows), new(rows), new(rows) if c["entropy"] else None
-        kfac.kfac_token_logprob(kfac.TokenLogprob(s["logits"], s["target"], logp, lse, ent, c["temperature"]))
+        saved = new(2 * rows) if c["backward"] else None
+        kfac.kfac_token_logprob(kfac.TokenLogprob(s["logits"], s["target"], logp, lse, ent, c["temperature"], saved))
         out = {"logp": logp, "lse": lse}
         if c["entropy"]:
             out["entropy"] = ent
         if c["backward"]:
             kfac.kfac_token_logprob_grad(kfac.TokenLogprobGrad(
-                s["logits"], s["target"], lse, s["dlogp"], s["dlogits"], ent, s["dentropy"] if c["entropy"] else None, c["temperature"]))
+                s["logits"], s["target"], saved, s["dlogp"], s["dlogits"], ent, s["dentropy"] if c["entropy"] else None, c["temperature"]))
             out["dlogits"] = s["dlogits"]
         return out
     if c["op"] == "policy":
