@@ -14,6 +14,14 @@
  *   kfac_precondition    G^-1 grad A^-1                         (Eq. 7)
  *   kfac_bn_diag_fisher  diagonal Fisher of BatchNorm parameters and the
  *                        damped diagonal preconditioned gradient
+ * and the operators next to that step when the layer set is a language
+ * model's or a policy's: the losses that make the output gradients, and the
+ * bound on the step:
+ *   kfac_token_logprob, kfac_token_logprob_grad
+ *                        log-probabilities of chosen tokens from logits
+ *   kfac_policy_loss     clipped policy loss with a KL term, and its gradient
+ *   kfac_preference_loss loss over pairs of sequences, and its gradient
+ *   kfac_clip_norm       norm over many tensors, clipping, weight step
  *
  * Conventions shared by every entry point:
  *   - Every buffer pointer inside a descriptor is a DEVICE pointer on the
@@ -60,6 +68,8 @@
  *         without trapping; 8 is set when that drain wait ran out too.  The
  *         call's outputs are then undefined.
  *     A word of 0 means no kernel of the call saw either condition.
+ *     kfac_policy_loss, kfac_preference_loss and kfac_clip_norm write the
+ *     word too (with the bits that their sections name).
  */
 #ifndef KFAC_GB300_H
 #define KFAC_GB300_H
@@ -99,7 +109,8 @@ enum {
     KFAC_ERRW_TIMEOUT_STAGE = 2,
     KFAC_ERRW_TIMEOUT_ACCUM = 4,
     KFAC_ERRW_TIMEOUT_DRAIN = 8,
-    KFAC_ERRW_NONFINITE = 16
+    KFAC_ERRW_NONFINITE = 16,
+    KFAC_ERRW_TARGET = 32      /* a target that is not below the vocabulary's size */
 };
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -337,6 +348,220 @@ typedef struct {
 
 kfac_status kfac_bn_diag_fisher(const kfac_bn_desc *descs, int count, int n_samples,
                                 float gamma, float xi, void *stream);
+
+/* ======================================================================
+ * Losses on logits.
+ *
+ * The rows of `logits` [rows][ld] (dtype KFAC_BF16, KFAC_F16 or KFAC_F32,
+ * `vocab` wide) are scores z of one token each; with the temperature tau,
+ *     lse  = ln sum_j exp(z_j / tau),   p_j = exp(z_j / tau - lse),
+ *     logp = z_target / tau - lse,      H = - sum_j p_j ln p_j,
+ *     d logp / d z_j = (1[j = target] - p_j) / tau,
+ *     d H / d z_j    = - p_j (ln p_j + H) / tau.
+ * Sums, statistics and coefficients are fp32 or wider; a gradient is rounded
+ * once to the logits' dtype.
+ *   - target [rows], int64 or (target_i32 != 0) int32.  A row whose target is
+ *     negative is ignored: its logits are not read, its gradient is zeros and
+ *     its other outputs are 0.  A target >= vocab is ignored too, and sets
+ *     KFAC_ERRW_TARGET in the error word of the calls that have one
+ *     (kfac_token_logprob writes NaN as its logp).
+ *   - Logits of -inf are tokens that cannot be chosen: p = 0, gradient 0.  A
+ *     row whose logits are all -inf has no distribution: logp = lse = -inf,
+ *     H = 0, gradient 0, and the losses leave it out.  NaN or +inf logits of a
+ *     row that is not ignored give NaN for the row, as computed.
+ *   - Rows may start at any element boundary and ld may be any value >= vocab.
+ *     Rows of logits and dlogits whose starts agree modulo 16 bytes (equal ld
+ *     and bases on 16-byte boundaries, for one) are stored 16 bytes at a time.
+ *   - dlogits must not overlap logits.  Every element [row][j < vocab] is
+ *     written; elements past the vocabulary are neither read nor written.
+ *   - vocab is at most 2^24 and rows at most 2^31 - 1 (UNSUPPORTED beyond).
+ *   - tau must be positive and finite.
+ * Results are bitwise reproducible run to run.
+ * ==================================================================== */
+
+/* kfac_token_logprob -- log-probabilities of the targets (and, where not NULL,
+ * lse and H) of every row.  `saved` [rows][2] (NULL: not wanted) receives the
+ * row's maximum m = max_j z_j and sum_j exp((z_j - m) / tau) for the gradient (0,
+ * 0 for an ignored row); m and the sum stay apart because lse loses the
+ * sum's bits where |m| is large, as in a row masked with the lowest value.  Errors: INVALID for null logits/target/logp,
+ * rows < 0, vocab < 1, ld < vocab, a bad dtype or tau, saved not on an 8-byte boundary.
+ * No workspace, no error word.  rows = 0 does nothing. */
+typedef struct {
+    int32_t dtype;
+    const void *logits; int64_t ld;
+    int64_t rows; int32_t vocab;
+    const void *target; int32_t target_i32;
+    float temperature;
+    float *logp;                /* [rows] */
+    float *lse;                 /* [rows], may be NULL */
+    float *entropy;             /* [rows], may be NULL */
+    float *saved;               /* [rows][2], may be NULL */
+} kfac_logprob_desc;
+
+kfac_status kfac_token_logprob(const kfac_logprob_desc *desc, void *stream);
+
+/* kfac_token_logprob_grad -- the logits' gradient from the gradients of logp
+ * and (optionally) H, with the saved values and H that kfac_token_logprob gave:
+ *     dlogits_j = dlogp (1[j = target] - p_j) / tau - dentropy p_j (ln p_j + H) / tau.
+ * A row with dlogp = 0 (and dentropy = 0) is not read and gets zeros.  Errors:
+ * as above, null saved/dlogp/dlogits, dentropy without entropy.  No workspace,
+ * no error word. */
+typedef struct {
+    int32_t dtype;
+    const void *logits; int64_t ld;
+    int64_t rows; int32_t vocab;
+    const void *target; int32_t target_i32;
+    float temperature;
+    const float *saved;         /* [rows][2] */
+    const float *entropy;       /* [rows]; needed with dentropy */
+    const float *dlogp;         /* [rows] */
+    const float *dentropy;      /* [rows], may be NULL */
+    void *dlogits; int64_t ld_d;
+} kfac_logprob_grad_desc;
+
+kfac_status kfac_token_logprob_grad(const kfac_logprob_grad_desc *desc, void *stream);
+
+/* kfac_policy_loss -- clipped policy loss with a KL term and an entropy bonus,
+ * and the gradient of its logits in the same call.  Per row that is not
+ * ignored, with the advantage A, the log-probability `old` under the policy
+ * that drew the token and `ref` under the reference policy:
+ *     r = exp(logp - old),  c = min(max(r, 1 - clip_low), 1 + clip_high),
+ *     pg = - min(r A, c A),
+ *     kl = exp(ref - logp) - (ref - logp) - 1      (0 without ref_logp),
+ *     l  = pg + kl_coef kl - entropy_coef H,
+ *     loss = sum over rows of w l,
+ *     dl / dlogp = - r A [r A <= c A] + kl_coef (1 - exp(ref - logp)),
+ *     dlogits = grad_scale * dloss / dz.
+ *   - w is `weight` [rows] where given (a row with w = 0 is ignored), else 1 / N, N
+ *     the number of rows with a valid target; with seq_mean != 0, 1 / (seqs n_s),
+ *     n_s the number of such rows of the row's sequence.
+ *   - advantage is [rows], or [seqs] when seq_offsets (device int32 [seqs + 1],
+ *     non-decreasing) is given: sequence s holds rows seq_offsets[s] ..
+ *     seq_offsets[s + 1] - 1, and rows of no sequence are ignored.  Offsets
+ *     outside 0 .. rows are read as the nearest of the two.
+ *   - stats [5] receives the sums over rows of w l, w pg, w kl, w H and
+ *     w [the clipped branch was taken].  H is computed when entropy_coef != 0
+ *     or `entropy` is not NULL (else stats[3] = 0).
+ *   - logp, kl, entropy: [rows], optional.  dlogits NULL: the loss only.
+ * Error word (first int32 of the workspace): KFAC_ERRW_TARGET, and
+ * KFAC_ERRW_NONFINITE when a counted row's logp, loss term or gradient
+ * coefficient, or the loss, is NaN or infinite (a gradient that overflows
+ * fp16 as it is rounded does not set it).
+ * Errors: INVALID for null logits/target/advantage/old_logp/stats, rows < 0, vocab < 1,
+ *   ld or ld_d < vocab, clip_low or clip_high negative or NaN, a coefficient that is not
+ *   finite, seqs < 1 with seq_offsets, seq_mean without seq_offsets or with weight,
+ *   kl_coef != 0 or kl without ref_logp, a bad dtype or tau.
+ * Workspace: kfac_policy_loss_workspace_size(desc) bytes. */
+typedef struct {
+    int32_t dtype;
+    const void *logits; int64_t ld;
+    int64_t rows; int32_t vocab;
+    const void *target; int32_t target_i32;
+    float temperature;
+    const float *advantage;
+    const float *old_logp;      /* [rows] */
+    const float *ref_logp;      /* [rows], may be NULL */
+    const float *weight;        /* [rows], may be NULL */
+    const int32_t *seq_offsets; int32_t seqs; int32_t seq_mean;
+    float clip_low, clip_high, kl_coef, entropy_coef, grad_scale;
+    float *stats;               /* [5] */
+    float *logp, *kl, *entropy; /* [rows] each, may be NULL */
+    void *dlogits; int64_t ld_d;
+} kfac_policy_desc;
+
+size_t kfac_policy_loss_workspace_size(const kfac_policy_desc *desc);
+kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *workspace, size_t workspace_bytes, void *stream);
+
+/* kfac_preference_loss -- loss over pairs of sequences (paired log ratios
+ * against a reference), and the gradient of its logits.  Sequence k holds rows
+ * seq_offsets[k] .. seq_offsets[k + 1] - 1; sequences 2 b and 2 b + 1 are the
+ * preferred and the other one of pair b.  With l_k the sum (average != 0: the
+ * mean) of logp over the rows of sequence k with a valid target (0 when it
+ * has none) and the reference's same quantity ref_k,
+ *     h = (l_2b - ref_2b) - (l_2b+1 - ref_2b+1),
+ *     KFAC_PREF_SIGMOID  f = - (1 - e) ln sigma(beta h) - e ln sigma(-beta h)
+ *     KFAC_PREF_HINGE    f = max(0, 1 - beta h)
+ *     KFAC_PREF_IPO      f = (h - 1 / (2 beta))^2
+ *     loss = sum over pairs of v f,   dlogits = grad_scale * dloss / dz,
+ * e the label_smoothing (SIGMOID only), v `pair_weight` [pairs] or 1 / pairs.
+ * The sums over a sequence and h are formed in fp64.  Rows of no sequence are
+ * ignored; offsets as in kfac_policy_loss.
+ *   - ref_logp [2 pairs], may be NULL (0: no reference).
+ *   - loss [1]; pair_loss [pairs] (f), seq_logp [2 pairs] (l) and
+ *     token_logp [rows] are optional.  dlogits NULL: the loss only.
+ * Error word: as kfac_policy_loss (logp of a counted row, l, f, the loss).
+ * Errors: INVALID for null logits/target/seq_offsets/loss, rows < 0, pairs < 1,
+ *   vocab < 1, ld or ld_d < vocab, an unknown kind, beta not positive and
+ *   finite, label_smoothing outside [0, 1) or with another kind, a grad_scale
+ *   that is not finite, a bad dtype or tau.
+ * Workspace: kfac_preference_loss_workspace_size(desc) bytes. */
+typedef enum { KFAC_PREF_SIGMOID = 0, KFAC_PREF_HINGE = 1, KFAC_PREF_IPO = 2 } kfac_pref_kind;
+
+typedef struct {
+    int32_t dtype;
+    const void *logits; int64_t ld;
+    int64_t rows; int32_t vocab;
+    const void *target; int32_t target_i32;
+    float temperature;
+    const int32_t *seq_offsets; int32_t pairs;   /* [2 pairs + 1] */
+    const float *ref_logp;
+    const float *pair_weight;
+    int32_t kind; int32_t average;
+    float beta, label_smoothing, grad_scale;
+    float *loss;
+    float *pair_loss, *seq_logp, *token_logp;
+    void *dlogits; int64_t ld_d;
+} kfac_preference_desc;
+
+size_t kfac_preference_loss_workspace_size(const kfac_preference_desc *desc);
+kfac_status kfac_preference_loss(const kfac_preference_desc *desc, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* ======================================================================
+ * kfac_clip_norm -- norm over many tensors, clipping, and the weight step.
+ *
+ * Over all descriptors, with y = x where y is NULL,
+ *     norm  = sqrt(sum x y)     (0 where the sum is negative),
+ *     scale = max_norm / norm if norm > max_norm, else 1,
+ *     out   = scale x                         (where out is not NULL)
+ *     w    <- w - eta scale x                 (fp32, where w is not NULL).
+ * With y = NULL this is clipping by the global Euclidean norm.  With x the
+ * preconditioned gradients and y the gradients, sum x y = g^T F^-1 g is the
+ * squared length of the natural gradient step in the Fisher metric, and
+ * max_norm = sqrt(kappa) / eta bounds the step's second-order KL change by
+ * kappa / 2.
+ *   - x, y: [rows][ld] of dtype (KFAC_BF16, KFAC_F16, KFAC_F32), cols wide; a
+ *     vector is one row.  out: [rows][ld_out] of out_dtype; w: [rows][ld_w] fp32.
+ *     Any ld >= cols and any element-aligned base; rows that run on without a
+ *     gap (ld = cols) or start on 16-byte boundaries are read 16 bytes at a
+ *     time.  rows or cols = 0: the tensor adds nothing.
+ *   - out may be x itself (same dtype and ld); then nothing is rewritten when
+ *     scale = 1.  Otherwise no output may overlap an input or another output.
+ *   - max_norm > 0; +inf never clips.
+ *   - norm [1], scale [1]: device, optional.
+ * Finite inputs give the right norm as long as it fits fp32 itself: sums whose
+ * fp32 squares overflow or vanish are formed again from scaled values, and
+ * partial sums are added in fp64 in a fixed order (bitwise reproducible).
+ * Non-finite inputs propagate as computed (an infinite norm gives scale 0, a
+ * NaN norm scale NaN) and set KFAC_ERRW_NONFINITE in the error word, which a
+ * caller that skips such steps reads.
+ * Errors: INVALID for count < 0, null x of a tensor that is not empty, negative
+ *   sizes, ld < cols, a bad dtype, out = x with another dtype or ld, a base that
+ *   is not element-aligned, max_norm not positive or NaN, eta not finite.
+ * Workspace: kfac_clip_norm_workspace_size(descs, count) bytes.
+ * ==================================================================== */
+typedef struct {
+    const void *x; int64_t ld;
+    const void *y; int64_t ld_y;       /* may be NULL */
+    void *out;     int64_t ld_out;     /* may be NULL */
+    float *w;      int64_t ld_w;       /* may be NULL */
+    int64_t rows, cols;
+    int32_t dtype, out_dtype;
+} kfac_clip_desc;
+
+size_t kfac_clip_norm_workspace_size(const kfac_clip_desc *descs, int count);
+kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, float max_norm, float eta, float *norm,
+                           float *scale, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,7 @@
 
 static_assert(kfac::ERR_TIMEOUT_FULL == KFAC_ERRW_TIMEOUT_OPERAND && kfac::ERR_TIMEOUT_EMPTY == KFAC_ERRW_TIMEOUT_STAGE &&
                   kfac::ERR_TIMEOUT_ACC == KFAC_ERRW_TIMEOUT_ACCUM && kfac::ERR_TIMEOUT_DRAIN == KFAC_ERRW_TIMEOUT_DRAIN &&
-                  kfac::ERR_NONFINITE == KFAC_ERRW_NONFINITE,
+                  kfac::ERR_NONFINITE == KFAC_ERRW_NONFINITE && kfac::ERR_TARGET == KFAC_ERRW_TARGET,
               "device error word bits match the public header");
 
 namespace kfac {
@@ -309,7 +309,7 @@ extern "C" const char *kfac_status_string(int status) {
     }
 }
 
-extern "C" int kfac_version(void) { return 100; }
+extern "C" int kfac_version(void) { return 200; }
 
 extern "C" long long kfac_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
@@ -323,7 +323,8 @@ extern "C" int kfac_timing_enable(int on) {
 extern "C" const char *kfac_timing_kind_name(int k) {
     static const char *names[KK_COUNT] = {"tc_gemm_bf16", "tc_gemm_tf32x3", "inv_diag", "inv_prep",
                                           "damping", "im2col", "colsum", "sgemm_f32", "bn_fisher",
-                                          "map_copy"};
+                                          "map_copy", "loss_rows", "loss_grad", "loss_small", "clip_norm",
+                                          "clip_apply"};
     return (k >= 0 && k < KK_COUNT) ? names[k] : "";
 }
 

@@ -34,7 +34,8 @@ void count_launch();
 // Kernel kinds for the optional per-kernel timing (kfac_timing_*).
 enum KernelKind : int {
     KK_TC_BF16 = 0, KK_TC_TF32X3, KK_DIAG, KK_PREP, KK_DAMPING, KK_IM2COL, KK_COLSUM,
-    KK_SGEMM, KK_BN, KK_MAPCOPY, KK_COUNT
+    KK_SGEMM, KK_BN, KK_MAPCOPY, KK_LOSS_ROWS, KK_LOSS_GRAD, KK_LOSS_SMALL, KK_CLIP_NORM,
+    KK_CLIP_APPLY, KK_COUNT
 };
 // Returns a slot (>= 0) after recording a start event on `st` when timing is
 // enabled, -1 otherwise; timing_end records the matching end event.
@@ -130,7 +131,8 @@ enum : int {
     ERR_TIMEOUT_EMPTY = 2,
     ERR_TIMEOUT_ACC = 4,
     ERR_TIMEOUT_DRAIN = 8,
-    ERR_NONFINITE = 16
+    ERR_NONFINITE = 16,
+    ERR_TARGET = 32  // a target token past the vocabulary
 };
 
 __device__ __forceinline__ bool finite4(float4 v) {

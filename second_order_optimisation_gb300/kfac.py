@@ -10,6 +10,10 @@ The functions keep the C names:
   kfac_damp_invert     (Eq. 6, pi-split Tikhonov damping)
   kfac_precondition    (Eq. 7)
   kfac_bn_diag_fisher  (diagonal BatchNorm Fisher, section 1)
+and, next to the step, the losses that make a policy's or language model's
+output gradients and the bound on the step over all tensors:
+  kfac_token_logprob, kfac_token_logprob_grad, kfac_policy_loss,
+  kfac_preference_loss, kfac_clip_norm
 """
 from __future__ import annotations
 
@@ -28,12 +32,17 @@ KFAC_BF16, KFAC_F32, KFAC_F16 = 0, 1, 2
 KFAC_LAYOUT_FULL, KFAC_LAYOUT_PACKED_UPPER = 0, 1
 # bits of the device error word (the first int32 of a call's workspace)
 ERRW_TIMEOUT_OPERAND, ERRW_TIMEOUT_STAGE, ERRW_TIMEOUT_ACCUM, ERRW_TIMEOUT_DRAIN, ERRW_NONFINITE = 1, 2, 4, 8, 16
+ERRW_TARGET = 32
+KFAC_PREF_SIGMOID, KFAC_PREF_HINGE, KFAC_PREF_IPO = 0, 1, 2
 
 EXPORTS = ("kfac_status_string", "kfac_version", "kfac_launch_count", "kfac_timing_enable",
            "kfac_timing_read", "kfac_timing_kind_name", "kfac_factor_update_workspace_size",
            "kfac_factor_update", "kfac_damp_invert_workspace_size", "kfac_damp_invert",
            "kfac_precondition_workspace_size", "kfac_precondition", "kfac_bn_diag_fisher",
-           "kfac_noalloc_scratch_bytes", "kfac_precondition_noalloc", "kfac_timing_read_launches")
+           "kfac_noalloc_scratch_bytes", "kfac_precondition_noalloc", "kfac_timing_read_launches",
+           "kfac_token_logprob", "kfac_token_logprob_grad", "kfac_policy_loss_workspace_size", "kfac_policy_loss",
+           "kfac_preference_loss_workspace_size", "kfac_preference_loss", "kfac_clip_norm_workspace_size",
+           "kfac_clip_norm")
 
 
 class KfacError(RuntimeError):
@@ -80,6 +89,54 @@ class BnDesc(ctypes.Structure):
                 ("grad_mean", ctypes.c_void_p), ("precond", ctypes.c_void_p)]
 
 
+class LogprobDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("target", ctypes.c_void_p), ("target_i32", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("logp", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p),
+                ("saved", ctypes.c_void_p)]
+
+
+class LogprobGradDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("target", ctypes.c_void_p), ("target_i32", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("saved", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("dlogp", ctypes.c_void_p),
+                ("dentropy", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("ld_d", ctypes.c_int64)]
+
+
+class PolicyDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("target", ctypes.c_void_p), ("target_i32", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("advantage", ctypes.c_void_p), ("old_logp", ctypes.c_void_p), ("ref_logp", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("seq_offsets", ctypes.c_void_p), ("seqs", ctypes.c_int32),
+                ("seq_mean", ctypes.c_int32),
+                ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("entropy_coef", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("stats", ctypes.c_void_p), ("logp", ctypes.c_void_p), ("kl", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("ld_d", ctypes.c_int64)]
+
+
+class PreferenceDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("target", ctypes.c_void_p), ("target_i32", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("seq_offsets", ctypes.c_void_p), ("pairs", ctypes.c_int32),
+                ("ref_logp", ctypes.c_void_p), ("pair_weight", ctypes.c_void_p),
+                ("kind", ctypes.c_int32), ("average", ctypes.c_int32),
+                ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("grad_scale", ctypes.c_float),
+                ("loss", ctypes.c_void_p), ("pair_loss", ctypes.c_void_p), ("seq_logp", ctypes.c_void_p),
+                ("token_logp", ctypes.c_void_p), ("dlogits", ctypes.c_void_p), ("ld_d", ctypes.c_int64)]
+
+
+class ClipDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld", ctypes.c_int64), ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("w", ctypes.c_void_p), ("ld_w", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -120,8 +177,18 @@ def load() -> ctypes.CDLL:
         lib.kfac_bn_diag_fisher.argtypes = [vp, i32, i32, f32, f32, vp]
         lib.kfac_noalloc_scratch_bytes.restype = sz
         lib.kfac_precondition_noalloc.argtypes = [vp, i32, i32, vp]
+        lib.kfac_token_logprob.argtypes = [vp, vp]
+        lib.kfac_token_logprob_grad.argtypes = [vp, vp]
+        for f in ("kfac_policy_loss", "kfac_preference_loss"):
+            getattr(lib, f).argtypes = [vp, vp, sz, vp]
+            getattr(lib, f + "_workspace_size").argtypes = [vp]
+            getattr(lib, f + "_workspace_size").restype = sz
+        lib.kfac_clip_norm_workspace_size.argtypes = [vp, i32]
+        lib.kfac_clip_norm_workspace_size.restype = sz
+        lib.kfac_clip_norm.argtypes = [vp, i32, f32, f32, vp, vp, vp, sz, vp]
         for f in ("kfac_factor_update", "kfac_damp_invert", "kfac_precondition", "kfac_bn_diag_fisher",
-                  "kfac_precondition_noalloc"):
+                  "kfac_precondition_noalloc", "kfac_token_logprob", "kfac_token_logprob_grad", "kfac_policy_loss",
+                  "kfac_preference_loss", "kfac_clip_norm"):
             getattr(lib, f).restype = i32
         _lib = lib
     return _lib
@@ -163,7 +230,10 @@ def timing_read_launches(n: int = 65536) -> list:
     sm = (ctypes.c_ulonglong * n)()
     cnt = lib.kfac_timing_read_launches(st, du, kd, sm, n)
     if cnt < 0:
-        raise KfacError(KFAC_ERR_CUDA, "kfac_timing_read_launches")
+        raise KfacError(KFAC_ERR_CUDA, "kfac_timing_read_launches",
+           "kfac_token_logprob", "kfac_token_logprob_grad", "kfac_policy_loss_workspace_size", "kfac_policy_loss",
+           "kfac_preference_loss_workspace_size", "kfac_preference_loss", "kfac_clip_norm_workspace_size",
+           "kfac_clip_norm")
     ids = {}
     return [(st[i], du[i], lib.kfac_timing_kind_name(kd[i]).decode(), ids.setdefault(sm[i], len(ids)))
             for i in range(min(cnt, n))]
@@ -438,3 +508,278 @@ def kfac_bn_diag_fisher(items: Sequence[BnItem], gamma: float, xi: float = 0.0, 
                         it.precond.data_ptr())
     _check(lib.kfac_bn_diag_fisher(arr, len(items), ns, float(gamma), float(xi), _stream(stream)),
            "kfac_bn_diag_fisher")
+
+
+# ------------------------------------------------------------ losses on logits
+
+def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
+    """The caller's workspace, or a new one that may be dropped while a call on
+    `stream` (an own stream, or None) still uses it."""
+    ws = _workspace(nbytes, device, workspace)
+    if workspace is None and stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+        ws.record_stream(stream)
+    return ws
+
+
+def _rowvec(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.float32) -> Optional[int]:
+    """Address of a dense vector of n values (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} dense values, got shape {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _logits_args(logits: torch.Tensor, target: torch.Tensor, temperature: float):
+    """The descriptor fields from dtype to temperature, the same for every call on logits."""
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    if target.dtype is not torch.int64 and target.dtype is not torch.int32:
+        raise TypeError(f"target must be int64 or int32, got {target.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, vocab] with unit column stride")
+    rows, vocab = logits.shape
+    if target.numel() != rows or not target.is_contiguous():
+        raise ValueError(f"target must be {rows} dense values, got shape {tuple(target.shape)}")
+    return (_DTYPES[logits.dtype], logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows, vocab,
+            target.data_ptr(), int(target.dtype is torch.int32), temperature)
+
+
+def _dlogits_args(logits: torch.Tensor, dlogits: Optional[torch.Tensor]):
+    if dlogits is None:
+        return None, 0
+    if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
+        raise TypeError("dlogits must have the logits' shape and dtype")
+    if dlogits.shape[1] > 1 and dlogits.stride(1) != 1:
+        raise ValueError("dlogits must have unit column stride")
+    return dlogits.data_ptr(), dlogits.stride(0) if dlogits.shape[0] > 1 else dlogits.shape[1]
+
+
+@dataclass
+class TokenLogprob:
+    """Log-probabilities of target [rows] under logits [rows, vocab] (bf16, fp16
+    or fp32; target int64 or int32, negative: ignored), and optionally the
+    rows' lse and entropy (fp32 [rows] each) and what the gradient needs of them
+    (saved, fp32 [rows, 2])."""
+    logits: torch.Tensor
+    target: torch.Tensor
+    logp: torch.Tensor
+    lse: Optional[torch.Tensor] = None
+    entropy: Optional[torch.Tensor] = None
+    temperature: float = 1.0
+    saved: Optional[torch.Tensor] = None
+
+
+def kfac_token_logprob(item: TokenLogprob, stream=None) -> None:
+    t = item
+    n = t.logits.shape[0]
+    d = LogprobDesc(*_logits_args(t.logits, t.target, t.temperature), _rowvec(t.logp, n, "logp"),
+                    _rowvec(t.lse, n, "lse"), _rowvec(t.entropy, n, "entropy"), _rowvec(t.saved, 2 * n, "saved"))
+    _check(load().kfac_token_logprob(ctypes.byref(d), _stream(stream)), "kfac_token_logprob")
+
+
+@dataclass
+class TokenLogprobGrad:
+    """dlogits (the logits' shape and dtype) from the gradients of logp and,
+    optionally, of the entropy; saved and entropy as kfac_token_logprob gave them."""
+    logits: torch.Tensor
+    target: torch.Tensor
+    saved: torch.Tensor
+    dlogp: torch.Tensor
+    dlogits: torch.Tensor
+    entropy: Optional[torch.Tensor] = None
+    dentropy: Optional[torch.Tensor] = None
+    temperature: float = 1.0
+
+
+def kfac_token_logprob_grad(item: TokenLogprobGrad, stream=None) -> None:
+    t = item
+    n = t.logits.shape[0]
+    d = LogprobGradDesc(*_logits_args(t.logits, t.target, t.temperature), _rowvec(t.saved, 2 * n, "saved"),
+                        _rowvec(t.entropy, n, "entropy"), _rowvec(t.dlogp, n, "dlogp"),
+                        _rowvec(t.dentropy, n, "dentropy"), *_dlogits_args(t.logits, t.dlogits))
+    _check(load().kfac_token_logprob_grad(ctypes.byref(d), _stream(stream)), "kfac_token_logprob_grad")
+
+
+@dataclass
+class PolicyLoss:
+    """Clipped policy loss with a KL term and an entropy bonus (formulas in
+    kfac.h).  advantage: [rows], or [seqs] with seq_offsets int32 [seqs + 1].
+    stats fp32 [5] receives the loss and the weighted sums of its policy term,
+    the KL, the entropy and the clipped share; dlogits (optional) the gradient."""
+    logits: torch.Tensor
+    target: torch.Tensor
+    advantage: torch.Tensor
+    old_logp: torch.Tensor
+    stats: torch.Tensor
+    logp: Optional[torch.Tensor] = None
+    dlogits: Optional[torch.Tensor] = None
+    ref_logp: Optional[torch.Tensor] = None
+    weight: Optional[torch.Tensor] = None
+    seq_offsets: Optional[torch.Tensor] = None
+    seq_mean: bool = False
+    kl: Optional[torch.Tensor] = None
+    entropy: Optional[torch.Tensor] = None
+    clip_low: float = 0.2
+    clip_high: float = 0.2
+    kl_coef: float = 0.0
+    entropy_coef: float = 0.0
+    temperature: float = 1.0
+    grad_scale: float = 1.0
+
+
+def _policy_desc(t: PolicyLoss) -> PolicyDesc:
+    n = t.logits.shape[0]
+    seqs = 0 if t.seq_offsets is None else t.seq_offsets.numel() - 1
+    return PolicyDesc(*_logits_args(t.logits, t.target, t.temperature),
+                      _rowvec(t.advantage, n if t.seq_offsets is None else seqs, "advantage"),
+                      _rowvec(t.old_logp, n, "old_logp"), _rowvec(t.ref_logp, n, "ref_logp"),
+                      _rowvec(t.weight, n, "weight"), _rowvec(t.seq_offsets, seqs + 1, "seq_offsets", torch.int32),
+                      seqs, bool(t.seq_mean), t.clip_low, t.clip_high, t.kl_coef, t.entropy_coef, t.grad_scale,
+                      _rowvec(t.stats, 5, "stats"), _rowvec(t.logp, n, "logp"), _rowvec(t.kl, n, "kl"),
+                      _rowvec(t.entropy, n, "entropy"), *_dlogits_args(t.logits, t.dlogits))
+
+
+def kfac_policy_loss_workspace_size(item: PolicyLoss) -> int:
+    return int(load().kfac_policy_loss_workspace_size(ctypes.byref(_policy_desc(item))))
+
+
+def kfac_policy_loss(item: PolicyLoss, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue the loss and its gradient; returns the workspace used (its first
+    int32 is the device error word: ERRW_TARGET, ERRW_NONFINITE)."""
+    lib = load()
+    d = _policy_desc(item)
+    p = ctypes.byref(d)
+    ws = _scratch(lib.kfac_policy_loss_workspace_size(p), item.logits.device, workspace, stream)
+    _check(lib.kfac_policy_loss(p, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
+           "kfac_policy_loss")
+    return ws
+
+
+_PREF_KINDS = {"sigmoid": KFAC_PREF_SIGMOID, "hinge": KFAC_PREF_HINGE, "ipo": KFAC_PREF_IPO}
+
+
+@dataclass
+class PreferenceLoss:
+    """Loss over pairs of sequences (formulas in kfac.h): sequences 2 b and
+    2 b + 1 of seq_offsets (int32 [2 pairs + 1]) are the preferred and the other
+    one of pair b.  loss fp32 [1]; seq_logp and ref_logp [2 pairs]; kind is
+    "sigmoid", "hinge" or "ipo"."""
+    logits: torch.Tensor
+    target: torch.Tensor
+    seq_offsets: torch.Tensor
+    loss: torch.Tensor
+    seq_logp: Optional[torch.Tensor] = None
+    dlogits: Optional[torch.Tensor] = None
+    ref_logp: Optional[torch.Tensor] = None
+    pair_weight: Optional[torch.Tensor] = None
+    pair_loss: Optional[torch.Tensor] = None
+    token_logp: Optional[torch.Tensor] = None
+    kind: str = "sigmoid"
+    beta: float = 0.1
+    label_smoothing: float = 0.0
+    average: bool = False
+    temperature: float = 1.0
+    grad_scale: float = 1.0
+
+
+def _preference_desc(t: PreferenceLoss) -> PreferenceDesc:
+    n, m = t.logits.shape[0], t.seq_offsets.numel() - 1
+    if m < 2 or m % 2:
+        raise ValueError(f"seq_offsets must hold 2 pairs + 1 values, got {m + 1}")
+    if t.kind not in _PREF_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_PREF_KINDS)}, got {t.kind!r}")
+    return PreferenceDesc(*_logits_args(t.logits, t.target, t.temperature),
+                          _rowvec(t.seq_offsets, m + 1, "seq_offsets", torch.int32), m // 2,
+                          _rowvec(t.ref_logp, m, "ref_logp"), _rowvec(t.pair_weight, m // 2, "pair_weight"),
+                          _PREF_KINDS[t.kind], bool(t.average), t.beta, t.label_smoothing, t.grad_scale,
+                          _rowvec(t.loss, 1, "loss"), _rowvec(t.pair_loss, m // 2, "pair_loss"),
+                          _rowvec(t.seq_logp, m, "seq_logp"), _rowvec(t.token_logp, n, "token_logp"),
+                          *_dlogits_args(t.logits, t.dlogits))
+
+
+def kfac_preference_loss_workspace_size(item: PreferenceLoss) -> int:
+    return int(load().kfac_preference_loss_workspace_size(ctypes.byref(_preference_desc(item))))
+
+
+def kfac_preference_loss(item: PreferenceLoss, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue the loss and its gradient; returns the workspace used (its first
+    int32 is the device error word: ERRW_TARGET, ERRW_NONFINITE)."""
+    lib = load()
+    d = _preference_desc(item)
+    p = ctypes.byref(d)
+    ws = _scratch(lib.kfac_preference_loss_workspace_size(p), item.logits.device, workspace, stream)
+    _check(lib.kfac_preference_loss(p, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
+           "kfac_preference_loss")
+    return ws
+
+
+# ------------------------------------------------------------ norm, clipping, weight step
+
+@dataclass
+class ClipTensor:
+    """One tensor of kfac_clip_norm: x (and y, its dual under the metric) are
+    read; out = scale * x and w -= eta * scale * x are written where given.  All
+    of one shape: dense, or 2-D with unit column stride.  out may be x."""
+    x: torch.Tensor
+    out: Optional[torch.Tensor] = None
+    y: Optional[torch.Tensor] = None
+    w: Optional[torch.Tensor] = None
+
+
+def _clip_desc(t: ClipTensor) -> ClipDesc:
+    x = t.x
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    ops = [o for o in (x, t.y, t.out, t.w) if o is not None]
+    if any(o.shape != x.shape for o in ops):
+        raise ValueError("x, y, out and w must have one shape")
+    if t.y is not None and t.y.dtype is not x.dtype:
+        raise TypeError("y must have x's dtype")
+    if t.w is not None and t.w.dtype is not torch.float32:
+        raise TypeError("w must be fp32")
+    if t.out is not None and t.out.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {t.out.dtype}")
+    if all(o.is_contiguous() for o in ops):
+        rows, cols = 1, x.numel()
+        ld = lambda o: cols  # noqa: E731
+    else:
+        if x.dim() != 2 or any(o.shape[1] > 1 and o.stride(1) != 1 for o in ops):
+            raise ValueError("tensors must be dense, or matrices with unit column stride")
+        rows, cols = x.shape
+        ld = lambda o: o.stride(0) if rows > 1 else cols  # noqa: E731
+    a = [v for o in (x, t.y, t.out, t.w) for v in ((None, 0) if o is None else (o.data_ptr(), ld(o)))]
+    return ClipDesc(*a, rows, cols, _DTYPES[x.dtype], _DTYPES[t.out.dtype] if t.out is not None else _DTYPES[x.dtype])
+
+
+class ClipList:
+    """A list of ClipTensor whose descriptors are made once: for callers that
+    clip the same buffers at every step."""
+
+    def __init__(self, tensors: Sequence[ClipTensor]):
+        self.tensors = list(tensors)
+        self.descs = (ClipDesc * max(len(self.tensors), 1))(*[_clip_desc(t) for t in self.tensors])
+        self.device = self.tensors[0].x.device if self.tensors else torch.device("cuda")
+        self.need = int(load().kfac_clip_norm_workspace_size(self.descs, len(self.tensors)))
+
+
+def kfac_clip_norm_workspace_size(tensors) -> int:
+    return (tensors if isinstance(tensors, ClipList) else ClipList(tensors)).need
+
+
+def kfac_clip_norm(tensors, max_norm: float, norm: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                   eta: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue norm, clipping and weight step over `tensors` (a sequence of
+    ClipTensor, or a ClipList); norm and scale (fp32 [1]) receive the global
+    norm and the factor applied.  Returns the workspace used (its first int32
+    is the device error word: ERRW_NONFINITE)."""
+    c = tensors if isinstance(tensors, ClipList) else ClipList(tensors)
+    ws = _scratch(c.need, c.device, workspace, stream)
+    _check(load().kfac_clip_norm(c.descs, len(c.tensors), max_norm, eta, _rowvec(norm, 1, "norm"),
+                                 _rowvec(scale, 1, "scale"), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 _stream(stream)), "kfac_clip_norm")
+    return ws
