@@ -77,6 +77,26 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The same for a grid of clusters of `cluster` CTAs along x (a divisor of grid.x).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), unsigned cluster, dim3 grid, dim3 block, size_t smem,
+                            cudaStream_t st, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // KFAC_LAUNCH(kind, stream, kernel, grid, block, dynamic smem, args...)
 #define KFAC_LAUNCH(kind, st, kernel, grid, block, smem, ...)                                  \
     do {                                                                                       \
@@ -86,6 +106,16 @@ cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_
         ::kfac::timing_end(slot_, (st));                                                       \
         ::kfac::count_launch();                                                                \
         if (e_ != cudaSuccess || cudaGetLastError() != cudaSuccess) return KFAC_ERR_CUDA;      \
+    } while (0)
+
+#define KFAC_LAUNCH_CLUSTERS(kind, st, kernel, cluster, grid, block, smem, ...)                       \
+    do {                                                                                              \
+        const int slot_ = ::kfac::timing_begin((kind), (st));                                         \
+        const cudaError_t e_ = ::kfac::launch_clusters((kernel), (cluster), dim3(grid), dim3(block),   \
+                                                       (smem), (st), __VA_ARGS__);                    \
+        ::kfac::timing_end(slot_, (st));                                                              \
+        ::kfac::count_launch();                                                                       \
+        if (e_ != cudaSuccess || cudaGetLastError() != cudaSuccess) return KFAC_ERR_CUDA;             \
     } while (0)
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

@@ -23,6 +23,63 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= F32_MAX; }
 
+// Two fp32 values in one 64-bit register pair: one instruction for both.
+struct f2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 both(f2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ f2 add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f2 mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ f2 fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ f2 ex2(f2 a) {
+    const float2 x = both(a);
+    return pair(ex2(x.x), ex2(x.y));
+}
+__device__ __forceinline__ f2 max2(f2 a, float b) {
+    const float2 x = both(a);
+    return pair(fmaxf(x.x, b), fmaxf(x.y, b));
+}
+
+// A sum of many terms that may differ by more than fp32's 24 bits: s + c, c the
+// bits that the additions to s have lost (a row's most likely token gives a
+// term of 1; without c, thousands of terms near 2^-25 would vanish beside it).
+struct Sum2 {
+    f2 s, c;
+    __device__ __forceinline__ Sum2() : s(pair(0.f, 0.f)), c(s) {}
+    __device__ __forceinline__ void add(f2 b) {
+        const f2 m1 = pair(-1.f, -1.f);
+        const f2 t = kfac::add(s, b), bb = fma(s, m1, t);                 // bb = t - s
+        const f2 ds = fma(fma(bb, m1, t), m1, s), db = fma(bb, m1, b);    // s - (t - bb), b - bb
+        c = kfac::add(c, kfac::add(ds, db));
+        s = t;
+    }
+    __device__ __forceinline__ float total() const {
+        const float2 a = both(s), b = both(c);
+        return (a.x + a.y) + (b.x + b.y);
+    }
+};
+
 // A 16-byte group of elements of one type, as bits and as fp32 values.
 template <int DT>
 struct Elem;
@@ -32,6 +89,17 @@ struct Elem<KFAC_F32> {
     static constexpr int N = 4;
     static constexpr uint32_t NEG_INF = 0xff800000u;  // -inf in every element of a 32-bit word
     static __device__ __forceinline__ float value(bits b) { return __uint_as_float(b); }
+    using two = f2;  // running maximum of groups (NaN is passed over)
+    static __device__ __forceinline__ two lowest() { return pair(-F32_MAX, -F32_MAX); }
+    static __device__ __forceinline__ two raise(two m, uint4 u) {
+        const float2 a = both(m);
+        return pair(fmaxf(a.x, fmaxf(__uint_as_float(u.x), __uint_as_float(u.y))),
+                    fmaxf(a.y, fmaxf(__uint_as_float(u.z), __uint_as_float(u.w))));
+    }
+    static __device__ __forceinline__ float largest(two m) {
+        const float2 a = both(m);
+        return fmaxf(a.x, a.y);
+    }
     static __device__ __forceinline__ bits round(float v) { return __float_as_uint(v); }
     static __device__ __forceinline__ void unpack(uint4 u, float *v) {
         v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
@@ -48,6 +116,13 @@ struct Elem<KFAC_BF16> {
     static constexpr int N = 8;
     static constexpr uint32_t NEG_INF = 0xff80ff80u;
     static __device__ __forceinline__ float value(bits b) { return __uint_as_float((uint32_t)b << 16); }
+    using two = __nv_bfloat162;  // running maximum of groups (NaN is passed over)
+    static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
+    static __device__ __forceinline__ two lowest() { return as_two(0xff7fff7fu); }
+    static __device__ __forceinline__ two raise(two m, uint4 u) {
+        return __hmax2(m, __hmax2(__hmax2(as_two(u.x), as_two(u.y)), __hmax2(as_two(u.z), as_two(u.w))));
+    }
+    static __device__ __forceinline__ float largest(two m) { return fmaxf(__low2float(m), __high2float(m)); }
     static __device__ __forceinline__ bits round(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
     static __device__ __forceinline__ void unpack2(uint32_t u, float *v) {
         v[0] = __uint_as_float(u << 16);
@@ -70,6 +145,13 @@ struct Elem<KFAC_F16> {
     static constexpr int N = 8;
     static constexpr uint32_t NEG_INF = 0xfc00fc00u;
     static __device__ __forceinline__ float value(bits b) { return __half2float(__ushort_as_half(b)); }
+    using two = __half2;  // running maximum of groups (NaN is passed over)
+    static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
+    static __device__ __forceinline__ two lowest() { return as_two(0xfbfffbffu); }
+    static __device__ __forceinline__ two raise(two m, uint4 u) {
+        return __hmax2(m, __hmax2(__hmax2(as_two(u.x), as_two(u.y)), __hmax2(as_two(u.z), as_two(u.w))));
+    }
+    static __device__ __forceinline__ float largest(two m) { return fmaxf(__low2float(m), __high2float(m)); }
     static __device__ __forceinline__ bits round(float v) { return __half_as_ushort(__float2half_rn(v)); }
     static __device__ __forceinline__ void unpack2(uint32_t u, float *v) {
         const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&u));
@@ -104,23 +186,30 @@ struct Row {
     __device__ __forceinline__ int groups() const { return (phase + n + E::N - 1) / E::N; }
     __device__ __forceinline__ int first(int g) const { return g * E::N - phase; }
     __device__ __forceinline__ bool whole(int g) const { return first(g) >= 0 && first(g) + E::N <= n; }
-    // The group's bits, -inf where there is no element.
-    __device__ __forceinline__ uint4 load(int g) const {
-        const char *p = base + (size_t)g * 16;
+    // Whole groups are begin() .. end() - 1; the elements of group 0 before them
+    // (where phase > 0) and those of group end() behind them are the edges.
+    __device__ __forceinline__ int begin() const { return phase > 0; }
+    __device__ __forceinline__ int end() const { return max((phase + n) / E::N, begin()); }
+    __device__ __forceinline__ bool has_front() const { return phase > 0; }
+    __device__ __forceinline__ bool has_back() const { return end() * E::N < phase + n; }
+    __device__ __forceinline__ uint4 load_whole(int g) const {
         uint4 u;
-        if (whole(g)) {
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                         : "l"(p)
-                         : "memory");
-            return u;
-        }
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(base + (size_t)g * 16)
+                     : "memory");
+        return u;
+    }
+    static __device__ __forceinline__ uint4 none() { return make_uint4(E::NEG_INF, E::NEG_INF, E::NEG_INF, E::NEG_INF); }
+    // An edge group's bits, -inf where there is no element.
+    __device__ __forceinline__ uint4 load_edge(int g) const { return edge_group(base + (size_t)g * 16, first(g), n); }
+    static __device__ __noinline__ uint4 edge_group(const char *at, int e0, int n) {
+        const bits *p = reinterpret_cast<const bits *>(at);
         uint32_t w[4] = {E::NEG_INF, E::NEG_INF, E::NEG_INF, E::NEG_INF};
-        const int e0 = first(g);
 #pragma unroll
         for (int i = 0; i < E::N; ++i) {
             if (e0 + i < 0 || e0 + i >= n) continue;
-            const uint32_t b = reinterpret_cast<const bits *>(p)[i];
+            const uint32_t b = p[i];
             if (E::N == 4)
                 w[i] = b;
             else
@@ -128,71 +217,100 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
+    // Writes an edge group's elements to the row at `out`.
+    static __device__ __noinline__ void store_edge(void *out, int e0, int n, uint4 u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < E::N; ++i)
+            if (e0 + i >= 0 && e0 + i < n) ((bits *)out)[e0 + i] = (bits)(E::N == 4 ? w[i] : w[i / 2] >> (i & 1) * 16);
+    }
+    __device__ __forceinline__ uint4 load(int g) const { return whole(g) ? load_whole(g) : load_edge(g); }
 };
 
-// Writes the group's values (element first(g) + i at v[i]) to the row at `out`.
-template <int DT>
-__device__ __forceinline__ void store_group(const Row<DT> &r, int g, void *out, bool same_phase, const float *v) {
-    using E = Elem<DT>;
-    typename E::bits *o = (typename E::bits *)out + r.first(g);
-    if (same_phase && r.whole(g)) {
-        *reinterpret_cast<uint4 *>(o) = E::pack(v);
-        return;
-    }
-    const int e0 = r.first(g);
-#pragma unroll
-    for (int i = 0; i < E::N; ++i)
-        if (e0 + i >= 0 && e0 + i < r.n) o[i] = E::round(v[i]);
+// Statistics of a part of a row: m its maximum (at least the lowest finite
+// value, so that z = -inf gives 2^-inf = 0), s = sum_j 2^y_j and (ENT) t =
+// sum_j 2^y_j y_j with y_j = (z_j - m) k.  A NaN or +inf makes s NaN.
+struct Part {
+    float m, s, t;
+};
+
+// Lanes' maximum, the same on each of `width` lanes.
+__device__ __forceinline__ float lanes_max(float v, int width) {
+    for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float lanes_sum(float v, int width) {
+    for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
-// Running statistics of sum_j 2^((z_j - m) k): the maximum m, the sum s, and
-// (ENT) t = sum_j 2^y y with y = (z_j - m) k.  m starts at the lowest finite
-// value, so that z = -inf gives 2^-inf = 0; a NaN or +inf makes s NaN.
-template <bool ENT>
-struct Stat {
-    float m, s, t;
-    __device__ __forceinline__ Stat() : m(-F32_MAX), s(0.f), t(0.f) {}
-    __device__ __forceinline__ void raise(float mx, float k) {
-        if (mx > m) {
-            const float d = (m - mx) * k, c = ex2(d);
-            if (s != 0.f) {  // (a NaN sum stays)
-                if (ENT) t = c * (t + fmaxf(d, Y_FLOOR) * s);
-                s *= c;
-            }
-            m = mx;
-        }
-    }
-    template <int N>
-    __device__ __forceinline__ void add(const float *z, float k) {
-        float mx = z[0];
+// A group's values as pairs.
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(uint4 u, f2 *v) {
+    float f[Elem<DT>::N];
+    Elem<DT>::unpack(u, f);
 #pragma unroll
-        for (int i = 1; i < N; ++i) mx = fmaxf(mx, z[i]);
-        raise(mx, k);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float y = (z[i] - m) * k, e = ex2(y);
-            s += e;
-            if (ENT) t = fmaf(e, fmaxf(y, Y_FLOOR), t);
-        }
+    for (int i = 0; i < Elem<DT>::N / 2; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
+// (z - m) k in one multiply-add, z k - c with c = m k rounded: exact but for the
+// result's own rounding, and for delta = m k - c, which is the same for the whole
+// row and is put back into the sums (2^y (z) = 2^-delta 2^(z k - c)).  `ok` is false
+// where m k is so large that c or delta would be (rows at the type's lowest value):
+// then the difference is formed before the product.
+struct Shift {
+    float m, k, c, delta;
+    bool ok;
+    __device__ __forceinline__ Shift(float m_, float k_) : m(m_), k(k_), c(m_ * k_) {
+        ok = fabsf(c) < 1048576.f;
+        delta = ok ? fmaf(m, k, -c) : 0.f;
     }
-    __device__ __forceinline__ void merge(float m2, float s2, float t2, float k) {
-        if (m2 > m) {
-            raise(m2, k);
-            s += s2;
-            if (ENT) t += t2;
-        } else if (s2 != 0.f) {
-            const float d = (m2 - m) * k, c = ex2(d);
-            if (ENT) t += c * (t2 + fmaxf(d, Y_FLOOR) * s2);
-            s = fmaf(s2, c, s);
-        }
-    }
-    __device__ __forceinline__ void merge_lanes(float k, int width = 32) {
-        for (int o = width / 2; o > 0; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-            const float t2 = ENT ? __shfl_xor_sync(0xffffffffu, t, o) : 0.f;
-            merge(m2, s2, t2, k);
-        }
+    template <bool FAST>
+    __device__ __forceinline__ f2 apply(f2 z) const {
+        return FAST ? fma(z, pair(k, k), pair(-c, -c)) : mul(add(z, pair(-m, -m)), pair(k, k));
     }
 };
+
+// Sums over groups whose maximum is at most the shift's.  A thread adds few
+// groups, each summed as a tree first; a long run of groups takes Sum2's way.
+template <int DT, bool ENT>
+struct Sums {
+    f2 s, t;
+    __device__ __forceinline__ Sums() : s(pair(0.f, 0.f)), t(s) {}
+    template <bool FAST>
+    __device__ __forceinline__ f2 group(uint4 u, const Shift &h) {
+        constexpr int H = Elem<DT>::N / 2;
+        f2 v[H];
+        unpack_pairs<DT>(u, v);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const f2 y = h.apply<FAST>(v[i]);
+            v[i] = ex2(y);
+            if (ENT) t = fma(v[i], max2(y, Y_FLOOR), t);
+        }
+        if constexpr (H == 4) return kfac::add(kfac::add(v[0], v[1]), kfac::add(v[2], v[3]));
+        else return kfac::add(v[0], v[1]);
+    }
+    template <bool FAST>
+    __device__ __forceinline__ void add(uint4 u, const Shift &h) {
+        s = kfac::add(s, group<FAST>(u, h));
+    }
+    __device__ __forceinline__ Part part(const Shift &h, int width) const {
+        const float2 ss = both(s), tt = both(t);
+        Part p{h.m, lanes_sum(ss.x + ss.y, width), ENT ? lanes_sum(tt.x + tt.y, width) : 0.f};
+        const float c = ex2(-h.delta);
+        if (ENT) p.t = c * fmaf(-h.delta, p.s, p.t);
+        p.s *= c;
+        return p;
+    }
+};
+
+// A part's sums, relative to a maximum M >= p.m.
+template <bool ENT>
+__device__ __forceinline__ Part relative_to(Part p, float M, float k) {
+    const float d = (p.m - M) * k, c = ex2(d);
+    // an empty part is 0 whatever d is
+    return p.s == 0.f ? Part{M, 0.f, 0.f} : Part{M, p.s * c, ENT ? c * (p.t + fmaxf(d, Y_FLOOR) * p.s) : 0.f};
+}
 
 }  // namespace kfac

@@ -10,6 +10,7 @@
 //   b = - gh ln 2 / s,   a = - (g + gh (H - ln 2 log2 s)) / s.
 // The maximum is subtracted before the scaling, so that rows whose logits are
 // all the type's lowest value stay finite.
+#include <algorithm>
 #include <cmath>
 
 #include "logits.cuh"
@@ -42,71 +43,438 @@ __device__ __forceinline__ float logit_at(const void *row, long long j) {
 struct RowResult {
     float logp, lse, h;
 };
-__device__ __forceinline__ RowResult row_result(float m, float s, float t, float z_t, float tau) {
+__device__ __forceinline__ RowResult row_result(const Part &p, float z_t, float tau) {
     RowResult r;
-    if (s == 0.f) {
+    if (p.s == 0.f) {
         r.logp = r.lse = -INFINITY;
         r.h = 0.f;
         return r;
     }
-    const float l2 = log2f(s);
-    r.logp = (z_t - m) / tau - LN2 * l2;
-    r.lse = m / tau + LN2 * l2;
-    r.h = LN2 * (l2 - t / s);
+    const float l2 = log2f(p.s);
+    r.logp = (z_t - p.m) / tau - LN2 * l2;
+    r.lse = p.m / tau + LN2 * l2;
+    r.h = LN2 * (l2 - p.t / p.s);
     return r;
 }
 
-// ------------------------------------------------------------ statistics
+// What a row's gradient needs: d_j = 2^y_j (a + b y_j) + g [j = target]; none: zeros.
+struct Coef {
+    float m, a, b, g;
+    bool none;
+};
+// From the gradients g of logp and gh of H, times the call's scale over tau.
+template <bool ENT>
+__device__ __forceinline__ Coef coef_of(float m, float s, float h, float g, float gh) {
+    Coef c;
+    const float inv = 1.f / s;
+    c.m = m;
+    c.g = g;
+    c.b = ENT ? -gh * LN2 * inv : 0.f;
+    c.a = ENT ? -(g + gh * (h - LN2 * log2f(s))) * inv : -g * inv;
+    c.none = s == 0.f || (g == 0.f && gh == 0.f);
+    return c;
+}
+// The gradient of a group of logits, without the target's g.
+template <int DT, bool ENT, bool FAST>
+__device__ __forceinline__ uint4 grad_group(uint4 u, const Coef &c, const Shift &h) {
+    constexpr int H = Elem<DT>::N / 2;
+    f2 v[H];
+    unpack_pairs<DT>(u, v);
+    const f2 a = pair(c.a, c.a), b = pair(c.b, c.b);
+    float f[Elem<DT>::N];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+        const f2 y = h.apply<FAST>(v[i]), e = ex2(y);
+        const float2 d = both(ENT ? mul(e, fma(b, max2(y, Y_FLOOR), a)) : mul(e, a));
+        f[2 * i] = d.x;
+        f[2 * i + 1] = d.y;
+    }
+    return Elem<DT>::pack(f);
+}
+// The coefficients for exponents that are delta too large.
+__device__ __forceinline__ Coef shifted(Coef c, const Shift &h) {
+    const float f = ex2(-h.delta);
+    c.a = f * fmaf(-c.b, h.delta, c.a);
+    c.b *= f;
+    return c;
+}
+template <bool ENT>
+__device__ __forceinline__ float grad_target(float z_t, const Coef &c, float k) {
+    const float y = (z_t - c.m) * k;
+    return ex2(y) * (ENT ? fmaf(c.b, fmaxf(y, Y_FLOOR), c.a) : c.a) + c.g;
+}
 
-struct StatsParams {
-    LogitsIn in;
-    const float *row_w;  // a row with weight 0 is ignored (may be null)
-    const int32_t *off;  // rows before off[0] and from off[last] on are ignored (may be null)
-    int last;
-    float *logp, *lse, *entropy;
-    float2 *ms;          // (m, s) of each row (s = 0: nothing to differentiate), may be null
-    bool nan_target;     // a target past the vocabulary gives NaN (else it is ignored)
+// Zeros to n elements that start anywhere, by threads tid of nt.
+template <int DT>
+__device__ __forceinline__ void zero_row(char *out, int n, int tid, int nt) {
+    const Row<DT> o(out, n);
+    for (int g = o.begin() + tid; g < o.end(); g += nt)
+        *reinterpret_cast<uint4 *>(const_cast<char *>(o.base) + (size_t)g * 16) = make_uint4(0, 0, 0, 0);
+    typename Elem<DT>::bits *e = (typename Elem<DT>::bits *)out;
+    const int front = min(n, o.first(o.begin())), back = max(front, o.first(o.end()));
+    for (int i = tid; i < front; i += nt) e[i] = 0;
+    for (int i = back + tid; i < n; i += nt) e[i] = 0;
+}
+// The gradient of a whole row, read again from its logits, by threads tid of
+// nt, 16 bytes at a time where both rows allow it.
+template <int DT, bool ENT>
+__device__ __forceinline__ void grad_row(const char *z, char *out, int n, long long tgt, const Coef &c, float k, int tid,
+                                         int nt) {
+    using bits = typename Elem<DT>::bits;
+    const Row<DT> o(out, n), r(z, n);
+    const Shift h(c.m, k);
+    const bool same = (((uintptr_t)out ^ (uintptr_t)z) & 15) == 0;
+    for (int g = tid; g < o.groups(); g += nt) {
+        const int e0 = o.first(g);
+        uint4 u;
+        if (same) {
+            u = r.load(g);
+        } else {
+            bits b[Elem<DT>::N];
+#pragma unroll
+            for (int i = 0; i < Elem<DT>::N; ++i) b[i] = e0 + i >= 0 && e0 + i < n ? ((const bits *)z)[e0 + i] : 0;
+            u = *reinterpret_cast<const uint4 *>(b);
+        }
+        const uint4 d = grad_group<DT, ENT, false>(u, c, h);
+        if (o.whole(g)) {
+            *reinterpret_cast<uint4 *>((bits *)out + e0) = d;
+        } else {
+            Row<DT>::store_edge(out, e0, n, d);
+        }
+        if (tgt >= e0 && tgt < e0 + Elem<DT>::N)
+            ((bits *)out)[tgt] = Elem<DT>::round(grad_target<ENT>(logit_at<DT>(z, tgt), c, k));
+    }
+}
+
+// ------------------------------------------------------------ rows
+
+// A row of the policy loss: its target (-1: ignored), weight, advantage and
+// log-probability under the policy that drew it.
+struct __align__(16) PolicyRow {
+    int target;
+    float weight, advantage, old_logp;
 };
 
-template <int DT, bool ENT>
-__global__ void __launch_bounds__(THREADS) stats_kernel(const StatsParams P) {
-    pdl_wait();
-    pdl_trigger();
-    const long long row = blockIdx.x;
-    const long long tgt = target_of(P.in, row);
-    const bool bad = tgt >= P.in.vocab;
-    if (tgt < 0 || bad || (P.row_w && P.row_w[row] == 0.f) ||
-        (P.off && (row < P.off[0] || row >= P.off[P.last]))) {
-        if (threadIdx.x == 0) {
-            if (P.logp) P.logp[row] = bad && P.nan_target ? __int_as_float(0x7fffffff) : 0.f;
-            if (P.lse) P.lse[row] = 0.f;
-            if (P.entropy) P.entropy[row] = 0.f;
-            if (P.ms) P.ms[row] = make_float2(0.f, 0.f);
+struct RowParams {
+    LogitsIn in;
+    long long rows;
+    const int32_t *off;        // rows before off[0] and from off[last] on are ignored (may be null)
+    int last;
+    bool nan_target;           // a target past the vocabulary gives NaN (else it is ignored)
+    float *logp, *lse, *entropy;
+    float2 *ms;                // (m, s) of each row (s = 0: nothing to differentiate), may be null
+    // policy loss
+    const PolicyRow *meta;     // not null: the policy loss
+    const float *ref_logp;
+    float clip_low, clip_high, kl_coef, entropy_coef;
+    float *kl;
+    float4 *terms;             // w l, w pg, w kl, w H of each row
+    float2 *flags;             // w [clipped], and not 0 where something is not finite
+    float2 *g;                 // gradients of logp and H, where the logits' gradient comes later (may be null)
+    float scale;               // the call's scale / tau
+    char *dlogits;             // may be null
+    long long ld_d_bytes;
+};
+
+// A row's inputs besides its logits.  target < 0: ignored.
+__device__ __forceinline__ PolicyRow row_meta(const RowParams &P, long long row) {
+    if (P.meta) return *reinterpret_cast<const PolicyRow *>(P.meta + row);
+    const long long t = target_of(P.in, row);
+    PolicyRow q{t >= 0 && t < P.in.vocab ? (int)t : -1, 0.f, 0.f, 0.f};
+    if (P.off && (row < P.off[0] || row >= P.off[P.last])) q.target = -1;
+    return q;
+}
+
+// An ignored row's outputs.
+__device__ __forceinline__ void ignore_row(const RowParams &P, long long row) {
+    if (P.logp)
+        P.logp[row] = P.nan_target && target_of(P.in, row) >= P.in.vocab ? __int_as_float(0x7fffffff) : 0.f;
+    if (P.lse) P.lse[row] = 0.f;
+    if (P.entropy) P.entropy[row] = 0.f;
+    if (P.ms) P.ms[row] = make_float2(0.f, 0.f);
+    if (P.kl) P.kl[row] = 0.f;
+    if (P.terms) {
+        P.terms[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+        P.flags[row] = make_float2(0.f, 0.f);
+    }
+    if (P.g) P.g[row] = make_float2(0.f, 0.f);
+}
+
+// A row's outputs (where `write`) and the coefficients of its gradient.
+template <bool ENT>
+__device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, const PolicyRow &q, const Part &p,
+                                           float z_t, bool write) {
+    const RowResult r = row_result(p, z_t, P.in.tau);
+    if (write) {
+        if (P.logp) P.logp[row] = r.logp;
+        if (P.lse) P.lse[row] = r.lse;
+        if (P.entropy) P.entropy[row] = r.h;
+        if (P.ms) P.ms[row] = make_float2(p.m, p.s);
+    }
+    if (!P.meta) return Coef{};
+    float g = 0.f, gh = 0.f, kl = 0.f, clipped = 0.f, bad = 1.f;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.s != 0.f) {
+        const float w = q.weight, ratio = expf(r.logp - q.old_logp);
+        const float c = fminf(fmaxf(ratio, 1.f - P.clip_low), 1.f + P.clip_high);
+        const float u = ratio * q.advantage, v = c * q.advantage;
+        const bool open = !(u > v);
+        const float pg = open ? -u : -v;
+        float dlp = open ? -u : 0.f;
+        if (P.ref_logp) {
+            const float d = P.ref_logp[row] - r.logp, e = expf(d);
+            kl = e - d - 1.f;
+            dlp += P.kl_coef * (1.f - e);
         }
+        const float h = ENT ? r.h : 0.f, l = pg + P.kl_coef * kl - P.entropy_coef * h;
+        t = make_float4(w * l, w * pg, w * kl, w * h);
+        clipped = open ? 0.f : w;
+        g = w * dlp;
+        gh = -w * P.entropy_coef;
+        bad = finite(r.logp) && finite(t.x) && finite(g) ? 0.f : 1.f;
+    }
+    if (write) {
+        if (P.kl) P.kl[row] = kl;
+        P.terms[row] = t;
+        P.flags[row] = make_float2(clipped, bad);
+        if (P.g) P.g[row] = make_float2(g, gh);
+    }
+    return coef_of<ENT>(p.m, p.s, r.h, g * P.scale, gh * P.scale);
+}
+
+// The groups of a row that a thread keeps in registers between the row's
+// statistics and its gradient: group first + i step for i < count (at most VPT),
+// below `end`, and perhaps one of the row's edges.
+template <int DT, int VPT>
+struct Kept {
+    uint4 u[VPT];
+    int g0, step, end, at;
+    // `most`: how many groups any thread of the row has at most.  A thread without
+    // the last one loads the row's last whole group in its place.
+    __device__ __forceinline__ void load(const Row<DT> &r, int g0_, int step_, int end_, int most, int at_) {
+        g0 = g0_;
+        step = step_;
+        end = end_;
+        at = at_;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i < most) u[i] = r.load_whole(min(g0 + i * step, end - 1));
+    }
+    __device__ __forceinline__ float largest(const Row<DT> &r, int most) const {
+        auto m = Elem<DT>::lowest();
+        if (at >= 0) m = Elem<DT>::raise(m, r.load_edge(at));
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i < most) m = Elem<DT>::raise(m, u[i]);
+        return Elem<DT>::largest(m);
+    }
+    template <bool ENT>
+    __device__ __forceinline__ Sums<DT, ENT> sums(const Row<DT> &r, const Shift &h, int most, bool edges) const {
+        Sums<DT, ENT> s;
+        if (h.ok) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (i < most && g0 + i * step < end) s.template add<true>(u[i], h);
+        } else {
+            for (int g = g0; g < end; g += step) s.template add<false>(r.load_whole(g), h);
+        }
+        if (edges) {
+            const uint4 u = at >= 0 ? r.load_edge(at) : Row<DT>::none();
+            if (h.ok) s.template add<true>(u, h);
+            else s.template add<false>(u, h);
+        }
+        return s;
+    }
+    // The gradient of its groups; `out` starts as the row does modulo 16 bytes.
+    template <bool ENT>
+    __device__ __forceinline__ void gradient(const Row<DT> &r, char *out, const Coef &c, const Shift &h, int most) const {
+        char *o = out - r.phase * sizeof(typename Row<DT>::bits);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i < most && g0 + i * step < end)
+                *reinterpret_cast<uint4 *>(o + (size_t)(g0 + i * step) * 16) = grad_group<DT, ENT, true>(u[i], c, h);
+        if (at >= 0) Row<DT>::store_edge(out, r.first(at), r.n, grad_group<DT, ENT, true>(r.load_edge(at), c, h));
+    }
+    // Whether this thread writes the target's element.
+    __device__ __forceinline__ bool owns(const Row<DT> &r, int target) const {
+        const int g = (target + r.phase) / Elem<DT>::N;
+        return g == at || (g >= g0 && g < end && (g - g0) % step == 0);
+    }
+};
+
+// The gradient of a row whose thread's share is in `kept`.
+template <int DT, bool ENT, int VPT>
+__device__ __forceinline__ void write_gradient(const Kept<DT, VPT> &kept, const Row<DT> &r, const char *z, char *out,
+                                               int target, float z_t, const Coef &c, float k, int most, int tid, int nt) {
+    if (c.none) {
+        zero_row<DT>(out, r.n, tid, nt);
         return;
     }
-    const char *z = P.in.logits + row * P.in.ld_bytes;
-    const Row<DT> r(z, P.in.vocab);
-    const float k = P.in.k;
-    Stat<ENT> st;
-    const int G = r.groups();
-    for (int g = threadIdx.x; g < G; g += THREADS) {
-        float v[Elem<DT>::N];
-        Elem<DT>::unpack(r.load(g), v);
-        st.template add<Elem<DT>::N>(v, k);
+    const Shift h(c.m, k);
+    if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
+        grad_row<DT, ENT>(z, out, r.n, target, c, k, tid, nt);
+        return;
     }
-    st.merge_lanes(k);
-    __shared__ float3 part[THREADS / 32];
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = make_float3(st.m, st.s, st.t);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        Stat<ENT> all;
-        for (int i = 0; i < THREADS / 32; ++i) all.merge(part[i].x, part[i].y, part[i].z, k);
-        const RowResult q = row_result(all.m, all.s, all.t, logit_at<DT>(z, tgt), P.in.tau);
-        if (P.logp) P.logp[row] = q.logp;
-        if (P.lse) P.lse[row] = q.lse;
-        if (P.entropy) P.entropy[row] = q.h;
-        if (P.ms) P.ms[row] = make_float2(all.m, all.s);
+    kept.template gradient<ENT>(r, out, shifted(c, h), h, most);
+    // the thread that wrote the target's group adds its g
+    if (kept.owns(r, target))
+        ((typename Row<DT>::bits *)out)[target] = Elem<DT>::round(grad_target<ENT>(z_t, c, k));
+}
+
+// One row to L lanes of a warp (L = 8 or 32): rows of at most NV L whole groups.
+constexpr int SMALL_THREADS = 256, NV = 8;
+template <int DT, bool ENT, int L>
+__global__ void __launch_bounds__(SMALL_THREADS) lane_rows_kernel(const __grid_constant__ RowParams P) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x % L;
+    const float k = P.in.k;
+    // all lanes of a warp go round together: the reductions name them all
+    for (long long first = (long long)blockIdx.x * (SMALL_THREADS / L) + threadIdx.x / 32 * (32 / L); first < P.rows;
+         first += (long long)gridDim.x * (SMALL_THREADS / L)) {
+        const long long row = first + threadIdx.x % 32 / L;
+        const bool in = row < P.rows;
+        PolicyRow q{-1, 0.f, 0.f, 0.f};
+        if (in) q = row_meta(P, row);
+        const bool live = q.target >= 0;
+        const char *z = P.in.logits + (in ? row : 0) * P.in.ld_bytes;
+        const Row<DT> r(z, P.in.vocab);
+        const int most = live ? (r.end() - r.begin() + L - 1) / L : 0;
+        Kept<DT, NV> kept;
+        kept.load(r, r.begin() + lane, L, live ? r.end() : 0, most,
+                  !live ? -1 : lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? r.end() : -1);
+        const float z_t = live ? logit_at<DT>(z, q.target) : 0.f;
+        const Shift h(lanes_max(kept.largest(r, most), L), k);
+        const Part p = kept.template sums<ENT>(r, h, most, true).part(h, L);
+        char *out = P.dlogits ? P.dlogits + (in ? row : 0) * P.ld_d_bytes : nullptr;
+        if (!live) {
+            if (in && lane == 0) ignore_row(P, row);
+            if (in && out) zero_row<DT>(out, P.in.vocab, lane, L);
+            continue;
+        }
+        const Coef c = finish_row<ENT>(P, row, q, p, z_t, lane == 0);
+        if (out) write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, c, k, most, lane, L);
+    }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Stores a part into CTA `rank`'s copy of a shared variable.
+__device__ __forceinline__ void store_part(const float4 *local, int rank, float4 v) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+// One row to a cluster of CTAs of T threads, which keep it in registers
+// between its statistics and its gradient: rows of at most VPT T whole groups
+// a CTA.  Each warp sums relative to its own maximum; the warps' parts go to
+// every CTA of the cluster, whose first warp joins them.
+#ifndef BIG_T
+#define BIG_T 512
+#endif
+constexpr int MAX_CLUSTER = 8;
+template <int DT, bool ENT, int T, int VPT>
+__global__ void __launch_bounds__(T, VPT > NV ? 512 / T : 1024 / T) rows_kernel(const __grid_constant__ RowParams P, int cs) {
+    constexpr int W = T / 32;
+    __shared__ float4 parts[2][MAX_CLUSTER * W];
+    __shared__ Coef shared_coef;
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, rank = cs > 1 ? blockIdx.x % cs : 0;
+    const float k = P.in.k;
+    const long long step = gridDim.x / cs;
+    int turn = 0;
+    for (long long row = blockIdx.x / cs; row < P.rows; row += step) {
+        const PolicyRow q = row_meta(P, row);
+        char *out = P.dlogits ? P.dlogits + row * P.ld_d_bytes : nullptr;
+        if (q.target < 0) {
+            if (rank == 0 && tid == 0) ignore_row(P, row);
+            if (out) zero_row<DT>(out, P.in.vocab, rank * T + tid, cs * T);
+            continue;
+        }
+        const char *z = P.in.logits + row * P.in.ld_bytes;
+        const Row<DT> r(z, P.in.vocab);
+        // each CTA a run of groups
+        const int per = (r.end() - r.begin() + cs - 1) / cs;
+        const int c0 = r.begin() + rank * per, g1 = min(r.end(), c0 + per), most = (g1 - c0 + T - 1) / T;
+        Kept<DT, VPT> kept;
+        kept.load(r, c0 + tid, T, g1, most,
+                  rank != 0 ? -1 : tid == 0 && r.has_front() ? 0 : tid == 1 && r.has_back() ? r.end() : -1);
+        const float z_t = logit_at<DT>(z, q.target);
+        const Shift h(lanes_max(kept.largest(r, most), 32), k);
+        const Part mine = kept.template sums<ENT>(r, h, most, tid < 32).part(h, 32);
+        const float4 packed = make_float4(mine.m, mine.s, mine.t, 0.f);
+        if (cs > 1) {
+            if (tid % 32 < cs) store_part(&parts[turn][rank * W + tid / 32], tid % 32, packed);
+            cluster_sync();
+        } else {
+            if (tid % 32 == 0) parts[turn][tid / 32] = packed;
+            __syncthreads();
+        }
+        if (tid < 32) {
+            float M = -F32_MAX;
+            for (int i = tid; i < cs * W; i += 32) M = fmaxf(M, parts[turn][i].x);
+            M = lanes_max(M, 32);
+            Part all{M, 0.f, 0.f};
+            for (int i = tid; i < cs * W; i += 32) {
+                const float4 v = parts[turn][i];
+                const Part p = relative_to<ENT>(Part{v.x, v.y, v.z}, M, k);
+                all.s += p.s;
+                all.t += p.t;
+            }
+            all.s = lanes_sum(all.s, 32);
+            if (ENT) all.t = lanes_sum(all.t, 32);
+            const Coef c = finish_row<ENT>(P, row, q, all, z_t, rank == 0 && tid == 0);
+            if (tid == 0) shared_coef = c;
+        }
+        // the parts of the row after next come after the next row's barrier
+        turn ^= 1;
+        if (!out) continue;
+        __syncthreads();
+        write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, shared_coef, k, most, rank * T + tid, cs * T);
+    }
+}
+
+// Statistics of rows that are too long to be kept: one CTA to a row, which it
+// reads twice, once for each warp's maximum and once for the sums.
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(THREADS) long_rows_kernel(const __grid_constant__ RowParams P) {
+    pdl_wait();
+    pdl_trigger();
+    __shared__ Part parts[THREADS / 32];
+    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
+        const PolicyRow q = row_meta(P, row);
+        if (q.target < 0) {
+            if (threadIdx.x == 0) ignore_row(P, row);
+            continue;
+        }
+        const char *z = P.in.logits + row * P.in.ld_bytes;
+        const Row<DT> r(z, P.in.vocab);
+        const float k = P.in.k;
+        auto best = Elem<DT>::lowest();
+        for (int g = threadIdx.x; g < r.groups(); g += THREADS) best = Elem<DT>::raise(best, r.load(g));
+        const Shift h(lanes_max(Elem<DT>::largest(best), 32), k);
+        Sums<DT, ENT> sums;
+        Sum2 s;
+        for (int g = threadIdx.x; g < r.groups(); g += THREADS) s.add(sums.template group<false>(r.load(g), h));
+        sums.s = pair(s.total(), 0.f);
+        const Part mine = sums.part(Shift(h.m, 0.f), 32);
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = mine;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            Part all{-F32_MAX, 0.f, 0.f};
+            for (int i = 0; i < THREADS / 32; ++i) all.m = fmaxf(all.m, parts[i].m);
+            for (int i = 0; i < THREADS / 32; ++i) {
+                const Part p = relative_to<ENT>(parts[i], all.m, k);
+                all.s += p.s;
+                all.t += p.t;
+            }
+            finish_row<ENT>(P, row, q, all, logit_at<DT>(z, q.target), true);
+        }
     }
 }
 
@@ -114,49 +482,30 @@ __global__ void __launch_bounds__(THREADS) stats_kernel(const StatsParams P) {
 
 struct GradParams {
     LogitsIn in;
+    long long rows;
     const float2 *ms;       // (m, s) of each row
     const float *entropy;   // with gh
-    const float *g, *gh;    // gradients of logp and H (gh may be null)
+    const float *g, *gh;    // gradients of logp and H (gh may be null), gs apart
+    int gs;
     float scale;            // the call's scale / tau
     char *out;
     long long ld_out_bytes;
 };
 
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(THREADS) grad_kernel(const GradParams P) {
-    using E = Elem<DT>;
+__global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ GradParams P) {
     pdl_wait();
     pdl_trigger();
-    const long long row = blockIdx.x;
-    const long long tgt = target_of(P.in, row);
-    const Row<DT> r(P.in.logits + row * P.in.ld_bytes, P.in.vocab);
-    char *out = P.out + row * P.ld_out_bytes;
-    const bool same = (((uintptr_t)out ^ (uintptr_t)(P.in.logits + row * P.in.ld_bytes)) & 15) == 0;
-    const float k = P.in.k;
-    float g = P.g[row] * P.scale, gh = ENT ? P.gh[row] * P.scale : 0.f;
-    const float m = P.ms[row].x, s = P.ms[row].y;
-    const int G = r.groups();
-    if (tgt < 0 || tgt >= P.in.vocab || s == 0.f || (g == 0.f && gh == 0.f)) {
-        float v[E::N];
-#pragma unroll
-        for (int i = 0; i < E::N; ++i) v[i] = 0.f;
-        for (int q = threadIdx.x; q < G; q += THREADS) store_group<DT>(r, q, out, same, v);
-        return;
-    }
-    const float inv = 1.f / s;
-    const float b = ENT ? -gh * LN2 * inv : 0.f;
-    const float a = ENT ? -(g + gh * (P.entropy[row] - LN2 * log2f(s))) * inv : -g * inv;
-    for (int q = threadIdx.x; q < G; q += THREADS) {
-        float v[E::N];
-        E::unpack(r.load(q), v);
-        const int e0 = r.first(q);
-#pragma unroll
-        for (int i = 0; i < E::N; ++i) {
-            const float y = (v[i] - m) * k, e = ex2(y);
-            v[i] = ENT ? e * fmaf(b, fmaxf(y, Y_FLOOR), a) : e * a;
-            if (e0 + i == tgt) v[i] += g;
-        }
-        store_group<DT>(r, q, out, same, v);
+    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
+        const long long tgt = target_of(P.in, row);
+        const float2 ms = P.ms[row];
+        const Coef c = coef_of<ENT>(ms.x, ms.y, ENT ? P.entropy[row] : 0.f, P.g[row * P.gs] * P.scale,
+                                    ENT ? P.gh[row * P.gs] * P.scale : 0.f);
+        char *out = P.out + row * P.ld_out_bytes;
+        if (tgt < 0 || tgt >= P.in.vocab || c.none)
+            zero_row<DT>(out, P.in.vocab, threadIdx.x, THREADS);
+        else
+            grad_row<DT, ENT>(P.in.logits + row * P.in.ld_bytes, out, P.in.vocab, tgt, c, P.in.k, threadIdx.x, THREADS);
     }
 }
 
@@ -187,36 +536,31 @@ __device__ __forceinline__ T block_sum(T v, T *part) {
 }
 
 struct PolicyRows {
-    const void *target;
-    int target_i32, vocab;
+    LogitsIn in;
     long long rows;
-    const float *weight;
-    const float *advantage;
+    const float *weight, *advantage, *old_logp;
     const int32_t *off;
     int seqs, seq_mean;
-    float *row_w, *row_a;  // weight (0: ignored) and advantage of every row
+    PolicyRow *meta;
     int *err;
 };
 
-// One CTA: each row's weight and advantage.
-__global__ void __launch_bounds__(1024) policy_rows_kernel(const PolicyRows P) {
+// One CTA: every row's target, weight, advantage and old log-probability in one place.
+__global__ void __launch_bounds__(1024) policy_rows_kernel(const __grid_constant__ PolicyRows P) {
     pdl_wait();
     pdl_trigger();
     __shared__ int part[32];
-    auto target = [&](long long row) {
-        return P.target_i32 ? (long long)((const int32_t *)P.target)[row] : (long long)((const int64_t *)P.target)[row];
-    };
     int n = 0, bad = 0;
-    const int ends = P.seqs + 1;
     for (long long row = threadIdx.x; row < P.rows; row += blockDim.x) {
-        const long long t = target(row);
-        bad |= t >= P.vocab;
-        int seq = 0;
-        if (P.off) seq = sequence_of(P.off, ends, row);
-        const bool in = t >= 0 && t < P.vocab && seq >= 0 && (!P.off || seq < P.seqs);
-        n += in;
-        P.row_w[row] = in ? (P.weight ? P.weight[row] : 1.f) : 0.f;
-        P.row_a[row] = in ? P.advantage[P.off ? seq : row] : 0.f;
+        const long long t = target_of(P.in, row);
+        bad |= t >= P.in.vocab;
+        const int seq = P.off ? sequence_of(P.off, P.seqs + 1, row) : 0;
+        const float w = P.weight ? P.weight[row] : 1.f;
+        PolicyRow q{-1, 0.f, 0.f, 0.f};
+        if (t >= 0 && t < P.in.vocab && w != 0.f && seq >= 0 && (!P.off || seq < P.seqs))
+            q = PolicyRow{(int)t, w, P.advantage[P.off ? seq : row], P.old_logp[row]};
+        n += q.target >= 0;
+        P.meta[row] = q;
     }
     bad = block_sum(bad, part);
     if (threadIdx.x == 0) *P.err = bad ? ERR_TARGET : 0;
@@ -224,81 +568,50 @@ __global__ void __launch_bounds__(1024) policy_rows_kernel(const PolicyRows P) {
     if (P.weight) return;
     if (!P.seq_mean) {
         for (long long row = threadIdx.x; row < P.rows; row += blockDim.x)
-            if (P.row_w[row] != 0.f) P.row_w[row] = 1.f / (float)n;
+            if (P.meta[row].target >= 0) P.meta[row].weight = 1.f / (float)n;
         return;
     }
-    __syncthreads();
     for (int q = threadIdx.x / 32; q < P.seqs; q += blockDim.x / 32) {
         const long long r0 = clamp_row(P.off[q], P.rows), r1 = clamp_row(P.off[q + 1], P.rows);
         int c = 0;
-        for (long long row = r0 + (threadIdx.x & 31); row < r1; row += 32) c += P.row_w[row] != 0.f;
+        for (long long row = r0 + (threadIdx.x & 31); row < r1; row += 32) c += P.meta[row].target >= 0;
         c = __reduce_add_sync(0xffffffffu, c);
-        __syncwarp();
         for (long long row = r0 + (threadIdx.x & 31); row < r1; row += 32)
-            if (P.row_w[row] != 0.f) P.row_w[row] = 1.f / ((float)P.seqs * (float)c);
+            if (P.meta[row].target >= 0) P.meta[row].weight = 1.f / ((float)P.seqs * (float)c);
     }
 }
 
-struct PolicyTerms {
+struct PolicySum {
     long long rows;
-    const float *row_w, *row_a, *old_logp, *ref_logp;
-    const float *logp, *entropy;
-    const float2 *ms;
-    float clip_low, clip_high, kl_coef, entropy_coef;
-    float *kl;            // user's, may be null
-    float *g, *gh;        // gradients of logp and H (gh may be null)
+    const float4 *terms;
+    const float2 *flags;
     float *stats;
     int *err;
 };
 
-// One CTA: the loss terms of every row, their sums and the gradients.
-__global__ void __launch_bounds__(1024) policy_terms_kernel(const PolicyTerms P) {
+// One CTA: the sums of the rows' terms.
+__global__ void __launch_bounds__(1024) policy_sum_kernel(const __grid_constant__ PolicySum P) {
     pdl_wait();
     pdl_trigger();
     __shared__ double part[32];
     double sum[5] = {0, 0, 0, 0, 0};
     int bad = 0;
     for (long long row = threadIdx.x; row < P.rows; row += blockDim.x) {
-        const float w = P.row_w[row];
-        float g = 0.f, gh = 0.f, kl = 0.f;
-        if (w != 0.f) {
-            if (P.ms[row].y == 0.f) {
-                bad = 1;
-            } else {
-                const float lp = P.logp[row], a = P.row_a[row], h = P.entropy ? P.entropy[row] : 0.f;
-                const float r = expf(lp - P.old_logp[row]);
-                const float c = fminf(fmaxf(r, 1.f - P.clip_low), 1.f + P.clip_high);
-                const float u = r * a, v = c * a;
-                const bool open = !(u > v);
-                const float pg = open ? -u : -v;
-                float dlp = open ? -u : 0.f;
-                if (P.ref_logp) {
-                    const float d = P.ref_logp[row] - lp, e = expf(d);
-                    kl = e - d - 1.f;
-                    dlp += P.kl_coef * (1.f - e);
-                }
-                const float l = pg + P.kl_coef * kl - P.entropy_coef * h;
-                sum[0] += (double)w * l;
-                sum[1] += (double)w * pg;
-                sum[2] += (double)w * kl;
-                sum[3] += (double)w * h;
-                sum[4] += open ? 0. : (double)w;
-                g = w * dlp;
-                gh = -w * P.entropy_coef;
-                bad |= !finite(lp) || !finite(l) || !finite(g);
-            }
-        }
-        P.g[row] = g;
-        if (P.gh) P.gh[row] = gh;
-        if (P.kl) P.kl[row] = kl;
+        const float4 t = P.terms[row];
+        const float2 f = P.flags[row];
+        sum[0] += t.x;
+        sum[1] += t.y;
+        sum[2] += t.z;
+        sum[3] += t.w;
+        sum[4] += f.x;
+        bad |= f.y != 0.f;
     }
     for (int i = 0; i < 5; ++i) {
         const double s = block_sum(sum[i], part);
         if (threadIdx.x == 0) P.stats[i] = (float)s;
         if (i == 0) bad |= !finite((float)s);
     }
-    __shared__ int ipart[32];
-    bad = block_sum(bad, ipart);
+    bad = __syncthreads_or(bad);
     if (threadIdx.x == 0 && bad) *P.err |= ERR_NONFINITE;
 }
 
@@ -420,23 +733,50 @@ kfac_status by_type(int dtype, bool ent, F &&f) {
     return ent ? f.template run<KFAC_F32, true>() : f.template run<KFAC_F32, false>();
 }
 
-struct RunStats {
-    const StatsParams &P;
-    long long rows;
+struct RunRows {
+    const RowParams &P;
     cudaStream_t st;
+    // Whether a row of the call's width is kept on the chip.
+    static bool kept(int dtype, int vocab) {
+        return vocab / (dtype == KFAC_F32 ? 4 : 8) <= MAX_CLUSTER * BIG_T * 2 * NV;
+    }
     template <int DT, bool ENT>
     kfac_status run() {
-        KFAC_LAUNCH(KK_LOSS_ROWS, st, (stats_kernel<DT, ENT>), (unsigned)rows, THREADS, 0, P);
+        const long long whole = P.in.vocab / Elem<DT>::N;  // whole groups of a row, at most
+        if (whole <= 32 * NV) {
+            const int per = SMALL_THREADS / (whole <= 8 * NV ? 8 : 32);
+            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, per), 1 << 20);
+            if (whole <= 8 * NV)
+                KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 8>), grid, SMALL_THREADS, 0, P);
+            else
+                KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 32>), grid, SMALL_THREADS, 0, P);
+            return KFAC_OK;
+        }
+        const int T = whole <= 128 * NV ? 128 : BIG_T;
+        int cs = 1;
+        while (cs < MAX_CLUSTER && whole > (long long)cs * T * NV) cs *= 2;
+        // few rows: more CTAs to each, while a thread keeps two groups
+        while (cs < MAX_CLUSTER && P.rows * cs * 2 <= device_sm_count() && whole >= (long long)cs * T * 4) cs *= 2;
+        const unsigned grid = (unsigned)std::min<long long>(P.rows, 1 << 20) * cs;
+        if (T == 128)
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (rows_kernel<DT, ENT, 128, NV>), cs, grid, T, 0, P, cs);
+        else if (whole <= (long long)cs * T * NV)
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (rows_kernel<DT, ENT, BIG_T, NV>), cs, grid, T, 0, P, cs);
+        else if (kept(DT, P.in.vocab))
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (rows_kernel<DT, ENT, BIG_T, 2 * NV>), cs, grid, T, 0, P, cs);
+        else
+            KFAC_LAUNCH(KK_LOSS_ROWS, st, (long_rows_kernel<DT, ENT>), (unsigned)std::min<long long>(P.rows, 1 << 20),
+                        THREADS, 0, P);
         return KFAC_OK;
     }
 };
 struct RunGrad {
     const GradParams &P;
-    long long rows;
     cudaStream_t st;
     template <int DT, bool ENT>
     kfac_status run() {
-        KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT>), (unsigned)rows, THREADS, 0, P);
+        KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT>), (unsigned)std::min<long long>(P.rows, 1 << 20), THREADS, 0,
+                    P);
         return KFAC_OK;
     }
 };
@@ -481,20 +821,23 @@ kfac_status check_policy(const kfac_policy_desc *d) {
 
 struct PolicyPlan {
     int *err;
-    float *row_w, *row_a, *g, *gh, *logp, *h;
-    float2 *ms;
+    PolicyRow *meta;
+    float4 *terms;
+    float2 *flags, *ms, *g;
+    float *h;
 };
 PolicyPlan plan_policy(const kfac_policy_desc &d, Arena &ws) {
-    PolicyPlan p;
+    PolicyPlan p{};
     const size_t n = (size_t)d.rows;
     p.err = ws.take<int>(64);
-    p.row_w = ws.take<float>(n);
-    p.row_a = ws.take<float>(n);
-    p.g = ws.take<float>(n);
-    p.gh = ws.take<float>(n);
-    p.logp = ws.take<float>(n);
-    p.h = ws.take<float>(n);
-    p.ms = ws.take<float2>(n);
+    p.meta = ws.take<PolicyRow>(n);
+    p.terms = ws.take<float4>(n);
+    p.flags = ws.take<float2>(n);
+    if (!RunRows::kept(d.dtype, d.vocab)) {
+        p.ms = ws.take<float2>(n);
+        p.g = ws.take<float2>(n);
+        p.h = ws.take<float>(n);
+    }
     return p;
 }
 
@@ -546,8 +889,15 @@ extern "C" kfac_status kfac_token_logprob(const kfac_logprob_desc *desc, void *s
     if (d.rows == 0) return KFAC_OK;
     if (!d.logp || (uintptr_t)d.saved % 8) return KFAC_ERR_INVALID;
     if (!all_on_this_device({d.logits, d.target, d.logp, d.lse, d.entropy, d.saved})) return KFAC_ERR_INVALID;
-    StatsParams P{logits_in(d), nullptr, nullptr, 0, d.logp, d.lse, d.entropy, (float2 *)d.saved, true};
-    return by_type(d.dtype, d.entropy != nullptr, RunStats{P, d.rows, (cudaStream_t)stream});
+    RowParams P{};
+    P.in = logits_in(d);
+    P.rows = d.rows;
+    P.nan_target = true;
+    P.logp = d.logp;
+    P.lse = d.lse;
+    P.entropy = d.entropy;
+    P.ms = (float2 *)d.saved;
+    return by_type(d.dtype, d.entropy != nullptr, RunRows{P, (cudaStream_t)stream});
 }
 
 extern "C" kfac_status kfac_token_logprob_grad(const kfac_logprob_grad_desc *desc, void *stream) {
@@ -561,9 +911,9 @@ extern "C" kfac_status kfac_token_logprob_grad(const kfac_logprob_grad_desc *des
     if (s != KFAC_OK || d.rows == 0) return s;
     if (!all_on_this_device({d.logits, d.target, d.saved, d.entropy, d.dlogp, d.dentropy, d.dlogits}))
         return KFAC_ERR_INVALID;
-    GradParams P{logits_in(d), (const float2 *)d.saved, d.entropy, d.dlogp, d.dentropy, 1.f / d.temperature,
-                 (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
-    return by_type(d.dtype, d.dentropy != nullptr, RunGrad{P, d.rows, (cudaStream_t)stream});
+    GradParams P{logits_in(d), d.rows, (const float2 *)d.saved, d.entropy, d.dlogp, d.dentropy, 1,
+                 1.f / d.temperature, (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
+    return by_type(d.dtype, d.dentropy != nullptr, RunGrad{P, (cudaStream_t)stream});
 }
 
 extern "C" size_t kfac_policy_loss_workspace_size(const kfac_policy_desc *desc) {
@@ -586,23 +936,43 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
                              d.stats, d.logp, d.kl, d.entropy, d.dlogits}))
         return KFAC_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;
-    const bool ent = d.entropy_coef != 0.f || d.entropy;
-    float *h = d.entropy ? d.entropy : p.h, *logp = d.logp ? d.logp : p.logp;
-    PolicyRows R{d.target, d.target_i32, d.vocab, d.rows, d.weight, d.advantage, d.seq_offsets, d.seqs, d.seq_mean,
-                 p.row_w, p.row_a, p.err};
+    const LogitsIn in = logits_in(d);
+    PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta, p.err};
     KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_rows_kernel, 1, 1024, 0, R);
+    const bool kept = RunRows::kept(d.dtype, d.vocab), ent = d.entropy_coef != 0.f || d.entropy;
+    const float scale = d.grad_scale / d.temperature;
+    const long long ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
     if (d.rows > 0) {
-        StatsParams S{logits_in(d), p.row_w, nullptr, 0, logp, nullptr, ent ? h : nullptr, p.ms, false};
-        if ((s = by_type(d.dtype, ent, RunStats{S, d.rows, st})) != KFAC_OK) return s;
+        RowParams P{};
+        P.in = in;
+        P.rows = d.rows;
+        P.logp = d.logp;
+        P.entropy = d.entropy ? d.entropy : ent && !kept ? p.h : nullptr;
+        P.ms = p.ms;
+        P.meta = p.meta;
+        P.ref_logp = d.ref_logp;
+        P.clip_low = d.clip_low;
+        P.clip_high = d.clip_high;
+        P.kl_coef = d.kl_coef;
+        P.entropy_coef = d.entropy_coef;
+        P.kl = d.kl;
+        P.terms = p.terms;
+        P.flags = p.flags;
+        P.g = p.g;
+        P.scale = scale;
+        if (kept) {
+            P.dlogits = (char *)d.dlogits;
+            P.ld_d_bytes = ld_d_bytes;
+        }
+        if ((s = by_type(d.dtype, ent, RunRows{P, st})) != KFAC_OK) return s;
     }
+    PolicySum U{d.rows, p.terms, p.flags, d.stats, p.err};
+    KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_sum_kernel, 1, 1024, 0, U);
+    if (kept || !d.dlogits || d.rows == 0) return KFAC_OK;
     const bool ent_grad = d.entropy_coef != 0.f;
-    PolicyTerms T{d.rows, p.row_w, p.row_a, d.old_logp, d.ref_logp, logp, ent ? h : nullptr, p.ms, d.clip_low,
-                  d.clip_high, d.kl_coef, d.entropy_coef, d.kl, p.g, ent_grad ? p.gh : nullptr, d.stats, p.err};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_terms_kernel, 1, 1024, 0, T);
-    if (!d.dlogits || d.rows == 0) return KFAC_OK;
-    GradParams G{logits_in(d), p.ms, h, p.g, ent_grad ? p.gh : nullptr, d.grad_scale / d.temperature,
-                 (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
-    return by_type(d.dtype, ent_grad, RunGrad{G, d.rows, st});
+    GradParams G{in, d.rows, p.ms, d.entropy ? d.entropy : p.h, (const float *)p.g, (const float *)p.g + 1, 2, scale,
+                 (char *)d.dlogits, ld_d_bytes};
+    return by_type(d.dtype, ent_grad, RunGrad{G, st});
 }
 
 extern "C" size_t kfac_preference_loss_workspace_size(const kfac_preference_desc *desc) {
@@ -628,8 +998,14 @@ extern "C" kfac_status kfac_preference_loss(const kfac_preference_desc *desc, vo
     float *logp = d.token_logp ? d.token_logp : p.logp;
     KFAC_CUDA_TRY(cudaMemsetAsync(p.row_g, 0, (size_t)d.rows * sizeof(float), st));  // rows of no sequence
     if (d.rows > 0) {
-        StatsParams S{logits_in(d), nullptr, d.seq_offsets, 2 * d.pairs, logp, nullptr, nullptr, p.ms, false};
-        if ((s = by_type(d.dtype, false, RunStats{S, d.rows, st})) != KFAC_OK) return s;
+        RowParams P{};
+        P.in = logits_in(d);
+        P.rows = d.rows;
+        P.off = d.seq_offsets;
+        P.last = 2 * d.pairs;
+        P.logp = logp;
+        P.ms = p.ms;
+        if ((s = by_type(d.dtype, false, RunRows{P, st})) != KFAC_OK) return s;
     }
     PrefPairs Q{d.target, d.target_i32, d.vocab, d.rows, d.seq_offsets, d.pairs, d.ref_logp, d.pair_weight, d.kind,
                 d.average, d.beta, d.label_smoothing, logp, p.ms, p.row_g, p.terms, p.bad, d.pair_loss, d.seq_logp};
@@ -637,7 +1013,7 @@ extern "C" kfac_status kfac_preference_loss(const kfac_preference_desc *desc, vo
     PrefSum U{p.terms, p.bad, d.pairs, d.loss, p.err};
     KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_sum_kernel, 1, 256, 0, U);
     if (!d.dlogits || d.rows == 0) return KFAC_OK;
-    GradParams G{logits_in(d), p.ms, nullptr, p.row_g, nullptr, d.grad_scale / d.temperature,
+    GradParams G{logits_in(d), d.rows, p.ms, nullptr, p.row_g, nullptr, 1, d.grad_scale / d.temperature,
                  (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
-    return by_type(d.dtype, false, RunGrad{G, d.rows, st});
+    return by_type(d.dtype, false, RunGrad{G, st});
 }
