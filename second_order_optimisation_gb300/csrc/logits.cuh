@@ -305,6 +305,55 @@ struct Sums {
     }
 };
 
+// A thread's statistics of many groups, taken in batches: its maximum rises as
+// it goes, and the sums so far are scaled down with it.
+template <int DT, bool ENT>
+struct Running {
+    Sum2 s;
+    f2 t;
+    float m, k;
+    __device__ __forceinline__ explicit Running(float k_) : t(pair(0.f, 0.f)), m(-F32_MAX), k(k_) {}
+    __device__ __forceinline__ void raise(float to) {
+        if (to > m) {
+            const float d = (m - to) * k, c = ex2(d), f = fmaxf(d, Y_FLOOR);
+            const f2 c2 = pair(c, c);
+            if (ENT) t = mul(c2, fma(pair(f, f), s.s, t));
+            s.s = mul(s.s, c2);
+            s.c = mul(s.c, c2);
+            m = to;
+        }
+    }
+    // The groups u[i], i < most, that lie below `end` (the i-th at g + i step).
+    template <int VPT>
+    __device__ __forceinline__ void add(const uint4 *u, int most, int g, int step, int end) {
+        auto best = Elem<DT>::lowest();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            if (i < most) best = Elem<DT>::raise(best, u[i]);
+        raise(Elem<DT>::largest(best));
+        const Shift h(m, k);
+        Sums<DT, ENT> batch;
+        if (h.ok) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (i < most && g + i * step < end) batch.template add<true>(u[i], h);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                if (i < most && g + i * step < end) batch.template add<false>(u[i], h);
+        }
+        const float f = ex2(-h.delta);
+        if (ENT) t = kfac::add(t, mul(pair(f, f), fma(pair(-h.delta, -h.delta), batch.s, batch.t)));
+        s.add(mul(pair(f, f), batch.s));
+    }
+    // The warp's.
+    __device__ __forceinline__ Part part() {
+        raise(lanes_max(m, 32));
+        const float2 tt = both(t);
+        return Part{m, lanes_sum(s.total(), 32), ENT ? lanes_sum(tt.x + tt.y, 32) : 0.f};
+    }
+};
+
 // A part's sums, relative to a maximum M >= p.m.
 template <bool ENT>
 __device__ __forceinline__ Part relative_to(Part p, float M, float k) {

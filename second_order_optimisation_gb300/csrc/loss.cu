@@ -11,6 +11,7 @@
 // The maximum is subtracted before the scaling, so that rows whose logits are
 // all the type's lowest value stay finite.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "logits.cuh"
@@ -171,6 +172,7 @@ struct RowParams {
     float4 *terms;             // w l, w pg, w kl, w H of each row
     float2 *flags;             // w [clipped], and not 0 where something is not finite
     float2 *g;                 // gradients of logp and H, where the logits' gradient comes later (may be null)
+    int *err;
     float scale;               // the call's scale / tau
     char *dlogits;             // may be null
     long long ld_d_bytes;
@@ -202,8 +204,8 @@ __device__ __forceinline__ void ignore_row(const RowParams &P, long long row) {
 
 // A row's outputs (where `write`) and the coefficients of its gradient.
 template <bool ENT>
-__device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, const PolicyRow &q, const Part &p,
-                                           float z_t, bool write) {
+__device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, const PolicyRow &q, float ref,
+                                           const Part &p, float z_t, bool write) {
     const RowResult r = row_result(p, z_t, P.in.tau);
     if (write) {
         if (P.logp) P.logp[row] = r.logp;
@@ -222,7 +224,7 @@ __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, co
         const float pg = open ? -u : -v;
         float dlp = open ? -u : 0.f;
         if (P.ref_logp) {
-            const float d = P.ref_logp[row] - r.logp, e = expf(d);
+            const float d = ref - r.logp, e = expf(d);
             kl = e - d - 1.f;
             dlp += P.kl_coef * (1.f - e);
         }
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(SMALL_THREADS) lane_rows_kernel(const __grid_c
         Kept<DT, NV> kept;
         kept.load(r, r.begin() + lane, L, live ? r.end() : 0, most,
                   !live ? -1 : lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? r.end() : -1);
-        const float z_t = live ? logit_at<DT>(z, q.target) : 0.f;
+        const float z_t = live ? logit_at<DT>(z, q.target) : 0.f, ref = live && P.ref_logp ? P.ref_logp[row] : 0.f;
         const Shift h(lanes_max(kept.largest(r, most), L), k);
         const Part p = kept.template sums<ENT>(r, h, most, true).part(h, L);
         char *out = P.dlogits ? P.dlogits + (in ? row : 0) * P.ld_d_bytes : nullptr;
@@ -352,11 +354,12 @@ __global__ void __launch_bounds__(SMALL_THREADS) lane_rows_kernel(const __grid_c
             if (in && out) zero_row<DT>(out, P.in.vocab, lane, L);
             continue;
         }
-        const Coef c = finish_row<ENT>(P, row, q, p, z_t, lane == 0);
+        const Coef c = finish_row<ENT>(P, row, q, ref, p, z_t, lane == 0);
         if (out) write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, c, k, most, lane, L);
     }
 }
 
+constexpr int MAX_CLUSTER = 8;
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -368,19 +371,32 @@ __device__ __forceinline__ void store_part(const float4 *local, int rank, float4
                  : "memory");
 }
 
-// One row to a cluster of CTAs of T threads, which keep it in registers
-// between its statistics and its gradient: rows of at most VPT T whole groups
-// a CTA.  Each warp sums relative to its own maximum; the warps' parts go to
-// every CTA of the cluster, whose first warp joins them.
-#ifndef BIG_T
-#define BIG_T 512
-#endif
-constexpr int MAX_CLUSTER = 8;
-template <int DT, bool ENT, int T, int VPT>
-__global__ void __launch_bounds__(T, VPT > NV ? 512 / T : 1024 / T) rows_kernel(const __grid_constant__ RowParams P, int cs) {
-    constexpr int W = T / 32;
+// The parts of one row from all warps that worked on it, joined by one warp.
+template <bool ENT>
+__device__ __forceinline__ Part join_parts(const float4 *parts, int n, float k) {
+    const int lane = threadIdx.x % 32;
+    float M = -F32_MAX;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, parts[i].x);
+    M = lanes_max(M, 32);
+    Part all{M, 0.f, 0.f};
+    for (int i = lane; i < n; i += 32) {
+        const float4 v = parts[i];
+        const Part p = relative_to<ENT>(Part{v.x, v.y, v.z}, M, k);
+        all.s += p.s;
+        all.t += p.t;
+    }
+    all.s = lanes_sum(all.s, 32);
+    if (ENT) all.t = lanes_sum(all.t, 32);
+    return all;
+}
+
+// Statistics only: one row to a CTA or, where there are few rows, to a cluster
+// of cs CTAs, each with a run of the row's groups.
+constexpr int STREAM_THREADS = 256, BATCH = 4;
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(STREAM_THREADS, 6) stream_rows_kernel(const __grid_constant__ RowParams P, int cs) {
+    constexpr int T = STREAM_THREADS, W = T / 32;
     __shared__ float4 parts[2][MAX_CLUSTER * W];
-    __shared__ Coef shared_coef;
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, rank = cs > 1 ? blockIdx.x % cs : 0;
@@ -389,23 +405,30 @@ __global__ void __launch_bounds__(T, VPT > NV ? 512 / T : 1024 / T) rows_kernel(
     int turn = 0;
     for (long long row = blockIdx.x / cs; row < P.rows; row += step) {
         const PolicyRow q = row_meta(P, row);
-        char *out = P.dlogits ? P.dlogits + row * P.ld_d_bytes : nullptr;
         if (q.target < 0) {
             if (rank == 0 && tid == 0) ignore_row(P, row);
-            if (out) zero_row<DT>(out, P.in.vocab, rank * T + tid, cs * T);
             continue;
         }
         const char *z = P.in.logits + row * P.in.ld_bytes;
         const Row<DT> r(z, P.in.vocab);
-        // each CTA a run of groups
         const int per = (r.end() - r.begin() + cs - 1) / cs;
-        const int c0 = r.begin() + rank * per, g1 = min(r.end(), c0 + per), most = (g1 - c0 + T - 1) / T;
-        Kept<DT, VPT> kept;
-        kept.load(r, c0 + tid, T, g1, most,
-                  rank != 0 ? -1 : tid == 0 && r.has_front() ? 0 : tid == 1 && r.has_back() ? r.end() : -1);
-        const float z_t = logit_at<DT>(z, q.target);
-        const Shift h(lanes_max(kept.largest(r, most), 32), k);
-        const Part mine = kept.template sums<ENT>(r, h, most, tid < 32).part(h, 32);
+        const int c0 = r.begin() + rank * per, g1 = min(r.end(), c0 + per);
+        const int at = rank != 0 ? -1 : tid == 0 && r.has_front() ? 0 : tid == 1 && r.has_back() ? r.end() : -1;
+        const float z_t = logit_at<DT>(z, q.target), ref = P.ref_logp ? P.ref_logp[row] : 0.f;
+        Running<DT, ENT> run(k);
+        for (int g = c0; g < g1; g += BATCH * T) {
+            uint4 u[BATCH];
+            const int most = min(BATCH, (g1 - g + T - 1) / T);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (i < most) u[i] = r.load_whole(min(g + i * T + tid, g1 - 1));
+            run.template add<BATCH>(u, most, g + tid, T, g1);
+        }
+        if (at >= 0) {
+            const uint4 u = r.load_edge(at);
+            run.template add<1>(&u, 1, 0, 1, 1);
+        }
+        const Part mine = run.part();
         const float4 packed = make_float4(mine.m, mine.s, mine.t, 0.f);
         if (cs > 1) {
             if (tid % 32 < cs) store_part(&parts[turn][rank * W + tid / 32], tid % 32, packed);
@@ -415,67 +438,232 @@ __global__ void __launch_bounds__(T, VPT > NV ? 512 / T : 1024 / T) rows_kernel(
             __syncthreads();
         }
         if (tid < 32) {
-            float M = -F32_MAX;
-            for (int i = tid; i < cs * W; i += 32) M = fmaxf(M, parts[turn][i].x);
-            M = lanes_max(M, 32);
-            Part all{M, 0.f, 0.f};
-            for (int i = tid; i < cs * W; i += 32) {
-                const float4 v = parts[turn][i];
-                const Part p = relative_to<ENT>(Part{v.x, v.y, v.z}, M, k);
-                all.s += p.s;
-                all.t += p.t;
-            }
-            all.s = lanes_sum(all.s, 32);
-            if (ENT) all.t = lanes_sum(all.t, 32);
-            const Coef c = finish_row<ENT>(P, row, q, all, z_t, rank == 0 && tid == 0);
-            if (tid == 0) shared_coef = c;
+            const Part all = join_parts<ENT>(parts[turn], cs * W, k);
+            finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && tid == 0);
         }
-        // the parts of the row after next come after the next row's barrier
-        turn ^= 1;
-        if (!out) continue;
-        __syncthreads();
-        write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, shared_coef, k, most, rank * T + tid, cs * T);
+        turn ^= 1;  // the parts of the row after next come after the next row's barrier
     }
 }
 
-// Statistics of rows that are too long to be kept: one CTA to a row, which it
-// reads twice, once for each warp's maximum and once for the sums.
+// Statistics and gradient of rows that a cluster of cs CTAs keeps in shared
+// memory: a persistent CTA on each SM, a warp that fetches the coming rows' runs
+// of groups into a ring of stages (one bulk copy each), and two teams of warps
+// that take the rows in turn, so that one computes while the other waits for
+// its row's statistics to be joined.  A team's warps send their parts to every
+// CTA of the cluster, each of which joins them itself.
+constexpr int TEAMS = 2, TEAM = 256, TEAM_WARPS = TEAM / 32, RING_THREADS = TEAMS * TEAM + 32, MAX_STAGES = 8;
+constexpr int RING_BYTES = 221184;  // of shared memory for the stages: three of 4608 groups
+
+struct StageRow {
+    PolicyRow q;
+    float ref, z_t;
+};
+struct RingShared {
+    float4 parts[TEAMS][2][MAX_CLUSTER * TEAM_WARPS];
+    Coef coef[TEAMS][2];
+    StageRow row[MAX_STAGES];
+    long long given[MAX_STAGES];  // the row (counted within the cluster) that the stage was given to last
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES], joined[TEAMS][2];
+    int dead;
+};
+
+// Stores a part into CTA `rank`'s copy of a shared variable and counts its
+// bytes on that CTA's barrier.
+__device__ __forceinline__ void send_part(const float4 *local, const uint64_t *bar, int rank, float4 v) {
+    uint32_t a, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(a),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(b)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// The team's barrier; whether any of its threads gave true, the same for all of them.
+__device__ __forceinline__ bool team_any(int team, bool v) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(team + 1), "r"(TEAM), "r"((uint32_t)v)
+        : "memory");
+    return any != 0;
+}
+
+// Waits for the stage that holds the cluster's row n.  The stage's last use may
+// have been the other team's, its copy still under way; the barrier's parity tells
+// one use from the next only once the stage has been given to row n.
+__device__ __forceinline__ bool wait_stage(RingShared &sh, int st, long long n, int parity) {
+    const volatile long long *given = &sh.given[st];
+    if (!mbar_wait(&sh.full[st], parity)) return false;
+    if (*given != n) {
+        const uint64_t t0 = global_timer_ns();
+        while (*given != n)
+            if (global_timer_ns() - t0 > 2000000000ull) return false;
+        if (!mbar_wait(&sh.full[st], parity)) return false;
+    }
+    return true;
+}
+
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(THREADS) long_rows_kernel(const __grid_constant__ RowParams P) {
+__global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid_constant__ RowParams P, int cs, int stages,
+                                                                    int stage_bytes) {
+    extern __shared__ __align__(128) char ring[];
+    __shared__ RingShared sh;
+    const int tid = threadIdx.x, rank = blockIdx.x % cs;
+    const float k = P.in.k;
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            sh.given[i] = -1;
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], TEAM_WARPS);
+        }
+        for (int i = 0; i < 2 * TEAMS; ++i) mbar_init(&sh.joined[i / 2][i % 2], 1);
+        sh.dead = 0;
+        fence_barrier_init();
+    }
+    cluster_sync();
     pdl_wait();
     pdl_trigger();
-    __shared__ Part parts[THREADS / 32];
-    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
-        const PolicyRow q = row_meta(P, row);
-        if (q.target < 0) {
-            if (threadIdx.x == 0) ignore_row(P, row);
-            continue;
-        }
-        const char *z = P.in.logits + row * P.in.ld_bytes;
-        const Row<DT> r(z, P.in.vocab);
-        const float k = P.in.k;
-        auto best = Elem<DT>::lowest();
-        for (int g = threadIdx.x; g < r.groups(); g += THREADS) best = Elem<DT>::raise(best, r.load(g));
-        const Shift h(lanes_max(Elem<DT>::largest(best), 32), k);
-        Sums<DT, ENT> sums;
-        Sum2 s;
-        for (int g = threadIdx.x; g < r.groups(); g += THREADS) s.add(sums.template group<false>(r.load(g), h));
-        sums.s = pair(s.total(), 0.f);
-        const Part mine = sums.part(Shift(h.m, 0.f), 32);
-        __syncthreads();
-        if (threadIdx.x % 32 == 0) parts[threadIdx.x / 32] = mine;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            Part all{-F32_MAX, 0.f, 0.f};
-            for (int i = 0; i < THREADS / 32; ++i) all.m = fmaxf(all.m, parts[i].m);
-            for (int i = 0; i < THREADS / 32; ++i) {
-                const Part p = relative_to<ENT>(parts[i], all.m, k);
-                all.s += p.s;
-                all.t += p.t;
+    const long long first = blockIdx.x / cs, step = gridDim.x / cs;
+    const long long count = first < P.rows ? (P.rows - first + step - 1) / step : 0;  // rows of this cluster
+    // a CTA's run of a row's whole groups
+    auto run_of = [&](const Row<DT> &r, int &c0, int &g1) {
+        const int per = (r.end() - r.begin() + cs - 1) / cs;
+        c0 = r.begin() + rank * per;
+        g1 = min(r.end(), c0 + per);
+    };
+
+    if (tid >= TEAMS * TEAM) {  // ---- the warp that fetches
+        const int lane = tid % 32;
+        bool ok = true;
+        for (long long n0 = 0; n0 < count && ok; n0 += 32) {
+            // the inputs of 32 rows at once, one to a lane
+            StageRow mine{{-1, 0.f, 0.f, 0.f}, 0.f, 0.f};
+            if (n0 + lane < count) {
+                const long long row = first + (n0 + lane) * step;
+                mine.q = row_meta(P, row);
+                if (mine.q.target >= 0) {
+                    mine.z_t = logit_at<DT>(P.in.logits + row * P.in.ld_bytes, mine.q.target);
+                    if (P.ref_logp) mine.ref = P.ref_logp[row];
+                }
             }
-            finish_row<ENT>(P, row, q, all, logit_at<DT>(z, q.target), true);
+            for (int j = 0; j < 32 && n0 + j < count; ++j) {
+                const long long n = n0 + j;
+                const int st = (int)(n % stages);
+                ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[st], (int)(n / stages & 1) ^ 1));
+                if (!ok) break;
+                if (lane == j) {
+                    sh.row[st] = mine;
+                    *(volatile long long *)&sh.given[st] = n;
+                    const Row<DT> r(P.in.logits + (first + n * step) * P.in.ld_bytes, P.in.vocab);
+                    int c0, g1;
+                    run_of(r, c0, g1);
+                    if (mine.q.target >= 0 && g1 > c0) {
+                        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)(g1 - c0) * 16);
+                        bulk_load(ring + (size_t)st * stage_bytes, r.base + (size_t)c0 * 16, (uint32_t)(g1 - c0) * 16,
+                                  &sh.full[st]);
+                    } else {
+                        mbar_arrive(&sh.full[st]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok && lane == 0) {
+            atomicOr(P.err, ERR_TIMEOUT_EMPTY);
+            sh.dead = 1;
+        }
+    } else {  // ---- the teams
+        const int team = tid / TEAM, t = tid % TEAM;
+        int turn = 0;  // counts the team's rows that are not ignored
+        for (long long n = team; n < count; n += TEAMS) {
+            const long long row = first + n * step;
+            const int st = (int)(n % stages);
+            // A wait that runs out is noted, and the team leaves after its next barrier.
+            if (!wait_stage(sh, st, n, (int)(n / stages & 1))) {
+                if (t % 32 == 0) atomicOr(P.err, ERR_TIMEOUT_FULL);
+                *(volatile int *)&sh.dead = 1;
+            }
+            const StageRow in = sh.row[st];
+            char *out = P.dlogits + row * P.ld_d_bytes;
+            const char *z = P.in.logits + row * P.in.ld_bytes;
+            if (in.q.target < 0) {
+                __syncwarp();
+                if (t % 32 == 0) mbar_arrive(&sh.empty[st]);
+                if (rank == 0 && t == 0) ignore_row(P, row);
+                zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
+                if (team_any(team, *(volatile int *)&sh.dead != 0)) break;
+                continue;
+            }
+            const Row<DT> r(z, P.in.vocab);
+            int c0, g1;
+            run_of(r, c0, g1);
+            const int G = g1 - c0;
+            const uint4 *stage = (const uint4 *)(ring + (size_t)st * stage_bytes);
+            const int at = rank != 0 ? -1 : t == 0 && r.has_front() ? 0 : t == 1 && r.has_back() ? r.end() : -1;
+            Running<DT, ENT> run(k);
+            for (int g = 0; g < G; g += NV * TEAM) {
+                uint4 u[NV];
+                const int most = min(NV, (G - g + TEAM - 1) / TEAM);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (i < most) u[i] = stage[min(g + i * TEAM + t, G - 1)];
+                run.template add<NV>(u, most, g + t, TEAM, G);
+            }
+            if (at >= 0) {
+                const uint4 u = r.load_edge(at);
+                run.template add<1>(&u, 1, 0, 1, 1);
+            }
+            const Part mine = run.part();
+            const int b = turn & 1;
+            if (t % 32 < cs)
+                send_part(&sh.parts[team][b][rank * TEAM_WARPS + t / 32], &sh.joined[team][b], t % 32,
+                          make_float4(mine.m, mine.s, mine.t, 0.f));
+            if (t < 32) {
+                if (t == 0) mbar_arrive_expect_tx(&sh.joined[team][b], cs * TEAM_WARPS * 16);
+                if (!mbar_wait(&sh.joined[team][b], turn >> 1 & 1)) {
+                    if (t == 0) atomicOr(P.err, ERR_TIMEOUT_ACC);
+                    *(volatile int *)&sh.dead = 1;
+                }
+                const Part all = join_parts<ENT>(sh.parts[team][b], cs * TEAM_WARPS, k);
+                const Coef c = finish_row<ENT>(P, row, in.q, in.ref, all, in.z_t, rank == 0 && t == 0);
+                if (t == 0) sh.coef[team][b] = c;
+            }
+            ++turn;
+            if (team_any(team, *(volatile int *)&sh.dead != 0)) break;
+            const Coef c = sh.coef[team][b];
+            const Shift h(c.m, k);
+            if (c.none) {
+                zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
+            } else if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
+                grad_row<DT, ENT>(z, out, P.in.vocab, in.q.target, c, k, rank * TEAM + t, cs * TEAM);
+            } else {
+                const Coef d = shifted(c, h);
+                uint4 *o = (uint4 *)(out - r.phase * sizeof(typename Row<DT>::bits)) + c0;
+#pragma unroll 4
+                for (int g = t; g < G; g += TEAM) o[g] = grad_group<DT, ENT, true>(stage[g], d, h);
+                if (at >= 0)
+                    Row<DT>::store_edge(out, r.first(at), r.n, grad_group<DT, ENT, true>(r.load_edge(at), d, h));
+                // the thread that wrote the target's group adds its g
+                const int tg = (in.q.target + r.phase) / Elem<DT>::N;
+                if (tg == at || (tg >= c0 && tg < g1 && (tg - c0) % TEAM == t))
+                    ((typename Row<DT>::bits *)out)[in.q.target] = Elem<DT>::round(grad_target<ENT>(in.z_t, c, k));
+            }
+            __syncwarp();
+            if (t % 32 == 0) mbar_arrive(&sh.empty[st]);
         }
     }
+    __syncthreads();
+    if (sh.dead && tid == 0)  // copies in flight land before the CTA leaves
+        for (int i = 0; i < stages; ++i)
+            if (!mbar_wait(&sh.full[i], 0, 100000000ull)) mbar_wait(&sh.full[i], 1, 100000000ull);
+    // no CTA leaves while others may still write into its shared memory
+    cluster_sync();
 }
 
 // ------------------------------------------------------------ gradient
@@ -733,16 +921,29 @@ kfac_status by_type(int dtype, bool ent, F &&f) {
     return ent ? f.template run<KFAC_F32, true>() : f.template run<KFAC_F32, false>();
 }
 
+// How rows are kept in shared memory: by how many CTAs, in how many stages.
+struct Ring {
+    int cs, stages, bytes;  // cs = 0: they do not fit
+};
+Ring ring_of(int dtype, int vocab, long long rows) {
+    const long long whole = vocab / (dtype == KFAC_F32 ? 4 : 8);  // whole groups of a row, at most
+    Ring g{1, 0, 0};
+    auto bytes = [&](int cs) { return ceil_div(whole, cs) * 16; };
+    while (g.cs < MAX_CLUSTER && bytes(g.cs) > RING_BYTES / 3) g.cs *= 2;
+    // few rows: more CTAs to each, while a thread has two groups
+    while (g.cs < MAX_CLUSTER && rows * g.cs * 2 <= device_sm_count() && whole >= (long long)g.cs * TEAM * 4) g.cs *= 2;
+    if (bytes(g.cs) > RING_BYTES / 2) return Ring{0, 0, 0};
+    g.bytes = (int)align_up((size_t)bytes(g.cs), 128);
+    g.stages = (int)std::min<long long>(MAX_STAGES, RING_BYTES / std::max(g.bytes, 128));
+    return g;
+}
+
 struct RunRows {
     const RowParams &P;
     cudaStream_t st;
-    // Whether a row of the call's width is kept on the chip.
-    static bool kept(int dtype, int vocab) {
-        return vocab / (dtype == KFAC_F32 ? 4 : 8) <= MAX_CLUSTER * BIG_T * 2 * NV;
-    }
     template <int DT, bool ENT>
     kfac_status run() {
-        const long long whole = P.in.vocab / Elem<DT>::N;  // whole groups of a row, at most
+        const long long whole = P.in.vocab / Elem<DT>::N;
         if (whole <= 32 * NV) {
             const int per = SMALL_THREADS / (whole <= 8 * NV ? 8 : 32);
             const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, per), 1 << 20);
@@ -752,21 +953,41 @@ struct RunRows {
                 KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 32>), grid, SMALL_THREADS, 0, P);
             return KFAC_OK;
         }
-        const int T = whole <= 128 * NV ? 128 : BIG_T;
+        const Ring g = P.dlogits ? ring_of(DT, P.in.vocab, P.rows) : Ring{0, 0, 0};
+        if (g.cs) {
+            auto kernel = ring_rows_kernel<DT, ENT>;
+            static std::atomic<int> ready[64][4];  // by device and cluster size: clusters that run at once
+            int dev = 0, lg = 0;
+            if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KFAC_ERR_CUDA;
+            while ((1 << lg) < g.cs) ++lg;
+            int most = ready[dev][lg].load(std::memory_order_relaxed);
+            if (most == 0) {
+                KFAC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES));
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(device_sm_count() / g.cs * g.cs);
+                cfg.blockDim = dim3(RING_THREADS);
+                cfg.dynamicSmemBytes = RING_BYTES;
+                cudaLaunchAttribute attr[1];
+                attr[0].id = cudaLaunchAttributeClusterDimension;
+                attr[0].val.clusterDim.x = g.cs;
+                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+                cfg.attrs = attr;
+                cfg.numAttrs = 1;
+                KFAC_CUDA_TRY(cudaOccupancyMaxActiveClusters(&most, kernel, &cfg));
+                if (most < 1) return KFAC_ERR_CUDA;
+                ready[dev][lg].store(most, std::memory_order_relaxed);
+            }
+            const unsigned grid = (unsigned)std::min<long long>(P.rows, most) * g.cs;
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, kernel, g.cs, grid, RING_THREADS, (size_t)g.stages * g.bytes, P, g.cs,
+                                 g.stages, g.bytes);
+            return KFAC_OK;
+        }
+        // few rows: more CTAs to each, while a thread has two groups
         int cs = 1;
-        while (cs < MAX_CLUSTER && whole > (long long)cs * T * NV) cs *= 2;
-        // few rows: more CTAs to each, while a thread keeps two groups
-        while (cs < MAX_CLUSTER && P.rows * cs * 2 <= device_sm_count() && whole >= (long long)cs * T * 4) cs *= 2;
+        while (cs < MAX_CLUSTER && P.rows * cs * 2 <= device_sm_count() && whole >= (long long)cs * STREAM_THREADS * 4)
+            cs *= 2;
         const unsigned grid = (unsigned)std::min<long long>(P.rows, 1 << 20) * cs;
-        if (T == 128)
-            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (rows_kernel<DT, ENT, 128, NV>), cs, grid, T, 0, P, cs);
-        else if (whole <= (long long)cs * T * NV)
-            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (rows_kernel<DT, ENT, BIG_T, NV>), cs, grid, T, 0, P, cs);
-        else if (kept(DT, P.in.vocab))
-            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (rows_kernel<DT, ENT, BIG_T, 2 * NV>), cs, grid, T, 0, P, cs);
-        else
-            KFAC_LAUNCH(KK_LOSS_ROWS, st, (long_rows_kernel<DT, ENT>), (unsigned)std::min<long long>(P.rows, 1 << 20),
-                        THREADS, 0, P);
+        KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (stream_rows_kernel<DT, ENT>), cs, grid, STREAM_THREADS, 0, P, cs);
         return KFAC_OK;
     }
 };
@@ -823,9 +1044,13 @@ struct PolicyPlan {
     int *err;
     PolicyRow *meta;
     float4 *terms;
-    float2 *flags, *ms, *g;
+    float2 *flags, *ms, *g;  // ms, g, h: for rows that do not fit the chip
     float *h;
 };
+bool rows_kept(const kfac_policy_desc &d) {
+    const long long whole = d.vocab / (d.dtype == KFAC_F32 ? 4 : 8);
+    return whole <= 32 * NV || ring_of(d.dtype, d.vocab, d.rows).cs;
+}
 PolicyPlan plan_policy(const kfac_policy_desc &d, Arena &ws) {
     PolicyPlan p{};
     const size_t n = (size_t)d.rows;
@@ -833,7 +1058,7 @@ PolicyPlan plan_policy(const kfac_policy_desc &d, Arena &ws) {
     p.meta = ws.take<PolicyRow>(n);
     p.terms = ws.take<float4>(n);
     p.flags = ws.take<float2>(n);
-    if (!RunRows::kept(d.dtype, d.vocab)) {
+    if (!rows_kept(d)) {
         p.ms = ws.take<float2>(n);
         p.g = ws.take<float2>(n);
         p.h = ws.take<float>(n);
@@ -939,9 +1164,8 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
     const LogitsIn in = logits_in(d);
     PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta, p.err};
     KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_rows_kernel, 1, 1024, 0, R);
-    const bool kept = RunRows::kept(d.dtype, d.vocab), ent = d.entropy_coef != 0.f || d.entropy;
+    const bool kept = rows_kept(d), ent = d.entropy_coef != 0.f || d.entropy;
     const float scale = d.grad_scale / d.temperature;
-    const long long ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
     if (d.rows > 0) {
         RowParams P{};
         P.in = in;
@@ -949,6 +1173,8 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
         P.logp = d.logp;
         P.entropy = d.entropy ? d.entropy : ent && !kept ? p.h : nullptr;
         P.ms = p.ms;
+        P.g = p.g;
+        P.err = p.err;
         P.meta = p.meta;
         P.ref_logp = d.ref_logp;
         P.clip_low = d.clip_low;
@@ -958,21 +1184,17 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
         P.kl = d.kl;
         P.terms = p.terms;
         P.flags = p.flags;
-        P.g = p.g;
         P.scale = scale;
-        if (kept) {
-            P.dlogits = (char *)d.dlogits;
-            P.ld_d_bytes = ld_d_bytes;
-        }
+        if (kept) P.dlogits = (char *)d.dlogits;
+        P.ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
         if ((s = by_type(d.dtype, ent, RunRows{P, st})) != KFAC_OK) return s;
     }
     PolicySum U{d.rows, p.terms, p.flags, d.stats, p.err};
     KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_sum_kernel, 1, 1024, 0, U);
     if (kept || !d.dlogits || d.rows == 0) return KFAC_OK;
-    const bool ent_grad = d.entropy_coef != 0.f;
     GradParams G{in, d.rows, p.ms, d.entropy ? d.entropy : p.h, (const float *)p.g, (const float *)p.g + 1, 2, scale,
-                 (char *)d.dlogits, ld_d_bytes};
-    return by_type(d.dtype, ent_grad, RunGrad{G, st});
+                 (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
+    return by_type(d.dtype, d.entropy_coef != 0.f, RunGrad{G, st});
 }
 
 extern "C" size_t kfac_preference_loss_workspace_size(const kfac_preference_desc *desc) {
