@@ -23,6 +23,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= F32_MAX; }
 
+
 // Two fp32 values in one 64-bit register pair: one instruction for both.
 struct f2 {
     unsigned long long v;
@@ -78,6 +79,34 @@ struct Sum2 {
         const float2 a = both(s), b = both(c);
         return (a.x + a.y) + (b.x + b.y);
     }
+};
+
+// A sum kept as hi + lo (about 45 bits): fp64 additions are too slow here to be
+// made by every thread.
+struct Wide {
+    float hi, lo;
+    __device__ __forceinline__ Wide(float v = 0.f) : hi(v), lo(0.f) {}
+    __device__ __forceinline__ void add(float b) {
+        const float t = __fadd_rn(hi, b), bb = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, bb)), __fsub_rn(b, bb)));
+        hi = t;
+    }
+    __device__ __forceinline__ void add(Wide b) {
+        add(b.hi);
+        lo = __fadd_rn(lo, b.lo);
+    }
+    __device__ __forceinline__ Wide shuffled(int o) const {
+        Wide r;
+        r.hi = __shfl_xor_sync(0xffffffffu, hi, o);
+        r.lo = __shfl_xor_sync(0xffffffffu, lo, o);
+        return r;
+    }
+    // Over the lanes of a warp; lane 0's is the one to take.
+    __device__ __forceinline__ void add_lanes() {
+        for (int o = 16; o > 0; o >>= 1) add(shuffled(o));
+    }
+    // An overflow to infinity leaves hi at it and NaN in lo.
+    __device__ __forceinline__ double value() const { return finite(hi) ? (double)hi + (double)lo : (double)hi; }
 };
 
 // A 16-byte group of elements of one type, as bits and as fp32 values.

@@ -166,6 +166,7 @@ struct RowParams {
     float2 *ms;                // (m, s) of each row (s = 0: nothing to differentiate), may be null
     // policy loss
     const PolicyRow *meta;     // not null: the policy loss
+    const int *order;          // the order in which the ring takes the rows
     const float *ref_logp;
     float clip_low, clip_high, kl_coef, entropy_coef;
     float *kl;
@@ -456,6 +457,7 @@ constexpr int RING_BYTES = 221184;  // of shared memory for the stages: three of
 
 struct StageRow {
     PolicyRow q;
+    int row;
     float ref, z_t;
 };
 struct RingShared {
@@ -543,9 +545,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         bool ok = true;
         for (long long n0 = 0; n0 < count && ok; n0 += 32) {
             // the inputs of 32 rows at once, one to a lane
-            StageRow mine{{-1, 0.f, 0.f, 0.f}, 0.f, 0.f};
+            StageRow mine{{-1, 0.f, 0.f, 0.f}, 0, 0.f, 0.f};
             if (n0 + lane < count) {
-                const long long row = first + (n0 + lane) * step;
+                const long long row = P.order[first + (n0 + lane) * step];
+                mine.row = (int)row;
                 mine.q = row_meta(P, row);
                 if (mine.q.target >= 0) {
                     mine.z_t = logit_at<DT>(P.in.logits + row * P.in.ld_bytes, mine.q.target);
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 if (lane == j) {
                     sh.row[st] = mine;
                     *(volatile long long *)&sh.given[st] = n;
-                    const Row<DT> r(P.in.logits + (first + n * step) * P.in.ld_bytes, P.in.vocab);
+                    const Row<DT> r(P.in.logits + mine.row * P.in.ld_bytes, P.in.vocab);
                     int c0, g1;
                     run_of(r, c0, g1);
                     if (mine.q.target >= 0 && g1 > c0) {
@@ -582,7 +585,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         const int team = tid / TEAM, t = tid % TEAM;
         int turn = 0;  // counts the team's rows that are not ignored
         for (long long n = team; n < count; n += TEAMS) {
-            const long long row = first + n * step;
             const int st = (int)(n % stages);
             // A wait that runs out is noted, and the team leaves after its next barrier.
             if (!wait_stage(sh, st, n, (int)(n / stages & 1))) {
@@ -590,6 +592,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 *(volatile int *)&sh.dead = 1;
             }
             const StageRow in = sh.row[st];
+            const long long row = in.row;
             char *out = P.dlogits + row * P.ld_d_bytes;
             const char *z = P.in.logits + row * P.in.ld_bytes;
             if (in.q.target < 0) {
@@ -712,15 +715,34 @@ __device__ __forceinline__ long long clamp_row(int32_t v, long long rows) {
     return v < 0 ? 0 : v > rows ? rows : v;
 }
 
-template <class T>
-__device__ __forceinline__ T block_sum(T v, T *part) {
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// Sum over a block; every thread gets it.
+__device__ __forceinline__ int block_sum(int v, int *part) {
+    v = __reduce_add_sync(0xffffffffu, v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    T all = 0;
-    for (int i = 0; i < (int)blockDim.x / 32; ++i) all += part[i];
+    int all = (int)(threadIdx.x & 31) < (int)blockDim.x / 32 ? part[threadIdx.x & 31] : 0;
+    return __reduce_add_sync(0xffffffffu, all);
+}
+// Sum over a block, in a fixed order; thread 0 gets it.
+__device__ __forceinline__ Wide block_sum(Wide v, Wide *part) {
+    v.add_lanes();
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    Wide all;
+    if (threadIdx.x < 32) {
+        if ((int)threadIdx.x < (int)blockDim.x / 32) all = part[threadIdx.x];
+        all.add_lanes();
+    }
     return all;
+}
+// Another CTA's copy of a shared variable.
+template <class T>
+__device__ __forceinline__ T *peer(T *local, int rank) {
+    T *p;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(p) : "l"(local), "r"(rank));
+    return p;
 }
 
 struct PolicyRows {
@@ -730,16 +752,22 @@ struct PolicyRows {
     const int32_t *off;
     int seqs, seq_mean;
     PolicyRow *meta;
+    int *order;
     int *err;
 };
 
-// One CTA: every row's target, weight, advantage and old log-probability in one place.
-__global__ void __launch_bounds__(1024) policy_rows_kernel(const __grid_constant__ PolicyRows P) {
+// One cluster of CTAs, each a run of rows: every row's target, weight, advantage
+// and old log-probability in one place, and the rows that are not ignored before
+// the ignored ones, so that CTAs that stride over them get equal shares.
+constexpr int SMALL_CLUSTER = 8, ROWS_THREADS = 512;
+__global__ void __launch_bounds__(ROWS_THREADS) policy_rows_kernel(const __grid_constant__ PolicyRows P) {
+    __shared__ int part[32], live_of[SMALL_CLUSTER], bad_of[SMALL_CLUSTER], warp_live[ROWS_THREADS / 32];
     pdl_wait();
     pdl_trigger();
-    __shared__ int part[32];
+    const int tid = threadIdx.x, lane = tid % 32, rank = blockIdx.x, ctas = gridDim.x;
+    const long long per = (P.rows + ctas - 1) / ctas, r0 = min(P.rows, rank * per), r1 = min(P.rows, r0 + per);
     int n = 0, bad = 0;
-    for (long long row = threadIdx.x; row < P.rows; row += blockDim.x) {
+    for (long long row = r0 + tid; row < r1; row += ROWS_THREADS) {
         const long long t = target_of(P.in, row);
         bad |= t >= P.in.vocab;
         const int seq = P.off ? sequence_of(P.off, P.seqs + 1, row) : 0;
@@ -750,22 +778,48 @@ __global__ void __launch_bounds__(1024) policy_rows_kernel(const __grid_constant
         n += q.target >= 0;
         P.meta[row] = q;
     }
-    bad = block_sum(bad, part);
-    if (threadIdx.x == 0) *P.err = bad ? ERR_TARGET : 0;
     n = block_sum(n, part);
-    if (P.weight) return;
-    if (!P.seq_mean) {
-        for (long long row = threadIdx.x; row < P.rows; row += blockDim.x)
-            if (P.meta[row].target >= 0) P.meta[row].weight = 1.f / (float)n;
-        return;
+    bad = block_sum(bad, part);
+    if (tid < ctas) {
+        *peer(&live_of[rank], tid) = n;
+        *peer(&bad_of[rank], tid) = bad;
     }
-    for (int q = threadIdx.x / 32; q < P.seqs; q += blockDim.x / 32) {
-        const long long r0 = clamp_row(P.off[q], P.rows), r1 = clamp_row(P.off[q + 1], P.rows);
+    cluster_sync();
+    int live = 0, before = 0, any = 0;
+    for (int i = 0; i < ctas; ++i) {
+        live += live_of[i];
+        if (i < rank) before += live_of[i];
+        any += bad_of[i];
+    }
+    if (rank == 0 && tid == 0) *P.err = any ? ERR_TARGET : 0;
+    // (a CTA writes what its own threads have written, so its own barriers order it)
+    const float w = 1.f / (float)live;
+    for (long long base = r0; base < r1; base += ROWS_THREADS) {
+        const long long row = base + tid;
+        const bool in = row < r1, is = in && P.meta[row].target >= 0;
+        const unsigned votes = __ballot_sync(0xffffffffu, is);
+        __syncthreads();
+        if (lane == 0) warp_live[tid / 32] = __popc(votes);
+        __syncthreads();
+        int mine = before + __popc(votes & ((1u << lane) - 1)), tile = 0;
+        for (int i = 0; i < ROWS_THREADS / 32; ++i) {
+            if (i < tid / 32) mine += warp_live[i];
+            tile += warp_live[i];
+        }
+        // ignored rows so far: all rows before this one less the live ones before it
+        if (in) P.order[is ? mine : live + (row - mine)] = (int)row;
+        if (is && !P.weight && !P.seq_mean) P.meta[row].weight = w;
+        before += tile;
+    }
+    if (!P.seq_mean) return;
+    cluster_sync();  // the other CTAs' rows
+    for (int q = rank * (ROWS_THREADS / 32) + tid / 32; q < P.seqs; q += ctas * (ROWS_THREADS / 32)) {
+        const long long q0 = clamp_row(P.off[q], P.rows), q1 = clamp_row(P.off[q + 1], P.rows);
         int c = 0;
-        for (long long row = r0 + (threadIdx.x & 31); row < r1; row += 32) c += P.meta[row].target >= 0;
+        for (long long row = q0 + lane; row < q1; row += 32) c += __ldcg(&P.meta[row].target) >= 0;
         c = __reduce_add_sync(0xffffffffu, c);
-        for (long long row = r0 + (threadIdx.x & 31); row < r1; row += 32)
-            if (P.meta[row].target >= 0) P.meta[row].weight = 1.f / ((float)P.seqs * (float)c);
+        for (long long row = q0 + lane; row < q1; row += 32)
+            if (__ldcg(&P.meta[row].target) >= 0) P.meta[row].weight = 1.f / ((float)P.seqs * (float)c);
     }
 }
 
@@ -777,30 +831,45 @@ struct PolicySum {
     int *err;
 };
 
-// One CTA: the sums of the rows' terms.
-__global__ void __launch_bounds__(1024) policy_sum_kernel(const __grid_constant__ PolicySum P) {
+// One cluster of CTAs, each a run of rows: the sums of the rows' terms.
+__global__ void __launch_bounds__(ROWS_THREADS) policy_sum_kernel(const __grid_constant__ PolicySum P) {
+    __shared__ Wide part[32], all[SMALL_CLUSTER][5];
+    __shared__ int bad_of[SMALL_CLUSTER];
     pdl_wait();
     pdl_trigger();
-    __shared__ double part[32];
-    double sum[5] = {0, 0, 0, 0, 0};
+    const int rank = blockIdx.x, ctas = gridDim.x;
+    const long long per = (P.rows + ctas - 1) / ctas, r0 = min(P.rows, rank * per), r1 = min(P.rows, r0 + per);
+    Wide sum[5];
     int bad = 0;
-    for (long long row = threadIdx.x; row < P.rows; row += blockDim.x) {
+    for (long long row = r0 + threadIdx.x; row < r1; row += ROWS_THREADS) {
         const float4 t = P.terms[row];
         const float2 f = P.flags[row];
-        sum[0] += t.x;
-        sum[1] += t.y;
-        sum[2] += t.z;
-        sum[3] += t.w;
-        sum[4] += f.x;
+        sum[0].add(t.x);
+        sum[1].add(t.y);
+        sum[2].add(t.z);
+        sum[3].add(t.w);
+        sum[4].add(f.x);
         bad |= f.y != 0.f;
     }
-    for (int i = 0; i < 5; ++i) {
-        const double s = block_sum(sum[i], part);
-        if (threadIdx.x == 0) P.stats[i] = (float)s;
-        if (i == 0) bad |= !finite((float)s);
-    }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0 && bad) *P.err |= ERR_NONFINITE;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+        const Wide s = block_sum(sum[i], part);
+        if (threadIdx.x == 0) *peer(&all[rank][i], 0) = s;
+    }
+    if (threadIdx.x == 0) *peer(&bad_of[rank], 0) = bad;
+    cluster_sync();
+    if (rank != 0 || threadIdx.x >= 32) return;
+    const int i = threadIdx.x;
+    Wide s;
+    int flag = 0;
+    for (int c = 0; c < ctas; ++c) {
+        if (i < 5) s.add(all[c][i]);
+        flag |= bad_of[c];
+    }
+    const float v = (float)s.value();
+    if (i < 5) P.stats[i] = v;
+    if (i == 0 && (flag || !finite(v))) *P.err |= ERR_NONFINITE;
 }
 
 struct PrefPairs {
@@ -815,30 +884,33 @@ struct PrefPairs {
     const float *logp;   // of every row (0 where ignored)
     const float2 *ms;
     float *row_g;        // gradient of every row's logp
-    double *terms;       // [pairs] weighted f
+    float *terms;        // [pairs] weighted f
     int *bad;            // [pairs] error bits
     float *pair_loss, *seq_logp;
 };
 
 // ln(1 + e^-x) = -ln sigma(x) without overflow.
-__device__ __forceinline__ double softplus_neg(double x) {
-    return (x < 0 ? -x : 0.) + log1p(exp(-fabs(x)));
-}
+__device__ __forceinline__ float softplus_neg(float x) { return fmaxf(-x, 0.f) + log1pf(expf(-fabsf(x))); }
 
-// One CTA per pair: the sums of its two sequences, f and its derivative.
-__global__ void __launch_bounds__(256) pref_pairs_kernel(const PrefPairs P) {
+// One CTA per pair: the sums of its two sequences, f and its derivative.  h is
+// formed in more than fp32 (two sums that nearly cancel), f from it in fp32.
+constexpr int PAIR_THREADS = 256;
+__global__ void __launch_bounds__(PAIR_THREADS) pref_pairs_kernel(const __grid_constant__ PrefPairs P) {
+    __shared__ Wide part[32];
+    __shared__ int ipart[32];
+    __shared__ float slope[2];
     pdl_wait();
     pdl_trigger();
-    __shared__ double part[8];
-    __shared__ int ipart[8];
     const int b = blockIdx.x;
-    double l[2];
+    long long r0[2], r1[2];
+    double l[2] = {0., 0.};
     int n[2], bad = 0;
     for (int q = 0; q < 2; ++q) {
-        const long long r0 = clamp_row(P.off[2 * b + q], P.rows), r1 = clamp_row(P.off[2 * b + q + 1], P.rows);
-        double s = 0;
+        r0[q] = clamp_row(P.off[2 * b + q], P.rows);
+        r1[q] = clamp_row(P.off[2 * b + q + 1], P.rows);
+        Wide s;
         int c = 0;
-        for (long long row = r0 + threadIdx.x; row < r1; row += blockDim.x) {
+        for (long long row = r0[q] + threadIdx.x; row < r1[q]; row += PAIR_THREADS) {
             const long long t = P.target_i32 ? (long long)((const int32_t *)P.target)[row]
                                              : (long long)((const int64_t *)P.target)[row];
             if (t >= P.vocab) bad |= ERR_TARGET;
@@ -848,67 +920,77 @@ __global__ void __launch_bounds__(256) pref_pairs_kernel(const PrefPairs P) {
                 bad |= ERR_NONFINITE;
                 continue;
             }
-            if (!finite(P.logp[row])) bad |= ERR_NONFINITE;
-            s += P.logp[row];
+            const float v = P.logp[row];
+            if (!finite(v)) bad |= ERR_NONFINITE;
+            s.add(v);
         }
         s = block_sum(s, part);
         n[q] = block_sum(c, ipart);
-        l[q] = P.average && n[q] > 0 ? s / n[q] : s;
-        if (!finite((float)l[q])) bad |= ERR_NONFINITE;
-        if (threadIdx.x == 0 && P.seq_logp) P.seq_logp[2 * b + q] = (float)l[q];
+        if (threadIdx.x == 0) {
+            l[q] = P.average && n[q] > 0 ? s.value() / n[q] : s.value();
+            if (!finite((float)l[q])) bad |= ERR_NONFINITE;
+            if (P.seq_logp) P.seq_logp[2 * b + q] = (float)l[q];
+        }
     }
-    const double h = (l[0] - (P.ref ? P.ref[2 * b] : 0.f)) - (l[1] - (P.ref ? P.ref[2 * b + 1] : 0.f));
-    const double beta = P.beta, e = P.smooth, x = beta * h;
-    double f, d;
-    if (P.kind == KFAC_PREF_SIGMOID) {
-        f = (1 - e) * softplus_neg(x) + (e > 0 ? e * softplus_neg(-x) : 0.);
-        d = beta * (e / (1 + exp(-x)) - (1 - e) / (1 + exp(x)));
-    } else if (P.kind == KFAC_PREF_HINGE) {
-        f = x < 1 ? 1 - x : x >= 1 ? 0. : x;  // (NaN stays)
-        d = x < 1 ? -beta : x >= 1 ? 0. : x;
-    } else {
-        const double o = h - 0.5 / beta;
-        f = o * o;
-        d = 2 * o;
-    }
-    const double v = P.pair_weight ? (double)P.pair_weight[b] : 1.0 / P.pairs;
-    if (!finite((float)f)) bad |= ERR_NONFINITE;
-    bad = __syncthreads_or(bad & ERR_NONFINITE ? 1 : 0) * ERR_NONFINITE | __syncthreads_or(bad & ERR_TARGET ? 1 : 0) * ERR_TARGET;
     if (threadIdx.x == 0) {
-        P.terms[b] = v == 0. ? 0. : v * f;
+        double h = l[0] - l[1];
+        if (P.ref) h -= (double)P.ref[2 * b] - (double)P.ref[2 * b + 1];
+        const float beta = P.beta, e = P.smooth, x = (float)(beta * h);
+        float f, d;
+        if (P.kind == KFAC_PREF_SIGMOID) {
+            f = (1.f - e) * softplus_neg(x) + (e > 0.f ? e * softplus_neg(-x) : 0.f);
+            d = beta * ((e > 0.f ? e / (1.f + expf(-x)) : 0.f) - (1.f - e) / (1.f + expf(x)));
+        } else if (P.kind == KFAC_PREF_HINGE) {
+            f = x < 1.f ? (float)(1. - beta * h) : x >= 1.f ? 0.f : x;  // (NaN stays)
+            d = x < 1.f ? -beta : x >= 1.f ? 0.f : x;
+        } else {
+            const float o = (float)(h - 0.5 / beta);
+            f = o * o;
+            d = 2.f * o;
+        }
+        const float v = P.pair_weight ? P.pair_weight[b] : 1.f / (float)P.pairs;
+        if (!finite(f)) bad |= ERR_NONFINITE;
+        P.terms[b] = v == 0.f ? 0.f : v * f;
+        if (P.pair_loss) P.pair_loss[b] = f;
+        for (int q = 0; q < 2; ++q)
+            slope[q] = v == 0.f ? 0.f : v * d * (q ? -1.f : 1.f) / (P.average && n[q] > 0 ? (float)n[q] : 1.f);
+    }
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) ipart[threadIdx.x / 32] = bad;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < PAIR_THREADS / 32; ++i) bad |= ipart[i];
         P.bad[b] = bad;
-        if (P.pair_loss) P.pair_loss[b] = (float)f;
     }
-    for (int q = 0; q < 2; ++q) {
-        const long long r0 = clamp_row(P.off[2 * b + q], P.rows), r1 = clamp_row(P.off[2 * b + q + 1], P.rows);
-        const double dl = v == 0. ? 0. : v * d * (q ? -1 : 1) / (P.average && n[q] > 0 ? n[q] : 1);
-        for (long long row = r0 + threadIdx.x; row < r1; row += blockDim.x) P.row_g[row] = (float)dl;
-    }
+    for (int q = 0; q < 2; ++q)
+        for (long long row = r0[q] + threadIdx.x; row < r1[q]; row += PAIR_THREADS) P.row_g[row] = slope[q];
 }
 
 struct PrefSum {
-    const double *terms;
+    const float *terms;
     const int *bad;
     int pairs;
     float *loss;
     int *err;
 };
-__global__ void __launch_bounds__(256) pref_sum_kernel(const PrefSum P) {
+__global__ void __launch_bounds__(PAIR_THREADS) pref_sum_kernel(const __grid_constant__ PrefSum P) {
+    __shared__ Wide part[32];
+    __shared__ int ipart[32];
     pdl_wait();
     pdl_trigger();
-    __shared__ double part[8];
-    __shared__ int ipart[8];
-    double s = 0;
+    Wide s;
     int bad = 0;
-    for (int b = threadIdx.x; b < P.pairs; b += blockDim.x) {
-        s += P.terms[b];
+    for (int b = threadIdx.x; b < P.pairs; b += PAIR_THREADS) {
+        s.add(P.terms[b]);
         bad |= P.bad[b];
     }
     s = block_sum(s, part);
     const int nf = block_sum(bad & ERR_NONFINITE ? 1 : 0, ipart), tg = block_sum(bad & ERR_TARGET ? 1 : 0, ipart);
     if (threadIdx.x == 0) {
-        *P.loss = (float)s;
-        *P.err = (nf || !finite((float)s) ? ERR_NONFINITE : 0) | (tg ? ERR_TARGET : 0);
+        const float loss = (float)s.value();
+        *P.loss = loss;
+        *P.err = (nf || !finite(loss) ? ERR_NONFINITE : 0) | (tg ? ERR_TARGET : 0);
     }
 }
 
@@ -1043,6 +1125,7 @@ kfac_status check_policy(const kfac_policy_desc *d) {
 struct PolicyPlan {
     int *err;
     PolicyRow *meta;
+    int *order;
     float4 *terms;
     float2 *flags, *ms, *g;  // ms, g, h: for rows that do not fit the chip
     float *h;
@@ -1056,6 +1139,7 @@ PolicyPlan plan_policy(const kfac_policy_desc &d, Arena &ws) {
     const size_t n = (size_t)d.rows;
     p.err = ws.take<int>(64);
     p.meta = ws.take<PolicyRow>(n);
+    p.order = ws.take<int>(n);
     p.terms = ws.take<float4>(n);
     p.flags = ws.take<float2>(n);
     if (!rows_kept(d)) {
@@ -1087,7 +1171,7 @@ struct PrefPlan {
     int *err, *bad;
     float *logp, *row_g;
     float2 *ms;
-    double *terms;
+    float *terms;
 };
 PrefPlan plan_preference(const kfac_preference_desc &d, Arena &ws) {
     PrefPlan p;
@@ -1096,7 +1180,7 @@ PrefPlan plan_preference(const kfac_preference_desc &d, Arena &ws) {
     p.logp = ws.take<float>(n);
     p.row_g = ws.take<float>(n);
     p.ms = ws.take<float2>(n);
-    p.terms = ws.take<double>((size_t)d.pairs);
+    p.terms = ws.take<float>((size_t)d.pairs);
     p.bad = ws.take<int>((size_t)d.pairs);
     return p;
 }
@@ -1162,8 +1246,10 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
         return KFAC_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;
     const LogitsIn in = logits_in(d);
-    PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta, p.err};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_rows_kernel, 1, 1024, 0, R);
+    PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta,
+                 p.order, p.err};
+    const unsigned small = d.rows > ROWS_THREADS ? SMALL_CLUSTER : 1;
+    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_rows_kernel, small, small, ROWS_THREADS, 0, R);
     const bool kept = rows_kept(d), ent = d.entropy_coef != 0.f || d.entropy;
     const float scale = d.grad_scale / d.temperature;
     if (d.rows > 0) {
@@ -1176,6 +1262,7 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
         P.g = p.g;
         P.err = p.err;
         P.meta = p.meta;
+        P.order = p.order;
         P.ref_logp = d.ref_logp;
         P.clip_low = d.clip_low;
         P.clip_high = d.clip_high;
@@ -1190,7 +1277,7 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
         if ((s = by_type(d.dtype, ent, RunRows{P, st})) != KFAC_OK) return s;
     }
     PolicySum U{d.rows, p.terms, p.flags, d.stats, p.err};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, policy_sum_kernel, 1, 1024, 0, U);
+    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_sum_kernel, small, small, ROWS_THREADS, 0, U);
     if (kept || !d.dlogits || d.rows == 0) return KFAC_OK;
     GradParams G{in, d.rows, p.ms, d.entropy ? d.entropy : p.h, (const float *)p.g, (const float *)p.g + 1, 2, scale,
                  (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
@@ -1231,9 +1318,9 @@ extern "C" kfac_status kfac_preference_loss(const kfac_preference_desc *desc, vo
     }
     PrefPairs Q{d.target, d.target_i32, d.vocab, d.rows, d.seq_offsets, d.pairs, d.ref_logp, d.pair_weight, d.kind,
                 d.average, d.beta, d.label_smoothing, logp, p.ms, p.row_g, p.terms, p.bad, d.pair_loss, d.seq_logp};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_pairs_kernel, (unsigned)d.pairs, 256, 0, Q);
+    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_pairs_kernel, (unsigned)d.pairs, PAIR_THREADS, 0, Q);
     PrefSum U{p.terms, p.bad, d.pairs, d.loss, p.err};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_sum_kernel, 1, 256, 0, U);
+    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_sum_kernel, 1, PAIR_THREADS, 0, U);
     if (!d.dlogits || d.rows == 0) return KFAC_OK;
     GradParams G{logits_in(d), d.rows, p.ms, nullptr, p.row_g, nullptr, 1, d.grad_scale / d.temperature,
                  (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
