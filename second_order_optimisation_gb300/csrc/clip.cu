@@ -4,11 +4,14 @@
 //   norm = sqrt(sum x y)  (y = x: the Euclidean norm),  scale = min(1, max_norm / norm),
 //   out = scale x,  w <- w - eta scale x.
 //
-// Two passes over a list of chunks: every CTA sums its chunks' products (fp32
-// in the threads, fp64 across them and across chunks, in a fixed order), then
-// every chunk is scaled.  A chunk whose fp32 sum overflows or vanishes is
-// summed again from values scaled by a power of two, so that any finite input
-// gives its norm.
+// Bound by memory: x (and y) are read for the norm, x (and w) again for the
+// step.  The tensors are cut into octets of eight elements, numbered through all
+// tensors, and every CTA takes an equal run of them in both passes; the second
+// pass walks its run from the end, so that what the first has read last is still
+// in the L2 cache.  A thread adds up to 32 products in fp32 and those sums in
+// two fp32 words; the CTAs' sums are added in fp64 in a fixed order.  A run
+// whose sum overflows or vanishes in fp32 is summed again from values scaled by
+// a power of two, so that any finite input gives its norm.
 #include <algorithm>
 #include <cmath>
 #include <memory>
@@ -18,9 +21,8 @@
 namespace kfac {
 namespace {
 
-constexpr int CLIP_MAX = 256;      // tensors of one launch (kernel parameters)
-constexpr int CLIP_THREADS = 256;
-constexpr int CHUNK = 8192;        // elements of a chunk
+constexpr int CLIP_FEW = 16, CLIP_MANY = 216;  // tensors of one launch (kernel parameters)
+constexpr int CLIP_THREADS = 512, CLIP_PER_SM = 2, OCTET = 8;
 
 struct ClipJob {
     const char *x, *y;
@@ -28,55 +30,130 @@ struct ClipJob {
     float *w;
     long long ld, ld_y, ld_out, ld_w;
     long long rows, cols;  // a tensor without gaps is one row
-    int dtype, out_dtype;
-    int per_row;           // chunks of a row
-    int first;             // index of its first chunk in the launch
+    long long first;       // its first octet of the launch
+    long long per_row;     // octets of a row
+    uint8_t dtype, out_dtype;
+    uint8_t shift;         // octet 0 starts this many elements before the row
+    uint8_t vec;           // octets are taken 16 bytes at a time
+    uint8_t out_vec;       // ... and stored so
 };
+template <int MAX>
 struct ClipParams {
-    ClipJob job[CLIP_MAX];
-    int n, chunks;
-    int part0;             // where this launch's partial sums start
-    double *part;          // one for each chunk
-    const float *scale;
-    float eta;
+    ClipJob job[MAX];
+    int n;
+    long long octets;
+    double *part;        // one for each CTA of each launch
+    int part0, parts;    // this launch's first, and all launches'
+    float max_norm, eta;
+    float *norm, *scale;
+    int *err;            // set by the first launch of the second pass
 };
 
 template <int DT>
 __device__ __forceinline__ float elem(const char *p, long long i) {
     return Elem<DT>::value(((const typename Elem<DT>::bits *)p)[i]);
 }
-__device__ __forceinline__ float elem(int dt, const char *p, long long i) {
-    return dt == KFAC_BF16 ? elem<KFAC_BF16>(p, i) : dt == KFAC_F16 ? elem<KFAC_F16>(p, i) : elem<KFAC_F32>(p, i);
+
+// Eight elements from any element boundary, by aligned 16-byte loads (`off` is
+// the address modulo 16): the pieces they lie in belong to the row wherever eight
+// more elements exist on both sides.
+__device__ __forceinline__ uint4 ld16(const char *p) {
+    return *reinterpret_cast<const uint4 *>(p);
+}
+template <int DT>
+__device__ __forceinline__ void load8(const char *p, int off, float *v) {
+    constexpr int Q = Elem<DT>::N == 4 ? 2 : 1;  // 16-byte pieces of eight elements
+    if (off == 0) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) Elem<DT>::unpack(ld16(p + 16 * q), v + 4 * q);
+        return;
+    }
+    uint32_t w[4 * (Q + 1)];
+#pragma unroll
+    for (int q = 0; q <= Q; ++q) {
+        const uint4 u = ld16(p - off + 16 * q);
+        w[4 * q] = u.x, w[4 * q + 1] = u.y, w[4 * q + 2] = u.z, w[4 * q + 3] = u.w;
+    }
+    // left by 8, 4 and 2 bytes as the offset has them
+    if (off & 8)
+#pragma unroll
+        for (int i = 0; i + 2 < 4 * (Q + 1); ++i) w[i] = w[i + 2];
+    if (off & 4)
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = w[i + 1];
+    if (off & 2)
+#pragma unroll
+        for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        Elem<DT>::unpack(make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]), v + 4 * q);
+}
+template <int DT>
+__device__ __forceinline__ void store8(char *p, const float *v) {
+    constexpr int Q = Elem<DT>::N == 4 ? 2 : 1;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) *reinterpret_cast<uint4 *>(p + 16 * q) = Elem<DT>::pack(v + 4 * q);
 }
 
-__device__ __forceinline__ const ClipJob &job_of(const ClipParams &P, int chunk) {
-    int lo = 0, hi = P.n - 1;
+// Where octet i of a tensor lies: row, first column (may be negative), and
+// whether all its elements, and eight on both sides, exist.
+struct Place {
+    long long row, col;
+    bool whole, inner;
+};
+__device__ __forceinline__ Place place_of(const ClipJob &j, long long i) {
+    Place p;
+    p.row = 0;
+    if (j.rows > 1) {
+        p.row = j.rows * j.per_row <= 0xffffffffLL ? (long long)((uint32_t)i / (uint32_t)j.per_row) : i / j.per_row;
+        i -= p.row * j.per_row;
+    }
+    p.col = i * OCTET - j.shift;
+    p.whole = p.col >= 0 && p.col + OCTET <= j.cols;
+    p.inner = p.col >= OCTET && p.col + 2 * OCTET <= j.cols;
+    return p;
+}
+template <int DT>
+__device__ __forceinline__ void octet(const char *base, long long ld, const Place &p, long long cols, bool vec, float *v) {
+    constexpr int ES = Elem<DT>::N == 4 ? 4 : 2;
+    const char *row = base + p.row * ld * ES, *at = row + p.col * ES;
+    const int off = (int)((uintptr_t)at & 15);
+    if (vec && (p.inner || (p.whole && off == 0))) {
+        load8<DT>(at, off, v);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < OCTET; ++e) v[e] = p.col + e >= 0 && p.col + e < cols ? elem<DT>(row, p.col + e) : 0.f;
+}
+
+template <class P>
+__device__ __forceinline__ int job_of(const P &p, long long i) {
+    int lo = 0, hi = p.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (P.job[mid].first <= chunk) lo = mid; else hi = mid - 1;
+        if (p.job[mid].first <= i) lo = mid; else hi = mid - 1;
     }
-    return P.job[lo];
+    return lo;
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-    __shared__ double part[CLIP_THREADS / 32];
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ Wide block_wide(Wide v) {
+    __shared__ Wide part[CLIP_THREADS / 32];
+    v.add_lanes();
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    double all = 0;
-    for (int i = 0; i < CLIP_THREADS / 32; ++i) all += part[i];
-    return all;
+    v = threadIdx.x % 32 < CLIP_THREADS / 32 ? part[threadIdx.x % 32] : Wide{};
+    v.add_lanes();
+    return v;
 }
 __device__ __forceinline__ unsigned block_max(unsigned v) {
     __shared__ unsigned part[CLIP_THREADS / 32];
     v = __reduce_max_sync(0xffffffffu, v);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    unsigned all = 0;
-    for (int i = 0; i < CLIP_THREADS / 32; ++i) all = max(all, part[i]);
-    return all;
+    v = threadIdx.x % 32 < CLIP_THREADS / 32 ? part[threadIdx.x % 32] : 0;
+    return __reduce_max_sync(0xffffffffu, v);
 }
 
 // 2^n as fp32, n in -126 .. 127.
@@ -86,88 +163,169 @@ __device__ __forceinline__ int to_one(unsigned magnitude) {
     return max(-126, min(126, 127 - (int)(magnitude >> 23)));
 }
 
-__global__ void __launch_bounds__(CLIP_THREADS) clip_norm_kernel(const __grid_constant__ ClipParams P) {
-    pdl_wait();
-    pdl_trigger();
-    const int chunk = blockIdx.x;
-    const ClipJob &j = job_of(P, chunk);
-    const int rel = chunk - j.first;
-    const long long row = rel / j.per_row, c0 = (long long)(rel % j.per_row) * CHUNK;
-    const int n = (int)min((long long)CHUNK, j.cols - c0);
-    const int es = j.dtype == KFAC_F32 ? 4 : 2;
-    const char *x = j.x + (row * j.ld + c0) * es, *y = j.y ? j.y + (row * j.ld_y + c0) * es : x;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < n; i += CLIP_THREADS) s = fmaf(elem(j.dtype, x, i), elem(j.dtype, y, i), s);
-    double all = block_sum((double)s);
-    // squares overflow from 2^64 and lose bits below 2^-63
-    if (!(fabs(all) <= (double)F32_MAX) || fabs(all) < 1e-28) {
-        unsigned mx = 0, my = 0;
-        for (int i = threadIdx.x; i < n; i += CLIP_THREADS) {
-            mx = max(mx, __float_as_uint(elem(j.dtype, x, i)) & 0x7fffffffu);
-            my = max(my, __float_as_uint(elem(j.dtype, y, i)) & 0x7fffffffu);
+// This thread's sum of x y over octets lo .. hi - 1 of a tensor.
+template <int DT, bool METRIC>
+__device__ __forceinline__ Wide products(const ClipJob &j, long long lo, long long hi) {
+    constexpr int UNROLL = METRIC ? 2 : 4;  // octets in flight
+    Wide sum{};
+    for (long long i = lo + threadIdx.x; i < hi; i += UNROLL * CLIP_THREADS) {
+        float x[UNROLL][OCTET], y[UNROLL][OCTET];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const long long at = i + u * CLIP_THREADS;
+            if (at < hi) {
+                const Place p = place_of(j, at);
+                octet<DT>(j.x, j.ld, p, j.cols, j.vec, x[u]);
+                if (METRIC) octet<DT>(j.y, j.ld_y, p, j.cols, j.vec, y[u]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < OCTET; ++e) x[u][e] = y[u][e] = 0.f;
+            }
         }
-        mx = block_max(mx);
-        my = block_max(my);
-        if (mx < 0x7f800000u && my < 0x7f800000u) {
-            const int ex = to_one(mx), ey = to_one(my);
-            s = 0.f;
-            for (int i = threadIdx.x; i < n; i += CLIP_THREADS)
-                s = fmaf(elem(j.dtype, x, i) * pow2(ex), elem(j.dtype, y, i) * pow2(ey), s);
-            all = ldexp(block_sum((double)s), -ex - ey);
+        float t = 0.f;
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            float q[OCTET];
+#pragma unroll
+            for (int e = 0; e < OCTET; ++e) q[e] = x[u][e] * (METRIC ? y[u][e] : x[u][e]);
+            t += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+        }
+        sum.add(t);
+    }
+    return sum;
+}
+// The same over the block, from values scaled by powers of two; `plain` where a
+// value is not finite.
+template <int DT>
+__device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long long hi, double plain) {
+    const char *yb = j.y ? j.y : j.x;
+    const long long ld_y = j.y ? j.ld_y : j.ld;
+    unsigned mx = 0, my = 0;
+    float x[OCTET], y[OCTET];
+    for (long long i = lo + threadIdx.x; i < hi; i += CLIP_THREADS) {
+        const Place p = place_of(j, i);
+        octet<DT>(j.x, j.ld, p, j.cols, false, x);
+        octet<DT>(yb, ld_y, p, j.cols, false, y);
+        for (int e = 0; e < OCTET; ++e) {
+            mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
+            my = max(my, __float_as_uint(y[e]) & 0x7fffffffu);
         }
     }
-    if (threadIdx.x == 0) P.part[P.part0 + chunk] = all;
+    mx = block_max(mx);
+    my = block_max(my);
+    if (mx >= 0x7f800000u || my >= 0x7f800000u) return plain;
+    const int ex = to_one(mx), ey = to_one(my);
+    const float fx = pow2(ex), fy = pow2(ey);
+    Wide sum{};
+    for (long long i = lo + threadIdx.x; i < hi; i += CLIP_THREADS) {
+        const Place p = place_of(j, i);
+        octet<DT>(j.x, j.ld, p, j.cols, false, x);
+        octet<DT>(yb, ld_y, p, j.cols, false, y);
+        for (int e = 0; e < OCTET; ++e) sum.add((x[e] * fx) * (y[e] * fy));
+    }
+    return ldexp(block_wide(sum).value(), -ex - ey);
+}
+template <int DT>
+__device__ __forceinline__ double run_sum(const ClipJob &j, long long lo, long long hi) {
+    const Wide s = block_wide(j.y ? products<DT, true>(j, lo, hi) : products<DT, false>(j, lo, hi));
+    // every warp has joined the warps' sums, and hi is the same for all threads
+    const double plain = s.value();
+    return finite(s.hi) && fabsf(s.hi) >= 1e-28f ? plain : scaled_sum<DT>(j, lo, hi, plain);
 }
 
-struct ClipTotal {
-    const double *part;
-    long long n;
-    float max_norm;
-    float *norm, *scale_out, *scale;
-    int *err;
-};
-__global__ void __launch_bounds__(CLIP_THREADS) clip_total_kernel(const ClipTotal P) {
+template <int MAX>
+__global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(const __grid_constant__ ClipParams<MAX> P) {
     pdl_wait();
     pdl_trigger();
-    double s = 0;
-    for (long long i = threadIdx.x; i < P.n; i += CLIP_THREADS) s += P.part[i];
-    s = block_sum(s);
-    if (threadIdx.x == 0) {
-        const float norm = (float)sqrt(s < 0 ? 0. : s);
-        const float scale = norm > P.max_norm ? P.max_norm / norm : norm <= P.max_norm ? 1.f : norm;
-        *P.scale = scale;
-        if (P.norm) *P.norm = norm;
-        if (P.scale_out) *P.scale_out = scale;
-        *P.err = finite(norm) ? 0 : ERR_NONFINITE;
+    const long long lo = P.octets * blockIdx.x / gridDim.x, hi = P.octets * (blockIdx.x + 1) / gridDim.x;
+    double sum = 0;
+    for (int n = job_of(P, lo); n < P.n && P.job[n].first < hi; ++n) {
+        const ClipJob &j = P.job[n];
+        const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
+        sum += j.dtype == KFAC_BF16 ? run_sum<KFAC_BF16>(j, a, b)
+               : j.dtype == KFAC_F16 ? run_sum<KFAC_F16>(j, a, b) : run_sum<KFAC_F32>(j, a, b);
     }
+    if (threadIdx.x == 0) P.part[P.part0 + blockIdx.x] = sum;
 }
 
 template <int DT>
-__device__ __forceinline__ void put(char *p, long long i, float v) {
-    ((typename Elem<DT>::bits *)p)[i] = Elem<DT>::round(v);
+__device__ __forceinline__ void apply_run(const ClipJob &j, long long lo, long long hi, float scale, float eta) {
+    const int es_out = j.out_dtype == KFAC_F32 ? 4 : 2;
+    // from the end of the run
+    for (long long i = hi - 1 - threadIdx.x; i >= lo; i -= CLIP_THREADS) {
+        const Place p = place_of(j, i);
+        float x[OCTET];
+        octet<DT>(j.x, j.ld, p, j.cols, j.vec, x);
+#pragma unroll
+        for (int e = 0; e < OCTET; ++e) x[e] *= scale;
+        if (j.out) {
+            char *row = j.out + p.row * j.ld_out * es_out;
+            if (j.out_vec && p.whole) {
+                char *at = row + p.col * es_out;
+                if (j.out_dtype == KFAC_BF16) store8<KFAC_BF16>(at, x);
+                else if (j.out_dtype == KFAC_F16) store8<KFAC_F16>(at, x);
+                else store8<KFAC_F32>(at, x);
+            } else {
+#pragma unroll
+                for (int e = 0; e < OCTET; ++e) {
+                    const long long c = p.col + e;
+                    if (c < 0 || c >= j.cols) continue;
+                    if (j.out_dtype == KFAC_BF16) ((uint16_t *)row)[c] = Elem<KFAC_BF16>::round(x[e]);
+                    else if (j.out_dtype == KFAC_F16) ((uint16_t *)row)[c] = Elem<KFAC_F16>::round(x[e]);
+                    else ((float *)row)[c] = x[e];
+                }
+            }
+        }
+        if (j.w) {
+            float *row = j.w + p.row * j.ld_w;
+            if (j.vec && p.whole) {
+                float4 *at = reinterpret_cast<float4 *>(row + p.col);
+                float4 a = at[0], b = at[1];
+                a.x -= eta * x[0]; a.y -= eta * x[1]; a.z -= eta * x[2]; a.w -= eta * x[3];
+                b.x -= eta * x[4]; b.y -= eta * x[5]; b.z -= eta * x[6]; b.w -= eta * x[7];
+                at[0] = a;
+                at[1] = b;
+            } else {
+#pragma unroll
+                for (int e = 0; e < OCTET; ++e)
+                    if (p.col + e >= 0 && p.col + e < j.cols) row[p.col + e] -= eta * x[e];
+            }
+        }
+    }
 }
 
-__global__ void __launch_bounds__(CLIP_THREADS) clip_apply_kernel(const __grid_constant__ ClipParams P) {
+// Every CTA adds up the first pass's sums itself (the same sum in the same order).
+template <int MAX>
+__global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_apply_kernel(const __grid_constant__ ClipParams<MAX> P) {
+    __shared__ float shared_scale;
     pdl_wait();
     pdl_trigger();
-    const int chunk = blockIdx.x;
-    const ClipJob &j = job_of(P, chunk);
-    const float scale = *P.scale;
-    if (!j.w && (!j.out || (j.out == j.x && scale == 1.f))) return;
-    const int rel = chunk - j.first;
-    const long long row = rel / j.per_row, c0 = (long long)(rel % j.per_row) * CHUNK;
-    const int n = (int)min((long long)CHUNK, j.cols - c0);
-    const char *x = j.x + (row * j.ld + c0) * (j.dtype == KFAC_F32 ? 4 : 2);
-    char *out = j.out ? j.out + (row * j.ld_out + c0) * (j.out_dtype == KFAC_F32 ? 4 : 2) : nullptr;
-    float *w = j.w ? j.w + row * j.ld_w + c0 : nullptr;
-    for (int i = threadIdx.x; i < n; i += CLIP_THREADS) {
-        const float v = scale * elem(j.dtype, x, i);
-        if (out) {
-            if (j.out_dtype == KFAC_BF16) put<KFAC_BF16>(out, i, v);
-            else if (j.out_dtype == KFAC_F16) put<KFAC_F16>(out, i, v);
-            else put<KFAC_F32>(out, i, v);
+    if (threadIdx.x < 32) {
+        double s = 0;
+        for (int i = threadIdx.x; i < P.parts; i += 32) s += P.part[i];
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
+        if (threadIdx.x == 0) {
+            const float norm = (float)sqrt(s < 0 ? 0. : s);
+            const float scale = norm > P.max_norm ? P.max_norm / norm : norm <= P.max_norm ? 1.f : norm;
+            shared_scale = scale;
+            if (blockIdx.x == 0 && P.err) {
+                if (P.norm) *P.norm = norm;
+                if (P.scale) *P.scale = scale;
+                *P.err = finite(norm) ? 0 : ERR_NONFINITE;
+            }
         }
-        if (w) w[i] -= P.eta * v;
+    }
+    __syncthreads();
+    const float scale = shared_scale;
+    const long long lo = P.octets * blockIdx.x / gridDim.x, hi = P.octets * (blockIdx.x + 1) / gridDim.x;
+    if (lo >= hi) return;
+    for (int n = job_of(P, hi - 1); n >= 0 && P.job[n].first + P.job[n].rows * P.job[n].per_row > lo; --n) {
+        const ClipJob &j = P.job[n];
+        if (!j.w && (!j.out || (j.out == j.x && scale == 1.f))) continue;
+        const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
+        if (j.dtype == KFAC_BF16) apply_run<KFAC_BF16>(j, a, b, scale, P.eta);
+        else if (j.dtype == KFAC_F16) apply_run<KFAC_F16>(j, a, b, scale, P.eta);
+        else apply_run<KFAC_F32>(j, a, b, scale, P.eta);
     }
 }
 
@@ -193,34 +351,91 @@ kfac_status check_clip(const kfac_clip_desc *descs, int count, float max_norm, f
 
 ClipJob job_from(const kfac_clip_desc &d) {
     ClipJob j{(const char *)d.x, (const char *)d.y, (char *)d.out, d.w, d.ld, d.ld_y, d.ld_out, d.ld_w,
-              d.rows, d.cols, d.dtype, d.out_dtype, 1, 0};
+              d.rows, d.cols, 0, 0, (uint8_t)d.dtype, (uint8_t)d.out_dtype, 0, 0, 0};
     if (d.rows == 1 || (d.ld == d.cols && (!d.y || d.ld_y == d.cols) && (!d.out || d.ld_out == d.cols) &&
                         (!d.w || d.ld_w == d.cols))) {
         j.cols = d.rows * d.cols;
         j.rows = 1;
     }
+    // The octets lie so that w, else out, else x is taken on 16-byte boundaries; what
+    // is only read may lie anywhere.  What is read and written has to be on them.
+    const int es = size_of(d.dtype), es_out = size_of(d.out_dtype);
+    const uintptr_t lead = d.w ? (uintptr_t)d.w : d.out ? (uintptr_t)d.out : (uintptr_t)d.x;
+    const int es_lead = d.w ? 4 : d.out ? es_out : es;
+    // rows that start alike modulo 16 bytes: ld a multiple of 8 elements, or one row
+    const bool alike = j.rows == 1 || (d.ld % OCTET == 0 && (!d.y || d.ld_y % OCTET == 0) &&
+                                       (!d.out || d.ld_out % OCTET == 0) && (!d.w || d.ld_w % OCTET == 0));
+    if (alike) {
+        j.shift = (uint8_t)((lead & 15) / es_lead);
+        const auto aligned = [&](const void *p, int size) { return ((uintptr_t)p - (uintptr_t)j.shift * size) % 16 == 0; };
+        j.out_vec = d.out && aligned(d.out, es_out);
+        j.vec = d.out != d.x || j.out_vec;
+    }
+    j.per_row = ceil_div(j.cols + j.shift, OCTET);
     return j;
-}
-long long chunks_of(const ClipJob &j) { return j.rows * ceil_div(j.cols, CHUNK); }
-
-long long all_chunks(const kfac_clip_desc *descs, int count) {
-    long long n = 0;
-    for (int i = 0; i < count; ++i)
-        if (descs[i].rows > 0 && descs[i].cols > 0) n += chunks_of(job_from(descs[i]));
-    return n;
 }
 
 struct ClipPlan {
     int *err;
-    float *scale;
     double *part;
+    int parts;
 };
-ClipPlan plan_clip(long long chunks, Arena &ws) {
+// CTAs of a launch over `octets`.
+int ctas_of(long long octets) {
+    return (int)std::max<long long>(1, std::min<long long>(device_sm_count() * CLIP_PER_SM, ceil_div(octets, CLIP_THREADS)));
+}
+int tensors_of(int count) { return count <= CLIP_FEW ? CLIP_FEW : CLIP_MANY; }
+ClipPlan plan_clip(int count, Arena &ws) {
     ClipPlan p;
     p.err = ws.take<int>(64);
-    p.scale = ws.take<float>(1);
-    p.part = ws.take<double>((size_t)chunks);
+    // (at most; a launch of few octets has fewer CTAs)
+    p.parts = (int)std::max<long long>(1, ceil_div(count, tensors_of(count))) * device_sm_count() * CLIP_PER_SM;
+    p.part = ws.take<double>((size_t)p.parts);
     return p;
+}
+
+// Both passes, in launches of MAX tensors.
+template <int MAX>
+kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, float eta, float *norm, float *scale,
+                     const ClipPlan &plan, cudaStream_t st) {
+    std::unique_ptr<ClipParams<MAX>> P(new ClipParams<MAX>);
+    P->part = plan.part;
+    P->max_norm = max_norm;
+    P->eta = eta;
+    P->norm = norm;
+    P->scale = scale;
+    const int launches = std::max(1, (count + MAX - 1) / MAX);
+    auto fill = [&](int launch) {
+        P->n = 0;
+        P->octets = 0;
+        for (int i = launch * MAX; i < std::min(count, launch * MAX + MAX); ++i) {
+            if (descs[i].rows == 0 || descs[i].cols == 0) continue;
+            ClipJob j = job_from(descs[i]);
+            j.first = P->octets;
+            P->octets += j.rows * j.per_row;
+            P->job[P->n++] = j;
+        }
+    };
+    int parts = 0;
+    for (int l = 0; l < launches; ++l) {
+        fill(l);
+        P->part0 = parts;
+        if (P->n == 0) continue;
+        const int ctas = ctas_of(P->octets);
+        parts += ctas;
+        KFAC_LAUNCH(KK_CLIP_NORM, st, (clip_norm_kernel<MAX>), ctas, CLIP_THREADS, 0, *P);
+    }
+    P->parts = parts;
+    for (int l = 0; l < launches; ++l) {
+        if (launches > 1) fill(l);
+        bool writes = false;
+        for (int i = 0; i < P->n; ++i) writes |= P->job[i].out || P->job[i].w;
+        if (l > 0 && !writes) continue;
+        P->err = l == 0 ? plan.err : nullptr;
+        if (!writes) P->octets = 0;
+        KFAC_LAUNCH(KK_CLIP_APPLY, st, (clip_apply_kernel<MAX>), writes ? ctas_of(P->octets) : 1, CLIP_THREADS, 0, *P);
+    }
+    return KFAC_OK;
 }
 
 }  // namespace
@@ -231,7 +446,7 @@ using namespace kfac;
 extern "C" size_t kfac_clip_norm_workspace_size(const kfac_clip_desc *descs, int count) {
     if (check_clip(descs, count, 1.f, 0.f) != KFAC_OK) return 0;
     Arena a;
-    plan_clip(all_chunks(descs, count), a);
+    plan_clip(count, a);
     return a.used;
 }
 
@@ -240,47 +455,15 @@ extern "C" kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, fl
     kfac_status s = check_clip(descs, count, max_norm, eta);
     if (s != KFAC_OK) return s;
     if (!workspace || ((uintptr_t)workspace % 256) != 0) return KFAC_ERR_WORKSPACE;
-    const long long chunks = all_chunks(descs, count);
-    if (chunks > 0x7fffffffLL) return KFAC_ERR_UNSUPPORTED;
     Arena ws(workspace, workspace_bytes);
-    const ClipPlan p = plan_clip(chunks, ws);
+    const ClipPlan plan = plan_clip(count, ws);
     if (!ws.fits()) return KFAC_ERR_WORKSPACE;
-    bool writes = false;
     for (int i = 0; i < count; ++i) {
         const kfac_clip_desc &d = descs[i];
         if (!all_on_this_device({d.x, d.y, d.out, d.w})) return KFAC_ERR_INVALID;
-        writes |= d.out || d.w;
     }
     if (!all_on_this_device({norm, scale})) return KFAC_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;
-    std::unique_ptr<ClipParams> P(new ClipParams);
-    auto pass = [&](bool apply) -> kfac_status {
-        int part0 = 0;
-        for (int i = 0; i < count;) {
-            P->n = P->chunks = 0;
-            for (; i < count && P->n < CLIP_MAX; ++i) {
-                if (descs[i].rows == 0 || descs[i].cols == 0) continue;
-                ClipJob j = job_from(descs[i]);
-                j.per_row = (int)ceil_div(j.cols, CHUNK);
-                j.first = P->chunks;
-                P->chunks += (int)chunks_of(j);
-                P->job[P->n++] = j;
-            }
-            if (P->n == 0) break;
-            P->part0 = part0;
-            P->part = p.part;
-            P->scale = p.scale;
-            P->eta = eta;
-            part0 += P->chunks;
-            if (apply)
-                KFAC_LAUNCH(KK_CLIP_APPLY, st, clip_apply_kernel, P->chunks, CLIP_THREADS, 0, *P);
-            else
-                KFAC_LAUNCH(KK_CLIP_NORM, st, clip_norm_kernel, P->chunks, CLIP_THREADS, 0, *P);
-        }
-        return KFAC_OK;
-    };
-    if ((s = pass(false)) != KFAC_OK) return s;
-    ClipTotal T{p.part, chunks, max_norm, norm, scale, p.scale, p.err};
-    KFAC_LAUNCH(KK_CLIP_NORM, st, clip_total_kernel, 1, CLIP_THREADS, 0, T);
-    return writes ? pass(true) : KFAC_OK;
+    return count <= CLIP_FEW ? run_clip<CLIP_FEW>(descs, count, max_norm, eta, norm, scale, plan, st)
+                             : run_clip<CLIP_MANY>(descs, count, max_norm, eta, norm, scale, plan, st);
 }

@@ -85,7 +85,6 @@ struct Sum2 {
 // made by every thread.
 struct Wide {
     float hi, lo;
-    __device__ __forceinline__ Wide(float v = 0.f) : hi(v), lo(0.f) {}
     __device__ __forceinline__ void add(float b) {
         const float t = __fadd_rn(hi, b), bb = __fsub_rn(t, hi);
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, bb)), __fsub_rn(b, bb)));

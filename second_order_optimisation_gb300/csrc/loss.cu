@@ -730,7 +730,7 @@ __device__ __forceinline__ Wide block_sum(Wide v, Wide *part) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
     __syncthreads();
-    Wide all;
+    Wide all{};
     if (threadIdx.x < 32) {
         if ((int)threadIdx.x < (int)blockDim.x / 32) all = part[threadIdx.x];
         all.add_lanes();
@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_sum_kernel(const __grid_c
     pdl_trigger();
     const int rank = blockIdx.x, ctas = gridDim.x;
     const long long per = (P.rows + ctas - 1) / ctas, r0 = min(P.rows, rank * per), r1 = min(P.rows, r0 + per);
-    Wide sum[5];
+    Wide sum[5] = {};
     int bad = 0;
     for (long long row = r0 + threadIdx.x; row < r1; row += ROWS_THREADS) {
         const float4 t = P.terms[row];
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_sum_kernel(const __grid_c
     cluster_sync();
     if (rank != 0 || threadIdx.x >= 32) return;
     const int i = threadIdx.x;
-    Wide s;
+    Wide s{};
     int flag = 0;
     for (int c = 0; c < ctas; ++c) {
         if (i < 5) s.add(all[c][i]);
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(PAIR_THREADS) pref_pairs_kernel(const __grid_c
     for (int q = 0; q < 2; ++q) {
         r0[q] = clamp_row(P.off[2 * b + q], P.rows);
         r1[q] = clamp_row(P.off[2 * b + q + 1], P.rows);
-        Wide s;
+        Wide s{};
         int c = 0;
         for (long long row = r0[q] + threadIdx.x; row < r1[q]; row += PAIR_THREADS) {
             const long long t = P.target_i32 ? (long long)((const int32_t *)P.target)[row]
@@ -979,7 +979,7 @@ __global__ void __launch_bounds__(PAIR_THREADS) pref_sum_kernel(const __grid_con
     __shared__ int ipart[32];
     pdl_wait();
     pdl_trigger();
-    Wide s;
+    Wide s{};
     int bad = 0;
     for (int b = threadIdx.x; b < P.pairs; b += PAIR_THREADS) {
         s.add(P.terms[b]);
