@@ -22,7 +22,7 @@ namespace kfac {
 namespace {
 
 constexpr int CLIP_FEW = 16, CLIP_MANY = 216;  // tensors of one launch (kernel parameters)
-constexpr int CLIP_THREADS = 512, CLIP_PER_SM = 2, OCTET = 8;
+constexpr int CLIP_THREADS = 512, CLIP_PER_SM = 2, OCTET = 8, SHORT_RUN = 192;
 
 struct ClipJob {
     const char *x, *y;
@@ -61,32 +61,43 @@ __device__ __forceinline__ uint4 ld16(const char *p) {
     return *reinterpret_cast<const uint4 *>(p);
 }
 template <int DT>
+struct Raw {
+    static constexpr int Q = Elem<DT>::N == 4 ? 2 : 1;  // 16-byte pieces of eight elements
+    uint4 u[Q + 1];
+    __device__ __forceinline__ void load(const char *p, int off) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) u[q] = ld16(p - off + 16 * q);
+        if (off) u[Q] = ld16(p - off + 16 * Q);
+    }
+    __device__ __forceinline__ void values(int off, float *v) const {
+        if (off == 0) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) Elem<DT>::unpack(u[q], v + 4 * q);
+            return;
+        }
+        uint32_t w[4 * (Q + 1)];
+#pragma unroll
+        for (int q = 0; q <= Q; ++q) w[4 * q] = u[q].x, w[4 * q + 1] = u[q].y, w[4 * q + 2] = u[q].z, w[4 * q + 3] = u[q].w;
+        // left by 8, 4 and 2 bytes as the offset has them
+        if (off & 8)
+#pragma unroll
+            for (int i = 0; i + 2 < 4 * (Q + 1); ++i) w[i] = w[i + 2];
+        if (off & 4)
+#pragma unroll
+            for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = w[i + 1];
+        if (Elem<DT>::N == 8 && (off & 2))
+#pragma unroll
+            for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            Elem<DT>::unpack(make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]), v + 4 * q);
+    }
+};
+template <int DT>
 __device__ __forceinline__ void load8(const char *p, int off, float *v) {
-    constexpr int Q = Elem<DT>::N == 4 ? 2 : 1;  // 16-byte pieces of eight elements
-    if (off == 0) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) Elem<DT>::unpack(ld16(p + 16 * q), v + 4 * q);
-        return;
-    }
-    uint32_t w[4 * (Q + 1)];
-#pragma unroll
-    for (int q = 0; q <= Q; ++q) {
-        const uint4 u = ld16(p - off + 16 * q);
-        w[4 * q] = u.x, w[4 * q + 1] = u.y, w[4 * q + 2] = u.z, w[4 * q + 3] = u.w;
-    }
-    // left by 8, 4 and 2 bytes as the offset has them
-    if (off & 8)
-#pragma unroll
-        for (int i = 0; i + 2 < 4 * (Q + 1); ++i) w[i] = w[i + 2];
-    if (off & 4)
-#pragma unroll
-        for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = w[i + 1];
-    if (off & 2)
-#pragma unroll
-        for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-        Elem<DT>::unpack(make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]), v + 4 * q);
+    Raw<DT> r;
+    r.load(p, off);
+    r.values(off, v);
 }
 template <int DT>
 __device__ __forceinline__ void store8(char *p, const float *v) {
@@ -163,16 +174,89 @@ __device__ __forceinline__ int to_one(unsigned magnitude) {
     return max(-126, min(126, 127 - (int)(magnitude >> 23)));
 }
 
-// This thread's sum of x y over octets lo .. hi - 1 of a tensor.
+// The octets of lo .. hi - 1 of a tensor without gaps that have eight elements on
+// both sides: they are taken from moving pointers, with no test of each.
+__device__ __forceinline__ void inner_run(const ClipJob &j, long long lo, long long hi, long long &a, long long &b) {
+    a = b = lo;
+    if (j.rows > 1 || !j.vec) return;
+    a = max(lo, (long long)(2 * OCTET + j.shift - 1) / OCTET);
+    b = max(a, min(hi, (j.cols + j.shift) / OCTET - 1));
+    if (a >= hi) a = b = lo;
+}
+__device__ __forceinline__ float sum_of_products(const float *x, const float *y) {
+    float q[OCTET];
+#pragma unroll
+    for (int e = 0; e < OCTET; ++e) q[e] = x[e] * y[e];
+    return ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+}
 template <int DT, bool METRIC>
-__device__ __forceinline__ Wide products(const ClipJob &j, long long lo, long long hi) {
+__device__ __noinline__ Wide inner_products(const ClipJob &j, long long a, long long b, Wide sum) {
+    constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, UNROLL = (METRIC ? 2 : 4) * (ES == 2 ? 2 : 1), STEP = CLIP_THREADS * OCTET * ES;
+    const char *x = j.x + (a * OCTET - j.shift) * ES + threadIdx.x * (OCTET * ES);
+    const char *y = METRIC ? j.y + (a * OCTET - j.shift) * ES + threadIdx.x * (OCTET * ES) : x;
+    const int oy = (int)((uintptr_t)y & 15);  // (x is on its boundaries)
+    long long left = b - a - threadIdx.x;  // octets from this thread's on
+    for (; left > (UNROLL - 1) * CLIP_THREADS; left -= UNROLL * CLIP_THREADS) {
+        Raw<DT> u[UNROLL], v[METRIC ? UNROLL : 1];
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {
+            u[k].load(x + k * STEP, 0);
+            if (METRIC) v[k].load(y + k * STEP, oy);
+        }
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < UNROLL; ++k) {
+            float f[OCTET], h[OCTET];
+            u[k].values(0, f);
+            if (METRIC) v[k].values(oy, h);
+            t += sum_of_products(f, METRIC ? h : f);
+        }
+        sum.add(t);
+        x += UNROLL * STEP;
+        y += UNROLL * STEP;
+    }
+    for (; left > 0; left -= CLIP_THREADS) {
+        float f[OCTET], h[OCTET];
+        load8<DT>(x, 0, f);
+        if (METRIC) load8<DT>(y, oy, h);
+        sum.add(sum_of_products(f, METRIC ? h : f));
+        x += STEP;
+        y += STEP;
+    }
+    return sum;
+}
+
+template <int DT, bool METRIC>
+__device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long long hi, int tid, int nt, Wide sum);
+// This thread's sum of x y over octets lo .. hi - 1 of a tensor, added to `sum`.
+// A short run, and a long one's ends, are one warp's, the n-th of them the
+// n-th warp's, so that many small tensors go on side by side.
+template <int DT, bool METRIC>
+__device__ __forceinline__ void products(const ClipJob &j, int n, long long lo, long long hi, Wide &sum) {
+    const int lane = threadIdx.x % 32;
+    const bool mine = (int)threadIdx.x / 32 == n % (CLIP_THREADS / 32);
+    if (hi - lo < SHORT_RUN) {
+        if (mine) sum = outer_products<DT, METRIC>(j, lo, hi, lane, 32, sum);
+        return;
+    }
+    long long a, b;
+    inner_run(j, lo, hi, a, b);
+    if (b > a) {
+        if (mine) sum = outer_products<DT, METRIC>(j, lo, a, lane, 32, sum);
+        if (mine) sum = outer_products<DT, METRIC>(j, b, hi, lane, 32, sum);
+        sum = inner_products<DT, METRIC>(j, a, b, sum);
+    } else {
+        sum = outer_products<DT, METRIC>(j, lo, hi, threadIdx.x, CLIP_THREADS, sum);
+    }
+}
+template <int DT, bool METRIC>
+__device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long long hi, int tid, int nt, Wide sum) {
     constexpr int UNROLL = METRIC ? 2 : 4;  // octets in flight
-    Wide sum{};
-    for (long long i = lo + threadIdx.x; i < hi; i += UNROLL * CLIP_THREADS) {
+    for (long long i = lo + tid; i < hi; i += UNROLL * nt) {
         float x[UNROLL][OCTET], y[UNROLL][OCTET];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const long long at = i + u * CLIP_THREADS;
+            const long long at = i + u * nt;
             if (at < hi) {
                 const Place p = place_of(j, at);
                 octet<DT>(j.x, j.ld, p, j.cols, j.vec, x[u]);
@@ -185,19 +269,16 @@ __device__ __forceinline__ Wide products(const ClipJob &j, long long lo, long lo
         float t = 0.f;
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            float q[OCTET];
-#pragma unroll
-            for (int e = 0; e < OCTET; ++e) q[e] = x[u][e] * (METRIC ? y[u][e] : x[u][e]);
-            t += ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
+            t += sum_of_products(x[u], METRIC ? y[u] : x[u]);
         }
         sum.add(t);
     }
     return sum;
 }
-// The same over the block, from values scaled by powers of two; `plain` where a
-// value is not finite.
+// The same over the block, from values scaled by powers of two (unscaled where
+// one is not finite).
 template <int DT>
-__device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long long hi, double plain) {
+__device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long long hi) {
     const char *yb = j.y ? j.y : j.x;
     const long long ld_y = j.y ? j.ld_y : j.ld;
     unsigned mx = 0, my = 0;
@@ -213,8 +294,8 @@ __device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long l
     }
     mx = block_max(mx);
     my = block_max(my);
-    if (mx >= 0x7f800000u || my >= 0x7f800000u) return plain;
-    const int ex = to_one(mx), ey = to_one(my);
+    const bool scale = mx < 0x7f800000u && my < 0x7f800000u;
+    const int ex = scale ? to_one(mx) : 0, ey = scale ? to_one(my) : 0;
     const float fx = pow2(ex), fy = pow2(ey);
     Wide sum{};
     for (long long i = lo + threadIdx.x; i < hi; i += CLIP_THREADS) {
@@ -225,34 +306,130 @@ __device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long l
     }
     return ldexp(block_wide(sum).value(), -ex - ey);
 }
-template <int DT>
-__device__ __forceinline__ double run_sum(const ClipJob &j, long long lo, long long hi) {
-    const Wide s = block_wide(j.y ? products<DT, true>(j, lo, hi) : products<DT, false>(j, lo, hi));
-    // every warp has joined the warps' sums, and hi is the same for all threads
-    const double plain = s.value();
-    return finite(s.hi) && fabsf(s.hi) >= 1e-28f ? plain : scaled_sum<DT>(j, lo, hi, plain);
-}
-
 template <int MAX>
 __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(const __grid_constant__ ClipParams<MAX> P) {
     pdl_wait();
     pdl_trigger();
     const long long lo = P.octets * blockIdx.x / gridDim.x, hi = P.octets * (blockIdx.x + 1) / gridDim.x;
-    double sum = 0;
-    for (int n = job_of(P, lo); n < P.n && P.job[n].first < hi; ++n) {
+    const int first = job_of(P, lo);
+    Wide mine{};
+    for (int n = first; n < P.n && P.job[n].first < hi; ++n) {
         const ClipJob &j = P.job[n];
         const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
-        sum += j.dtype == KFAC_BF16 ? run_sum<KFAC_BF16>(j, a, b)
-               : j.dtype == KFAC_F16 ? run_sum<KFAC_F16>(j, a, b) : run_sum<KFAC_F32>(j, a, b);
+        if (j.dtype == KFAC_BF16) {
+            if (j.y) products<KFAC_BF16, true>(j, n, a, b, mine);
+            else products<KFAC_BF16, false>(j, n, a, b, mine);
+        } else if (j.dtype == KFAC_F16) {
+            if (j.y) products<KFAC_F16, true>(j, n, a, b, mine);
+            else products<KFAC_F16, false>(j, n, a, b, mine);
+        } else {
+            if (j.y) products<KFAC_F32, true>(j, n, a, b, mine);
+            else products<KFAC_F32, false>(j, n, a, b, mine);
+        }
+    }
+    // every warp joins the warps' sums, and hi is the same for all threads
+    const Wide s = block_wide(mine);
+    double sum = s.value();
+    if (!finite(s.hi) || fabsf(s.hi) < 1e-28f) {
+        sum = 0;
+        for (int n = first; n < P.n && P.job[n].first < hi; ++n) {
+            const ClipJob &j = P.job[n];
+            const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
+            sum += j.dtype == KFAC_BF16 ? scaled_sum<KFAC_BF16>(j, a, b)
+                   : j.dtype == KFAC_F16 ? scaled_sum<KFAC_F16>(j, a, b) : scaled_sum<KFAC_F32>(j, a, b);
+        }
     }
     if (threadIdx.x == 0) P.part[P.part0 + blockIdx.x] = sum;
 }
 
+// N octets of a tensor without gaps: one at x (and out, w), the others each
+// `back` octets before it.
+template <int DT, bool W, int N>
+__device__ __forceinline__ void apply_octets(const char *x, int ox, char *out, int out_dtype, float *w, float scale,
+                                             float eta) {
+    constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, BACK = CLIP_THREADS * OCTET;
+    const int es_out = out_dtype == KFAC_F32 ? 4 : 2;
+    Raw<DT> r[N];
+    float4 p[N][2];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        r[k].load(x - k * BACK * ES, ox);
+        if (W) {
+            const float4 *q = reinterpret_cast<const float4 *>(w - k * BACK);
+            p[k][0] = q[0];
+            p[k][1] = q[1];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float v[OCTET];
+        r[k].values(ox, v);
+#pragma unroll
+        for (int e = 0; e < OCTET; ++e) v[e] *= scale;
+        if (out) {
+            char *o = out - k * BACK * es_out;
+            if (out_dtype == KFAC_BF16) store8<KFAC_BF16>(o, v);
+            else if (out_dtype == KFAC_F16) store8<KFAC_F16>(o, v);
+            else store8<KFAC_F32>(o, v);
+        }
+        if (W) {
+            float4 *q = reinterpret_cast<float4 *>(w - k * BACK);
+            q[0] = make_float4(p[k][0].x - eta * v[0], p[k][0].y - eta * v[1], p[k][0].z - eta * v[2],
+                               p[k][0].w - eta * v[3]);
+            q[1] = make_float4(p[k][1].x - eta * v[4], p[k][1].y - eta * v[5], p[k][1].z - eta * v[6],
+                               p[k][1].w - eta * v[7]);
+        }
+    }
+}
+// The octets inside a tensor without gaps, from the end.
+template <int DT, bool W>
+__device__ __noinline__ void apply_inner(const ClipJob &j, long long a, long long b, float scale, float eta) {
+    constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, N = W ? 2 : 4;
+    const int es_out = j.out_dtype == KFAC_F32 ? 4 : 2;
+    long long left = b - a - threadIdx.x;             // octets up to this thread's
+    const long long c = (a + left - 1) * OCTET - j.shift;  // its first element
+    const char *x = j.x + c * ES;
+    char *out = j.out ? j.out + c * es_out : nullptr;
+    float *w = W ? j.w + c : nullptr;
+    const int ox = (int)((uintptr_t)x & 15);
+    auto back = [&](int n) {
+        x -= (long long)n * CLIP_THREADS * OCTET * ES;
+        if (out) out -= (long long)n * CLIP_THREADS * OCTET * es_out;
+        if (W) w -= (long long)n * CLIP_THREADS * OCTET;
+        left -= n * CLIP_THREADS;
+    };
+    for (; left > (N - 1) * CLIP_THREADS; back(N)) apply_octets<DT, W, N>(x, ox, out, j.out_dtype, w, scale, eta);
+    for (; left > 0; back(1)) apply_octets<DT, W, 1>(x, ox, out, j.out_dtype, w, scale, eta);
+}
 template <int DT>
-__device__ __forceinline__ void apply_run(const ClipJob &j, long long lo, long long hi, float scale, float eta) {
+__device__ __noinline__ void apply_outer(const ClipJob &j, long long lo, long long hi, int tid, int nt, float scale,
+                                            float eta);
+// (short runs and ends as in the first pass)
+template <int DT>
+__device__ __forceinline__ void apply_run(const ClipJob &j, int n, long long lo, long long hi, float scale, float eta) {
+    const int lane = threadIdx.x % 32;
+    const bool mine = (int)threadIdx.x / 32 == n % (CLIP_THREADS / 32);
+    if (hi - lo < SHORT_RUN) {
+        if (mine) apply_outer<DT>(j, lo, hi, lane, 32, scale, eta);
+        return;
+    }
+    long long a, b;
+    inner_run(j, lo, hi, a, b);
+    if (b > a && (!j.out || j.out_vec)) {
+        if (mine) apply_outer<DT>(j, b, hi, lane, 32, scale, eta);
+        if (mine) apply_outer<DT>(j, lo, a, lane, 32, scale, eta);
+        if (j.w) apply_inner<DT, true>(j, a, b, scale, eta);
+        else apply_inner<DT, false>(j, a, b, scale, eta);
+    } else {
+        apply_outer<DT>(j, lo, hi, threadIdx.x, CLIP_THREADS, scale, eta);
+    }
+}
+template <int DT>
+__device__ __noinline__ void apply_outer(const ClipJob &j, long long lo, long long hi, int tid, int nt, float scale,
+                                            float eta) {
     const int es_out = j.out_dtype == KFAC_F32 ? 4 : 2;
     // from the end of the run
-    for (long long i = hi - 1 - threadIdx.x; i >= lo; i -= CLIP_THREADS) {
+    for (long long i = hi - 1 - tid; i >= lo; i -= nt) {
         const Place p = place_of(j, i);
         float x[OCTET];
         octet<DT>(j.x, j.ld, p, j.cols, j.vec, x);
@@ -323,9 +500,9 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_apply_kernel(c
         const ClipJob &j = P.job[n];
         if (!j.w && (!j.out || (j.out == j.x && scale == 1.f))) continue;
         const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
-        if (j.dtype == KFAC_BF16) apply_run<KFAC_BF16>(j, a, b, scale, P.eta);
-        else if (j.dtype == KFAC_F16) apply_run<KFAC_F16>(j, a, b, scale, P.eta);
-        else apply_run<KFAC_F32>(j, a, b, scale, P.eta);
+        if (j.dtype == KFAC_BF16) apply_run<KFAC_BF16>(j, n, a, b, scale, P.eta);
+        else if (j.dtype == KFAC_F16) apply_run<KFAC_F16>(j, n, a, b, scale, P.eta);
+        else apply_run<KFAC_F32>(j, n, a, b, scale, P.eta);
     }
 }
 
@@ -349,7 +526,7 @@ kfac_status check_clip(const kfac_clip_desc *descs, int count, float max_norm, f
     return KFAC_OK;
 }
 
-ClipJob job_from(const kfac_clip_desc &d) {
+ClipJob job_from(const kfac_clip_desc &d, bool apply) {
     ClipJob j{(const char *)d.x, (const char *)d.y, (char *)d.out, d.w, d.ld, d.ld_y, d.ld_out, d.ld_w,
               d.rows, d.cols, 0, 0, (uint8_t)d.dtype, (uint8_t)d.out_dtype, 0, 0, 0};
     if (d.rows == 1 || (d.ld == d.cols && (!d.y || d.ld_y == d.cols) && (!d.out || d.ld_out == d.cols) &&
@@ -357,11 +534,12 @@ ClipJob job_from(const kfac_clip_desc &d) {
         j.cols = d.rows * d.cols;
         j.rows = 1;
     }
-    // The octets lie so that w, else out, else x is taken on 16-byte boundaries; what
-    // is only read may lie anywhere.  What is read and written has to be on them.
+    // The octets lie so that x is taken on 16-byte boundaries in the first pass, and
+    // w, else out, in the second; what is only read may lie anywhere.  What is read
+    // and written has to be on the boundaries.
     const int es = size_of(d.dtype), es_out = size_of(d.out_dtype);
-    const uintptr_t lead = d.w ? (uintptr_t)d.w : d.out ? (uintptr_t)d.out : (uintptr_t)d.x;
-    const int es_lead = d.w ? 4 : d.out ? es_out : es;
+    const uintptr_t lead = !apply ? (uintptr_t)d.x : d.w ? (uintptr_t)d.w : (uintptr_t)d.out;
+    const int es_lead = !apply ? es : d.w ? 4 : es_out;
     // rows that start alike modulo 16 bytes: ld a multiple of 8 elements, or one row
     const bool alike = j.rows == 1 || (d.ld % OCTET == 0 && (!d.y || d.ld_y % OCTET == 0) &&
                                        (!d.out || d.ld_out % OCTET == 0) && (!d.w || d.ld_w % OCTET == 0));
@@ -369,7 +547,7 @@ ClipJob job_from(const kfac_clip_desc &d) {
         j.shift = (uint8_t)((lead & 15) / es_lead);
         const auto aligned = [&](const void *p, int size) { return ((uintptr_t)p - (uintptr_t)j.shift * size) % 16 == 0; };
         j.out_vec = d.out && aligned(d.out, es_out);
-        j.vec = d.out != d.x || j.out_vec;
+        j.vec = !apply || d.out != d.x || j.out_vec;
     }
     j.per_row = ceil_div(j.cols + j.shift, OCTET);
     return j;
@@ -405,12 +583,12 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
     P->norm = norm;
     P->scale = scale;
     const int launches = std::max(1, (count + MAX - 1) / MAX);
-    auto fill = [&](int launch) {
+    auto fill = [&](int launch, bool apply) {
         P->n = 0;
         P->octets = 0;
         for (int i = launch * MAX; i < std::min(count, launch * MAX + MAX); ++i) {
             if (descs[i].rows == 0 || descs[i].cols == 0) continue;
-            ClipJob j = job_from(descs[i]);
+            ClipJob j = job_from(descs[i], apply);
             j.first = P->octets;
             P->octets += j.rows * j.per_row;
             P->job[P->n++] = j;
@@ -418,7 +596,7 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
     };
     int parts = 0;
     for (int l = 0; l < launches; ++l) {
-        fill(l);
+        fill(l, false);
         P->part0 = parts;
         if (P->n == 0) continue;
         const int ctas = ctas_of(P->octets);
@@ -427,7 +605,7 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
     }
     P->parts = parts;
     for (int l = 0; l < launches; ++l) {
-        if (launches > 1) fill(l);
+        fill(l, true);
         bool writes = false;
         for (int i = 0; i < P->n; ++i) writes |= P->job[i].out || P->job[i].w;
         if (l > 0 && !writes) continue;
