@@ -137,6 +137,42 @@ bool on_this_device(const void *p) {
     return a.device == dev;
 }
 
+namespace {
+typedef CUresult (*AddressRangeFn)(CUdeviceptr *, size_t *, CUdeviceptr);
+AddressRangeFn address_range_fn() {
+    static std::once_flag once;
+    static AddressRangeFn fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (AddressRangeFn)p;
+    });
+    return fn;
+}
+}  // namespace
+
+bool DeviceMemory::holds(const void *p) {
+    if (!p) return true;
+    const uintptr_t a = (uintptr_t)p;
+    if (n && a >= seen[last].begin && a < seen[last].end) return true;
+    for (int i = 0; i < n; ++i)
+        if (a >= seen[i].begin && a < seen[i].end) {
+            last = i;
+            return true;
+        }
+    if (!on_this_device(p)) return false;
+    CUdeviceptr base = 0;
+    size_t size = 0;
+    const AddressRangeFn range = address_range_fn();
+    if (n < MOST && range && range(&base, &size, (CUdeviceptr)a) == CUDA_SUCCESS) {
+        last = n;
+        seen[n++] = Range{(uintptr_t)base, (uintptr_t)base + size};
+    }
+    return true;
+}
+
 bool all_on_this_device(std::initializer_list<const void *> ps) {
     for (const void *p : ps)
         if (!on_this_device(p)) return false;

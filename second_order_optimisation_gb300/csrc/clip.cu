@@ -22,7 +22,7 @@ namespace kfac {
 namespace {
 
 constexpr int CLIP_FEW = 16, CLIP_MANY = 216;  // tensors of one launch (kernel parameters)
-constexpr int CLIP_THREADS = 512, CLIP_PER_SM = 2, OCTET = 8, SHORT_RUN = 192;
+constexpr int CLIP_THREADS = 256, CLIP_PER_SM = 3, OCTET = 8, SHORT_RUN = 192, TILE = 4096;
 
 struct ClipJob {
     const char *x, *y;
@@ -41,7 +41,7 @@ template <int MAX>
 struct ClipParams {
     ClipJob job[MAX];
     int n;
-    long long octets;
+    long long octets, tile;
     double *part;        // one for each CTA of each launch
     int part0, parts;    // this launch's first, and all launches'
     float max_norm, eta;
@@ -310,10 +310,10 @@ template <int MAX>
 __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(const __grid_constant__ ClipParams<MAX> P) {
     pdl_wait();
     pdl_trigger();
-    const long long lo = P.octets * blockIdx.x / gridDim.x, hi = P.octets * (blockIdx.x + 1) / gridDim.x;
-    const int first = job_of(P, lo);
     Wide mine{};
-    for (int n = first; n < P.n && P.job[n].first < hi; ++n) {
+    for (long long lo = P.tile * blockIdx.x; lo < P.octets; lo += P.tile * gridDim.x) {
+    const long long hi = min(P.octets, lo + P.tile);
+    for (int n = job_of(P, lo); n < P.n && P.job[n].first < hi; ++n) {
         const ClipJob &j = P.job[n];
         const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
         if (j.dtype == KFAC_BF16) {
@@ -327,16 +327,20 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(co
             else products<KFAC_F32, false>(j, n, a, b, mine);
         }
     }
+    }
     // every warp joins the warps' sums, and hi is the same for all threads
     const Wide s = block_wide(mine);
     double sum = s.value();
     if (!finite(s.hi) || fabsf(s.hi) < 1e-28f) {
         sum = 0;
-        for (int n = first; n < P.n && P.job[n].first < hi; ++n) {
+        for (long long lo = P.tile * blockIdx.x; lo < P.octets; lo += P.tile * gridDim.x) {
+        const long long hi = min(P.octets, lo + P.tile);
+        for (int n = job_of(P, lo); n < P.n && P.job[n].first < hi; ++n) {
             const ClipJob &j = P.job[n];
             const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
             sum += j.dtype == KFAC_BF16 ? scaled_sum<KFAC_BF16>(j, a, b)
                    : j.dtype == KFAC_F16 ? scaled_sum<KFAC_F16>(j, a, b) : scaled_sum<KFAC_F32>(j, a, b);
+        }
         }
     }
     if (threadIdx.x == 0) P.part[P.part0 + blockIdx.x] = sum;
@@ -494,8 +498,9 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_apply_kernel(c
     }
     __syncthreads();
     const float scale = shared_scale;
-    const long long lo = P.octets * blockIdx.x / gridDim.x, hi = P.octets * (blockIdx.x + 1) / gridDim.x;
-    if (lo >= hi) return;
+    const long long tiles = (P.octets + P.tile - 1) / P.tile;
+    for (long long t = tiles - 1 - blockIdx.x; t >= 0; t -= gridDim.x) {
+    const long long lo = t * P.tile, hi = min(P.octets, lo + P.tile);
     for (int n = job_of(P, hi - 1); n >= 0 && P.job[n].first + P.job[n].rows * P.job[n].per_row > lo; --n) {
         const ClipJob &j = P.job[n];
         if (!j.w && (!j.out || (j.out == j.x && scale == 1.f))) continue;
@@ -503,6 +508,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_apply_kernel(c
         if (j.dtype == KFAC_BF16) apply_run<KFAC_BF16>(j, n, a, b, scale, P.eta);
         else if (j.dtype == KFAC_F16) apply_run<KFAC_F16>(j, n, a, b, scale, P.eta);
         else apply_run<KFAC_F32>(j, n, a, b, scale, P.eta);
+    }
     }
 }
 
@@ -593,6 +599,8 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
             P->octets += j.rows * j.per_row;
             P->job[P->n++] = j;
         }
+        P->tile = std::max<long long>(1, ceil_div(P->octets, ctas_of(P->octets)));
+        if (!apply) P->tile = std::min<long long>(P->tile, TILE);
     };
     int parts = 0;
     for (int l = 0; l < launches; ++l) {
@@ -636,9 +644,11 @@ extern "C" kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, fl
     Arena ws(workspace, workspace_bytes);
     const ClipPlan plan = plan_clip(count, ws);
     if (!ws.fits()) return KFAC_ERR_WORKSPACE;
+    DeviceMemory memory;
     for (int i = 0; i < count; ++i) {
         const kfac_clip_desc &d = descs[i];
-        if (!all_on_this_device({d.x, d.y, d.out, d.w})) return KFAC_ERR_INVALID;
+        if (!memory.holds(d.x) || !memory.holds(d.y) || !memory.holds(d.out) || !memory.holds(d.w))
+            return KFAC_ERR_INVALID;
     }
     if (!all_on_this_device({norm, scale})) return KFAC_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;

@@ -172,6 +172,20 @@ kfac_status colsum_run(const ColsumJob *jobs, int njobs, float *partial, cudaStr
 // null); the entry points reject every other operand before enqueueing.
 bool on_this_device(const void *p);
 bool all_on_this_device(std::initializer_list<const void *> ps);
+// The same test for many pointers of one call: an allocation that has passed is
+// remembered (until the object goes), so that pointers into it are not asked of
+// the driver one by one.
+class DeviceMemory {
+    struct Range {
+        uintptr_t begin, end;
+    };
+    static constexpr int MOST = 16;
+    Range seen[MOST];
+    int n = 0, last = 0;
+
+public:
+    bool holds(const void *p);
+};
 
 // ----------------------------------------------------- inversion
 struct InvMatrix {
