@@ -54,50 +54,28 @@ __device__ __forceinline__ float elem(const char *p, long long i) {
     return Elem<DT>::value(((const typename Elem<DT>::bits *)p)[i]);
 }
 
-// Eight elements from any element boundary, by aligned 16-byte loads (`off` is
-// the address modulo 16): the pieces they lie in belong to the row wherever eight
-// more elements exist on both sides.
-__device__ __forceinline__ uint4 ld16(const char *p) {
-    return *reinterpret_cast<const uint4 *>(p);
-}
-template <int DT>
-struct Raw {
-    static constexpr int Q = Elem<DT>::N == 4 ? 2 : 1;  // 16-byte pieces of eight elements
-    uint4 u[Q + 1];
-    __device__ __forceinline__ void load(const char *p, int off) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) u[q] = ld16(p - off + 16 * q);
-        if (off) u[Q] = ld16(p - off + 16 * Q);
-    }
+// Eight elements from any element boundary.
+template <int DT, bool ANY>
+struct Raw : Pieces<Elem<DT>::N == 4 ? 2 : 1, ANY> {
+    static constexpr int Q = Elem<DT>::N == 4 ? 2 : 1;
     __device__ __forceinline__ void values(int off, float *v) const {
-        if (off == 0) {
+        uint4 w[Q];
+        this->take(off, w);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) Elem<DT>::unpack(u[q], v + 4 * q);
-            return;
-        }
-        uint32_t w[4 * (Q + 1)];
-#pragma unroll
-        for (int q = 0; q <= Q; ++q) w[4 * q] = u[q].x, w[4 * q + 1] = u[q].y, w[4 * q + 2] = u[q].z, w[4 * q + 3] = u[q].w;
-        // left by 8, 4 and 2 bytes as the offset has them
-        if (off & 8)
-#pragma unroll
-            for (int i = 0; i + 2 < 4 * (Q + 1); ++i) w[i] = w[i + 2];
-        if (off & 4)
-#pragma unroll
-            for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = w[i + 1];
-        if (Elem<DT>::N == 8 && (off & 2))
-#pragma unroll
-            for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            Elem<DT>::unpack(make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]), v + 4 * q);
+        for (int q = 0; q < Q; ++q) Elem<DT>::unpack(w[q], v + 4 * q);
     }
 };
 template <int DT>
 __device__ __forceinline__ void load8(const char *p, int off, float *v) {
-    Raw<DT> r;
-    r.load(p, off);
-    r.values(off, v);
+    if (off == 0) {
+        Raw<DT, false> r;
+        r.load(p, off);
+        r.values(off, v);
+    } else {
+        Raw<DT, true> r;
+        r.load(p, off);
+        r.values(off, v);
+    }
 }
 template <int DT>
 __device__ __forceinline__ void store8(char *p, const float *v) {
@@ -189,7 +167,7 @@ __device__ __forceinline__ float sum_of_products(const float *x, const float *y)
     for (int e = 0; e < OCTET; ++e) q[e] = x[e] * y[e];
     return ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
 }
-template <int DT, bool METRIC>
+template <int DT, bool METRIC, bool ANY>
 __device__ __noinline__ Wide inner_products(const ClipJob &j, long long a, long long b, Wide sum) {
     constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, UNROLL = (METRIC ? 2 : 4) * (ES == 2 ? 2 : 1), STEP = CLIP_THREADS * OCTET * ES;
     const char *x = j.x + (a * OCTET - j.shift) * ES + threadIdx.x * (OCTET * ES);
@@ -197,7 +175,8 @@ __device__ __noinline__ Wide inner_products(const ClipJob &j, long long a, long 
     const int oy = (int)((uintptr_t)y & 15);  // (x is on its boundaries)
     long long left = b - a - threadIdx.x;  // octets from this thread's on
     for (; left > (UNROLL - 1) * CLIP_THREADS; left -= UNROLL * CLIP_THREADS) {
-        Raw<DT> u[UNROLL], v[METRIC ? UNROLL : 1];
+        Raw<DT, false> u[UNROLL];
+        Raw<DT, ANY> v[METRIC ? UNROLL : 1];
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             u[k].load(x + k * STEP, 0);
@@ -244,7 +223,8 @@ __device__ __forceinline__ void products(const ClipJob &j, int n, long long lo, 
     if (b > a) {
         if (mine) sum = outer_products<DT, METRIC>(j, lo, a, lane, 32, sum);
         if (mine) sum = outer_products<DT, METRIC>(j, b, hi, lane, 32, sum);
-        sum = inner_products<DT, METRIC>(j, a, b, sum);
+        if (METRIC && (((uintptr_t)j.x ^ (uintptr_t)j.y) & 15)) sum = inner_products<DT, METRIC, METRIC>(j, a, b, sum);
+        else sum = inner_products<DT, METRIC, false>(j, a, b, sum);
     } else {
         sum = outer_products<DT, METRIC>(j, lo, hi, threadIdx.x, CLIP_THREADS, sum);
     }
@@ -348,12 +328,12 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(co
 
 // N octets of a tensor without gaps: one at x (and out, w), the others each
 // `back` octets before it.
-template <int DT, bool W, int N>
+template <int DT, bool W, bool ANY, int N>
 __device__ __forceinline__ void apply_octets(const char *x, int ox, char *out, int out_dtype, float *w, float scale,
                                              float eta) {
     constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, BACK = CLIP_THREADS * OCTET;
     const int es_out = out_dtype == KFAC_F32 ? 4 : 2;
-    Raw<DT> r[N];
+    Raw<DT, ANY> r[N];
     float4 p[N][2];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -386,7 +366,7 @@ __device__ __forceinline__ void apply_octets(const char *x, int ox, char *out, i
     }
 }
 // The octets inside a tensor without gaps, from the end.
-template <int DT, bool W>
+template <int DT, bool W, bool ANY>
 __device__ __noinline__ void apply_inner(const ClipJob &j, long long a, long long b, float scale, float eta) {
     constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, N = W ? 2 : 4;
     const int es_out = j.out_dtype == KFAC_F32 ? 4 : 2;
@@ -402,8 +382,8 @@ __device__ __noinline__ void apply_inner(const ClipJob &j, long long a, long lon
         if (W) w -= (long long)n * CLIP_THREADS * OCTET;
         left -= n * CLIP_THREADS;
     };
-    for (; left > (N - 1) * CLIP_THREADS; back(N)) apply_octets<DT, W, N>(x, ox, out, j.out_dtype, w, scale, eta);
-    for (; left > 0; back(1)) apply_octets<DT, W, 1>(x, ox, out, j.out_dtype, w, scale, eta);
+    for (; left > (N - 1) * CLIP_THREADS; back(N)) apply_octets<DT, W, ANY, N>(x, ox, out, j.out_dtype, w, scale, eta);
+    for (; left > 0; back(1)) apply_octets<DT, W, ANY, 1>(x, ox, out, j.out_dtype, w, scale, eta);
 }
 template <int DT>
 __device__ __noinline__ void apply_outer(const ClipJob &j, long long lo, long long hi, int tid, int nt, float scale,
@@ -422,8 +402,14 @@ __device__ __forceinline__ void apply_run(const ClipJob &j, int n, long long lo,
     if (b > a && (!j.out || j.out_vec)) {
         if (mine) apply_outer<DT>(j, b, hi, lane, 32, scale, eta);
         if (mine) apply_outer<DT>(j, lo, a, lane, 32, scale, eta);
-        if (j.w) apply_inner<DT, true>(j, a, b, scale, eta);
-        else apply_inner<DT, false>(j, a, b, scale, eta);
+        const bool any = ((uintptr_t)j.x - (uintptr_t)j.shift * (Elem<DT>::N == 4 ? 4 : 2)) & 15;
+        if (j.w) {
+            if (any) apply_inner<DT, true, true>(j, a, b, scale, eta);
+            else apply_inner<DT, true, false>(j, a, b, scale, eta);
+        } else {
+            if (any) apply_inner<DT, false, true>(j, a, b, scale, eta);
+            else apply_inner<DT, false, false>(j, a, b, scale, eta);
+        }
     } else {
         apply_outer<DT>(j, lo, hi, threadIdx.x, CLIP_THREADS, scale, eta);
     }

@@ -198,6 +198,45 @@ struct Elem<KFAC_F16> {
     }
 };
 
+__device__ __forceinline__ uint4 ld16(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// Q times 16 bytes from any element boundary, by aligned loads.  ANY: `off` is the
+// address modulo 16, not 0 and the same for all threads, and the pieces that the
+// bytes lie in reach less than 16 bytes before and behind them.
+template <int Q, bool ANY>
+struct Pieces {
+    uint4 u[Q + ANY];
+    __device__ __forceinline__ void load(const char *p, int off) {
+#pragma unroll
+        for (int q = 0; q < Q + ANY; ++q) u[q] = ld16(ANY ? p - off + 16 * q : p + 16 * q);
+    }
+    __device__ __forceinline__ void take(int off, uint4 *v) const {
+        if constexpr (!ANY) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) v[q] = u[q];
+        } else {
+            shift(off, v);
+        }
+    }
+    __device__ __forceinline__ void shift(int off, uint4 *v) const {
+        uint32_t w[4 * (Q + 1)];
+#pragma unroll
+        for (int q = 0; q <= Q; ++q) w[4 * q] = u[q].x, w[4 * q + 1] = u[q].y, w[4 * q + 2] = u[q].z, w[4 * q + 3] = u[q].w;
+        // left by 8, 4 and 2 bytes as the offset has them
+        if (off & 8)
+#pragma unroll
+            for (int i = 0; i + 2 < 4 * (Q + 1); ++i) w[i] = w[i + 2];
+        if (off & 4)
+#pragma unroll
+            for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = w[i + 1];
+        if (off & 2)
+#pragma unroll
+            for (int i = 0; i + 1 < 4 * (Q + 1); ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    }
+};
+
 // A row of `n` elements that may start anywhere: group g holds the elements
 // g N - phase .. g N - phase + N - 1 that exist, and starts on a 16-byte boundary.
 template <int DT>

@@ -116,35 +116,65 @@ __device__ __forceinline__ void zero_row(char *out, int n, int tid, int nt) {
     for (int i = tid; i < front; i += nt) e[i] = 0;
     for (int i = back + tid; i < n; i += nt) e[i] = 0;
 }
-// The gradient of a whole row, read again from its logits, by threads tid of
-// nt, 16 bytes at a time where both rows allow it.
-template <int DT, bool ENT>
-__device__ __forceinline__ void grad_row(const char *z, char *out, int n, long long tgt, const Coef &c, float k, int tid,
-                                         int nt) {
+// The gradient of a whole row, read again from its logits, by threads tid of nt.
+// Groups lie as the output does; a logits' row that starts elsewhere modulo 16
+// bytes is read in shifted pieces.
+template <int DT, bool ENT, bool FAST, bool ANY>
+__device__ __forceinline__ void grad_groups(const char *z, char *out, int n, int tgt, const Coef &c, float d_t,
+                                            const Shift &h, int tid, int nt) {
     using bits = typename Elem<DT>::bits;
-    const Row<DT> o(out, n), r(z, n);
-    const Shift h(c.m, k);
-    const bool same = (((uintptr_t)out ^ (uintptr_t)z) & 15) == 0;
-    for (int g = tid; g < o.groups(); g += nt) {
-        const int e0 = o.first(g);
-        uint4 u;
-        if (same) {
-            u = r.load(g);
-        } else {
-            bits b[Elem<DT>::N];
+    constexpr int N = Elem<DT>::N, BATCH = 4;
+    const Row<DT> o(out, n);
+    const char *src = z - o.phase * (int)sizeof(bits);  // where the row's group 0 would start
+    const int off = (int)((uintptr_t)src & 15);
+    const int a = ANY ? (N + o.phase + N - 1) / N : o.begin(), b = ANY ? max(a, (n + o.phase) / N - 1) : o.end();
+    char *to = const_cast<char *>(o.base);
+    for (int g = a + tid; g < b; g += BATCH * nt) {
+        Pieces<1, ANY> u[BATCH];
+        if (g + (BATCH - 1) * nt < b) {
 #pragma unroll
-            for (int i = 0; i < Elem<DT>::N; ++i) b[i] = e0 + i >= 0 && e0 + i < n ? ((const bits *)z)[e0 + i] : 0;
-            u = *reinterpret_cast<const uint4 *>(b);
-        }
-        const uint4 d = grad_group<DT, ENT, false>(u, c, h);
-        if (o.whole(g)) {
-            *reinterpret_cast<uint4 *>((bits *)out + e0) = d;
+            for (int i = 0; i < BATCH; ++i) u[i].load(src + (size_t)(g + i * nt) * 16, off);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                uint4 v;
+                u[i].take(off, &v);
+                *reinterpret_cast<uint4 *>(to + (size_t)(g + i * nt) * 16) = grad_group<DT, ENT, FAST>(v, c, h);
+            }
         } else {
-            Row<DT>::store_edge(out, e0, n, d);
+            for (int q = g; q < b; q += nt) {
+                uint4 v;
+                u[0].load(src + (size_t)q * 16, off);
+                u[0].take(off, &v);
+                *reinterpret_cast<uint4 *>(to + (size_t)q * 16) = grad_group<DT, ENT, FAST>(v, c, h);
+            }
         }
-        if (tgt >= e0 && tgt < e0 + Elem<DT>::N)
-            ((bits *)out)[tgt] = Elem<DT>::round(grad_target<ENT>(logit_at<DT>(z, tgt), c, k));
     }
+    // the elements before and behind: groups 0 .. a - 1 and b .. , at most two of each
+    const int rest = min(a, o.groups()) + max(0, o.groups() - max(a, b));
+    for (int i = nt - 1 - tid; i < rest; i += nt) {
+        const int g = i < a ? i : max(a, b) + (i - a), e0 = o.first(g);
+        Row<DT>::store_edge(out, e0, n, grad_group<DT, ENT, FAST>(Row<DT>::edge_group(z + (long long)e0 * (int)sizeof(bits), e0, n), c, h));
+    }
+    // the thread that wrote the target's group writes the target's own value
+    const int tg = (tgt + o.phase) / N;
+    const int owner = tg >= a && tg < b ? (tg - a) % nt : nt - 1 - (tg < a ? tg : a + tg - max(a, b)) % nt;
+    if (tid == owner) ((bits *)out)[tgt] = Elem<DT>::round(d_t);
+}
+template <int DT, bool ENT>
+__device__ __noinline__ void grad_groups_slow(const char *z, char *out, int n, int tgt, const Coef &c, float d_t,
+                                              const Shift &h, int tid, int nt) {
+    grad_groups<DT, ENT, false, true>(z, out, n, tgt, c, d_t, h, tid, nt);
+}
+template <int DT, bool ENT>
+__device__ __forceinline__ void grad_row(const char *z, char *out, int n, int tgt, float z_t, const Coef &c, float k,
+                                         int tid, int nt) {
+    const Shift h(c.m, k);
+    const float d_t = grad_target<ENT>(z_t, c, k);
+    if (h.ok && (((uintptr_t)out ^ (uintptr_t)z) & 15) == 0)
+        grad_groups<DT, ENT, true, false>(z, out, n, tgt, shifted(c, h), d_t, h, tid, nt);
+    else if (h.ok)
+        grad_groups<DT, ENT, true, true>(z, out, n, tgt, shifted(c, h), d_t, h, tid, nt);
+    else grad_groups_slow<DT, ENT>(z, out, n, tgt, c, d_t, h, tid, nt);
 }
 
 // ------------------------------------------------------------ rows
@@ -315,7 +345,7 @@ __device__ __forceinline__ void write_gradient(const Kept<DT, VPT> &kept, const 
     }
     const Shift h(c.m, k);
     if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
-        grad_row<DT, ENT>(z, out, r.n, target, c, k, tid, nt);
+        grad_row<DT, ENT>(z, out, r.n, target, z_t, c, k, tid, nt);
         return;
     }
     kept.template gradient<ENT>(r, out, shifted(c, h), h, most);
@@ -644,7 +674,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             if (c.none) {
                 zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
             } else if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
-                grad_row<DT, ENT>(z, out, P.in.vocab, in.q.target, c, k, rank * TEAM + t, cs * TEAM);
+                grad_row<DT, ENT>(z, out, P.in.vocab, in.q.target, in.z_t, c, k, rank * TEAM + t, cs * TEAM);
             } else {
                 const Coef d = shifted(c, h);
                 uint4 *o = (uint4 *)(out - r.phase * sizeof(typename Row<DT>::bits)) + c0;
@@ -687,7 +717,8 @@ template <int DT, bool ENT>
 __global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ GradParams P) {
     pdl_wait();
     pdl_trigger();
-    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
+    // from the last row: what the statistics have read last is still in the L2 cache
+    for (long long row = P.rows - 1 - blockIdx.x; row >= 0; row -= gridDim.x) {
         const long long tgt = target_of(P.in, row);
         const float2 ms = P.ms[row];
         const Coef c = coef_of<ENT>(ms.x, ms.y, ENT ? P.entropy[row] : 0.f, P.g[row * P.gs] * P.scale,
@@ -695,8 +726,10 @@ __global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ G
         char *out = P.out + row * P.ld_out_bytes;
         if (tgt < 0 || tgt >= P.in.vocab || c.none)
             zero_row<DT>(out, P.in.vocab, threadIdx.x, THREADS);
-        else
-            grad_row<DT, ENT>(P.in.logits + row * P.in.ld_bytes, out, P.in.vocab, tgt, c, P.in.k, threadIdx.x, THREADS);
+        else {
+            const char *z = P.in.logits + row * P.in.ld_bytes;
+            grad_row<DT, ENT>(z, out, P.in.vocab, (int)tgt, logit_at<DT>(z, tgt), c, P.in.k, threadIdx.x, THREADS);
+        }
     }
 }
 
