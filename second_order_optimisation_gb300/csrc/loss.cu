@@ -177,6 +177,12 @@ __device__ __forceinline__ void grad_row(const char *z, char *out, int n, int tg
     else grad_groups_slow<DT, ENT>(z, out, n, tgt, c, d_t, h, tid, nt);
 }
 
+template <int DT, bool ENT>
+__device__ __noinline__ void grad_row_apart(const char *z, char *out, int n, int tgt, float z_t, const Coef &c, float k,
+                                            int tid, int nt) {
+    grad_row<DT, ENT>(z, out, n, tgt, z_t, c, k, tid, nt);
+}
+
 // ------------------------------------------------------------ rows
 
 // A row of the policy loss: its target (-1: ignored), weight, advantage and
@@ -526,6 +532,19 @@ __device__ __forceinline__ bool team_any(int team, bool v) {
     return any != 0;
 }
 
+// A thread's sums over its groups of a stage.
+template <int DT, bool ENT, bool FAST>
+__device__ __forceinline__ Sums<DT, ENT> stage_sums(const uint4 *stage, int t, int G, const Shift &h) {
+    Sums<DT, ENT> s;
+#pragma unroll 4
+    for (int g = t; g < G; g += TEAM) s.template add<FAST>(stage[g], h);
+    return s;
+}
+template <int DT, bool ENT>
+__device__ __noinline__ Sums<DT, ENT> stage_sums_slow(const uint4 *stage, int t, int G, const Shift &h) {
+    return stage_sums<DT, ENT, false>(stage, t, G, h);
+}
+
 // Waits for the stage that holds the cluster's row n.  The stage's last use may
 // have been the other team's, its copy still under way; the barrier's parity tells
 // one use from the next only once the stage has been given to row n.
@@ -639,20 +658,17 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             const int G = g1 - c0;
             const uint4 *stage = (const uint4 *)(ring + (size_t)st * stage_bytes);
             const int at = rank != 0 ? -1 : t == 0 && r.has_front() ? 0 : t == 1 && r.has_back() ? r.end() : -1;
-            Running<DT, ENT> run(k);
-            for (int g = 0; g < G; g += NV * TEAM) {
-                uint4 u[NV];
-                const int most = min(NV, (G - g + TEAM - 1) / TEAM);
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (i < most) u[i] = stage[min(g + i * TEAM + t, G - 1)];
-                run.template add<NV>(u, most, g + t, TEAM, G);
-            }
+            const uint4 edge = at >= 0 ? r.load_edge(at) : Row<DT>::none();
+            auto best = Elem<DT>::raise(Elem<DT>::lowest(), edge);
+#pragma unroll 4
+            for (int g = t; g < G; g += TEAM) best = Elem<DT>::raise(best, stage[g]);
+            const Shift hw(lanes_max(Elem<DT>::largest(best), 32), k);
+            Sums<DT, ENT> sums = hw.ok ? stage_sums<DT, ENT, true>(stage, t, G, hw) : stage_sums_slow<DT, ENT>(stage, t, G, hw);
             if (at >= 0) {
-                const uint4 u = r.load_edge(at);
-                run.template add<1>(&u, 1, 0, 1, 1);
+                if (hw.ok) sums.template add<true>(edge, hw);
+                else sums.template add<false>(edge, hw);
             }
-            const Part mine = run.part();
+            const Part mine = sums.part(hw, 32);
             const int b = turn & 1;
             if (t % 32 < cs)
                 send_part(&sh.parts[team][b][rank * TEAM_WARPS + t / 32], &sh.joined[team][b], t % 32,
@@ -674,7 +690,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             if (c.none) {
                 zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
             } else if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
-                grad_row<DT, ENT>(z, out, P.in.vocab, in.q.target, in.z_t, c, k, rank * TEAM + t, cs * TEAM);
+                grad_row_apart<DT, ENT>(z, out, P.in.vocab, in.q.target, in.z_t, c, k, rank * TEAM + t, cs * TEAM);
             } else {
                 const Coef d = shifted(c, h);
                 uint4 *o = (uint4 *)(out - r.phase * sizeof(typename Row<DT>::bits)) + c0;
