@@ -128,6 +128,14 @@ struct Elem<KFAC_F32> {
         const float2 a = both(m);
         return fmaxf(a.x, a.y);
     }
+    static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
+        asm("max.NaN.f32 %0, %0, 0fF0000000;" : "+r"(v));  // -1.6e29
+        return v;
+    }
+    static constexpr bool BOUNDS = true;
+    static __device__ __forceinline__ uint4 bounded(uint4 u) {
+        return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
+    }
     static __device__ __forceinline__ bits round(float v) { return __float_as_uint(v); }
     static __device__ __forceinline__ void unpack(uint4 u, float *v) {
         v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
@@ -147,6 +155,14 @@ struct Elem<KFAC_BF16> {
     using two = __nv_bfloat162;  // running maximum of groups (NaN is passed over)
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xff7fff7fu); }
+    static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
+        const two b = __hmax2_nan(as_two(v), as_two(0xf000f000u));  // -1.6e29
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static constexpr bool BOUNDS = true;
+    static __device__ __forceinline__ uint4 bounded(uint4 u) {
+        return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
+    }
     static __device__ __forceinline__ two raise(two m, uint4 u) {
         return __hmax2(m, __hmax2(__hmax2(as_two(u.x), as_two(u.y)), __hmax2(as_two(u.z), as_two(u.w))));
     }
@@ -176,6 +192,8 @@ struct Elem<KFAC_F16> {
     using two = __half2;  // running maximum of groups (NaN is passed over)
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xfbfffbffu); }
+    static constexpr bool BOUNDS = false;  // (its lowest value is a logit's, not far below all of them)
+    static __device__ __forceinline__ uint4 bounded(uint4 u) { return u; }
     static __device__ __forceinline__ two raise(two m, uint4 u) {
         return __hmax2(m, __hmax2(__hmax2(as_two(u.x), as_two(u.y)), __hmax2(as_two(u.z), as_two(u.w))));
     }
@@ -344,16 +362,17 @@ template <int DT, bool ENT>
 struct Sums {
     f2 s, t;
     __device__ __forceinline__ Sums() : s(pair(0.f, 0.f)), t(s) {}
+    // (a logit below the bound has 2^y = 0 in the FAST form, where |m k| is small; its y must stay finite)
     template <bool FAST>
     __device__ __forceinline__ f2 group(uint4 u, const Shift &h) {
         constexpr int H = Elem<DT>::N / 2;
         f2 v[H];
-        unpack_pairs<DT>(u, v);
+        unpack_pairs<DT>(ENT && FAST ? Elem<DT>::bounded(u) : u, v);
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const f2 y = h.apply<FAST>(v[i]);
             v[i] = ex2(y);
-            if (ENT) t = fma(v[i], max2(y, Y_FLOOR), t);
+            if (ENT) t = fma(v[i], FAST && Elem<DT>::BOUNDS ? y : max2(y, Y_FLOOR), t);
         }
         if constexpr (H == 4) return kfac::add(kfac::add(v[0], v[1]), kfac::add(v[2], v[3]));
         else return kfac::add(v[0], v[1]);
@@ -390,24 +409,28 @@ struct Running {
             m = to;
         }
     }
-    // The groups u[i], i < most, that lie below `end` (the i-th at g + i step).
+    // `count` groups, the i-th to be passed over where the i-th bit of `skip` is set.
     template <int VPT>
-    __device__ __forceinline__ void add(const uint4 *u, int most, int g, int step, int end) {
+    __device__ __forceinline__ void add(const uint4 *u, int count, unsigned skip) {
         auto best = Elem<DT>::lowest();
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if (i < most) best = Elem<DT>::raise(best, u[i]);
+            if (i < count) best = Elem<DT>::raise(best, u[i]);
         raise(Elem<DT>::largest(best));
         const Shift h(m, k);
         Sums<DT, ENT> batch;
         if (h.ok) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                if (i < most && g + i * step < end) batch.template add<true>(u[i], h);
+                if (i < count && !(skip >> i & 1)) batch.template add<true>(u[i], h);
         } else {
+#pragma unroll 1
+            for (int i = 0; i < VPT; ++i) {
+                uint4 v = u[0];
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
-                if (i < most && g + i * step < end) batch.template add<false>(u[i], h);
+                for (int q = 1; q < VPT; ++q) v = q == i ? u[q] : v;  // (registers have no index)
+                if (i < count && !(skip >> i & 1)) batch.template add<false>(v, h);
+            }
         }
         const float f = ex2(-h.delta);
         if (ENT) t = kfac::add(t, mul(pair(f, f), fma(pair(-h.delta, -h.delta), batch.s, batch.t)));

@@ -80,13 +80,13 @@ template <int DT, bool ENT, bool FAST>
 __device__ __forceinline__ uint4 grad_group(uint4 u, const Coef &c, const Shift &h) {
     constexpr int H = Elem<DT>::N / 2;
     f2 v[H];
-    unpack_pairs<DT>(u, v);
+    unpack_pairs<DT>(ENT && FAST ? Elem<DT>::bounded(u) : u, v);
     const f2 a = pair(c.a, c.a), b = pair(c.b, c.b);
     float f[Elem<DT>::N];
 #pragma unroll
     for (int i = 0; i < H; ++i) {
         const f2 y = h.apply<FAST>(v[i]), e = ex2(y);
-        const float2 d = both(ENT ? mul(e, fma(b, max2(y, Y_FLOOR), a)) : mul(e, a));
+        const float2 d = both(ENT ? mul(e, fma(b, FAST && Elem<DT>::BOUNDS ? y : max2(y, Y_FLOOR), a)) : mul(e, a));
         f[2 * i] = d.x;
         f[2 * i + 1] = d.y;
     }
@@ -429,9 +429,9 @@ __device__ __forceinline__ Part join_parts(const float4 *parts, int n, float k) 
 
 // Statistics only: one row to a CTA or, where there are few rows, to a cluster
 // of cs CTAs, each with a run of the row's groups.
-constexpr int STREAM_THREADS = 256, BATCH = 4;
+constexpr int STREAM_THREADS = 128, BATCH = 4;
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(STREAM_THREADS, 6) stream_rows_kernel(const __grid_constant__ RowParams P, int cs) {
+__global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __grid_constant__ RowParams P, int cs) {
     constexpr int T = STREAM_THREADS, W = T / 32;
     __shared__ float4 parts[2][MAX_CLUSTER * W];
     pdl_wait();
@@ -451,19 +451,29 @@ __global__ void __launch_bounds__(STREAM_THREADS, 6) stream_rows_kernel(const __
         const int per = (r.end() - r.begin() + cs - 1) / cs;
         const int c0 = r.begin() + rank * per, g1 = min(r.end(), c0 + per);
         const int at = rank != 0 ? -1 : tid == 0 && r.has_front() ? 0 : tid == 1 && r.has_back() ? r.end() : -1;
-        const float z_t = logit_at<DT>(z, q.target), ref = P.ref_logp ? P.ref_logp[row] : 0.f;
         Running<DT, ENT> run(k);
-        for (int g = c0; g < g1; g += BATCH * T) {
+        int g = c0 + tid;
+        for (; g - tid + BATCH * T <= g1; g += BATCH * T) {
             uint4 u[BATCH];
-            const int most = min(BATCH, (g1 - g + T - 1) / T);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) u[i] = r.load_whole(g + i * T);
+            run.template add<BATCH>(u, BATCH, 0);
+        }
+        if (g - tid < g1) {
+            uint4 u[BATCH];
+            const int most = (g1 - (g - tid) + T - 1) / T;
+            unsigned skip = 0;
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
-                if (i < most) u[i] = r.load_whole(min(g + i * T + tid, g1 - 1));
-            run.template add<BATCH>(u, most, g + tid, T, g1);
+                if (i < most) {
+                    u[i] = r.load_whole(min(g + i * T, g1 - 1));
+                    skip |= (g + i * T >= g1 ? 1u : 0u) << i;
+                }
+            run.template add<BATCH>(u, most, skip);
         }
         if (at >= 0) {
             const uint4 u = r.load_edge(at);
-            run.template add<1>(&u, 1, 0, 1, 1);
+            run.template add<1>(&u, 1, 0);
         }
         const Part mine = run.part();
         const float4 packed = make_float4(mine.m, mine.s, mine.t, 0.f);
@@ -475,6 +485,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 6) stream_rows_kernel(const __
             __syncthreads();
         }
         if (tid < 32) {
+            // (both are in the L2 cache or on their way to it)
+            const float z_t = logit_at<DT>(z, q.target), ref = P.ref_logp ? P.ref_logp[row] : 0.f;
             const Part all = join_parts<ENT>(parts[turn], cs * W, k);
             finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && tid == 0);
         }
