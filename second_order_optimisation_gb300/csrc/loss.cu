@@ -201,7 +201,8 @@ struct RowParams {
     float *logp, *lse, *entropy;
     float2 *ms;                // (m, s) of each row (s = 0: nothing to differentiate), may be null
     // policy loss
-    const PolicyRow *meta;     // not null: the policy loss
+    bool policy;               // the policy loss, its rows' other inputs in meta
+    const PolicyRow *meta;
     const int *order;          // the order in which the ring takes the rows
     const float *ref_logp;
     float clip_low, clip_high, kl_coef, entropy_coef;
@@ -210,6 +211,8 @@ struct RowParams {
     float2 *flags;             // w [clipped], and not 0 where something is not finite
     float2 *g;                 // gradients of logp and H, where the logits' gradient comes later (may be null)
     int *err;
+    unsigned *zero;            // a counter and a vector of the calls after this one: set to 0 here (rows that
+    float *zero_g;             // are ignored), both may be null
     float scale;               // the call's scale / tau
     char *dlogits;             // may be null
     long long ld_d_bytes;
@@ -237,12 +240,19 @@ __device__ __forceinline__ void ignore_row(const RowParams &P, long long row) {
         P.flags[row] = make_float2(0.f, 0.f);
     }
     if (P.g) P.g[row] = make_float2(0.f, 0.f);
+    if (P.zero_g) P.zero_g[row] = 0.f;
 }
 
-// A row's outputs (where `write`) and the coefficients of its gradient.
+// A row's terms of the policy loss: w l, w pg, w kl, w H, w [clipped], and whether
+// one of its values is not finite.
+struct Terms {
+    float4 t;
+    float2 f;
+};
+// A row's outputs (where `write`), its terms and the coefficients of its gradient.
 template <bool ENT>
 __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, const PolicyRow &q, float ref,
-                                           const Part &p, float z_t, bool write) {
+                                           const Part &p, float z_t, bool write, Terms &o) {
     const RowResult r = row_result(p, z_t, P.in.tau);
     if (write) {
         if (P.logp) P.logp[row] = r.logp;
@@ -250,7 +260,7 @@ __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, co
         if (P.entropy) P.entropy[row] = r.h;
         if (P.ms) P.ms[row] = make_float2(p.m, p.s);
     }
-    if (!P.meta) return Coef{};
+    if (!P.policy) return Coef{};
     float g = 0.f, gh = 0.f, kl = 0.f, clipped = 0.f, bad = 1.f;
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.s != 0.f) {
@@ -272,10 +282,14 @@ __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, co
         gh = -w * P.entropy_coef;
         bad = finite(r.logp) && finite(t.x) && finite(g) ? 0.f : 1.f;
     }
+    o.t = t;
+    o.f = make_float2(clipped, bad);
     if (write) {
         if (P.kl) P.kl[row] = kl;
-        P.terms[row] = t;
-        P.flags[row] = make_float2(clipped, bad);
+        if (P.terms) {
+            P.terms[row] = t;
+            P.flags[row] = o.f;
+        }
         if (P.g) P.g[row] = make_float2(g, gh);
     }
     return coef_of<ENT>(p.m, p.s, r.h, g * P.scale, gh * P.scale);
@@ -361,38 +375,44 @@ __device__ __forceinline__ void write_gradient(const Kept<DT, VPT> &kept, const 
 }
 
 // One row to L lanes of a warp (L = 8 or 32): rows of at most NV L whole groups.
+// All lanes of a warp come here together (the reductions name them all); `in`:
+// there is such a row.
 constexpr int SMALL_THREADS = 256, NV = 8;
+template <int DT, bool ENT, int L>
+__device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, bool in, const PolicyRow &q) {
+    const int lane = threadIdx.x % L;
+    const bool live = q.target >= 0;
+    const char *z = P.in.logits + (in ? row : 0) * P.in.ld_bytes;
+    const Row<DT> r(z, P.in.vocab);
+    const int most = live ? (r.end() - r.begin() + L - 1) / L : 0;
+    Kept<DT, NV> kept;
+    kept.load(r, r.begin() + lane, L, live ? r.end() : 0, most,
+              !live ? -1 : lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? r.end() : -1);
+    const float z_t = live ? logit_at<DT>(z, q.target) : 0.f, ref = live && P.ref_logp ? P.ref_logp[row] : 0.f;
+    const Shift h(lanes_max(kept.largest(r, most), L), P.in.k);
+    const Part p = kept.template sums<ENT>(r, h, most, true).part(h, L);
+    char *out = P.dlogits ? P.dlogits + (in ? row : 0) * P.ld_d_bytes : nullptr;
+    Terms terms{};
+    if (!live) {
+        if (in && lane == 0) ignore_row(P, row);
+        if (in && out) zero_row<DT>(out, P.in.vocab, lane, L);
+        return terms;
+    }
+    const Coef c = finish_row<ENT>(P, row, q, ref, p, z_t, lane == 0, terms);
+    if (out) write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, c, P.in.k, most, lane, L);
+    return terms;
+}
 template <int DT, bool ENT, int L>
 __global__ void __launch_bounds__(SMALL_THREADS) lane_rows_kernel(const __grid_constant__ RowParams P) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x % L;
-    const float k = P.in.k;
-    // all lanes of a warp go round together: the reductions name them all
+    if (P.zero && blockIdx.x == 0 && threadIdx.x == 0) *P.zero = 0;
     for (long long first = (long long)blockIdx.x * (SMALL_THREADS / L) + threadIdx.x / 32 * (32 / L); first < P.rows;
          first += (long long)gridDim.x * (SMALL_THREADS / L)) {
         const long long row = first + threadIdx.x % 32 / L;
-        const bool in = row < P.rows;
         PolicyRow q{-1, 0.f, 0.f, 0.f};
-        if (in) q = row_meta(P, row);
-        const bool live = q.target >= 0;
-        const char *z = P.in.logits + (in ? row : 0) * P.in.ld_bytes;
-        const Row<DT> r(z, P.in.vocab);
-        const int most = live ? (r.end() - r.begin() + L - 1) / L : 0;
-        Kept<DT, NV> kept;
-        kept.load(r, r.begin() + lane, L, live ? r.end() : 0, most,
-                  !live ? -1 : lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? r.end() : -1);
-        const float z_t = live ? logit_at<DT>(z, q.target) : 0.f, ref = live && P.ref_logp ? P.ref_logp[row] : 0.f;
-        const Shift h(lanes_max(kept.largest(r, most), L), k);
-        const Part p = kept.template sums<ENT>(r, h, most, true).part(h, L);
-        char *out = P.dlogits ? P.dlogits + (in ? row : 0) * P.ld_d_bytes : nullptr;
-        if (!live) {
-            if (in && lane == 0) ignore_row(P, row);
-            if (in && out) zero_row<DT>(out, P.in.vocab, lane, L);
-            continue;
-        }
-        const Coef c = finish_row<ENT>(P, row, q, ref, p, z_t, lane == 0);
-        if (out) write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, c, k, most, lane, L);
+        if (row < P.rows) q = row_meta(P, row);
+        lane_row<DT, ENT, L>(P, row, row < P.rows, q);
     }
 }
 
@@ -437,6 +457,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, rank = cs > 1 ? blockIdx.x % cs : 0;
+    if (P.zero && blockIdx.x == 0 && tid == 0) *P.zero = 0;
     const float k = P.in.k;
     const long long step = gridDim.x / cs;
     int turn = 0;
@@ -488,7 +509,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __
             // (both are in the L2 cache or on their way to it)
             const float z_t = logit_at<DT>(z, q.target), ref = P.ref_logp ? P.ref_logp[row] : 0.f;
             const Part all = join_parts<ENT>(parts[turn], cs * W, k);
-            finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && tid == 0);
+            Terms terms;
+            finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && tid == 0, terms);
         }
         turn ^= 1;  // the parts of the row after next come after the next row's barrier
     }
@@ -692,7 +714,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                     *(volatile int *)&sh.dead = 1;
                 }
                 const Part all = join_parts<ENT>(sh.parts[team][b], cs * TEAM_WARPS, k);
-                const Coef c = finish_row<ENT>(P, row, in.q, in.ref, all, in.z_t, rank == 0 && t == 0);
+                Terms terms;
+                const Coef c = finish_row<ENT>(P, row, in.q, in.ref, all, in.z_t, rank == 0 && t == 0, terms);
                 if (t == 0) sh.coef[team][b] = c;
             }
             ++turn;
@@ -817,6 +840,18 @@ struct PolicyRows {
     int *err;
 };
 
+// A row of the policy loss from the caller's arrays (weight 1 where none is given).
+__device__ __forceinline__ PolicyRow policy_row(const PolicyRows &P, long long row, int &bad) {
+    const long long t = target_of(P.in, row);
+    bad |= t >= P.in.vocab;
+    const int seq = P.off ? sequence_of(P.off, P.seqs + 1, row) : 0;
+    const float w = P.weight ? P.weight[row] : 1.f;
+    PolicyRow q{-1, 0.f, 0.f, 0.f};
+    if (t >= 0 && t < P.in.vocab && w != 0.f && seq >= 0 && (!P.off || seq < P.seqs))
+        q = PolicyRow{(int)t, w, P.advantage[P.off ? seq : row], P.old_logp[row]};
+    return q;
+}
+
 // One cluster of CTAs, each a run of rows: every row's target, weight, advantage
 // and old log-probability in one place, and the rows that are not ignored before
 // the ignored ones, so that CTAs that stride over them get equal shares.
@@ -829,13 +864,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_rows_kernel(const __grid_
     const long long per = (P.rows + ctas - 1) / ctas, r0 = min(P.rows, rank * per), r1 = min(P.rows, r0 + per);
     int n = 0, bad = 0;
     for (long long row = r0 + tid; row < r1; row += ROWS_THREADS) {
-        const long long t = target_of(P.in, row);
-        bad |= t >= P.in.vocab;
-        const int seq = P.off ? sequence_of(P.off, P.seqs + 1, row) : 0;
-        const float w = P.weight ? P.weight[row] : 1.f;
-        PolicyRow q{-1, 0.f, 0.f, 0.f};
-        if (t >= 0 && t < P.in.vocab && w != 0.f && seq >= 0 && (!P.off || seq < P.seqs))
-            q = PolicyRow{(int)t, w, P.advantage[P.off ? seq : row], P.old_logp[row]};
+        const PolicyRow q = policy_row(P, row, bad);
         n += q.target >= 0;
         P.meta[row] = q;
     }
@@ -884,6 +913,45 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_rows_kernel(const __grid_
     }
 }
 
+// The sums of the rows' terms over a cluster, in a fixed order, to stats and the
+// error word (`target`: a target is past the vocabulary).
+struct TermSums {
+    Wide sum[5];
+    int bad;
+    __device__ __forceinline__ void add(const Terms &o) {
+        sum[0].add(o.t.x);
+        sum[1].add(o.t.y);
+        sum[2].add(o.t.z);
+        sum[3].add(o.t.w);
+        sum[4].add(o.f.x);
+        bad |= o.f.y != 0.f;
+    }
+    __device__ __forceinline__ void finish(float *stats, int *err, int word) {
+        __shared__ Wide part[32], all[SMALL_CLUSTER][5];
+        __shared__ int bad_of[SMALL_CLUSTER];
+        const int rank = blockIdx.x, ctas = gridDim.x;
+        bad = __syncthreads_or(bad);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const Wide s = block_sum(sum[i], part);
+            if (threadIdx.x == 0) *peer(&all[rank][i], 0) = s;
+        }
+        if (threadIdx.x == 0) *peer(&bad_of[rank], 0) = bad;
+        cluster_sync();
+        if (rank != 0 || threadIdx.x >= 32) return;
+        const int i = threadIdx.x;
+        Wide s{};
+        int flag = 0;
+        for (int c = 0; c < ctas; ++c) {
+            if (i < 5) s.add(all[c][i]);
+            flag |= bad_of[c];
+        }
+        const float v = (float)s.value();
+        if (i < 5) stats[i] = v;
+        if (i == 0) *err = word | (flag || !finite(v) ? ERR_NONFINITE : 0);
+    }
+};
+
 struct PolicySum {
     long long rows;
     const float4 *terms;
@@ -892,45 +960,50 @@ struct PolicySum {
     int *err;
 };
 
-// One cluster of CTAs, each a run of rows: the sums of the rows' terms.
+// One cluster of CTAs, each a run of rows.
 __global__ void __launch_bounds__(ROWS_THREADS) policy_sum_kernel(const __grid_constant__ PolicySum P) {
-    __shared__ Wide part[32], all[SMALL_CLUSTER][5];
-    __shared__ int bad_of[SMALL_CLUSTER];
     pdl_wait();
     pdl_trigger();
     const int rank = blockIdx.x, ctas = gridDim.x;
     const long long per = (P.rows + ctas - 1) / ctas, r0 = min(P.rows, rank * per), r1 = min(P.rows, r0 + per);
-    Wide sum[5] = {};
-    int bad = 0;
-    for (long long row = r0 + threadIdx.x; row < r1; row += ROWS_THREADS) {
-        const float4 t = P.terms[row];
-        const float2 f = P.flags[row];
-        sum[0].add(t.x);
-        sum[1].add(t.y);
-        sum[2].add(t.z);
-        sum[3].add(t.w);
-        sum[4].add(f.x);
-        bad |= f.y != 0.f;
+    TermSums sums{};
+    for (long long row = r0 + threadIdx.x; row < r1; row += ROWS_THREADS) sums.add(Terms{P.terms[row], P.flags[row]});
+    sums.finish(P.stats, P.err, *P.err);
+}
+
+// The whole policy loss of few short rows in one cluster: every CTA counts the
+// rows for itself (where the weight is one over their number), its groups of lanes
+// take the rows in turn, and the terms are added up across the cluster.  One
+// launch in place of three, each of which would take longer to start than to run.
+constexpr int SMALL_ROUNDS = 4;
+template <int DT, bool ENT, int L>
+__global__ void __launch_bounds__(ROWS_THREADS) policy_small_kernel(const __grid_constant__ RowParams P,
+                                                                    const __grid_constant__ PolicyRows R, float *stats) {
+    __shared__ int part[32];
+    pdl_wait();
+    pdl_trigger();
+    int n = 0, bad = 0;
+    for (long long row = threadIdx.x; row < R.rows; row += ROWS_THREADS) {
+        const long long t = target_of(R.in, row);
+        bad |= t >= R.in.vocab;
+        n += t >= 0 && t < R.in.vocab && (!R.off || (row >= R.off[0] && row < R.off[R.seqs]));
     }
+    n = block_sum(n, part);
     bad = __syncthreads_or(bad);
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-        const Wide s = block_sum(sum[i], part);
-        if (threadIdx.x == 0) *peer(&all[rank][i], 0) = s;
+    const float w = 1.f / (float)n;
+    TermSums sums{};
+    constexpr int PER = ROWS_THREADS / L;
+    for (long long first = (long long)blockIdx.x * PER + threadIdx.x / 32 * (32 / L); first < R.rows;
+         first += (long long)gridDim.x * PER) {
+        const long long row = first + threadIdx.x % 32 / L;
+        PolicyRow q{-1, 0.f, 0.f, 0.f};
+        int unused = 0;
+        if (row < R.rows) q = policy_row(R, row, unused);
+        if (!R.weight) q.weight = w;
+        const Terms o = lane_row<DT, ENT, L>(P, row, row < R.rows, q);
+        if (threadIdx.x % L == 0) sums.add(o);
     }
-    if (threadIdx.x == 0) *peer(&bad_of[rank], 0) = bad;
-    cluster_sync();
-    if (rank != 0 || threadIdx.x >= 32) return;
-    const int i = threadIdx.x;
-    Wide s{};
-    int flag = 0;
-    for (int c = 0; c < ctas; ++c) {
-        if (i < 5) s.add(all[c][i]);
-        flag |= bad_of[c];
-    }
-    const float v = (float)s.value();
-    if (i < 5) P.stats[i] = v;
-    if (i == 0 && (flag || !finite(v))) *P.err |= ERR_NONFINITE;
+    sums.finish(stats, R.err, bad ? ERR_TARGET : 0);
 }
 
 struct PrefPairs {
@@ -953,16 +1026,16 @@ struct PrefPairs {
 // ln(1 + e^-x) = -ln sigma(x) without overflow.
 __device__ __forceinline__ float softplus_neg(float x) { return fmaxf(-x, 0.f) + log1pf(expf(-fabsf(x))); }
 
-// One CTA per pair: the sums of its two sequences, f and its derivative.  h is
-// formed in more than fp32 (two sums that nearly cancel), f from it in fp32.
+// The sums of a pair's two sequences, f and its derivative, by a team of T
+// threads (a warp or a block).  h is formed in more than fp32 (two sums that nearly
+// cancel), f from it in fp32.  (What other CTAs have written is read past L1.)
 constexpr int PAIR_THREADS = 256;
-__global__ void __launch_bounds__(PAIR_THREADS) pref_pairs_kernel(const __grid_constant__ PrefPairs P) {
+template <int T>
+__device__ __forceinline__ void pref_pair(const PrefPairs &P, int b) {
     __shared__ Wide part[32];
     __shared__ int ipart[32];
-    __shared__ float slope[2];
-    pdl_wait();
-    pdl_trigger();
-    const int b = blockIdx.x;
+    __shared__ float shared_slope[2];
+    const int t = threadIdx.x % T;
     long long r0[2], r1[2];
     double l[2] = {0., 0.};
     int n[2], bad = 0;
@@ -971,29 +1044,35 @@ __global__ void __launch_bounds__(PAIR_THREADS) pref_pairs_kernel(const __grid_c
         r1[q] = clamp_row(P.off[2 * b + q + 1], P.rows);
         Wide s{};
         int c = 0;
-        for (long long row = r0[q] + threadIdx.x; row < r1[q]; row += PAIR_THREADS) {
-            const long long t = P.target_i32 ? (long long)((const int32_t *)P.target)[row]
-                                             : (long long)((const int64_t *)P.target)[row];
-            if (t >= P.vocab) bad |= ERR_TARGET;
-            if (t < 0 || t >= P.vocab) continue;
+        for (long long row = r0[q] + t; row < r1[q]; row += T) {
+            const long long tg = P.target_i32 ? (long long)((const int32_t *)P.target)[row]
+                                              : (long long)((const int64_t *)P.target)[row];
+            if (tg >= P.vocab) bad |= ERR_TARGET;
+            if (tg < 0 || tg >= P.vocab) continue;
             ++c;
-            if (P.ms[row].y == 0.f) {  // every logit -inf: left out
+            if (__ldcg(&P.ms[row].y) == 0.f) {  // every logit -inf: left out
                 bad |= ERR_NONFINITE;
                 continue;
             }
-            const float v = P.logp[row];
+            const float v = __ldcg(&P.logp[row]);
             if (!finite(v)) bad |= ERR_NONFINITE;
             s.add(v);
         }
-        s = block_sum(s, part);
-        n[q] = block_sum(c, ipart);
-        if (threadIdx.x == 0) {
+        if constexpr (T == 32) {
+            s.add_lanes();
+            n[q] = __reduce_add_sync(0xffffffffu, c);
+        } else {
+            s = block_sum(s, part);
+            n[q] = block_sum(c, ipart);
+        }
+        if (t == 0) {
             l[q] = P.average && n[q] > 0 ? s.value() / n[q] : s.value();
             if (!finite((float)l[q])) bad |= ERR_NONFINITE;
             if (P.seq_logp) P.seq_logp[2 * b + q] = (float)l[q];
         }
     }
-    if (threadIdx.x == 0) {
+    float slope[2] = {0.f, 0.f};
+    if (t == 0) {
         double h = l[0] - l[1];
         if (P.ref) h -= (double)P.ref[2 * b] - (double)P.ref[2 * b + 1];
         const float beta = P.beta, e = P.smooth, x = (float)(beta * h);
@@ -1013,19 +1092,27 @@ __global__ void __launch_bounds__(PAIR_THREADS) pref_pairs_kernel(const __grid_c
         if (!finite(f)) bad |= ERR_NONFINITE;
         P.terms[b] = v == 0.f ? 0.f : v * f;
         if (P.pair_loss) P.pair_loss[b] = f;
-        for (int q = 0; q < 2; ++q)
+        for (int q = 0; q < 2; ++q) {
             slope[q] = v == 0.f ? 0.f : v * d * (q ? -1.f : 1.f) / (P.average && n[q] > 0 ? (float)n[q] : 1.f);
+            if (T > 32) shared_slope[q] = slope[q];
+        }
     }
     bad = __reduce_or_sync(0xffffffffu, bad);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) ipart[threadIdx.x / 32] = bad;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < PAIR_THREADS / 32; ++i) bad |= ipart[i];
-        P.bad[b] = bad;
+    if constexpr (T > 32) {
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) ipart[threadIdx.x / 32] = bad;
+        __syncthreads();
+        if (t == 0)
+            for (int i = 1; i < T / 32; ++i) bad |= ipart[i];
+        slope[0] = shared_slope[0];
+        slope[1] = shared_slope[1];
+    } else {
+        slope[0] = __shfl_sync(0xffffffffu, slope[0], 0);
+        slope[1] = __shfl_sync(0xffffffffu, slope[1], 0);
     }
+    if (t == 0) P.bad[b] = bad;
     for (int q = 0; q < 2; ++q)
-        for (long long row = r0[q] + threadIdx.x; row < r1[q]; row += PAIR_THREADS) P.row_g[row] = slope[q];
+        for (long long row = r0[q] + t; row < r1[q]; row += T) P.row_g[row] = slope[q];
 }
 
 struct PrefSum {
@@ -1034,17 +1121,17 @@ struct PrefSum {
     int pairs;
     float *loss;
     int *err;
+    unsigned *done;  // CTAs that have finished their pair
 };
-__global__ void __launch_bounds__(PAIR_THREADS) pref_sum_kernel(const __grid_constant__ PrefSum P) {
+// The loss over all pairs, by one block, in a fixed order.
+__device__ __forceinline__ void pref_sum(const PrefSum &P) {
     __shared__ Wide part[32];
     __shared__ int ipart[32];
-    pdl_wait();
-    pdl_trigger();
     Wide s{};
     int bad = 0;
-    for (int b = threadIdx.x; b < P.pairs; b += PAIR_THREADS) {
-        s.add(P.terms[b]);
-        bad |= P.bad[b];
+    for (int b = threadIdx.x; b < P.pairs; b += blockDim.x) {
+        s.add(__ldcg(&P.terms[b]));
+        bad |= __ldcg(&P.bad[b]);
     }
     s = block_sum(s, part);
     const int nf = block_sum(bad & ERR_NONFINITE ? 1 : 0, ipart), tg = block_sum(bad & ERR_TARGET ? 1 : 0, ipart);
@@ -1052,6 +1139,58 @@ __global__ void __launch_bounds__(PAIR_THREADS) pref_sum_kernel(const __grid_con
         const float loss = (float)s.value();
         *P.loss = loss;
         *P.err = (nf || !finite(loss) ? ERR_NONFINITE : 0) | (tg ? ERR_TARGET : 0);
+    }
+}
+
+// A CTA to each pair; the last to finish adds up the loss.
+__global__ void __launch_bounds__(PAIR_THREADS) pref_pairs_kernel(const __grid_constant__ PrefPairs P,
+                                                                  const __grid_constant__ PrefSum U) {
+    __shared__ bool last;
+    pdl_wait();
+    pdl_trigger();
+    pref_pair<PAIR_THREADS>(P, blockIdx.x);
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(U.done, 1u) == gridDim.x - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (last) pref_sum(U);
+}
+
+// The whole preference loss of few short rows in one cluster: rows, then pairs,
+// then the rows' gradients, with a cluster barrier after each.
+template <int DT, int L>
+__global__ void __launch_bounds__(ROWS_THREADS) pref_small_kernel(const __grid_constant__ RowParams P,
+                                                                  const __grid_constant__ PrefPairs Q,
+                                                                  const __grid_constant__ PrefSum U, char *dlogits) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int PER = ROWS_THREADS / L;
+    const long long start = (long long)blockIdx.x * PER + threadIdx.x / 32 * (32 / L), step = (long long)gridDim.x * PER;
+    for (long long first = start; first < P.rows; first += step) {
+        const long long row = first + threadIdx.x % 32 / L;
+        PolicyRow q{-1, 0.f, 0.f, 0.f};
+        if (row < P.rows) q = row_meta(P, row);
+        lane_row<DT, false, L>(P, row, row < P.rows, q);
+    }
+    cluster_sync();
+    for (int b = blockIdx.x * (ROWS_THREADS / 32) + threadIdx.x / 32; b < Q.pairs; b += gridDim.x * (ROWS_THREADS / 32))
+        pref_pair<32>(Q, b);
+    cluster_sync();
+    if (blockIdx.x == 0) pref_sum(U);
+    if (!dlogits) return;
+    const int lane = threadIdx.x % L;
+    for (long long first = start; first < P.rows; first += step) {
+        const long long row = first + threadIdx.x % 32 / L;
+        if (row >= P.rows) continue;
+        const PolicyRow q = row_meta(P, row);
+        const char *z = P.in.logits + row * P.in.ld_bytes;
+        char *out = dlogits + row * P.ld_d_bytes;
+        const float2 ms = __ldcg(&P.ms[row]);
+        const Coef c = coef_of<false>(ms.x, ms.y, 0.f, __ldcg(&Q.row_g[row]) * P.scale, 0.f);
+        if (q.target < 0 || c.none) zero_row<DT>(out, P.in.vocab, lane, L);
+        else grad_row<DT, false>(z, out, P.in.vocab, q.target, logit_at<DT>(z, q.target), c, P.in.k, lane, L);
     }
 }
 
@@ -1131,6 +1270,50 @@ struct RunRows {
             cs *= 2;
         const unsigned grid = (unsigned)std::min<long long>(P.rows, 1 << 20) * cs;
         KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (stream_rows_kernel<DT, ENT>), cs, grid, STREAM_THREADS, 0, P, cs);
+        return KFAC_OK;
+    }
+};
+// Lanes to a row of the small kernels (0: the call is not one of few short rows).
+int small_lanes(int dtype, int vocab, long long rows) {
+    const long long whole = vocab / (dtype == KFAC_F32 ? 4 : 8);
+    const int L = whole <= 8 * NV ? 8 : whole <= 32 * NV ? 32 : 0;
+    return L && rows * L <= SMALL_ROUNDS * SMALL_CLUSTER * ROWS_THREADS ? L : 0;
+}
+unsigned small_ctas(int L, long long rows) {
+    unsigned n = 1;
+    while (n < SMALL_CLUSTER && (long long)n * (ROWS_THREADS / L) < rows) n *= 2;
+    return n;
+}
+struct RunPolicySmall {
+    const RowParams &P;
+    const PolicyRows &R;
+    float *stats;
+    int L;
+    cudaStream_t st;
+    template <int DT, bool ENT>
+    kfac_status run() {
+        const unsigned n = small_ctas(L, R.rows);
+        if (L == 8)
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (policy_small_kernel<DT, ENT, 8>), n, n, ROWS_THREADS, 0, P, R, stats);
+        else
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (policy_small_kernel<DT, ENT, 32>), n, n, ROWS_THREADS, 0, P, R, stats);
+        return KFAC_OK;
+    }
+};
+struct RunPrefSmall {
+    const RowParams &P;
+    const PrefPairs &Q;
+    const PrefSum &U;
+    char *dlogits;
+    int L;
+    cudaStream_t st;
+    template <int DT, bool>
+    kfac_status run() {
+        const unsigned n = small_ctas(L, P.rows);
+        if (L == 8)
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (pref_small_kernel<DT, 8>), n, n, ROWS_THREADS, 0, P, Q, U, dlogits);
+        else
+            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (pref_small_kernel<DT, 32>), n, n, ROWS_THREADS, 0, P, Q, U, dlogits);
         return KFAC_OK;
     }
 };
@@ -1230,6 +1413,7 @@ kfac_status check_preference(const kfac_preference_desc *d) {
 
 struct PrefPlan {
     int *err, *bad;
+    unsigned *done;
     float *logp, *row_g;
     float2 *ms;
     float *terms;
@@ -1238,6 +1422,7 @@ PrefPlan plan_preference(const kfac_preference_desc &d, Arena &ws) {
     PrefPlan p;
     const size_t n = (size_t)d.rows;
     p.err = ws.take<int>(64);
+    p.done = ws.take<unsigned>(1);
     p.logp = ws.take<float>(n);
     p.row_g = ws.take<float>(n);
     p.ms = ws.take<float2>(n);
@@ -1309,36 +1494,39 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
     const LogitsIn in = logits_in(d);
     PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta,
                  p.order, p.err};
-    const unsigned small = d.rows > ROWS_THREADS ? SMALL_CLUSTER : 1;
-    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_rows_kernel, small, small, ROWS_THREADS, 0, R);
     const bool kept = rows_kept(d), ent = d.entropy_coef != 0.f || d.entropy;
     const float scale = d.grad_scale / d.temperature;
+    RowParams P{};
+    P.in = in;
+    P.rows = d.rows;
+    P.policy = true;
+    P.logp = d.logp;
+    P.entropy = d.entropy ? d.entropy : ent && !kept ? p.h : nullptr;
+    P.ref_logp = d.ref_logp;
+    P.clip_low = d.clip_low;
+    P.clip_high = d.clip_high;
+    P.kl_coef = d.kl_coef;
+    P.entropy_coef = d.entropy_coef;
+    P.kl = d.kl;
+    P.scale = scale;
+    if (kept) P.dlogits = (char *)d.dlogits;
+    P.ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
+    if (const int L = d.seq_mean ? 0 : small_lanes(d.dtype, d.vocab, d.rows))
+        return by_type(d.dtype, ent, RunPolicySmall{P, R, d.stats, L, st});
+    const unsigned ctas = d.rows > ROWS_THREADS ? SMALL_CLUSTER : 1;
+    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_rows_kernel, ctas, ctas, ROWS_THREADS, 0, R);
     if (d.rows > 0) {
-        RowParams P{};
-        P.in = in;
-        P.rows = d.rows;
-        P.logp = d.logp;
-        P.entropy = d.entropy ? d.entropy : ent && !kept ? p.h : nullptr;
+        P.meta = p.meta;
+        P.order = p.order;
+        P.terms = p.terms;
+        P.flags = p.flags;
         P.ms = p.ms;
         P.g = p.g;
         P.err = p.err;
-        P.meta = p.meta;
-        P.order = p.order;
-        P.ref_logp = d.ref_logp;
-        P.clip_low = d.clip_low;
-        P.clip_high = d.clip_high;
-        P.kl_coef = d.kl_coef;
-        P.entropy_coef = d.entropy_coef;
-        P.kl = d.kl;
-        P.terms = p.terms;
-        P.flags = p.flags;
-        P.scale = scale;
-        if (kept) P.dlogits = (char *)d.dlogits;
-        P.ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
         if ((s = by_type(d.dtype, ent, RunRows{P, st})) != KFAC_OK) return s;
     }
     PolicySum U{d.rows, p.terms, p.flags, d.stats, p.err};
-    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_sum_kernel, small, small, ROWS_THREADS, 0, U);
+    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_sum_kernel, ctas, ctas, ROWS_THREADS, 0, U);
     if (kept || !d.dlogits || d.rows == 0) return KFAC_OK;
     GradParams G{in, d.rows, p.ms, d.entropy ? d.entropy : p.h, (const float *)p.g, (const float *)p.g + 1, 2, scale,
                  (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
@@ -1366,24 +1554,26 @@ extern "C" kfac_status kfac_preference_loss(const kfac_preference_desc *desc, vo
         return KFAC_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;
     float *logp = d.token_logp ? d.token_logp : p.logp;
-    KFAC_CUDA_TRY(cudaMemsetAsync(p.row_g, 0, (size_t)d.rows * sizeof(float), st));  // rows of no sequence
-    if (d.rows > 0) {
-        RowParams P{};
-        P.in = logits_in(d);
-        P.rows = d.rows;
-        P.off = d.seq_offsets;
-        P.last = 2 * d.pairs;
-        P.logp = logp;
-        P.ms = p.ms;
-        if ((s = by_type(d.dtype, false, RunRows{P, st})) != KFAC_OK) return s;
-    }
+    RowParams P{};
+    P.in = logits_in(d);
+    P.rows = d.rows;
+    P.off = d.seq_offsets;
+    P.last = 2 * d.pairs;
+    P.logp = logp;
+    P.ms = p.ms;
+    P.zero = p.done;
+    P.zero_g = p.row_g;
+    P.scale = d.grad_scale / d.temperature;
+    P.ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
     PrefPairs Q{d.target, d.target_i32, d.vocab, d.rows, d.seq_offsets, d.pairs, d.ref_logp, d.pair_weight, d.kind,
                 d.average, d.beta, d.label_smoothing, logp, p.ms, p.row_g, p.terms, p.bad, d.pair_loss, d.seq_logp};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_pairs_kernel, (unsigned)d.pairs, PAIR_THREADS, 0, Q);
-    PrefSum U{p.terms, p.bad, d.pairs, d.loss, p.err};
-    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_sum_kernel, 1, PAIR_THREADS, 0, U);
-    if (!d.dlogits || d.rows == 0) return KFAC_OK;
-    GradParams G{logits_in(d), d.rows, p.ms, nullptr, p.row_g, nullptr, 1, d.grad_scale / d.temperature,
-                 (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
+    PrefSum U{p.terms, p.bad, d.pairs, d.loss, p.err, p.done};
+    // (a warp goes over a pair's rows and, in turn, over few pairs)
+    const int L = d.rows == 0 ? 8 : d.pairs <= SMALL_CLUSTER * ROWS_THREADS ? small_lanes(d.dtype, d.vocab, d.rows) : 0;
+    if (L) return by_type(d.dtype, false, RunPrefSmall{P, Q, U, (char *)d.dlogits, L, st});
+    if ((s = by_type(d.dtype, false, RunRows{P, st})) != KFAC_OK) return s;
+    KFAC_LAUNCH(KK_LOSS_SMALL, st, pref_pairs_kernel, (unsigned)d.pairs, PAIR_THREADS, 0, Q, U);
+    if (!d.dlogits) return KFAC_OK;
+    GradParams G{logits_in(d), d.rows, p.ms, nullptr, p.row_g, nullptr, 1, P.scale, (char *)d.dlogits, P.ld_d_bytes};
     return by_type(d.dtype, false, RunGrad{G, st});
 }

@@ -460,3 +460,13 @@ def test_offsets_past_two_to_the_31():
     rest = torch.ones(rows, dtype=torch.bool, device=DEV)
     rest[pick] = False
     assert int((d.view(torch.int16).ne(0).any(1) & rest).sum()) == 0
+
+
+@pytest.mark.parametrize("vocab", [10, 70001])
+def test_preference_without_rows(vocab):
+    loss, pl = torch.full((1,), SENTINEL, device=DEV), torch.full((2,), SENTINEL, device=DEV)
+    ws = kfac.kfac_preference_loss(kfac.PreferenceLoss(
+        torch.empty(0, vocab, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV),
+        torch.zeros(5, dtype=torch.int32, device=DEV), loss, pair_loss=pl))
+    assert word(ws) == 0
+    assert abs(float(loss) - math.log(2)) < 4 * ref.E and torch.allclose(pl, loss.expand(2), atol=4 * ref.E, rtol=0)
