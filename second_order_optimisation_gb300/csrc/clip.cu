@@ -22,7 +22,7 @@ namespace kfac {
 namespace {
 
 constexpr int CLIP_FEW = 16, CLIP_MANY = 216;  // tensors of one launch (kernel parameters)
-constexpr int CLIP_THREADS = 256, CLIP_PER_SM = 3, OCTET = 8, SHORT_RUN = 192, TILE = 4096;
+constexpr int CLIP_THREADS = 256, CLIP_PER_SM = 3, OCTET = 8, SHORT_RUN = 192, TILE = 4096, SMALL_OCTETS = 16384;
 
 struct ClipJob {
     const char *x, *y;
@@ -387,7 +387,7 @@ __device__ __noinline__ void apply_inner(const ClipJob &j, long long a, long lon
 }
 template <int DT>
 __device__ __noinline__ void apply_outer(const ClipJob &j, long long lo, long long hi, int tid, int nt, float scale,
-                                            float eta);
+                                         float eta);
 // (short runs and ends as in the first pass)
 template <int DT>
 __device__ __forceinline__ void apply_run(const ClipJob &j, int n, long long lo, long long hi, float scale, float eta) {
@@ -461,6 +461,74 @@ __device__ __noinline__ void apply_outer(const ClipJob &j, long long lo, long lo
     }
 }
 
+// norm and scale from the sum of products.
+__device__ __forceinline__ float scale_of(double sum, float max_norm, float &norm) {
+    norm = (float)sqrt(sum < 0 ? 0. : sum);
+    return norm > max_norm ? max_norm / norm : norm <= max_norm ? 1.f : norm;
+}
+
+// Few small tensors in one launch: a cluster of CTAs takes the sum of products,
+// joins it through shared memory, and applies the scale.
+constexpr int CLIP_CLUSTER = 8;
+__global__ void __launch_bounds__(CLIP_THREADS) clip_small_kernel(const __grid_constant__ ClipParams<CLIP_FEW> P) {
+    __shared__ double parts[CLIP_CLUSTER];
+    pdl_wait();
+    pdl_trigger();
+    const int rank = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
+    const long long lo = P.octets * rank / ctas, hi = P.octets * (rank + 1) / ctas;
+    Wide mine{};
+    for (int n = 0; n < P.n; ++n) {
+        const ClipJob &j = P.job[n];
+        const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
+        if (b <= a) continue;
+        if (j.dtype == KFAC_BF16)
+            mine = j.y ? outer_products<KFAC_BF16, true>(j, a, b, tid, CLIP_THREADS, mine)
+                       : outer_products<KFAC_BF16, false>(j, a, b, tid, CLIP_THREADS, mine);
+        else if (j.dtype == KFAC_F16)
+            mine = j.y ? outer_products<KFAC_F16, true>(j, a, b, tid, CLIP_THREADS, mine)
+                       : outer_products<KFAC_F16, false>(j, a, b, tid, CLIP_THREADS, mine);
+        else
+            mine = j.y ? outer_products<KFAC_F32, true>(j, a, b, tid, CLIP_THREADS, mine)
+                       : outer_products<KFAC_F32, false>(j, a, b, tid, CLIP_THREADS, mine);
+    }
+    const Wide s = block_wide(mine);
+    double sum = s.value();
+    if (!finite(s.hi) || fabsf(s.hi) < 1e-28f) {
+        sum = 0;
+        for (int n = 0; n < P.n; ++n) {
+            const ClipJob &j = P.job[n];
+            const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
+            if (b <= a) continue;
+            sum += j.dtype == KFAC_BF16 ? scaled_sum<KFAC_BF16>(j, a, b)
+                   : j.dtype == KFAC_F16 ? scaled_sum<KFAC_F16>(j, a, b) : scaled_sum<KFAC_F32>(j, a, b);
+        }
+    }
+    if (tid == 0)
+        for (int c = 0; c < ctas; ++c) {
+            double *there;
+            asm volatile("mapa.u64 %0, %1, %2;" : "=l"(there) : "l"(&parts[rank]), "r"(c));
+            *there = sum;
+        }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    double all = 0;
+    for (int c = 0; c < ctas; ++c) all += parts[c];
+    float norm;
+    const float scale = scale_of(all, P.max_norm, norm);
+    if (rank == 0 && tid == 0) {
+        if (P.norm) *P.norm = norm;
+        if (P.scale) *P.scale = scale;
+        *P.err = finite(norm) ? 0 : ERR_NONFINITE;
+    }
+    for (int n = 0; n < P.n; ++n) {
+        const ClipJob &j = P.job[n];
+        const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
+        if (b <= a || (!j.w && (!j.out || (j.out == j.x && scale == 1.f)))) continue;
+        if (j.dtype == KFAC_BF16) apply_outer<KFAC_BF16>(j, a, b, tid, CLIP_THREADS, scale, P.eta);
+        else if (j.dtype == KFAC_F16) apply_outer<KFAC_F16>(j, a, b, tid, CLIP_THREADS, scale, P.eta);
+        else apply_outer<KFAC_F32>(j, a, b, tid, CLIP_THREADS, scale, P.eta);
+    }
+}
+
 // Every CTA adds up the first pass's sums itself (the same sum in the same order).
 template <int MAX>
 __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_apply_kernel(const __grid_constant__ ClipParams<MAX> P) {
@@ -472,8 +540,8 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_apply_kernel(c
         for (int i = threadIdx.x; i < P.parts; i += 32) s += P.part[i];
         for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
         if (threadIdx.x == 0) {
-            const float norm = (float)sqrt(s < 0 ? 0. : s);
-            const float scale = norm > P.max_norm ? P.max_norm / norm : norm <= P.max_norm ? 1.f : norm;
+            float norm;
+            const float scale = scale_of(s, P.max_norm, norm);
             shared_scale = scale;
             if (blockIdx.x == 0 && P.err) {
                 if (P.norm) *P.norm = norm;
@@ -588,6 +656,16 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
         P->tile = std::max<long long>(1, ceil_div(P->octets, ctas_of(P->octets)));
         if (!apply) P->tile = std::min<long long>(P->tile, TILE);
     };
+    if constexpr (MAX == CLIP_FEW) {
+        fill(0, true);
+        if (P->octets <= SMALL_OCTETS) {
+            P->err = plan.err;
+            unsigned ctas = 1;
+            while (ctas < CLIP_CLUSTER && (long long)ctas * CLIP_THREADS * 2 < P->octets) ctas *= 2;
+            KFAC_LAUNCH_CLUSTERS(KK_CLIP_NORM, st, clip_small_kernel, ctas, ctas, CLIP_THREADS, 0, *P);
+            return KFAC_OK;
+        }
+    }
     int parts = 0;
     for (int l = 0; l < launches; ++l) {
         fill(l, false);
