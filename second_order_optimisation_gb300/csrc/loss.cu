@@ -185,6 +185,75 @@ __device__ __noinline__ void grad_row_apart(const char *z, char *out, int n, int
 
 // ------------------------------------------------------------ rows
 
+// Sum over a block; every thread gets it.
+__device__ __forceinline__ int block_sum(int v, int *part) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    int all = (int)(threadIdx.x & 31) < (int)blockDim.x / 32 ? part[threadIdx.x & 31] : 0;
+    return __reduce_add_sync(0xffffffffu, all);
+}
+// Sum over a block, in a fixed order; thread 0 gets it.
+__device__ __forceinline__ Wide block_sum(Wide v, Wide *part) {
+    v.add_lanes();
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    Wide all{};
+    if (threadIdx.x < 32) {
+        if ((int)threadIdx.x < (int)blockDim.x / 32) all = part[threadIdx.x];
+        all.add_lanes();
+    }
+    return all;
+}
+// Another CTA's copy of a shared variable.
+template <class T>
+__device__ __forceinline__ T *peer(T *local, int rank) {
+    T *p;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(p) : "l"(local), "r"(rank));
+    return p;
+}
+
+// A row's terms of the policy loss: w l, w pg, w kl, w H, w [clipped], and whether
+// one of its values is not finite.
+struct Terms {
+    float4 t;
+    float2 f;
+};
+// Sums of rows' terms.
+struct TermSums {
+    Wide sum[5];
+    int bad;
+    __device__ __forceinline__ void add(const Terms &o) {
+        sum[0].add(o.t.x);
+        sum[1].add(o.t.y);
+        sum[2].add(o.t.z);
+        sum[3].add(o.t.w);
+        sum[4].add(o.f.x);
+        bad |= o.f.y != 0.f;
+    }
+    __device__ __forceinline__ void add(const TermSums &o) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) sum[i].add(o.sum[i]);
+        bad |= o.bad;
+    }
+    // Over the block, in a fixed order; thread 0's is the one to take.
+    __device__ __forceinline__ void add_block() {
+        __shared__ Wide part[32];
+        bad = __syncthreads_or(bad);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) sum[i] = block_sum(sum[i], part);
+    }
+    __device__ __forceinline__ void write(float *stats, int *err, int word) const {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 4; i >= 0; --i) stats[i] = v = (float)sum[i].value();
+        if (bad || !finite(v)) word |= ERR_NONFINITE;
+        if (word) atomicOr(err, word);
+    }
+};
+
 // A row of the policy loss: its target (-1: ignored), weight, advantage and
 // log-probability under the policy that drew it.
 struct __align__(16) PolicyRow {
@@ -207,8 +276,9 @@ struct RowParams {
     const float *ref_logp;
     float clip_low, clip_high, kl_coef, entropy_coef;
     float *kl;
-    float4 *terms;             // w l, w pg, w kl, w H of each row
-    float2 *flags;             // w [clipped], and not 0 where something is not finite
+    TermSums *sums;            // one for each CTA (or cluster) of the launch, the last of which adds them up
+    unsigned *done;            // ... counted here (0 before the launch)
+    float *stats;
     float2 *g;                 // gradients of logp and H, where the logits' gradient comes later (may be null)
     int *err;
     unsigned *zero;            // a counter and a vector of the calls after this one: set to 0 here (rows that
@@ -235,20 +305,10 @@ __device__ __forceinline__ void ignore_row(const RowParams &P, long long row) {
     if (P.entropy) P.entropy[row] = 0.f;
     if (P.ms) P.ms[row] = make_float2(0.f, 0.f);
     if (P.kl) P.kl[row] = 0.f;
-    if (P.terms) {
-        P.terms[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-        P.flags[row] = make_float2(0.f, 0.f);
-    }
     if (P.g) P.g[row] = make_float2(0.f, 0.f);
     if (P.zero_g) P.zero_g[row] = 0.f;
 }
 
-// A row's terms of the policy loss: w l, w pg, w kl, w H, w [clipped], and whether
-// one of its values is not finite.
-struct Terms {
-    float4 t;
-    float2 f;
-};
 // A row's outputs (where `write`), its terms and the coefficients of its gradient.
 template <bool ENT>
 __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, const PolicyRow &q, float ref,
@@ -286,10 +346,6 @@ __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, co
     o.f = make_float2(clipped, bad);
     if (write) {
         if (P.kl) P.kl[row] = kl;
-        if (P.terms) {
-            P.terms[row] = t;
-            P.flags[row] = o.f;
-        }
         if (P.g) P.g[row] = make_float2(g, gh);
     }
     return coef_of<ENT>(p.m, p.s, r.h, g * P.scale, gh * P.scale);
@@ -374,6 +430,25 @@ __device__ __forceinline__ void write_gradient(const Kept<DT, VPT> &kept, const 
         ((typename Row<DT>::bits *)out)[target] = Elem<DT>::round(grad_target<ENT>(z_t, c, k));
 }
 
+// The end of a launch over rows of the policy loss: CTA (or cluster) i of n leaves its
+// sums, the last to come adds up all of them, in their order.  Every thread of the
+// block comes here; thread 0 holds the block's sums.
+__device__ __forceinline__ void leave_sums(const RowParams &P, const TermSums &mine, int i, int n) {
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
+        P.sums[i] = mine;
+        __threadfence();
+        last = atomicAdd(P.done, 1u) == (unsigned)n - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    TermSums all{};
+    for (int c = threadIdx.x; c < n; c += blockDim.x) all.add(P.sums[c]);
+    all.add_block();
+    if (threadIdx.x == 0) all.write(P.stats, P.err, 0);
+}
+
 // One row to L lanes of a warp (L = 8 or 32): rows of at most NV L whole groups.
 // All lanes of a warp come here together (the reductions name them all); `in`:
 // there is such a row.
@@ -403,17 +478,26 @@ __device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, boo
     return terms;
 }
 template <int DT, bool ENT, int L>
-__global__ void __launch_bounds__(SMALL_THREADS) lane_rows_kernel(const __grid_constant__ RowParams P) {
+__global__ void __launch_bounds__(SMALL_THREADS, 3) lane_rows_kernel(const __grid_constant__ RowParams P) {
     pdl_wait();
     pdl_trigger();
     if (P.zero && blockIdx.x == 0 && threadIdx.x == 0) *P.zero = 0;
+    __shared__ TermSums group_sums[SMALL_THREADS / L];  // (registers are short)
+    TermSums &mine = group_sums[threadIdx.x / L];
+    if (threadIdx.x % L == 0) mine = TermSums{};
     for (long long first = (long long)blockIdx.x * (SMALL_THREADS / L) + threadIdx.x / 32 * (32 / L); first < P.rows;
          first += (long long)gridDim.x * (SMALL_THREADS / L)) {
         const long long row = first + threadIdx.x % 32 / L;
         PolicyRow q{-1, 0.f, 0.f, 0.f};
         if (row < P.rows) q = row_meta(P, row);
-        lane_row<DT, ENT, L>(P, row, row < P.rows, q);
+        const Terms o = lane_row<DT, ENT, L>(P, row, row < P.rows, q);
+        if (P.policy && threadIdx.x % L == 0) mine.add(o);
     }
+    if (!P.policy) return;
+    __syncthreads();
+    TermSums sums = threadIdx.x < SMALL_THREADS / L ? group_sums[threadIdx.x] : TermSums{};
+    sums.add_block();
+    leave_sums(P, sums, blockIdx.x, gridDim.x);
 }
 
 constexpr int MAX_CLUSTER = 8;
@@ -461,6 +545,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __
     const float k = P.in.k;
     const long long step = gridDim.x / cs;
     int turn = 0;
+    __shared__ TermSums sums;  // (registers are short)
+    if (tid == 0) sums = TermSums{};
     for (long long row = blockIdx.x / cs; row < P.rows; row += step) {
         const PolicyRow q = row_meta(P, row);
         if (q.target < 0) {
@@ -509,11 +595,13 @@ __global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __
             // (both are in the L2 cache or on their way to it)
             const float z_t = logit_at<DT>(z, q.target), ref = P.ref_logp ? P.ref_logp[row] : 0.f;
             const Part all = join_parts<ENT>(parts[turn], cs * W, k);
-            Terms terms;
+            Terms terms{};
             finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && tid == 0, terms);
+            if (P.policy && tid == 0) sums.add(terms);
         }
         turn ^= 1;  // the parts of the row after next come after the next row's barrier
     }
+    if (P.policy && rank == 0) leave_sums(P, sums, blockIdx.x / cs, (int)step);
 }
 
 // Statistics and gradient of rows that a cluster of cs CTAs keeps in shared
@@ -536,6 +624,7 @@ struct RingShared {
     StageRow row[MAX_STAGES];
     long long given[MAX_STAGES];  // the row (counted within the cluster) that the stage was given to last
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], joined[TEAMS][2];
+    TermSums sums[TEAMS];
     int dead;
 };
 
@@ -609,6 +698,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         }
         for (int i = 0; i < 2 * TEAMS; ++i) mbar_init(&sh.joined[i / 2][i % 2], 1);
         sh.dead = 0;
+        for (int i = 0; i < TEAMS; ++i) sh.sums[i] = TermSums{};
         fence_barrier_init();
     }
     cluster_sync();
@@ -714,9 +804,12 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                     *(volatile int *)&sh.dead = 1;
                 }
                 const Part all = join_parts<ENT>(sh.parts[team][b], cs * TEAM_WARPS, k);
-                Terms terms;
+                Terms terms{};
                 const Coef c = finish_row<ENT>(P, row, in.q, in.ref, all, in.z_t, rank == 0 && t == 0, terms);
-                if (t == 0) sh.coef[team][b] = c;
+                if (t == 0) {
+                    sh.coef[team][b] = c;
+                    sh.sums[team].add(terms);
+                }
             }
             ++turn;
             if (team_any(team, *(volatile int *)&sh.dead != 0)) break;
@@ -748,6 +841,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             if (!mbar_wait(&sh.full[i], 0, 100000000ull)) mbar_wait(&sh.full[i], 1, 100000000ull);
     // no CTA leaves while others may still write into its shared memory
     cluster_sync();
+    if (rank != 0) return;
+    TermSums sums = sh.sums[0];
+    for (int i = 1; i < TEAMS; ++i) sums.add(sh.sums[i]);
+    leave_sums(P, sums, (int)first, (int)step);
 }
 
 // ------------------------------------------------------------ gradient
@@ -799,36 +896,6 @@ __device__ __forceinline__ long long clamp_row(int32_t v, long long rows) {
     return v < 0 ? 0 : v > rows ? rows : v;
 }
 
-// Sum over a block; every thread gets it.
-__device__ __forceinline__ int block_sum(int v, int *part) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    int all = (int)(threadIdx.x & 31) < (int)blockDim.x / 32 ? part[threadIdx.x & 31] : 0;
-    return __reduce_add_sync(0xffffffffu, all);
-}
-// Sum over a block, in a fixed order; thread 0 gets it.
-__device__ __forceinline__ Wide block_sum(Wide v, Wide *part) {
-    v.add_lanes();
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    Wide all{};
-    if (threadIdx.x < 32) {
-        if ((int)threadIdx.x < (int)blockDim.x / 32) all = part[threadIdx.x];
-        all.add_lanes();
-    }
-    return all;
-}
-// Another CTA's copy of a shared variable.
-template <class T>
-__device__ __forceinline__ T *peer(T *local, int rank) {
-    T *p;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(p) : "l"(local), "r"(rank));
-    return p;
-}
-
 struct PolicyRows {
     LogitsIn in;
     long long rows;
@@ -837,6 +904,7 @@ struct PolicyRows {
     int seqs, seq_mean;
     PolicyRow *meta;
     int *order;
+    unsigned *done;
     int *err;
 };
 
@@ -881,7 +949,10 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_rows_kernel(const __grid_
         if (i < rank) before += live_of[i];
         any += bad_of[i];
     }
-    if (rank == 0 && tid == 0) *P.err = any ? ERR_TARGET : 0;
+    if (rank == 0 && tid == 0) {
+        *P.err = any ? ERR_TARGET : 0;
+        *P.done = 0;
+    }
     // (a CTA writes what its own threads have written, so its own barriers order it)
     const float w = 1.f / (float)live;
     for (long long base = r0; base < r1; base += ROWS_THREADS) {
@@ -911,64 +982,6 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_rows_kernel(const __grid_
         for (long long row = q0 + lane; row < q1; row += 32)
             if (__ldcg(&P.meta[row].target) >= 0) P.meta[row].weight = 1.f / ((float)P.seqs * (float)c);
     }
-}
-
-// The sums of the rows' terms over a cluster, in a fixed order, to stats and the
-// error word (`target`: a target is past the vocabulary).
-struct TermSums {
-    Wide sum[5];
-    int bad;
-    __device__ __forceinline__ void add(const Terms &o) {
-        sum[0].add(o.t.x);
-        sum[1].add(o.t.y);
-        sum[2].add(o.t.z);
-        sum[3].add(o.t.w);
-        sum[4].add(o.f.x);
-        bad |= o.f.y != 0.f;
-    }
-    __device__ __forceinline__ void finish(float *stats, int *err, int word) {
-        __shared__ Wide part[32], all[SMALL_CLUSTER][5];
-        __shared__ int bad_of[SMALL_CLUSTER];
-        const int rank = blockIdx.x, ctas = gridDim.x;
-        bad = __syncthreads_or(bad);
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            const Wide s = block_sum(sum[i], part);
-            if (threadIdx.x == 0) *peer(&all[rank][i], 0) = s;
-        }
-        if (threadIdx.x == 0) *peer(&bad_of[rank], 0) = bad;
-        cluster_sync();
-        if (rank != 0 || threadIdx.x >= 32) return;
-        const int i = threadIdx.x;
-        Wide s{};
-        int flag = 0;
-        for (int c = 0; c < ctas; ++c) {
-            if (i < 5) s.add(all[c][i]);
-            flag |= bad_of[c];
-        }
-        const float v = (float)s.value();
-        if (i < 5) stats[i] = v;
-        if (i == 0) *err = word | (flag || !finite(v) ? ERR_NONFINITE : 0);
-    }
-};
-
-struct PolicySum {
-    long long rows;
-    const float4 *terms;
-    const float2 *flags;
-    float *stats;
-    int *err;
-};
-
-// One cluster of CTAs, each a run of rows.
-__global__ void __launch_bounds__(ROWS_THREADS) policy_sum_kernel(const __grid_constant__ PolicySum P) {
-    pdl_wait();
-    pdl_trigger();
-    const int rank = blockIdx.x, ctas = gridDim.x;
-    const long long per = (P.rows + ctas - 1) / ctas, r0 = min(P.rows, rank * per), r1 = min(P.rows, r0 + per);
-    TermSums sums{};
-    for (long long row = r0 + threadIdx.x; row < r1; row += ROWS_THREADS) sums.add(Terms{P.terms[row], P.flags[row]});
-    sums.finish(P.stats, P.err, *P.err);
 }
 
 // The whole policy loss of few short rows in one cluster: every CTA counts the
@@ -1003,7 +1016,16 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_small_kernel(const __grid
         const Terms o = lane_row<DT, ENT, L>(P, row, row < R.rows, q);
         if (threadIdx.x % L == 0) sums.add(o);
     }
-    sums.finish(stats, R.err, bad ? ERR_TARGET : 0);
+    __shared__ TermSums all[SMALL_CLUSTER];
+    sums.add_block();
+    if (threadIdx.x == 0) {
+        *peer(&all[blockIdx.x], 0) = sums;
+        if (blockIdx.x == 0) *R.err = bad ? ERR_TARGET : 0;
+    }
+    cluster_sync();
+    if (blockIdx.x != 0 || threadIdx.x != 0) return;
+    for (int c = 1; c < (int)gridDim.x; ++c) sums.add(all[c]);
+    sums.write(stats, R.err, 0);
 }
 
 struct PrefPairs {
@@ -1220,6 +1242,9 @@ Ring ring_of(int dtype, int vocab, long long rows) {
     return g;
 }
 
+// CTAs (clusters) of a launch over rows, at most: each leaves its sums.
+constexpr int MAX_CTAS = 1 << 14;
+
 struct RunRows {
     const RowParams &P;
     cudaStream_t st;
@@ -1228,7 +1253,7 @@ struct RunRows {
         const long long whole = P.in.vocab / Elem<DT>::N;
         if (whole <= 32 * NV) {
             const int per = SMALL_THREADS / (whole <= 8 * NV ? 8 : 32);
-            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, per), 1 << 20);
+            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, per), MAX_CTAS);
             if (whole <= 8 * NV)
                 KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 8>), grid, SMALL_THREADS, 0, P);
             else
@@ -1268,7 +1293,7 @@ struct RunRows {
         int cs = 1;
         while (cs < MAX_CLUSTER && P.rows * cs * 2 <= device_sm_count() && whole >= (long long)cs * STREAM_THREADS * 4)
             cs *= 2;
-        const unsigned grid = (unsigned)std::min<long long>(P.rows, 1 << 20) * cs;
+        const unsigned grid = (unsigned)std::min<long long>(P.rows, MAX_CTAS) * cs;
         KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (stream_rows_kernel<DT, ENT>), cs, grid, STREAM_THREADS, 0, P, cs);
         return KFAC_OK;
     }
@@ -1370,8 +1395,9 @@ struct PolicyPlan {
     int *err;
     PolicyRow *meta;
     int *order;
-    float4 *terms;
-    float2 *flags, *ms, *g;  // ms, g, h: for rows that do not fit the chip
+    TermSums *sums;
+    unsigned *done;
+    float2 *ms, *g;  // ms, g, h: for rows that do not fit the chip
     float *h;
 };
 bool rows_kept(const kfac_policy_desc &d) {
@@ -1384,8 +1410,8 @@ PolicyPlan plan_policy(const kfac_policy_desc &d, Arena &ws) {
     p.err = ws.take<int>(64);
     p.meta = ws.take<PolicyRow>(n);
     p.order = ws.take<int>(n);
-    p.terms = ws.take<float4>(n);
-    p.flags = ws.take<float2>(n);
+    p.sums = ws.take<TermSums>(std::min<size_t>(n, MAX_CTAS));
+    p.done = ws.take<unsigned>(1);
     if (!rows_kept(d)) {
         p.ms = ws.take<float2>(n);
         p.g = ws.take<float2>(n);
@@ -1493,7 +1519,7 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
     cudaStream_t st = (cudaStream_t)stream;
     const LogitsIn in = logits_in(d);
     PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta,
-                 p.order, p.err};
+                 p.order, p.done, p.err};
     const bool kept = rows_kept(d), ent = d.entropy_coef != 0.f || d.entropy;
     const float scale = d.grad_scale / d.temperature;
     RowParams P{};
@@ -1511,23 +1537,20 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
     P.scale = scale;
     if (kept) P.dlogits = (char *)d.dlogits;
     P.ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
-    if (const int L = d.seq_mean ? 0 : small_lanes(d.dtype, d.vocab, d.rows))
+    if (const int L = d.rows == 0 ? 8 : d.seq_mean ? 0 : small_lanes(d.dtype, d.vocab, d.rows))
         return by_type(d.dtype, ent, RunPolicySmall{P, R, d.stats, L, st});
     const unsigned ctas = d.rows > ROWS_THREADS ? SMALL_CLUSTER : 1;
     KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_rows_kernel, ctas, ctas, ROWS_THREADS, 0, R);
-    if (d.rows > 0) {
-        P.meta = p.meta;
-        P.order = p.order;
-        P.terms = p.terms;
-        P.flags = p.flags;
-        P.ms = p.ms;
-        P.g = p.g;
-        P.err = p.err;
-        if ((s = by_type(d.dtype, ent, RunRows{P, st})) != KFAC_OK) return s;
-    }
-    PolicySum U{d.rows, p.terms, p.flags, d.stats, p.err};
-    KFAC_LAUNCH_CLUSTERS(KK_LOSS_SMALL, st, policy_sum_kernel, ctas, ctas, ROWS_THREADS, 0, U);
-    if (kept || !d.dlogits || d.rows == 0) return KFAC_OK;
+    P.meta = p.meta;
+    P.order = p.order;
+    P.sums = p.sums;
+    P.done = p.done;
+    P.stats = d.stats;
+    P.ms = p.ms;
+    P.g = p.g;
+    P.err = p.err;
+    if ((s = by_type(d.dtype, ent, RunRows{P, st})) != KFAC_OK) return s;
+    if (kept || !d.dlogits) return KFAC_OK;
     GradParams G{in, d.rows, p.ms, d.entropy ? d.entropy : p.h, (const float *)p.g, (const float *)p.g + 1, 2, scale,
                  (char *)d.dlogits, d.ld_d * (long long)elem_size(d.dtype)};
     return by_type(d.dtype, d.entropy_coef != 0.f, RunGrad{G, st});
