@@ -132,7 +132,7 @@ struct Elem<KFAC_F32> {
         asm("max.NaN.f32 %0, %0, 0fF0000000;" : "+r"(v));  // -1.6e29
         return v;
     }
-    static constexpr bool BOUNDS = true;
+    static constexpr float M_MIN = -F32_MAX;
     static __device__ __forceinline__ uint4 bounded(uint4 u) {
         return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
     }
@@ -159,7 +159,7 @@ struct Elem<KFAC_BF16> {
         const two b = __hmax2_nan(as_two(v), as_two(0xf000f000u));  // -1.6e29
         return *reinterpret_cast<const uint32_t *>(&b);
     }
-    static constexpr bool BOUNDS = true;
+    static constexpr float M_MIN = -F32_MAX;
     static __device__ __forceinline__ uint4 bounded(uint4 u) {
         return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
     }
@@ -192,8 +192,14 @@ struct Elem<KFAC_F16> {
     using two = __half2;  // running maximum of groups (NaN is passed over)
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xfbfffbffu); }
-    static constexpr bool BOUNDS = false;  // (its lowest value is a logit's, not far below all of them)
-    static __device__ __forceinline__ uint4 bounded(uint4 u) { return u; }
+    static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
+        const two b = __hmax2_nan(as_two(v), as_two(0xfbfffbffu));  // the lowest finite value
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static constexpr float M_MIN = -32768.f;  // the bound is far below a larger maximum
+    static __device__ __forceinline__ uint4 bounded(uint4 u) {
+        return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
+    }
     static __device__ __forceinline__ two raise(two m, uint4 u) {
         return __hmax2(m, __hmax2(__hmax2(as_two(u.x), as_two(u.y)), __hmax2(as_two(u.z), as_two(u.w))));
     }
@@ -342,12 +348,12 @@ __device__ __forceinline__ void unpack_pairs(uint4 u, f2 *v) {
 // result's own rounding, and for delta = m k - c, which is the same for the whole
 // row and is put back into the sums (2^y (z) = 2^-delta 2^(z k - c)).  `ok` is false
 // where m k is so large that c or delta would be (rows at the type's lowest value):
-// then the difference is formed before the product.
+// then the difference is formed before the product.  (m_min: Elem::M_MIN.)
 struct Shift {
     float m, k, c, delta;
     bool ok;
-    __device__ __forceinline__ Shift(float m_, float k_) : m(m_), k(k_), c(m_ * k_) {
-        ok = fabsf(c) < 1048576.f;
+    __device__ __forceinline__ Shift(float m_, float k_, float m_min) : m(m_), k(k_), c(m_ * k_) {
+        ok = fabsf(c) < 1048576.f && m >= m_min;
         delta = ok ? fmaf(m, k, -c) : 0.f;
     }
     template <bool FAST>
@@ -372,7 +378,7 @@ struct Sums {
         for (int i = 0; i < H; ++i) {
             const f2 y = h.apply<FAST>(v[i]);
             v[i] = ex2(y);
-            if (ENT) t = fma(v[i], FAST && Elem<DT>::BOUNDS ? y : max2(y, Y_FLOOR), t);
+            if (ENT) t = fma(v[i], FAST ? y : max2(y, Y_FLOOR), t);
         }
         if constexpr (H == 4) return kfac::add(kfac::add(v[0], v[1]), kfac::add(v[2], v[3]));
         else return kfac::add(v[0], v[1]);
@@ -417,7 +423,7 @@ struct Running {
         for (int i = 0; i < VPT; ++i)
             if (i < count) best = Elem<DT>::raise(best, u[i]);
         raise(Elem<DT>::largest(best));
-        const Shift h(m, k);
+        const Shift h(m, k, Elem<DT>::M_MIN);
         Sums<DT, ENT> batch;
         if (h.ok) {
 #pragma unroll

@@ -16,6 +16,9 @@
 
 #include "logits.cuh"
 
+#ifndef XTEAM
+#define XTEAM 2560
+#endif
 namespace kfac {
 namespace {
 
@@ -86,7 +89,7 @@ __device__ __forceinline__ uint4 grad_group(uint4 u, const Coef &c, const Shift 
 #pragma unroll
     for (int i = 0; i < H; ++i) {
         const f2 y = h.apply<FAST>(v[i]), e = ex2(y);
-        const float2 d = both(ENT ? mul(e, fma(b, FAST && Elem<DT>::BOUNDS ? y : max2(y, Y_FLOOR), a)) : mul(e, a));
+        const float2 d = both(ENT ? mul(e, fma(b, FAST ? y : max2(y, Y_FLOOR), a)) : mul(e, a));
         f[2 * i] = d.x;
         f[2 * i + 1] = d.y;
     }
@@ -161,6 +164,11 @@ __device__ __forceinline__ void grad_groups(const char *z, char *out, int n, int
     if (tid == owner) ((bits *)out)[tgt] = Elem<DT>::round(d_t);
 }
 template <int DT, bool ENT>
+__device__ __noinline__ void grad_groups_any(const char *z, char *out, int n, int tgt, const Coef &c, float d_t,
+                                             const Shift &h, int tid, int nt) {
+    grad_groups<DT, ENT, true, true>(z, out, n, tgt, c, d_t, h, tid, nt);
+}
+template <int DT, bool ENT>
 __device__ __noinline__ void grad_groups_slow(const char *z, char *out, int n, int tgt, const Coef &c, float d_t,
                                               const Shift &h, int tid, int nt) {
     grad_groups<DT, ENT, false, true>(z, out, n, tgt, c, d_t, h, tid, nt);
@@ -168,12 +176,12 @@ __device__ __noinline__ void grad_groups_slow(const char *z, char *out, int n, i
 template <int DT, bool ENT>
 __device__ __forceinline__ void grad_row(const char *z, char *out, int n, int tgt, float z_t, const Coef &c, float k,
                                          int tid, int nt) {
-    const Shift h(c.m, k);
+    const Shift h(c.m, k, Elem<DT>::M_MIN);
     const float d_t = grad_target<ENT>(z_t, c, k);
     if (h.ok && (((uintptr_t)out ^ (uintptr_t)z) & 15) == 0)
         grad_groups<DT, ENT, true, false>(z, out, n, tgt, shifted(c, h), d_t, h, tid, nt);
     else if (h.ok)
-        grad_groups<DT, ENT, true, true>(z, out, n, tgt, shifted(c, h), d_t, h, tid, nt);
+        grad_groups_any<DT, ENT>(z, out, n, tgt, shifted(c, h), d_t, h, tid, nt);
     else grad_groups_slow<DT, ENT>(z, out, n, tgt, c, d_t, h, tid, nt);
 }
 
@@ -419,7 +427,7 @@ __device__ __forceinline__ void write_gradient(const Kept<DT, VPT> &kept, const 
         zero_row<DT>(out, r.n, tid, nt);
         return;
     }
-    const Shift h(c.m, k);
+    const Shift h(c.m, k, Elem<DT>::M_MIN);
     if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
         grad_row<DT, ENT>(z, out, r.n, target, z_t, c, k, tid, nt);
         return;
@@ -464,7 +472,7 @@ __device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, boo
     kept.load(r, r.begin() + lane, L, live ? r.end() : 0, most,
               !live ? -1 : lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? r.end() : -1);
     const float z_t = live ? logit_at<DT>(z, q.target) : 0.f, ref = live && P.ref_logp ? P.ref_logp[row] : 0.f;
-    const Shift h(lanes_max(kept.largest(r, most), L), P.in.k);
+    const Shift h(lanes_max(kept.largest(r, most), L), P.in.k, Elem<DT>::M_MIN);
     const Part p = kept.template sums<ENT>(r, h, most, true).part(h, L);
     char *out = P.dlogits ? P.dlogits + (in ? row : 0) * P.ld_d_bytes : nullptr;
     Terms terms{};
@@ -510,6 +518,78 @@ __device__ __forceinline__ void store_part(const float4 *local, int rank, float4
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
+}
+
+// Rows of middling length (up to WARP_GROUPS whole groups), each to one warp: a first
+// pass for the statistics, a second for the gradient, which finds the row in the
+// L2 cache (the rows in flight are at most 4864 x 16 KB).  No barriers, and the next
+// row's inputs are asked for before a row is begun.
+constexpr int WARP_GROUPS = 1024, WARP_THREADS = 256, WARP_PER_SM = 4;
+template <int DT, bool ENT>
+__global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(const __grid_constant__ RowParams P) {
+    constexpr int W = WARP_THREADS / 32, BATCH = 4;
+    __shared__ TermSums warp_sums[W];  // (registers are short)
+    pdl_wait();
+    pdl_trigger();
+    if (P.zero && blockIdx.x == 0 && threadIdx.x == 0) *P.zero = 0;
+    const int lane = threadIdx.x % 32;
+    const float k = P.in.k;
+    const long long step = (long long)gridDim.x * W;
+    long long row = (long long)blockIdx.x * W + threadIdx.x / 32;
+    if (lane == 0) warp_sums[threadIdx.x / 32] = TermSums{};
+    PolicyRow q{-1, 0.f, 0.f, 0.f};
+    if (row < P.rows) q = row_meta(P, row);
+    for (; row < P.rows; row += step) {
+        const PolicyRow now = q;
+        if (row + step < P.rows) q = row_meta(P, row + step);
+        char *out = P.dlogits ? P.dlogits + row * P.ld_d_bytes : nullptr;
+        if (now.target < 0) {
+            if (lane == 0) ignore_row(P, row);
+            if (out) zero_row<DT>(out, P.in.vocab, lane, 32);
+            continue;
+        }
+        const char *z = P.in.logits + row * P.in.ld_bytes;
+        const Row<DT> r(z, P.in.vocab);
+        const float z_t = logit_at<DT>(z, now.target), ref = P.ref_logp ? P.ref_logp[row] : 0.f;
+        Running<DT, ENT> run(k);
+        const int end = r.end();
+        int g = r.begin() + lane;
+        for (; g - lane + BATCH * 32 <= end; g += BATCH * 32) {
+            uint4 u[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) u[i] = r.load_whole(g + i * 32);
+            run.template add<BATCH>(u, BATCH, 0);
+        }
+        if (g - lane < end) {
+            uint4 u[BATCH];
+            const int most = (end - (g - lane) + 31) / 32;
+            unsigned skip = 0;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i)
+                if (i < most) {
+                    u[i] = r.load_whole(min(g + i * 32, end - 1));
+                    skip |= (g + i * 32 >= end ? 1u : 0u) << i;
+                }
+            run.template add<BATCH>(u, most, skip);
+        }
+        const int at = lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? end : -1;
+        if (at >= 0) {
+            const uint4 u = r.load_edge(at);
+            run.template add<1>(&u, 1, 0);
+        }
+        const Part p = run.part();
+        Terms terms{};
+        const Coef c = finish_row<ENT>(P, row, now, ref, p, z_t, lane == 0, terms);
+        if (P.policy && lane == 0) warp_sums[threadIdx.x / 32].add(terms);
+        if (!out) continue;
+        if (c.none) zero_row<DT>(out, P.in.vocab, lane, 32);
+        else grad_row<DT, ENT>(z, out, P.in.vocab, now.target, z_t, c, k, lane, 32);
+    }
+    if (!P.policy) return;
+    __syncthreads();
+    TermSums sums = threadIdx.x < W ? warp_sums[threadIdx.x] : TermSums{};
+    sums.add_block();
+    leave_sums(P, sums, blockIdx.x, gridDim.x);
 }
 
 // The parts of one row from all warps that worked on it, joined by one warp.
@@ -610,7 +690,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __
 // that take the rows in turn, so that one computes while the other waits for
 // its row's statistics to be joined.  A team's warps send their parts to every
 // CTA of the cluster, each of which joins them itself.
-constexpr int TEAMS = 2, TEAM = 256, TEAM_WARPS = TEAM / 32, RING_THREADS = TEAMS * TEAM + 32, MAX_STAGES = 8;
+constexpr int TEAM_THREADS = 512, RING_THREADS = TEAM_THREADS + 32, MAX_TEAMS = 4, MAX_STAGES = 8;
 constexpr int RING_BYTES = 221184;  // of shared memory for the stages: three of 4608 groups
 
 struct StageRow {
@@ -618,7 +698,9 @@ struct StageRow {
     int row;
     float ref, z_t;
 };
+template <int TEAMS>
 struct RingShared {
+    static constexpr int TEAM = TEAM_THREADS / TEAMS, TEAM_WARPS = TEAM / 32;
     float4 parts[TEAMS][2][MAX_CLUSTER * TEAM_WARPS];
     Coef coef[TEAMS][2];
     StageRow row[MAX_STAGES];
@@ -645,6 +727,7 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 // The team's barrier; whether any of its threads gave true, the same for all of them.
+template <int TEAM>
 __device__ __forceinline__ bool team_any(int team, bool v) {
     uint32_t any;
     asm volatile(
@@ -656,22 +739,23 @@ __device__ __forceinline__ bool team_any(int team, bool v) {
 }
 
 // A thread's sums over its groups of a stage.
-template <int DT, bool ENT, bool FAST>
+template <int DT, bool ENT, bool FAST, int TEAM>
 __device__ __forceinline__ Sums<DT, ENT> stage_sums(const uint4 *stage, int t, int G, const Shift &h) {
     Sums<DT, ENT> s;
 #pragma unroll 4
     for (int g = t; g < G; g += TEAM) s.template add<FAST>(stage[g], h);
     return s;
 }
-template <int DT, bool ENT>
+template <int DT, bool ENT, int TEAM>
 __device__ __noinline__ Sums<DT, ENT> stage_sums_slow(const uint4 *stage, int t, int G, const Shift &h) {
-    return stage_sums<DT, ENT, false>(stage, t, G, h);
+    return stage_sums<DT, ENT, false, TEAM>(stage, t, G, h);
 }
 
 // Waits for the stage that holds the cluster's row n.  The stage's last use may
 // have been the other team's, its copy still under way; the barrier's parity tells
 // one use from the next only once the stage has been given to row n.
-__device__ __forceinline__ bool wait_stage(RingShared &sh, int st, long long n, int parity) {
+template <class Shared>
+__device__ __forceinline__ bool wait_stage(Shared &sh, int st, long long n, int parity) {
     const volatile long long *given = &sh.given[st];
     if (!mbar_wait(&sh.full[st], parity)) return false;
     if (*given != n) {
@@ -683,11 +767,12 @@ __device__ __forceinline__ bool wait_stage(RingShared &sh, int st, long long n, 
     return true;
 }
 
-template <int DT, bool ENT>
+template <int DT, bool ENT, int TEAMS>
 __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid_constant__ RowParams P, int cs, int stages,
                                                                     int stage_bytes) {
+    constexpr int TEAM = RingShared<TEAMS>::TEAM, TEAM_WARPS = RingShared<TEAMS>::TEAM_WARPS;
     extern __shared__ __align__(128) char ring[];
-    __shared__ RingShared sh;
+    __shared__ RingShared<TEAMS> sh;
     const int tid = threadIdx.x, rank = blockIdx.x % cs;
     const float k = P.in.k;
     if (tid == 0) {
@@ -713,7 +798,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         g1 = min(r.end(), c0 + per);
     };
 
-    if (tid >= TEAMS * TEAM) {  // ---- the warp that fetches
+    if (tid >= TEAM_THREADS) {  // ---- the warp that fetches
         const int lane = tid % 32;
         bool ok = true;
         for (long long n0 = 0; n0 < count && ok; n0 += 32) {
@@ -773,7 +858,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 if (t % 32 == 0) mbar_arrive(&sh.empty[st]);
                 if (rank == 0 && t == 0) ignore_row(P, row);
                 zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
-                if (team_any(team, *(volatile int *)&sh.dead != 0)) break;
+                if (team_any<TEAM>(team, *(volatile int *)&sh.dead != 0)) break;
                 continue;
             }
             const Row<DT> r(z, P.in.vocab);
@@ -786,8 +871,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             auto best = Elem<DT>::raise(Elem<DT>::lowest(), edge);
 #pragma unroll 4
             for (int g = t; g < G; g += TEAM) best = Elem<DT>::raise(best, stage[g]);
-            const Shift hw(lanes_max(Elem<DT>::largest(best), 32), k);
-            Sums<DT, ENT> sums = hw.ok ? stage_sums<DT, ENT, true>(stage, t, G, hw) : stage_sums_slow<DT, ENT>(stage, t, G, hw);
+            const Shift hw(lanes_max(Elem<DT>::largest(best), 32), k, Elem<DT>::M_MIN);
+            Sums<DT, ENT> sums = hw.ok ? stage_sums<DT, ENT, true, TEAM>(stage, t, G, hw)
+                                            : stage_sums_slow<DT, ENT, TEAM>(stage, t, G, hw);
             if (at >= 0) {
                 if (hw.ok) sums.template add<true>(edge, hw);
                 else sums.template add<false>(edge, hw);
@@ -812,9 +898,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 }
             }
             ++turn;
-            if (team_any(team, *(volatile int *)&sh.dead != 0)) break;
+            if (team_any<TEAM>(team, *(volatile int *)&sh.dead != 0)) break;
             const Coef c = sh.coef[team][b];
-            const Shift h(c.m, k);
+            const Shift h(c.m, k, Elem<DT>::M_MIN);
             if (c.none) {
                 zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
             } else if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
@@ -861,22 +947,25 @@ struct GradParams {
     long long ld_out_bytes;
 };
 
-template <int DT, bool ENT>
+// T threads of a block of THREADS to a row: all of them, or a warp where rows are short.
+template <int DT, bool ENT, int T>
 __global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ GradParams P) {
     pdl_wait();
     pdl_trigger();
+    const int t = threadIdx.x % T;
     // from the last row: what the statistics have read last is still in the L2 cache
-    for (long long row = P.rows - 1 - blockIdx.x; row >= 0; row -= gridDim.x) {
+    for (long long row = P.rows - 1 - ((long long)blockIdx.x * (THREADS / T) + threadIdx.x / T); row >= 0;
+         row -= (long long)gridDim.x * (THREADS / T)) {
         const long long tgt = target_of(P.in, row);
         const float2 ms = P.ms[row];
         const Coef c = coef_of<ENT>(ms.x, ms.y, ENT ? P.entropy[row] : 0.f, P.g[row * P.gs] * P.scale,
                                     ENT ? P.gh[row * P.gs] * P.scale : 0.f);
         char *out = P.out + row * P.ld_out_bytes;
         if (tgt < 0 || tgt >= P.in.vocab || c.none)
-            zero_row<DT>(out, P.in.vocab, threadIdx.x, THREADS);
+            zero_row<DT>(out, P.in.vocab, t, T);
         else {
             const char *z = P.in.logits + row * P.in.ld_bytes;
-            grad_row<DT, ENT>(z, out, P.in.vocab, (int)tgt, logit_at<DT>(z, tgt), c, P.in.k, threadIdx.x, THREADS);
+            grad_row<DT, ENT>(z, out, P.in.vocab, (int)tgt, logit_at<DT>(z, tgt), c, P.in.k, t, T);
         }
     }
 }
@@ -1227,17 +1316,18 @@ kfac_status by_type(int dtype, bool ent, F &&f) {
 
 // How rows are kept in shared memory: by how many CTAs, in how many stages.
 struct Ring {
-    int cs, stages, bytes;  // cs = 0: they do not fit
+    int cs, stages, bytes, teams;  // cs = 0: they do not fit
 };
 Ring ring_of(int dtype, int vocab, long long rows) {
     const long long whole = vocab / (dtype == KFAC_F32 ? 4 : 8);  // whole groups of a row, at most
-    Ring g{1, 0, 0};
+    Ring g{1, 0, 0, 2};
     auto bytes = [&](int cs) { return ceil_div(whole, cs) * 16; };
     while (g.cs < MAX_CLUSTER && bytes(g.cs) > RING_BYTES / 3) g.cs *= 2;
     // few rows: more CTAs to each, while a thread has two groups
-    while (g.cs < MAX_CLUSTER && rows * g.cs * 2 <= device_sm_count() && whole >= (long long)g.cs * TEAM * 4) g.cs *= 2;
-    if (bytes(g.cs) > RING_BYTES / 2) return Ring{0, 0, 0};
+    while (g.cs < MAX_CLUSTER && rows * g.cs * 2 <= device_sm_count() && whole >= (long long)g.cs * 1024) g.cs *= 2;
+    if (bytes(g.cs) > RING_BYTES / 2) return Ring{0, 0, 0, 0};
     g.bytes = (int)align_up((size_t)bytes(g.cs), 128);
+    g.teams = bytes(g.cs) > XTEAM * 16 ? 2 : 4;
     g.stages = (int)std::min<long long>(MAX_STAGES, RING_BYTES / std::max(g.bytes, 128));
     return g;
 }
@@ -1248,47 +1338,51 @@ constexpr int MAX_CTAS = 1 << 14;
 struct RunRows {
     const RowParams &P;
     cudaStream_t st;
+    template <int DT, bool ENT, int TEAMS>
+    kfac_status ring(const Ring &g) {
+        auto kernel = ring_rows_kernel<DT, ENT, TEAMS>;
+        static std::atomic<int> ready[64][4];  // by device and cluster size: clusters that run at once
+        int dev = 0, lg = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KFAC_ERR_CUDA;
+        while ((1 << lg) < g.cs) ++lg;
+        int most = ready[dev][lg].load(std::memory_order_relaxed);
+        if (most == 0) {
+            KFAC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES));
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(device_sm_count() / g.cs * g.cs);
+            cfg.blockDim = dim3(RING_THREADS);
+            cfg.dynamicSmemBytes = RING_BYTES;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = g.cs;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            KFAC_CUDA_TRY(cudaOccupancyMaxActiveClusters(&most, kernel, &cfg));
+            if (most < 1) return KFAC_ERR_CUDA;
+            ready[dev][lg].store(most, std::memory_order_relaxed);
+        }
+        const unsigned grid = (unsigned)std::min<long long>(P.rows, most) * g.cs;
+        KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, kernel, g.cs, grid, RING_THREADS, (size_t)g.stages * g.bytes, P, g.cs,
+                             g.stages, g.bytes);
+        return KFAC_OK;
+    }
     template <int DT, bool ENT>
     kfac_status run() {
         const long long whole = P.in.vocab / Elem<DT>::N;
-        if (whole <= 32 * NV) {
-            const int per = SMALL_THREADS / (whole <= 8 * NV ? 8 : 32);
-            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, per), MAX_CTAS);
-            if (whole <= 8 * NV)
-                KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 8>), grid, SMALL_THREADS, 0, P);
-            else
-                KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 32>), grid, SMALL_THREADS, 0, P);
+        if (whole <= 8 * NV) {
+            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, SMALL_THREADS / 8), MAX_CTAS);
+            KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 8>), grid, SMALL_THREADS, 0, P);
             return KFAC_OK;
         }
-        const Ring g = P.dlogits ? ring_of(DT, P.in.vocab, P.rows) : Ring{0, 0, 0};
-        if (g.cs) {
-            auto kernel = ring_rows_kernel<DT, ENT>;
-            static std::atomic<int> ready[64][4];  // by device and cluster size: clusters that run at once
-            int dev = 0, lg = 0;
-            if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KFAC_ERR_CUDA;
-            while ((1 << lg) < g.cs) ++lg;
-            int most = ready[dev][lg].load(std::memory_order_relaxed);
-            if (most == 0) {
-                KFAC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_BYTES));
-                cudaLaunchConfig_t cfg = {};
-                cfg.gridDim = dim3(device_sm_count() / g.cs * g.cs);
-                cfg.blockDim = dim3(RING_THREADS);
-                cfg.dynamicSmemBytes = RING_BYTES;
-                cudaLaunchAttribute attr[1];
-                attr[0].id = cudaLaunchAttributeClusterDimension;
-                attr[0].val.clusterDim.x = g.cs;
-                attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-                cfg.attrs = attr;
-                cfg.numAttrs = 1;
-                KFAC_CUDA_TRY(cudaOccupancyMaxActiveClusters(&most, kernel, &cfg));
-                if (most < 1) return KFAC_ERR_CUDA;
-                ready[dev][lg].store(most, std::memory_order_relaxed);
-            }
-            const unsigned grid = (unsigned)std::min<long long>(P.rows, most) * g.cs;
-            KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, kernel, g.cs, grid, RING_THREADS, (size_t)g.stages * g.bytes, P, g.cs,
-                                 g.stages, g.bytes);
+        if (whole <= WARP_GROUPS && P.rows >= device_sm_count()) {
+            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, WARP_THREADS / 32),
+                                                                device_sm_count() * WARP_PER_SM);
+            KFAC_LAUNCH(KK_LOSS_ROWS, st, (warp_rows_kernel<DT, ENT>), grid, WARP_THREADS, 0, P);
             return KFAC_OK;
         }
+        const Ring g = P.dlogits ? ring_of(DT, P.in.vocab, P.rows) : Ring{0, 0, 0, 0};
+        if (g.cs) return g.teams == 2 ? ring<DT, ENT, 2>(g) : ring<DT, ENT, 4>(g);
         // few rows: more CTAs to each, while a thread has two groups
         int cs = 1;
         while (cs < MAX_CLUSTER && P.rows * cs * 2 <= device_sm_count() && whole >= (long long)cs * STREAM_THREADS * 4)
@@ -1347,8 +1441,12 @@ struct RunGrad {
     cudaStream_t st;
     template <int DT, bool ENT>
     kfac_status run() {
-        KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT>), (unsigned)std::min<long long>(P.rows, 1 << 20), THREADS, 0,
-                    P);
+        if (P.in.vocab / Elem<DT>::N <= WARP_GROUPS)
+            KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT, 32>),
+                        (unsigned)std::min<long long>(ceil_div(P.rows, THREADS / 32), 1 << 20), THREADS, 0, P);
+        else
+            KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT, THREADS>),
+                        (unsigned)std::min<long long>(P.rows, 1 << 20), THREADS, 0, P);
         return KFAC_OK;
     }
 };
@@ -1400,9 +1498,10 @@ struct PolicyPlan {
     float2 *ms, *g;  // ms, g, h: for rows that do not fit the chip
     float *h;
 };
+// Whether one launch makes statistics and gradient.
 bool rows_kept(const kfac_policy_desc &d) {
     const long long whole = d.vocab / (d.dtype == KFAC_F32 ? 4 : 8);
-    return whole <= 32 * NV || ring_of(d.dtype, d.vocab, d.rows).cs;
+    return whole <= WARP_GROUPS || ring_of(d.dtype, d.vocab, d.rows).cs;
 }
 PolicyPlan plan_policy(const kfac_policy_desc &d, Arena &ws) {
     PolicyPlan p{};
