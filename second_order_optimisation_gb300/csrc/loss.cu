@@ -16,9 +16,6 @@
 
 #include "logits.cuh"
 
-#ifndef XTEAM
-#define XTEAM 2560
-#endif
 namespace kfac {
 namespace {
 
@@ -613,9 +610,9 @@ __device__ __forceinline__ Part join_parts(const float4 *parts, int n, float k) 
 
 // Statistics only: one row to a CTA or, where there are few rows, to a cluster
 // of cs CTAs, each with a run of the row's groups.
-constexpr int STREAM_THREADS = 128, BATCH = 4;
+constexpr int STREAM_THREADS = 128, STREAM_PER_SM = 8, BATCH = 4;
 template <int DT, bool ENT>
-__global__ void __launch_bounds__(STREAM_THREADS, 8) stream_rows_kernel(const __grid_constant__ RowParams P, int cs) {
+__global__ void __launch_bounds__(STREAM_THREADS, STREAM_PER_SM) stream_rows_kernel(const __grid_constant__ RowParams P, int cs) {
     constexpr int T = STREAM_THREADS, W = T / 32;
     __shared__ float4 parts[2][MAX_CLUSTER * W];
     pdl_wait();
@@ -1322,12 +1319,12 @@ Ring ring_of(int dtype, int vocab, long long rows) {
     const long long whole = vocab / (dtype == KFAC_F32 ? 4 : 8);  // whole groups of a row, at most
     Ring g{1, 0, 0, 2};
     auto bytes = [&](int cs) { return ceil_div(whole, cs) * 16; };
-    while (g.cs < MAX_CLUSTER && bytes(g.cs) > RING_BYTES / 3) g.cs *= 2;
+    while (g.cs < MAX_CLUSTER && bytes(g.cs) > RING_BYTES / 2) g.cs *= 2;
     // few rows: more CTAs to each, while a thread has two groups
     while (g.cs < MAX_CLUSTER && rows * g.cs * 2 <= device_sm_count() && whole >= (long long)g.cs * 1024) g.cs *= 2;
     if (bytes(g.cs) > RING_BYTES / 2) return Ring{0, 0, 0, 0};
     g.bytes = (int)align_up((size_t)bytes(g.cs), 128);
-    g.teams = bytes(g.cs) > XTEAM * 16 ? 2 : 4;
+    g.teams = bytes(g.cs) > 2560 * 16 ? 2 : 4;
     g.stages = (int)std::min<long long>(MAX_STAGES, RING_BYTES / std::max(g.bytes, 128));
     return g;
 }
@@ -1383,9 +1380,10 @@ struct RunRows {
         }
         const Ring g = P.dlogits ? ring_of(DT, P.in.vocab, P.rows) : Ring{0, 0, 0, 0};
         if (g.cs) return g.teams == 2 ? ring<DT, ENT, 2>(g) : ring<DT, ENT, 4>(g);
-        // few rows: more CTAs to each, while a thread has two groups
+        // few rows: more CTAs to each, while there is room and a thread has two groups
         int cs = 1;
-        while (cs < MAX_CLUSTER && P.rows * cs * 2 <= device_sm_count() && whole >= (long long)cs * STREAM_THREADS * 4)
+        while (cs < MAX_CLUSTER && P.rows * cs < device_sm_count() * STREAM_PER_SM &&
+               whole >= (long long)cs * STREAM_THREADS * 4)
             cs *= 2;
         const unsigned grid = (unsigned)std::min<long long>(P.rows, MAX_CTAS) * cs;
         KFAC_LAUNCH_CLUSTERS(KK_LOSS_ROWS, st, (stream_rows_kernel<DT, ENT>), cs, grid, STREAM_THREADS, 0, P, cs);
