@@ -530,8 +530,9 @@ kfac_status kfac_preference_loss(const kfac_preference_desc *desc, void *workspa
  * squared length of the natural gradient step in the Fisher metric, and
  * max_norm = sqrt(kappa) / eta bounds the step's second-order KL change by
  * kappa / 2.
- *   - x, y: [rows][ld] of dtype (KFAC_BF16, KFAC_F16, KFAC_F32), cols wide; a
- *     vector is one row.  out: [rows][ld_out] of out_dtype; w: [rows][ld_w] fp32.
+ *   - x: [rows][ld] of dtype (KFAC_BF16, KFAC_F16, KFAC_F32), cols wide; a vector is
+ *     one row.  y: [rows][ld_y] of y_dtype, which is dtype or, with x in fp32, any of the
+ *     three (fp32 steps and the 16-bit gradients that they come from).  out: [rows][ld_out] of out_dtype; w: [rows][ld_w] fp32.
  *     Any ld >= cols and any element-aligned base; rows that run on without a
  *     gap (ld = cols) or start on 16-byte boundaries are read 16 bytes at a
  *     time.  rows or cols = 0: the tensor adds nothing.
@@ -546,7 +547,7 @@ kfac_status kfac_preference_loss(const kfac_preference_desc *desc, void *workspa
  * NaN norm scale NaN) and set KFAC_ERRW_NONFINITE in the error word, which a
  * caller that skips such steps reads.
  * Errors: INVALID for count < 0, null x of a tensor that is not empty, negative
- *   sizes, ld < cols, a bad dtype, out = x with another dtype or ld, a base that
+ *   sizes, ld < cols, a bad dtype (or pair of them), out = x with another dtype or ld, a base that
  *   is not element-aligned, max_norm not positive or NaN, eta not finite.
  * Workspace: kfac_clip_norm_workspace_size(descs, count) bytes.
  * ==================================================================== */
@@ -556,7 +557,7 @@ typedef struct {
     void *out;     int64_t ld_out;     /* may be NULL */
     float *w;      int64_t ld_w;       /* may be NULL */
     int64_t rows, cols;
-    int32_t dtype, out_dtype;
+    int32_t dtype, y_dtype, out_dtype;
 } kfac_clip_desc;
 
 size_t kfac_clip_norm_workspace_size(const kfac_clip_desc *descs, int count);

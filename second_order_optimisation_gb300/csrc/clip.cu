@@ -32,7 +32,7 @@ struct ClipJob {
     long long rows, cols;  // a tensor without gaps is one row
     long long first;       // its first octet of the launch
     long long per_row;     // octets of a row
-    uint8_t dtype, out_dtype;
+    uint8_t dtype, y_dtype, out_dtype;
     uint8_t shift;         // octet 0 starts this many elements before the row
     uint8_t vec;           // octets are taken 16 bytes at a time
     uint8_t out_vec;       // ... and stored so
@@ -145,6 +145,21 @@ __device__ __forceinline__ unsigned block_max(unsigned v) {
     return __reduce_max_sync(0xffffffffu, v);
 }
 
+// The types of a tensor's x and y (NO_Y: there is none), as template arguments.
+constexpr int NO_Y = -1;
+template <int DT_, int YT_>
+struct Types {
+    static constexpr int DT = DT_, YT = YT_;
+};
+template <class F>
+__device__ __forceinline__ auto by_types(const ClipJob &j, F &&f) {
+    if (j.dtype == KFAC_BF16) return j.y ? f(Types<KFAC_BF16, KFAC_BF16>{}) : f(Types<KFAC_BF16, NO_Y>{});
+    if (j.dtype == KFAC_F16) return j.y ? f(Types<KFAC_F16, KFAC_F16>{}) : f(Types<KFAC_F16, NO_Y>{});
+    if (!j.y) return f(Types<KFAC_F32, NO_Y>{});
+    return j.y_dtype == KFAC_BF16 ? f(Types<KFAC_F32, KFAC_BF16>{})
+           : j.y_dtype == KFAC_F16 ? f(Types<KFAC_F32, KFAC_F16>{}) : f(Types<KFAC_F32, KFAC_F32>{});
+}
+
 // 2^n as fp32, n in -126 .. 127.
 __device__ __forceinline__ float pow2(int n) { return __int_as_float((n + 127) << 23); }
 // A power of two (as its exponent) that brings the largest magnitude (its bits) near 1.
@@ -167,20 +182,22 @@ __device__ __forceinline__ float sum_of_products(const float *x, const float *y)
     for (int e = 0; e < OCTET; ++e) q[e] = x[e] * y[e];
     return ((q[0] + q[1]) + (q[2] + q[3])) + ((q[4] + q[5]) + (q[6] + q[7]));
 }
-template <int DT, bool METRIC, bool ANY>
+template <int DT, int YT, bool ANY>
 __device__ __noinline__ Wide inner_products(const ClipJob &j, long long a, long long b, Wide sum) {
+    constexpr bool METRIC = YT != NO_Y;
     constexpr int ES = Elem<DT>::N == 4 ? 4 : 2, UNROLL = (METRIC ? 2 : 4) * (ES == 2 ? 2 : 1), STEP = CLIP_THREADS * OCTET * ES;
+    constexpr int Y = METRIC ? YT : DT, ESY = Elem<Y>::N == 4 ? 4 : 2, STEPY = CLIP_THREADS * OCTET * ESY;
     const char *x = j.x + (a * OCTET - j.shift) * ES + threadIdx.x * (OCTET * ES);
-    const char *y = METRIC ? j.y + (a * OCTET - j.shift) * ES + threadIdx.x * (OCTET * ES) : x;
+    const char *y = METRIC ? j.y + (a * OCTET - j.shift) * ESY + threadIdx.x * (OCTET * ESY) : x;
     const int oy = (int)((uintptr_t)y & 15);  // (x is on its boundaries)
     long long left = b - a - threadIdx.x;  // octets from this thread's on
     for (; left > (UNROLL - 1) * CLIP_THREADS; left -= UNROLL * CLIP_THREADS) {
         Raw<DT, false> u[UNROLL];
-        Raw<DT, ANY> v[METRIC ? UNROLL : 1];
+        Raw<Y, ANY> v[METRIC ? UNROLL : 1];
 #pragma unroll
         for (int k = 0; k < UNROLL; ++k) {
             u[k].load(x + k * STEP, 0);
-            if (METRIC) v[k].load(y + k * STEP, oy);
+            if (METRIC) v[k].load(y + k * STEPY, oy);
         }
         float t = 0.f;
 #pragma unroll
@@ -192,46 +209,50 @@ __device__ __noinline__ Wide inner_products(const ClipJob &j, long long a, long 
         }
         sum.add(t);
         x += UNROLL * STEP;
-        y += UNROLL * STEP;
+        y += UNROLL * STEPY;
     }
     for (; left > 0; left -= CLIP_THREADS) {
         float f[OCTET], h[OCTET];
         load8<DT>(x, 0, f);
-        if (METRIC) load8<DT>(y, oy, h);
+        if (METRIC) load8<Y>(y, oy, h);
         sum.add(sum_of_products(f, METRIC ? h : f));
         x += STEP;
-        y += STEP;
+        y += STEPY;
     }
     return sum;
 }
 
-template <int DT, bool METRIC>
+template <int DT, int YT>
 __device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long long hi, int tid, int nt, Wide sum);
 // This thread's sum of x y over octets lo .. hi - 1 of a tensor, added to `sum`.
 // A short run, and a long one's ends, are one warp's, the n-th of them the
 // n-th warp's, so that many small tensors go on side by side.
-template <int DT, bool METRIC>
+template <int DT, int YT>
 __device__ __forceinline__ void products(const ClipJob &j, int n, long long lo, long long hi, Wide &sum) {
     const int lane = threadIdx.x % 32;
     const bool mine = (int)threadIdx.x / 32 == n % (CLIP_THREADS / 32);
     if (hi - lo < SHORT_RUN) {
-        if (mine) sum = outer_products<DT, METRIC>(j, lo, hi, lane, 32, sum);
+        if (mine) sum = outer_products<DT, YT>(j, lo, hi, lane, 32, sum);
         return;
     }
     long long a, b;
     inner_run(j, lo, hi, a, b);
     if (b > a) {
-        if (mine) sum = outer_products<DT, METRIC>(j, lo, a, lane, 32, sum);
-        if (mine) sum = outer_products<DT, METRIC>(j, b, hi, lane, 32, sum);
-        if (METRIC && (((uintptr_t)j.x ^ (uintptr_t)j.y) & 15)) sum = inner_products<DT, METRIC, METRIC>(j, a, b, sum);
-        else sum = inner_products<DT, METRIC, false>(j, a, b, sum);
+        if (mine) sum = outer_products<DT, YT>(j, lo, a, lane, 32, sum);
+        if (mine) sum = outer_products<DT, YT>(j, b, hi, lane, 32, sum);
+        constexpr int ESY = YT == KFAC_F32 ? 4 : 2;
+        if (YT != NO_Y && (((uintptr_t)j.y - (uintptr_t)j.shift * ESY) & 15))
+            sum = inner_products<DT, YT, YT != NO_Y>(j, a, b, sum);
+        else
+            sum = inner_products<DT, YT, false>(j, a, b, sum);
     } else {
-        sum = outer_products<DT, METRIC>(j, lo, hi, threadIdx.x, CLIP_THREADS, sum);
+        sum = outer_products<DT, YT>(j, lo, hi, threadIdx.x, CLIP_THREADS, sum);
     }
 }
-template <int DT, bool METRIC>
+template <int DT, int YT>
 __device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long long hi, int tid, int nt, Wide sum) {
-    constexpr int UNROLL = METRIC ? 2 : 4;  // octets in flight
+    constexpr bool METRIC = YT != NO_Y;
+    constexpr int Y = METRIC ? YT : DT, UNROLL = METRIC ? 2 : 4;  // octets in flight
     for (long long i = lo + tid; i < hi; i += UNROLL * nt) {
         float x[UNROLL][OCTET], y[UNROLL][OCTET];
 #pragma unroll
@@ -240,7 +261,7 @@ __device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long
             if (at < hi) {
                 const Place p = place_of(j, at);
                 octet<DT>(j.x, j.ld, p, j.cols, j.vec, x[u]);
-                if (METRIC) octet<DT>(j.y, j.ld_y, p, j.cols, j.vec, y[u]);
+                if (METRIC) octet<Y>(j.y, j.ld_y, p, j.cols, j.vec, y[u]);
             } else {
 #pragma unroll
                 for (int e = 0; e < OCTET; ++e) x[u][e] = y[u][e] = 0.f;
@@ -257,8 +278,9 @@ __device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long
 }
 // The same over the block, from values scaled by powers of two (unscaled where
 // one is not finite).
-template <int DT>
+template <int DT, int YT>
 __device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long long hi) {
+    constexpr int Y = YT != NO_Y ? YT : DT;
     const char *yb = j.y ? j.y : j.x;
     const long long ld_y = j.y ? j.ld_y : j.ld;
     unsigned mx = 0, my = 0;
@@ -266,7 +288,7 @@ __device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long l
     for (long long i = lo + threadIdx.x; i < hi; i += CLIP_THREADS) {
         const Place p = place_of(j, i);
         octet<DT>(j.x, j.ld, p, j.cols, false, x);
-        octet<DT>(yb, ld_y, p, j.cols, false, y);
+        octet<Y>(yb, ld_y, p, j.cols, false, y);
         for (int e = 0; e < OCTET; ++e) {
             mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
             my = max(my, __float_as_uint(y[e]) & 0x7fffffffu);
@@ -281,7 +303,7 @@ __device__ __noinline__ double scaled_sum(const ClipJob &j, long long lo, long l
     for (long long i = lo + threadIdx.x; i < hi; i += CLIP_THREADS) {
         const Place p = place_of(j, i);
         octet<DT>(j.x, j.ld, p, j.cols, false, x);
-        octet<DT>(yb, ld_y, p, j.cols, false, y);
+        octet<Y>(yb, ld_y, p, j.cols, false, y);
         for (int e = 0; e < OCTET; ++e) sum.add((x[e] * fx) * (y[e] * fy));
     }
     return ldexp(block_wide(sum).value(), -ex - ey);
@@ -296,16 +318,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(co
     for (int n = job_of(P, lo); n < P.n && P.job[n].first < hi; ++n) {
         const ClipJob &j = P.job[n];
         const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
-        if (j.dtype == KFAC_BF16) {
-            if (j.y) products<KFAC_BF16, true>(j, n, a, b, mine);
-            else products<KFAC_BF16, false>(j, n, a, b, mine);
-        } else if (j.dtype == KFAC_F16) {
-            if (j.y) products<KFAC_F16, true>(j, n, a, b, mine);
-            else products<KFAC_F16, false>(j, n, a, b, mine);
-        } else {
-            if (j.y) products<KFAC_F32, true>(j, n, a, b, mine);
-            else products<KFAC_F32, false>(j, n, a, b, mine);
-        }
+        by_types(j, [&](auto t) { products<t.DT, t.YT>(j, n, a, b, mine); });
     }
     }
     // every warp joins the warps' sums, and hi is the same for all threads
@@ -318,8 +331,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, CLIP_PER_SM) clip_norm_kernel(co
         for (int n = job_of(P, lo); n < P.n && P.job[n].first < hi; ++n) {
             const ClipJob &j = P.job[n];
             const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
-            sum += j.dtype == KFAC_BF16 ? scaled_sum<KFAC_BF16>(j, a, b)
-                   : j.dtype == KFAC_F16 ? scaled_sum<KFAC_F16>(j, a, b) : scaled_sum<KFAC_F32>(j, a, b);
+            sum += by_types(j, [&](auto t) { return scaled_sum<t.DT, t.YT>(j, a, b); });
         }
         }
     }
@@ -481,15 +493,7 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_small_kernel(const __grid_c
         const ClipJob &j = P.job[n];
         const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
         if (b <= a) continue;
-        if (j.dtype == KFAC_BF16)
-            mine = j.y ? outer_products<KFAC_BF16, true>(j, a, b, tid, CLIP_THREADS, mine)
-                       : outer_products<KFAC_BF16, false>(j, a, b, tid, CLIP_THREADS, mine);
-        else if (j.dtype == KFAC_F16)
-            mine = j.y ? outer_products<KFAC_F16, true>(j, a, b, tid, CLIP_THREADS, mine)
-                       : outer_products<KFAC_F16, false>(j, a, b, tid, CLIP_THREADS, mine);
-        else
-            mine = j.y ? outer_products<KFAC_F32, true>(j, a, b, tid, CLIP_THREADS, mine)
-                       : outer_products<KFAC_F32, false>(j, a, b, tid, CLIP_THREADS, mine);
+        mine = by_types(j, [&](auto t) { return outer_products<t.DT, t.YT>(j, a, b, tid, CLIP_THREADS, mine); });
     }
     const Wide s = block_wide(mine);
     double sum = s.value();
@@ -499,8 +503,7 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_small_kernel(const __grid_c
             const ClipJob &j = P.job[n];
             const long long a = max(lo, j.first) - j.first, b = min(hi - j.first, j.rows * j.per_row);
             if (b <= a) continue;
-            sum += j.dtype == KFAC_BF16 ? scaled_sum<KFAC_BF16>(j, a, b)
-                   : j.dtype == KFAC_F16 ? scaled_sum<KFAC_F16>(j, a, b) : scaled_sum<KFAC_F32>(j, a, b);
+            sum += by_types(j, [&](auto t) { return scaled_sum<t.DT, t.YT>(j, a, b); });
         }
     }
     if (tid == 0)
@@ -573,12 +576,14 @@ kfac_status check_clip(const kfac_clip_desc *descs, int count, float max_norm, f
     if (count < 0 || (count > 0 && !descs) || !(max_norm > 0.f) || !std::isfinite(eta)) return KFAC_ERR_INVALID;
     for (int i = 0; i < count; ++i) {
         const kfac_clip_desc &d = descs[i];
-        if (d.rows < 0 || d.cols < 0 || !known(d.dtype) || (d.out && !known(d.out_dtype))) return KFAC_ERR_INVALID;
+        if (d.rows < 0 || d.cols < 0 || !known(d.dtype) || (d.out && !known(d.out_dtype)) || (d.y && !known(d.y_dtype)))
+            return KFAC_ERR_INVALID;
+        if (d.y && d.y_dtype != d.dtype && d.dtype != KFAC_F32) return KFAC_ERR_INVALID;
         if (d.rows == 0 || d.cols == 0) continue;
         if (!d.x || d.ld < d.cols || (d.y && d.ld_y < d.cols) || (d.out && d.ld_out < d.cols) ||
             (d.w && d.ld_w < d.cols))
             return KFAC_ERR_INVALID;
-        if ((uintptr_t)d.x % size_of(d.dtype) || (uintptr_t)d.y % size_of(d.dtype) ||
+        if ((uintptr_t)d.x % size_of(d.dtype) || (d.y && (uintptr_t)d.y % size_of(d.y_dtype)) ||
             (d.out && (uintptr_t)d.out % size_of(d.out_dtype)) || (uintptr_t)d.w % 4)
             return KFAC_ERR_INVALID;
         if (d.out == d.x && (d.out_dtype != d.dtype || d.ld_out != d.ld)) return KFAC_ERR_INVALID;
@@ -588,7 +593,7 @@ kfac_status check_clip(const kfac_clip_desc *descs, int count, float max_norm, f
 
 ClipJob job_from(const kfac_clip_desc &d, bool apply) {
     ClipJob j{(const char *)d.x, (const char *)d.y, (char *)d.out, d.w, d.ld, d.ld_y, d.ld_out, d.ld_w,
-              d.rows, d.cols, 0, 0, (uint8_t)d.dtype, (uint8_t)d.out_dtype, 0, 0, 0};
+              d.rows, d.cols, 0, 0, (uint8_t)d.dtype, (uint8_t)d.y_dtype, (uint8_t)d.out_dtype, 0, 0, 0};
     if (d.rows == 1 || (d.ld == d.cols && (!d.y || d.ld_y == d.cols) && (!d.out || d.ld_out == d.cols) &&
                         (!d.w || d.ld_w == d.cols))) {
         j.cols = d.rows * d.cols;

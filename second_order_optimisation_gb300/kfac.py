@@ -134,7 +134,7 @@ class ClipDesc(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("ld", ctypes.c_int64), ("y", ctypes.c_void_p), ("ld_y", ctypes.c_int64),
                 ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("w", ctypes.c_void_p), ("ld_w", ctypes.c_int64),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
-                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+                ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -722,8 +722,8 @@ def kfac_preference_loss(item: PreferenceLoss, workspace: Optional[torch.Tensor]
 
 @dataclass
 class ClipTensor:
-    """One tensor of kfac_clip_norm: x (and y, its dual under the metric) are
-    read; out = scale * x and w -= eta * scale * x are written where given.  All
+    """One tensor of kfac_clip_norm: x (and y, its dual under the metric, of x's
+    dtype or, beside an fp32 x, 16-bit) are read; out = scale * x and w -= eta * scale * x are written where given.  All
     of one shape: dense, or 2-D with unit column stride.  out may be x."""
     x: torch.Tensor
     out: Optional[torch.Tensor] = None
@@ -738,8 +738,8 @@ def _clip_desc(t: ClipTensor) -> ClipDesc:
     ops = [o for o in (x, t.y, t.out, t.w) if o is not None]
     if any(o.shape != x.shape for o in ops):
         raise ValueError("x, y, out and w must have one shape")
-    if t.y is not None and t.y.dtype is not x.dtype:
-        raise TypeError("y must have x's dtype")
+    if t.y is not None and t.y.dtype is not x.dtype and (x.dtype is not torch.float32 or t.y.dtype not in _DTYPES):
+        raise TypeError("y must have x's dtype, or be bf16 or fp16 beside an fp32 x")
     if t.w is not None and t.w.dtype is not torch.float32:
         raise TypeError("w must be fp32")
     if t.out is not None and t.out.dtype not in _DTYPES:
@@ -753,7 +753,8 @@ def _clip_desc(t: ClipTensor) -> ClipDesc:
         rows, cols = x.shape
         ld = lambda o: o.stride(0) if rows > 1 else cols  # noqa: E731
     a = [v for o in (x, t.y, t.out, t.w) for v in ((None, 0) if o is None else (o.data_ptr(), ld(o)))]
-    return ClipDesc(*a, rows, cols, _DTYPES[x.dtype], _DTYPES[t.out.dtype] if t.out is not None else _DTYPES[x.dtype])
+    dt = [_DTYPES[(x if o is None else o).dtype] for o in (x, t.y, t.out)]
+    return ClipDesc(*a, rows, cols, *dt)
 
 
 class ClipList:

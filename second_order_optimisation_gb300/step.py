@@ -24,6 +24,11 @@ other steps precondition with the inverses of the last refresh.  A stale step
 skips the factor statistic as well as the inversion (the factors are
 "updated" less often, not only inverted less often).  With `weights` the
 preconditioner also applies w <- w - eta * P in its epilogue (Eq. 8).
+
+With `max_norm` the step over all layers is bounded first: kfac_clip_norm takes
+the length sqrt(sum P . grad) of the natural gradient step in the Fisher metric
+(`metric=False`: the Euclidean norm of P), and the weights move by
+eta * min(1, max_norm / length) * P; `norm` and `scale` hold the last step's.
 """
 from __future__ import annotations
 
@@ -67,7 +72,8 @@ class LayerState:
 class KfacStep:
     def __init__(self, layers: Sequence[Layer], batch: int, xi: float = 0.95, gamma: float = 1e-3,
                  device="cuda", update_every: int = 1, warmup: int = 0,
-                 weights: Optional[Sequence[torch.Tensor]] = None, eta: float = 0.0):
+                 weights: Optional[Sequence[torch.Tensor]] = None, eta: float = 0.0,
+                 max_norm: Optional[float] = None, metric: bool = True):
         self.layers = list(layers)
         self.batch = batch
         self.xi = xi
@@ -82,6 +88,10 @@ class KfacStep:
             raise ValueError("one weight tensor per layer")
         self.weights = list(weights) if weights is not None else None
         self.eta = float(eta)
+        self.max_norm = None if max_norm is None else float(max_norm)
+        self.metric = bool(metric)
+        self.norm = torch.zeros(1, device=self.device)    # of the last bounded step
+        self.scale = torch.ones(1, device=self.device)
         self.state: List[LayerState] = []
         for L in self.layers:
             dA, dG = L.d_a, L.d_g
@@ -121,7 +131,8 @@ class KfacStep:
         return [kfac.InvertPair(s.A, s.G, s.A_inv, s.G_inv, s.A_inv16, s.G_inv16) for s in self.state]
 
     def precond_items(self, grads):
-        ws = self.weights if self.weights is not None else [None] * len(self.state)
+        fused = self.weights is not None and self.max_norm is None
+        ws = self.weights if fused else [None] * len(self.state)
         return [kfac.PrecondItem(s.G_inv16, s.A_inv16, gr, s.out,
                                  w=w, eta=self.eta)
                 for s, gr, w in zip(self.state, grads, ws)]
@@ -148,6 +159,20 @@ class KfacStep:
         items = self.precond_items(grads)
         ws = self._workspace("precond", kfac.kfac_precondition_workspace_size(items))
         kfac.kfac_precondition(items, ws, stream)
+        if self.max_norm is not None:
+            self.clip(grads, stream)
+
+    def clip_tensors(self, grads):
+        ws = self.weights if self.weights is not None else [None] * len(self.state)
+        return [kfac.ClipTensor(s.out, None if w is not None else s.out, gr if self.metric else None, w)
+                for s, gr, w in zip(self.state, grads, ws)]
+
+    def clip(self, grads, stream=None):
+        """Bound the preconditioned gradients by max_norm and take the step on the
+        weights (without weights: scale the preconditioned gradients)."""
+        tensors = kfac.ClipList(self.clip_tensors(grads))
+        ws = self._workspace("clip", tensors.need)
+        kfac.kfac_clip_norm(tensors, self.max_norm, self.norm, self.scale, self.eta, ws, stream)
 
     def run(self, xs, gs, grads, stream=None):
         """One full step: factors + inverse + preconditioning for all layers."""

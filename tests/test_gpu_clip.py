@@ -89,6 +89,21 @@ def test_types_and_shapes(dtype, out, metric):
     check(ts, INF, use_list=True)
 
 
+@pytest.mark.parametrize("ydt", ["bf16", "f16"])
+def test_metric_of_fp32_steps_and_16_bit_gradients(ydt):
+    """The natural gradient step (fp32) and the gradient that it comes from."""
+    g = torch.Generator().manual_seed(11)
+    ts = []
+    for shape, ldx, ldy in [((64, 147), 192, None), ((64, 147), None, None), ((256, 576), None, None), ((1000, 2049), 2112, 2112),
+                            ((5,), None, None), ((400, 1000), None, 1003)]:
+        x = strided(shape, torch.float32, ldx, 0, g)
+        y = strided(shape, TYPES[ydt], ldy, 1 if len(shape) == 1 else 0, g, 0.1)
+        y.add_(x.to(y.dtype))
+        ts.append(kfac.ClipTensor(x, None, y, strided(shape, torch.float32, ldx and ldx + 1, 0, g)))
+    check(ts, 0.5, eta=0.25)
+    check(ts[:2] + ts[4:5], 0.5, eta=0.25)
+
+
 def test_norm_alone_and_no_tensors():
     g = torch.Generator().manual_seed(5)
     check([kfac.ClipTensor(strided((50, 60), torch.float32, gen=g))], 2.0)

@@ -164,14 +164,15 @@ def test_loss_workspaces(lib, make, run, size):
 
 
 def _cl(**kw):
-    d = dict(x=0x1000, ld=10, rows=3, cols=10, dtype=kfac.KFAC_F32, out=0x2000, ld_out=10, out_dtype=kfac.KFAC_F32)
+    d = dict(x=0x1000, ld=10, rows=3, cols=10, dtype=kfac.KFAC_F32, y_dtype=kfac.KFAC_F32, out=0x2000, ld_out=10, out_dtype=kfac.KFAC_F32)
     d.update(kw)
     return (kfac.ClipDesc * 1)(kfac.ClipDesc(**d))
 
 
 @pytest.mark.parametrize("bad", [dict(x=None), dict(ld=9), dict(rows=-1), dict(cols=-1), dict(dtype=9),
                                  dict(out_dtype=9), dict(ld_out=9), dict(y=0x3000, ld_y=9), dict(w=0x3000, ld_w=9),
-                                 dict(x=0x1002), dict(w=0x3002, ld_w=10), dict(y=0x3002, ld_y=10),
+                                 dict(x=0x1002), dict(w=0x3002, ld_w=10), dict(y=0x3002, ld_y=10), dict(y=0x3000, ld_y=10, y_dtype=9),
+                                 dict(dtype=kfac.KFAC_BF16, y=0x3000, ld_y=10), dict(dtype=kfac.KFAC_F16, y=0x3000, ld_y=10, y_dtype=kfac.KFAC_BF16),
                                  dict(out=0x1000, out_dtype=kfac.KFAC_BF16), dict(out=0x1000, ld_out=11)])
 def test_clip_refuses(lib, bad):
     arr = _cl(**bad)
@@ -218,6 +219,6 @@ def test_binding_refuses():
     with pytest.raises(ValueError):
         kfac.ClipList([kfac.ClipTensor(torch.zeros(6, 4).t())])
     with pytest.raises(TypeError):
-        kfac.ClipList([kfac.ClipTensor(z, y=z.half())])
+        kfac.ClipList([kfac.ClipTensor(z.half(), y=z)])
     with pytest.raises(TypeError):
         kfac.ClipList([kfac.ClipTensor(z, w=z.half())])
