@@ -659,7 +659,9 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
             P->job[P->n++] = j;
         }
         P->tile = std::max<long long>(1, ceil_div(P->octets, ctas_of(P->octets)));
-        if (!apply) P->tile = std::min<long long>(P->tile, TILE);
+        // in the first pass tiles of about TILE octets, the same number for every CTA, in
+        // steps that keep them on memory's boundaries
+        if (!apply) P->tile = (long long)align_up((size_t)ceil_div(P->tile, ceil_div(P->tile, TILE)), 512);
     };
     if constexpr (MAX == CLIP_FEW) {
         fill(0, true);

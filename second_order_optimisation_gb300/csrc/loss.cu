@@ -816,18 +816,19 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 ok = __all_sync(0xffffffffu, mbar_wait(&sh.empty[st], (int)(n / stages & 1) ^ 1));
                 if (!ok) break;
                 if (lane == j) {
-                    sh.row[st] = mine;
-                    *(volatile long long *)&sh.given[st] = n;
+                    // (the copy may count its bytes before they are expected: the stage stays open until
+                    // this thread has arrived, and then it holds the row's other inputs too)
                     const Row<DT> r(P.in.logits + mine.row * P.in.ld_bytes, P.in.vocab);
                     int c0, g1;
                     run_of(r, c0, g1);
-                    if (mine.q.target >= 0 && g1 > c0) {
-                        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)(g1 - c0) * 16);
+                    const bool loads = mine.q.target >= 0 && g1 > c0;
+                    if (loads)
                         bulk_load(ring + (size_t)st * stage_bytes, r.base + (size_t)c0 * 16, (uint32_t)(g1 - c0) * 16,
                                   &sh.full[st]);
-                    } else {
-                        mbar_arrive(&sh.full[st]);
-                    }
+                    sh.row[st] = mine;
+                    *(volatile long long *)&sh.given[st] = n;
+                    if (loads) mbar_arrive_expect_tx(&sh.full[st], (uint32_t)(g1 - c0) * 16);
+                    else mbar_arrive(&sh.full[st]);
                 }
                 __syncwarp();
             }
@@ -1141,44 +1142,65 @@ constexpr int PAIR_THREADS = 256;
 template <int T>
 __device__ __forceinline__ void pref_pair(const PrefPairs &P, int b) {
     __shared__ Wide part[32];
-    __shared__ int ipart[32];
+    __shared__ int ipart[32], ibad[16];
     __shared__ float shared_slope[2];
     const int t = threadIdx.x % T;
     long long r0[2], r1[2];
     double l[2] = {0., 0.};
-    int n[2], bad = 0;
+    Wide sum[2] = {};
+    int n[2] = {0, 0}, bad = 0;
+    const long long cut = clamp_row(P.off[2 * b + 1], P.rows);
+    r0[0] = clamp_row(P.off[2 * b], P.rows);
+    r1[0] = r0[1] = cut;
+    r1[1] = clamp_row(P.off[2 * b + 2], P.rows);
     for (int q = 0; q < 2; ++q) {
-        r0[q] = clamp_row(P.off[2 * b + q], P.rows);
-        r1[q] = clamp_row(P.off[2 * b + q + 1], P.rows);
-        Wide s{};
-        int c = 0;
         for (long long row = r0[q] + t; row < r1[q]; row += T) {
             const long long tg = P.target_i32 ? (long long)((const int32_t *)P.target)[row]
                                               : (long long)((const int64_t *)P.target)[row];
             if (tg >= P.vocab) bad |= ERR_TARGET;
             if (tg < 0 || tg >= P.vocab) continue;
-            ++c;
+            ++n[q];
             if (__ldcg(&P.ms[row].y) == 0.f) {  // every logit -inf: left out
                 bad |= ERR_NONFINITE;
                 continue;
             }
             const float v = __ldcg(&P.logp[row]);
             if (!finite(v)) bad |= ERR_NONFINITE;
-            s.add(v);
+            sum[q].add(v);
         }
-        if constexpr (T == 32) {
-            s.add_lanes();
-            n[q] = __reduce_add_sync(0xffffffffu, c);
-        } else {
-            s = block_sum(s, part);
-            n[q] = block_sum(c, ipart);
+    }
+    for (int q = 0; q < 2; ++q) {
+        sum[q].add_lanes();
+        n[q] = __reduce_add_sync(0xffffffffu, n[q]);
+    }
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if constexpr (T > 32) {
+        constexpr int W = T / 32;
+        if (threadIdx.x % 32 == 0) {
+            const int w = threadIdx.x / 32;
+            part[w] = sum[0];
+            part[W + w] = sum[1];
+            ipart[w] = n[0];
+            ipart[W + w] = n[1];
+            ibad[w] = bad;
         }
-        if (t == 0) {
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            for (int q = 0; q < 2; ++q) {
+                sum[q] = threadIdx.x < W ? part[q * W + threadIdx.x] : Wide{};
+                sum[q].add_lanes();
+                n[q] = __reduce_add_sync(0xffffffffu, threadIdx.x < W ? ipart[q * W + threadIdx.x] : 0);
+            }
+            bad = __reduce_or_sync(0xffffffffu, threadIdx.x < W ? ibad[threadIdx.x] : 0);
+        }
+    }
+    if (t == 0)
+        for (int q = 0; q < 2; ++q) {
+            const Wide s = sum[q];
             l[q] = P.average && n[q] > 0 ? s.value() / n[q] : s.value();
             if (!finite((float)l[q])) bad |= ERR_NONFINITE;
             if (P.seq_logp) P.seq_logp[2 * b + q] = (float)l[q];
         }
-    }
     float slope[2] = {0.f, 0.f};
     if (t == 0) {
         double h = l[0] - l[1];
@@ -1205,13 +1227,8 @@ __device__ __forceinline__ void pref_pair(const PrefPairs &P, int b) {
             if (T > 32) shared_slope[q] = slope[q];
         }
     }
-    bad = __reduce_or_sync(0xffffffffu, bad);
     if constexpr (T > 32) {
         __syncthreads();
-        if (threadIdx.x % 32 == 0) ipart[threadIdx.x / 32] = bad;
-        __syncthreads();
-        if (t == 0)
-            for (int i = 1; i < T / 32; ++i) bad |= ipart[i];
         slope[0] = shared_slope[0];
         slope[1] = shared_slope[1];
     } else {
