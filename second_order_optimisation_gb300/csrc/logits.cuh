@@ -325,13 +325,15 @@ struct Part {
     float m, s, t;
 };
 
-// Lanes' maximum, the same on each of `width` lanes.
-__device__ __forceinline__ float lanes_max(float v, int width) {
-    for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+// Lanes' maximum, the same on each of `width` lanes (`mask`: the lanes that come
+// here together).
+constexpr unsigned ALL_LANES = 0xffffffffu;
+__device__ __forceinline__ float lanes_max(float v, int width, unsigned mask = ALL_LANES) {
+    for (int o = width / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
     return v;
 }
-__device__ __forceinline__ float lanes_sum(float v, int width) {
-    for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+__device__ __forceinline__ float lanes_sum(float v, int width, unsigned mask = ALL_LANES) {
+    for (int o = width / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
     return v;
 }
 
@@ -442,11 +444,11 @@ struct Running {
         if (ENT) t = kfac::add(t, mul(pair(f, f), fma(pair(-h.delta, -h.delta), batch.s, batch.t)));
         s.add(mul(pair(f, f), batch.s));
     }
-    // The warp's.
-    __device__ __forceinline__ Part part() {
-        raise(lanes_max(m, 32));
+    // Of `width` lanes.
+    __device__ __forceinline__ Part part(int width = 32, unsigned mask = ALL_LANES) {
+        raise(lanes_max(m, width, mask));
         const float2 tt = both(t);
-        return Part{m, lanes_sum(s.total(), 32), ENT ? lanes_sum(tt.x + tt.y, 32) : 0.f};
+        return Part{m, lanes_sum(s.total(), width, mask), ENT ? lanes_sum(tt.x + tt.y, width, mask) : 0.f};
     }
 };
 

@@ -517,23 +517,26 @@ __device__ __forceinline__ void store_part(const float4 *local, int rank, float4
                  : "memory");
 }
 
-// Rows of middling length (up to WARP_GROUPS whole groups), each to one warp: a first
-// pass for the statistics, a second for the gradient, which finds the row in the
-// L2 cache (the rows in flight are at most 4864 x 16 KB).  No barriers, and the next
-// row's inputs are asked for before a row is begun.
+// Rows of middling length, each to L lanes of a warp (L = 8, 16 or 32, for at most 32 L
+// whole groups): a first pass for the statistics, a second for the gradient, which
+// finds the row in the L2 cache (the rows in flight hold at most 80 MB).  No
+// barriers, and the next row's inputs are asked for before a row is begun.  Fewer
+// lanes share a row's fixed work, about 600 instructions, among more rows.
 constexpr int WARP_GROUPS = 1024, WARP_THREADS = 256, WARP_PER_SM = 4;
-template <int DT, bool ENT>
+template <int DT, bool ENT, int L>
 __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(const __grid_constant__ RowParams P) {
-    constexpr int W = WARP_THREADS / 32, BATCH = 4;
-    __shared__ TermSums warp_sums[W];  // (registers are short)
+    constexpr int G = WARP_THREADS / L, BATCH = 4;
+    __shared__ TermSums group_sums[G];  // (registers are short)
     pdl_wait();
     pdl_trigger();
     if (P.zero && blockIdx.x == 0 && threadIdx.x == 0) *P.zero = 0;
-    const int lane = threadIdx.x % 32;
+    const int lane = threadIdx.x % L;
+    const unsigned mask = L == 32 ? ALL_LANES : ((1u << L) - 1) << (threadIdx.x % 32 / L * L);
     const float k = P.in.k;
-    const long long step = (long long)gridDim.x * W;
-    long long row = (long long)blockIdx.x * W + threadIdx.x / 32;
-    if (lane == 0) warp_sums[threadIdx.x / 32] = TermSums{};
+    const long long step = (long long)gridDim.x * G;
+    long long row = (long long)blockIdx.x * G + threadIdx.x / L;
+    TermSums &mine = group_sums[threadIdx.x / L];
+    if (lane == 0) mine = TermSums{};
     PolicyRow q{-1, 0.f, 0.f, 0.f};
     if (row < P.rows) q = row_meta(P, row);
     for (; row < P.rows; row += step) {
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(co
         char *out = P.dlogits ? P.dlogits + row * P.ld_d_bytes : nullptr;
         if (now.target < 0) {
             if (lane == 0) ignore_row(P, row);
-            if (out) zero_row<DT>(out, P.in.vocab, lane, 32);
+            if (out) zero_row<DT>(out, P.in.vocab, lane, L);
             continue;
         }
         const char *z = P.in.logits + row * P.in.ld_bytes;
@@ -551,21 +554,21 @@ __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(co
         Running<DT, ENT> run(k);
         const int end = r.end();
         int g = r.begin() + lane;
-        for (; g - lane + BATCH * 32 <= end; g += BATCH * 32) {
+        for (; g - lane + BATCH * L <= end; g += BATCH * L) {
             uint4 u[BATCH];
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) u[i] = r.load_whole(g + i * 32);
+            for (int i = 0; i < BATCH; ++i) u[i] = r.load_whole(g + i * L);
             run.template add<BATCH>(u, BATCH, 0);
         }
         if (g - lane < end) {
             uint4 u[BATCH];
-            const int most = (end - (g - lane) + 31) / 32;
+            const int most = (end - (g - lane) + L - 1) / L;
             unsigned skip = 0;
 #pragma unroll
             for (int i = 0; i < BATCH; ++i)
                 if (i < most) {
-                    u[i] = r.load_whole(min(g + i * 32, end - 1));
-                    skip |= (g + i * 32 >= end ? 1u : 0u) << i;
+                    u[i] = r.load_whole(min(g + i * L, end - 1));
+                    skip |= (g + i * L >= end ? 1u : 0u) << i;
                 }
             run.template add<BATCH>(u, most, skip);
         }
@@ -574,19 +577,26 @@ __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(co
             const uint4 u = r.load_edge(at);
             run.template add<1>(&u, 1, 0);
         }
-        const Part p = run.part();
+        __syncwarp(mask);
+        const Part p = run.part(L, mask);
         Terms terms{};
         const Coef c = finish_row<ENT>(P, row, now, ref, p, z_t, lane == 0, terms);
-        if (P.policy && lane == 0) warp_sums[threadIdx.x / 32].add(terms);
+        if (P.policy && lane == 0) mine.add(terms);
         if (!out) continue;
-        if (c.none) zero_row<DT>(out, P.in.vocab, lane, 32);
-        else grad_row<DT, ENT>(z, out, P.in.vocab, now.target, z_t, c, k, lane, 32);
+        if (c.none) zero_row<DT>(out, P.in.vocab, lane, L);
+        else grad_row<DT, ENT>(z, out, P.in.vocab, now.target, z_t, c, k, lane, L);
     }
     if (!P.policy) return;
     __syncthreads();
-    TermSums sums = threadIdx.x < W ? warp_sums[threadIdx.x] : TermSums{};
+    TermSums sums = threadIdx.x < G ? group_sums[threadIdx.x] : TermSums{};
     sums.add_block();
     leave_sums(P, sums, blockIdx.x, gridDim.x);
+}
+// The lanes to a row: as few as its length allows, while they fill the GPU.
+int lanes_of(long long whole, long long rows) {
+    int L = 32;
+    while (L > 8 && whole <= 16 * L && rows * L > device_sm_count() * 1024LL) L /= 2;
+    return L;
 }
 
 // The parts of one row from all warps that worked on it, joined by one warp.
@@ -1390,9 +1400,12 @@ struct RunRows {
             return KFAC_OK;
         }
         if (whole <= WARP_GROUPS && P.rows >= device_sm_count()) {
-            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, WARP_THREADS / 32),
+            const int L = lanes_of(whole, P.rows);
+            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, WARP_THREADS / L),
                                                                 device_sm_count() * WARP_PER_SM);
-            KFAC_LAUNCH(KK_LOSS_ROWS, st, (warp_rows_kernel<DT, ENT>), grid, WARP_THREADS, 0, P);
+            if (L == 8) KFAC_LAUNCH(KK_LOSS_ROWS, st, (warp_rows_kernel<DT, ENT, 8>), grid, WARP_THREADS, 0, P);
+            else if (L == 16) KFAC_LAUNCH(KK_LOSS_ROWS, st, (warp_rows_kernel<DT, ENT, 16>), grid, WARP_THREADS, 0, P);
+            else KFAC_LAUNCH(KK_LOSS_ROWS, st, (warp_rows_kernel<DT, ENT, 32>), grid, WARP_THREADS, 0, P);
             return KFAC_OK;
         }
         const Ring g = P.dlogits ? ring_of(DT, P.in.vocab, P.rows) : Ring{0, 0, 0, 0};
@@ -1456,9 +1469,13 @@ struct RunGrad {
     cudaStream_t st;
     template <int DT, bool ENT>
     kfac_status run() {
-        if (P.in.vocab / Elem<DT>::N <= WARP_GROUPS)
-            KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT, 32>),
-                        (unsigned)std::min<long long>(ceil_div(P.rows, THREADS / 32), 1 << 20), THREADS, 0, P);
+        const long long whole = P.in.vocab / Elem<DT>::N;
+        const int L = lanes_of(whole, P.rows);
+        const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, THREADS / L), 1 << 20);
+        if (whole <= WARP_GROUPS && L < 32)
+            KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT, 8>), (unsigned)std::min<long long>(ceil_div(P.rows, THREADS / 8), 1 << 20), THREADS, 0, P);
+        else if (whole <= WARP_GROUPS)
+            KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT, 32>), grid, THREADS, 0, P);
         else
             KFAC_LAUNCH(KK_LOSS_GRAD, st, (grad_kernel<DT, ENT, THREADS>),
                         (unsigned)std::min<long long>(P.rows, 1 << 20), THREADS, 0, P);
