@@ -248,10 +248,26 @@ struct TermSums {
     }
     // Over the block, in a fixed order; thread 0's is the one to take.
     __device__ __forceinline__ void add_block() {
-        __shared__ Wide part[32];
-        bad = __syncthreads_or(bad);
+        __shared__ Wide part[5][32];
+        __shared__ int bad_of[32];
+        const int lane = threadIdx.x % 32, w = threadIdx.x / 32, warps = blockDim.x / 32;
+        bad = __reduce_or_sync(ALL_LANES, bad);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) sum[i] = block_sum(sum[i], part);
+        for (int i = 0; i < 5; ++i) sum[i].add_lanes();
+        __syncthreads();
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) part[i][w] = sum[i];
+            bad_of[w] = bad;
+        }
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            sum[i] = lane < warps ? part[i][lane] : Wide{};
+            sum[i].add_lanes();
+        }
+        bad = __reduce_or_sync(ALL_LANES, lane < warps ? bad_of[lane] : 0);
     }
     __device__ __forceinline__ void write(float *stats, int *err, int word) const {
         float v = 0.f;
