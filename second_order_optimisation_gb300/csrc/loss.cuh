@@ -9,8 +9,16 @@
 // and the gradient of g logp + gh H (times the call's scale, over tau) is
 //   d_j = 2^y_j (a + b y_j) + g [j = target],
 //   b = - gh ln 2 / s,   a = - (g + gh (H - ln 2 log2 s)) / s.
-// The maximum is subtracted before the scaling, so that rows whose logits are
-// all the type's lowest value stay finite.
+//
+// All of it is bound by memory (a row is read once, its gradient written once; one
+// or two powers of two and some ten instructions an element), and by the fixed work
+// of a row where rows are short.  Which kernel takes a call, by the whole 16-byte
+// groups of a row (RunRows; both sides of each bound were measured):
+//   few rows of at most 256 groups    *_small_kernel    the whole loss in one launch
+//   up to 512 (1024 without gradient) warp_rows_kernel  8 to 32 lanes to a row, two passes
+//   with gradient                     ring_rows_kernel  kept in shared memory
+//   statistics alone, or rows that    stream_rows_kernel, then grad_kernel
+//   no cluster can keep
 #pragma once
 
 #include <algorithm>
@@ -296,7 +304,7 @@ struct RowParams {
     // policy loss
     bool policy;               // the policy loss, its rows' other inputs in meta
     const PolicyRow *meta;
-    const int *order;          // the order in which the ring takes the rows
+    const int *order;          // the order in which the ring takes the rows (live ones first)
     const float *ref_logp;
     float clip_low, clip_high, kl_coef, entropy_coef;
     float *kl;
@@ -475,8 +483,9 @@ __device__ __forceinline__ void leave_sums(const RowParams &P, const TermSums &m
 
 // One row to L lanes of a warp (L = 8 or 32): rows of at most NV L whole groups.
 // All lanes of a warp come here together (the reductions name them all); `in`:
-// there is such a row.
-constexpr int SMALL_THREADS = 256, NV = 8;
+// there is such a row.  (For many rows the two passes of warp_rows_kernel are as fast:
+// 60000 x 500 bf16 took 84 us by eight lanes of these and takes 82.)
+constexpr int NV = 8;
 template <int DT, bool ENT, int L>
 __device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, bool in, const PolicyRow &q) {
     const int lane = threadIdx.x % L;
@@ -501,33 +510,8 @@ __device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, boo
     if (out) write_gradient<DT, ENT>(kept, r, z, out, q.target, z_t, c, P.in.k, most, lane, L);
     return terms;
 }
-template <int DT, bool ENT, int L>
-__global__ void __launch_bounds__(SMALL_THREADS, 3) lane_rows_kernel(const __grid_constant__ RowParams P) {
-    pdl_wait();
-    pdl_trigger();
-    if (P.zero && blockIdx.x == 0 && threadIdx.x == 0) *P.zero = 0;
-    __shared__ TermSums group_sums[SMALL_THREADS / L];  // (registers are short)
-    TermSums &mine = group_sums[threadIdx.x / L];
-    if (threadIdx.x % L == 0) mine = TermSums{};
-    for (long long first = (long long)blockIdx.x * (SMALL_THREADS / L) + threadIdx.x / 32 * (32 / L); first < P.rows;
-         first += (long long)gridDim.x * (SMALL_THREADS / L)) {
-        const long long row = first + threadIdx.x % 32 / L;
-        PolicyRow q{-1, 0.f, 0.f, 0.f};
-        if (row < P.rows) q = row_meta(P, row);
-        const Terms o = lane_row<DT, ENT, L>(P, row, row < P.rows, q);
-        if (P.policy && threadIdx.x % L == 0) mine.add(o);
-    }
-    if (!P.policy) return;
-    __syncthreads();
-    TermSums sums = threadIdx.x < SMALL_THREADS / L ? group_sums[threadIdx.x] : TermSums{};
-    sums.add_block();
-    leave_sums(P, sums, blockIdx.x, gridDim.x);
-}
 
 constexpr int MAX_CLUSTER = 8;
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Stores a part into CTA `rank`'s copy of a shared variable.
 __device__ __forceinline__ void store_part(const float4 *local, int rank, float4 v) {
     uint32_t a;
@@ -540,8 +524,11 @@ __device__ __forceinline__ void store_part(const float4 *local, int rank, float4
 // whole groups): a first pass for the statistics, a second for the gradient, which
 // finds the row in the L2 cache (the rows in flight hold at most 80 MB).  No
 // barriers, and the next row's inputs are asked for before a row is begun.  Fewer
-// lanes share a row's fixed work, about 600 instructions, among more rows.
-constexpr int WARP_GROUPS = 1024, WARP_GRAD_GROUPS = 512, WARP_THREADS = 256, WARP_PER_SM = 4;
+// lanes share a row's fixed work, about 600 instructions, among more rows.  A call for
+// the log-probabilities of 16000 x 2100 bf16 (67 MB) takes 22 us (26 by 32 lanes always,
+// 55 by a CTA to a row), the policy loss of 16000 x 2040 57 us (131 MB) and of 8000 x 4096
+// 47: bound by the latency of the two passes over a row and of their reductions.
+constexpr int WARP_GROUPS = 1024, WARP_GRAD_GROUPS = 512, WARP_SHORT = 64, WARP_THREADS = 256, WARP_PER_SM = 4;
 template <int DT, bool ENT, int L>
 __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(const __grid_constant__ RowParams P) {
     constexpr int G = WARP_THREADS / L, BATCH = 4;
@@ -611,7 +598,8 @@ __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(co
     sums.add_block();
     leave_sums(P, sums, blockIdx.x, gridDim.x);
 }
-// The lanes to a row: as few as its length allows, while they fill the GPU.
+// The lanes to a row: as few as its length allows, while they fill the GPU (with 32
+// lanes always, log-probabilities of 16000 x 2100 bf16 take 26 us in place of 22).
 inline int lanes_of(long long whole, long long rows) {
     int L = 32;
     while (L > 8 && whole <= 16 * L && rows * L > device_sm_count() * 1024LL) L /= 2;
@@ -638,12 +626,18 @@ __device__ __forceinline__ Part join_parts(const float4 *parts, int n, float k) 
 }
 
 // Statistics only: one row to a CTA or, where there are few rows, to a cluster
-// of cs CTAs, each with a run of the row's groups.
+// of cs CTAs, each with a run of the row's groups.  Small CTAs, eight to an SM: the
+// time from a row's first load to its last sum, about 4 us beside the loads, is then
+// some other row's loading time.  12000 x 128000 bf16 (2.15 GB live) takes 328 us, 6.6 TB/s;
+// 4099 x 50001 fp16 (410 MB) 73 us, 5.6 TB/s.  256 threads, six to an SM, take 8% more at
+// 6000 x 32000 and the same elsewhere within 3%; four to an SM up to 6% more, batches of two
+// groups up to 15% more.  The rows through a shared-memory ring took 104 us in place of 73.
 constexpr int STREAM_THREADS = 128, STREAM_PER_SM = 8, BATCH = 4;
 template <int DT, bool ENT>
 __global__ void __launch_bounds__(STREAM_THREADS, STREAM_PER_SM) stream_rows_kernel(const __grid_constant__ RowParams P, int cs) {
     constexpr int T = STREAM_THREADS, W = T / 32;
     __shared__ float4 parts[2][MAX_CLUSTER * W];
+    if (cs > 1) cluster_arrive();
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, rank = cs > 1 ? blockIdx.x % cs : 0;
@@ -653,6 +647,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, STREAM_PER_SM) stream_rows_ker
     int turn = 0;
     __shared__ TermSums sums;  // (registers are short)
     if (tid == 0) sums = TermSums{};
+    if (cs > 1) cluster_wait();
     for (long long row = blockIdx.x / cs; row < P.rows; row += step) {
         const PolicyRow q = row_meta(P, row);
         if (q.target < 0) {
@@ -714,13 +709,20 @@ __global__ void __launch_bounds__(STREAM_THREADS, STREAM_PER_SM) stream_rows_ker
 // memory: a persistent CTA on each SM, a warp that fetches the coming rows' runs
 // of groups into a ring of stages (one bulk copy each), and two teams of warps
 // that take the rows in turn, so that one computes while the other waits for
-// its row's statistics to be joined.  A team's warps send their parts to every
-// CTA of the cluster, each of which joins them itself.
+// its row's statistics to be joined (four or eight teams where runs are short).  A
+// team's warps send their parts to every CTA of the cluster, each of which joins them
+// itself.  Three short passes over a stage (maximum, sums, gradient) need few registers
+// and no rescaling; the logits cross HBM once, the gradient is stored as it is made.
+// 16391 x 131072 bf16 (8.16 GB) takes 1208 us, 6.8 TB/s, as fast as a copy; a call on
+// 2048 x 32768 (242 MB) 51 us, 4.7 TB/s: there the first stages' loading and the last
+// ones' storing have nothing beside them.  The row in the registers of a cluster of
+// ordinary CTAs took 1770 us, a second pass over the row from memory 1980.
 constexpr int TEAM_THREADS = 512, RING_THREADS = TEAM_THREADS + 32, MAX_STAGES = 16;
 constexpr int RING_BYTES = 221184;  // of shared memory for the stages: three of 4608 groups
 
-struct StageRow {
+struct __align__(16) StageRow {
     PolicyRow q;
+    uint4 edge[2];  // the groups before and behind the whole ones (of the cluster's first CTA)
     int row;
     float ref, z_t;
 };
@@ -829,13 +831,20 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         bool ok = true;
         for (long long n0 = 0; n0 < count && ok; n0 += 32) {
             // the inputs of 32 rows at once, one to a lane
-            StageRow mine{{-1, 0.f, 0.f, 0.f}, 0, 0.f, 0.f};
+            StageRow mine{};
+            mine.q.target = -1;
             if (n0 + lane < count) {
                 const long long row = P.order[first + (n0 + lane) * step];
                 mine.row = (int)row;
                 mine.q = row_meta(P, row);
                 if (mine.q.target >= 0) {
-                    mine.z_t = logit_at<DT>(P.in.logits + row * P.in.ld_bytes, mine.q.target);
+                    const char *z = P.in.logits + row * P.in.ld_bytes;
+                    mine.z_t = logit_at<DT>(z, mine.q.target);
+                    if (rank == 0) {
+                        const Row<DT> r(z, P.in.vocab);
+                        if (r.has_front()) mine.edge[0] = r.load_edge(0);
+                        if (r.has_back()) mine.edge[1] = r.load_edge(r.end());
+                    }
                     if (P.ref_logp) mine.ref = P.ref_logp[row];
                 }
             }
@@ -876,11 +885,13 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 if (t % 32 == 0) atomicOr(P.err, ERR_TIMEOUT_FULL);
                 *(volatile int *)&sh.dead = 1;
             }
-            const StageRow in = sh.row[st];
-            const long long row = in.row;
+            const StageRow &at_stage = sh.row[st];
+            const PolicyRow q = at_stage.q;
+            const float ref = at_stage.ref, z_t = at_stage.z_t;
+            const long long row = at_stage.row;
             char *out = P.dlogits + row * P.ld_d_bytes;
             const char *z = P.in.logits + row * P.in.ld_bytes;
-            if (in.q.target < 0) {
+            if (q.target < 0) {
                 __syncwarp();
                 if (t % 32 == 0) mbar_arrive(&sh.empty[st]);
                 if (rank == 0 && t == 0) ignore_row(P, row);
@@ -894,7 +905,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             const int G = g1 - c0;
             const uint4 *stage = (const uint4 *)(ring + (size_t)st * stage_bytes);
             const int at = rank != 0 ? -1 : t == 0 && r.has_front() ? 0 : t == 1 && r.has_back() ? r.end() : -1;
-            const uint4 edge = at >= 0 ? r.load_edge(at) : Row<DT>::none();
+            const uint4 edge = at >= 0 ? at_stage.edge[t] : Row<DT>::none();  // (t is 0 or 1)
             auto best = Elem<DT>::raise(Elem<DT>::lowest(), edge);
 #pragma unroll 4
             for (int g = t; g < G; g += TEAM) best = Elem<DT>::raise(best, stage[g]);
@@ -918,7 +929,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                 }
                 const Part all = join_parts<ENT>(sh.parts[team][b], cs * TEAM_WARPS, k);
                 Terms terms{};
-                const Coef c = finish_row<ENT>(P, row, in.q, in.ref, all, in.z_t, rank == 0 && t == 0, terms);
+                const Coef c = finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && t == 0, terms);
                 if (t == 0) {
                     sh.coef[team][b] = c;
                     sh.sums[team].add(terms);
@@ -931,18 +942,18 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             if (c.none) {
                 zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
             } else if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
-                grad_row_apart<DT, ENT>(z, out, P.in.vocab, in.q.target, in.z_t, c, k, rank * TEAM + t, cs * TEAM);
+                grad_row_apart<DT, ENT>(z, out, P.in.vocab, q.target, z_t, c, k, rank * TEAM + t, cs * TEAM);
             } else {
                 const Coef d = shifted(c, h);
                 uint4 *o = (uint4 *)(out - r.phase * sizeof(typename Row<DT>::bits)) + c0;
 #pragma unroll 4
                 for (int g = t; g < G; g += TEAM) o[g] = grad_group<DT, ENT, true>(stage[g], d, h);
                 if (at >= 0)
-                    Row<DT>::store_edge(out, r.first(at), r.n, grad_group<DT, ENT, true>(r.load_edge(at), d, h));
+                    Row<DT>::store_edge(out, r.first(at), r.n, grad_group<DT, ENT, true>(at_stage.edge[t], d, h));
                 // the thread that wrote the target's group adds its g
-                const int tg = (in.q.target + r.phase) / Elem<DT>::N;
+                const int tg = (q.target + r.phase) / Elem<DT>::N;
                 if (tg == at || (tg >= c0 && tg < g1 && (tg - c0) % TEAM == t))
-                    ((typename Row<DT>::bits *)out)[in.q.target] = Elem<DT>::round(grad_target<ENT>(in.z_t, c, k));
+                    ((typename Row<DT>::bits *)out)[q.target] = Elem<DT>::round(grad_target<ENT>(z_t, c, k));
             }
             __syncwarp();
             if (t % 32 == 0) mbar_arrive(&sh.empty[st]);
@@ -974,7 +985,12 @@ struct GradParams {
     long long ld_out_bytes;
 };
 
-// T threads of a block of THREADS to a row: all of them, or a warp where rows are short.
+// The gradient from saved statistics: one read of the logits, one write, no reduction
+// and no barrier.  T threads of a block of THREADS to a row: all of them, or fewer where
+// rows are short.  Rows are taken from the last: the statistics' launch has left the last
+// of the logits in the L2 cache (of 5.2 GB that is little, of 384 MB about a third).
+// 12000 x 128000 bf16 (5.2 GB, 30% of the rows zeros) takes 770 us, 6.8 TB/s; 6000 x 32000
+// with an entropy's gradient (730 MB) 110 us, 6.6 TB/s.
 template <int DT, bool ENT, int T>
 __global__ void __launch_bounds__(THREADS) grad_kernel(const __grid_constant__ GradParams P) {
     pdl_wait();
@@ -1019,7 +1035,7 @@ struct PolicyRows {
     const int32_t *off;
     int seqs, seq_mean;
     PolicyRow *meta;
-    int *order;
+    int *order;  // may be null
     unsigned *done;
     int *err;
 };
@@ -1041,12 +1057,16 @@ constexpr int SMALL_CLUSTER = 8, ROWS_THREADS = 512;
 // The whole policy loss of few short rows in one cluster: every CTA counts the
 // rows for itself (where the weight is one over their number), its groups of lanes
 // take the rows in turn, and the terms are added up across the cluster.  One
-// launch in place of three, each of which would take longer to start than to run.
+// launch in place of three, each of which would take longer to start than to run:
+// a call on 100 x 1000 fp32 takes 35 us in three launches, 30 in this form.
+// Up to SMALL_ROUNDS rows to a group: at 2000 x 18 the GPU needs 22 us either way; with
+// 16 rounds 6000 x 18 takes 45 us here and 22 in three launches.
 constexpr int SMALL_ROUNDS = 4;
 template <int DT, bool ENT, int L>
 __global__ void __launch_bounds__(ROWS_THREADS) policy_small_kernel(const __grid_constant__ RowParams P,
                                                                     const __grid_constant__ PolicyRows R, float *stats) {
     __shared__ int part[32];
+    cluster_arrive();
     pdl_wait();
     pdl_trigger();
     int n = 0, bad = 0;
@@ -1072,6 +1092,7 @@ __global__ void __launch_bounds__(ROWS_THREADS) policy_small_kernel(const __grid
     }
     __shared__ TermSums all[SMALL_CLUSTER];
     sums.add_block();
+    cluster_wait();
     if (threadIdx.x == 0) {
         *peer(&all[blockIdx.x], 0) = sums;
         if (blockIdx.x == 0) *R.err = bad ? ERR_TARGET : 0;
@@ -1235,7 +1256,8 @@ __device__ __forceinline__ void pref_sum(const PrefSum &P) {
 }
 
 // The whole preference loss of few short rows in one cluster: rows, then pairs,
-// then the rows' gradients, with a cluster barrier after each.
+// then the rows' gradients, with a cluster barrier after each (a call on
+// two pairs of 97 rows x 1000 fp32 takes 41 us in four launches, 33 in this form).
 template <int DT, int L>
 __global__ void __launch_bounds__(ROWS_THREADS) pref_small_kernel(const __grid_constant__ RowParams P,
                                                                   const __grid_constant__ PrefPairs Q,
@@ -1280,18 +1302,36 @@ inline Ring ring_of(int dtype, int vocab, long long rows) {
     const long long whole = vocab / (dtype == KFAC_F32 ? 4 : 8);  // whole groups of a row, at most
     Ring g{1, 0, 0, 2};
     auto bytes = [&](int cs) { return ceil_div(whole, cs) * 16; };
+    // Three stages at least, for which a row goes to up to four CTAs: 2000 x 50001 takes
+    // 94 us in two stages of one CTA, 89 in four stages of two.  Eight CTAs only where two
+    // stages would not fit otherwise: 1500 x 200000 takes 274 us by eight, 235 by four in
+    // two stages.
+    while (g.cs < MAX_CLUSTER / 2 && bytes(g.cs) > RING_BYTES / 3) g.cs *= 2;
     while (g.cs < MAX_CLUSTER && bytes(g.cs) > RING_BYTES / 2) g.cs *= 2;
     // few rows: more CTAs to each, while a thread has two groups
     while (g.cs < MAX_CLUSTER && rows * g.cs * 2 <= device_sm_count() && whole >= (long long)g.cs * 1024) g.cs *= 2;
     if (bytes(g.cs) > RING_BYTES / 2) return Ring{0, 0, 0, 0};
     g.bytes = (int)align_up((size_t)bytes(g.cs), 128);
-    g.teams = bytes(g.cs) > 2560 * 16 ? 2 : bytes(g.cs) > 1536 * 16 ? 4 : 8;
+    // Shorter runs, more and smaller teams (the fixed work of a row is then shared out):
+    // 8000 x 8200 takes 107 us by two teams, 75 by four, 61 by eight; 6000 x 20000 takes
+    // 92 by four and 100 by eight, 4000 x 16001 in fp32 95 by two and 107 by four.
+    g.teams = bytes(g.cs) > 3500 * 16 ? 2 : bytes(g.cs) > 1536 * 16 ? 4 : 8;
     g.stages = (int)std::min<long long>(MAX_STAGES, RING_BYTES / std::max(g.bytes, 128));
     return g;
 }
 
 // CTAs (clusters) of a launch over rows, at most: each leaves its sums.
 constexpr int MAX_CTAS = 1 << 14;
+
+// Whether rows go to warps: a CTA's barriers cost more than a second pass over short
+// rows.  Statistics of 8000 x 6000 bf16 (750 groups) take 24 us by warps and 35 by CTAs, of
+// 8000 x 8192 28 and 36.  With the gradient 16000 x 2100 takes 60 us by warps and 86 in the
+// ring, 8000 x 4096 47 and 46, 8000 x 6000 70 and 52.  Fewer rows than SMs leave warps idle
+// unless they are very short.
+inline bool by_warps(long long whole, long long rows, bool gradient) {
+    return whole <= WARP_SHORT ||
+           (whole <= (gradient ? WARP_GRAD_GROUPS : WARP_GROUPS) && rows >= device_sm_count());
+}
 
 struct RunRows {
     const RowParams &P;
@@ -1328,12 +1368,7 @@ struct RunRows {
     template <int DT, bool ENT>
     kfac_status run() {
         const long long whole = P.in.vocab / Elem<DT>::N;
-        if (whole <= 8 * NV) {
-            const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, SMALL_THREADS / 8), MAX_CTAS);
-            KFAC_LAUNCH(KK_LOSS_ROWS, st, (lane_rows_kernel<DT, ENT, 8>), grid, SMALL_THREADS, 0, P);
-            return KFAC_OK;
-        }
-        if (whole <= (P.dlogits ? WARP_GRAD_GROUPS : WARP_GROUPS) && P.rows >= device_sm_count()) {
+        if (by_warps(whole, P.rows, P.dlogits)) {
             const int L = lanes_of(whole, P.rows);
             const unsigned grid = (unsigned)std::min<long long>(ceil_div(P.rows, WARP_THREADS / L),
                                                                 device_sm_count() * WARP_PER_SM);
