@@ -371,7 +371,7 @@ kfac_status kfac_bn_diag_fisher(const kfac_bn_desc *descs, int count, int n_samp
  *     row that is not ignored give NaN for the row, as computed.
  *   - Rows may start at any element boundary and ld may be any value >= vocab.
  *     Rows of logits and dlogits whose starts agree modulo 16 bytes (equal ld
- *     and bases on 16-byte boundaries, for one) are stored 16 bytes at a time.
+ *     and bases on 16-byte boundaries, for one) are the fastest.
  *   - dlogits must not overlap logits.  Every element [row][j < vocab] is
  *     written; elements past the vocabulary are neither read nor written.
  *   - vocab is at most 2^24 and rows at most 2^31 - 1 (UNSUPPORTED beyond).
@@ -382,9 +382,10 @@ kfac_status kfac_bn_diag_fisher(const kfac_bn_desc *descs, int count, int n_samp
 /* kfac_token_logprob -- log-probabilities of the targets (and, where not NULL,
  * lse and H) of every row.  `saved` [rows][2] (NULL: not wanted) receives the
  * row's maximum m = max_j z_j and sum_j exp((z_j - m) / tau) for the gradient (0,
- * 0 for an ignored row); m and the sum stay apart because lse loses the
- * sum's bits where |m| is large, as in a row masked with the lowest value.  Errors: INVALID for null logits/target/logp,
- * rows < 0, vocab < 1, ld < vocab, a bad dtype or tau, saved not on an 8-byte boundary.
+ * 0 for an ignored row); m and the sum stay apart because lse loses the sum's
+ * bits where |m| is large, as in a row masked with the lowest value.
+ * Errors: INVALID for null logits/target/logp, rows < 0, vocab < 1, ld < vocab,
+ * a bad dtype or tau, saved not on an 8-byte boundary.
  * No workspace, no error word.  rows = 0 does nothing. */
 typedef struct {
     int32_t dtype;
@@ -484,8 +485,8 @@ kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *workspace, size
  *     KFAC_PREF_IPO      f = (h - 1 / (2 beta))^2
  *     loss = sum over pairs of v f,   dlogits = grad_scale * dloss / dz,
  * e the label_smoothing (SIGMOID only), v `pair_weight` [pairs] or 1 / pairs.
- * The sums over a sequence and h are formed in fp64.  Rows of no sequence are
- * ignored; offsets as in kfac_policy_loss.
+ * The sums over a sequence are formed in pairs of fp32 words, h in fp64.  Rows
+ * of no sequence are ignored; offsets as in kfac_policy_loss.
  *   - ref_logp [2 pairs], may be NULL (0: no reference).
  *   - loss [1]; pair_loss [pairs] (f), seq_logp [2 pairs] (l) and
  *     token_logp [rows] are optional.  dlogits NULL: the loss only.
@@ -531,8 +532,9 @@ kfac_status kfac_preference_loss(const kfac_preference_desc *desc, void *workspa
  * max_norm = sqrt(kappa) / eta bounds the step's second-order KL change by
  * kappa / 2.
  *   - x: [rows][ld] of dtype (KFAC_BF16, KFAC_F16, KFAC_F32), cols wide; a vector is
- *     one row.  y: [rows][ld_y] of y_dtype, which is dtype or, with x in fp32, any of the
- *     three (fp32 steps and the 16-bit gradients that they come from).  out: [rows][ld_out] of out_dtype; w: [rows][ld_w] fp32.
+ *     one row.  y: [rows][ld_y] of y_dtype, which is dtype or, with x in fp32,
+ *     any of the three (fp32 steps and the 16-bit gradients that they come
+ *     from).  out: [rows][ld_out] of out_dtype; w: [rows][ld_w] fp32.
  *     Any ld >= cols and any element-aligned base; rows that run on without a
  *     gap (ld = cols) or start on 16-byte boundaries are read 16 bytes at a
  *     time.  rows or cols = 0: the tensor adds nothing.

@@ -153,22 +153,26 @@ AddressRangeFn address_range_fn() {
 }
 }  // namespace
 
-bool DeviceMemory::holds(const void *p) {
+bool DeviceMemory::holds(const void *p, int list) {
     if (!p) return true;
     const uintptr_t a = (uintptr_t)p;
-    if (n && a >= seen[last].begin && a < seen[last].end) return true;
-    for (int i = 0; i < n; ++i)
-        if (a >= seen[i].begin && a < seen[i].end) {
-            last = i;
-            return true;
-        }
+    if (last[list].has(a)) return true;
+    Range *at = std::upper_bound(seen, seen + n, a, [](uintptr_t x, const Range &r) { return x < r.end; });
+    if (at < seen + n && at->has(a)) {
+        last[list] = *at;
+        return true;
+    }
     if (!on_this_device(p)) return false;
     CUdeviceptr base = 0;
     size_t size = 0;
     const AddressRangeFn range = address_range_fn();
-    if (n < MOST && range && range(&base, &size, (CUdeviceptr)a) == CUDA_SUCCESS) {
-        last = n;
-        seen[n++] = Range{(uintptr_t)base, (uintptr_t)base + size};
+    if (range && range(&base, &size, (CUdeviceptr)a) == CUDA_SUCCESS) {
+        last[list] = Range{(uintptr_t)base, (uintptr_t)base + size};
+        if (n < MOST) {
+            std::copy_backward(at, seen + n, seen + n + 1);
+            *at = last[list];
+            ++n;
+        }
     }
     return true;
 }

@@ -731,7 +731,7 @@ extern "C" kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, fl
     DeviceMemory memory;
     for (int i = 0; i < count; ++i) {
         const kfac_clip_desc &d = descs[i];
-        if (!memory.holds(d.x) || !memory.holds(d.y) || !memory.holds(d.out) || !memory.holds(d.w))
+        if (!memory.holds(d.x, 0) || !memory.holds(d.y, 1) || !memory.holds(d.out, 2) || !memory.holds(d.w, 3))
             return KFAC_ERR_INVALID;
     }
     if (!all_on_this_device({norm, scale})) return KFAC_ERR_INVALID;

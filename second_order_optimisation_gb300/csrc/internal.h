@@ -174,17 +174,20 @@ bool on_this_device(const void *p);
 bool all_on_this_device(std::initializer_list<const void *> ps);
 // The same test for many pointers of one call: an allocation that has passed is
 // remembered (until the object goes), so that pointers into it are not asked of
-// the driver one by one.
+// the driver one by one.  Arrays of pointers tend to run through their allocations
+// in turn: the last one of each array (`list`) is looked at first.
 class DeviceMemory {
     struct Range {
         uintptr_t begin, end;
+        bool has(uintptr_t a) const { return a >= begin && a < end; }
     };
-    static constexpr int MOST = 16;
-    Range seen[MOST];
-    int n = 0, last = 0;
+    static constexpr int MOST = 256;
+    Range seen[MOST];  // by address
+    Range last[4] = {};
+    int n = 0;
 
 public:
-    bool holds(const void *p);
+    bool holds(const void *p, int list);
 };
 
 // ----------------------------------------------------- inversion
