@@ -30,6 +30,8 @@ namespace {
 
 constexpr int CLIP_FEW = 16, CLIP_MANY = 216;  // tensors of one launch (kernel parameters)
 constexpr int CLIP_THREADS = 256, CLIP_PER_SM = 3, OCTET = 8, SHORT_RUN = 192, TILE = 4096, SMALL_OCTETS = 16384;
+constexpr int CTA_OCTETS = 64;  // a CTA's least share
+constexpr int LINE = 8;         // octets of 16-bit values in 128 bytes
 
 struct ClipJob {
     const char *x, *y;
@@ -634,9 +636,10 @@ struct ClipPlan {
     double *part;
     int parts;
 };
-// CTAs of a launch over `octets`.
+// CTAs of a launch over `octets`.  (144 tensors of 17 or 306 values, with metric and
+// weights, take 14 us of the GPU's time; with 256 octets to a CTA at least, 24.)
 int ctas_of(long long octets) {
-    return (int)std::max<long long>(1, std::min<long long>(device_sm_count() * CLIP_PER_SM, ceil_div(octets, CLIP_THREADS)));
+    return (int)std::max<long long>(1, std::min<long long>(device_sm_count() * CLIP_PER_SM, ceil_div(octets, CTA_OCTETS)));
 }
 int tensors_of(int count) { return count <= CLIP_FEW ? CLIP_FEW : CLIP_MANY; }
 ClipPlan plan_clip(int count, Arena &ws) {
@@ -666,13 +669,16 @@ kfac_status run_clip(const kfac_clip_desc *descs, int count, float max_norm, flo
             if (descs[i].rows == 0 || descs[i].cols == 0) continue;
             ClipJob j = job_from(descs[i], apply);
             j.first = P->octets;
-            P->octets += j.rows * j.per_row;
+            P->octets += (long long)align_up((size_t)(j.rows * j.per_row), LINE);
             P->job[P->n++] = j;
         }
         P->tile = std::max<long long>(1, ceil_div(P->octets, ctas_of(P->octets)));
-        // in the first pass tiles of about TILE octets, the same number for every CTA, in
-        // steps that keep them on memory's boundaries
-        if (!apply) P->tile = (long long)align_up((size_t)ceil_div(P->tile, ceil_div(P->tile, TILE)), 512);
+        // In the first pass tiles of about TILE octets, the same number for every CTA.  Tiles
+        // and tensors begin on memory's lines: 1.0e9 bf16 values take 973 us, 1007 where they
+        // begin anywhere.
+        long long unit = apply ? 64 : 512;
+        while (unit > LINE && unit * 8 > P->tile) unit /= 2;
+        P->tile = (long long)align_up((size_t)(apply ? P->tile : ceil_div(P->tile, ceil_div(P->tile, TILE))), unit);
     };
     if constexpr (MAX == CLIP_FEW) {
         fill(0, true);
