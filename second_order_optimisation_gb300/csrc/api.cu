@@ -138,16 +138,16 @@ bool on_this_device(const void *p) {
 }
 
 namespace {
-typedef CUresult (*AddressRangeFn)(CUdeviceptr *, size_t *, CUdeviceptr);
-AddressRangeFn address_range_fn() {
+typedef CUresult (*PointerAttributesFn)(unsigned, CUpointer_attribute *, void **, CUdeviceptr);
+PointerAttributesFn pointer_attributes_fn() {
     static std::once_flag once;
-    static AddressRangeFn fn = nullptr;
+    static PointerAttributesFn fn = nullptr;
     std::call_once(once, [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        if (cudaGetDriverEntryPointByVersion("cuPointerGetAttributes", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = (AddressRangeFn)p;
+            fn = (PointerAttributesFn)p;
     });
     return fn;
 }
@@ -162,11 +162,20 @@ bool DeviceMemory::holds(const void *p, int list) {
         last[list] = *at;
         return true;
     }
-    if (!on_this_device(p)) return false;
-    CUdeviceptr base = 0;
+    // one question to the driver for the kind of memory and its range
+    unsigned type = 0, managed = 0;
+    int device = -1, current = -1;
+    unsigned long long base = 0;
     size_t size = 0;
-    const AddressRangeFn range = address_range_fn();
-    if (range && range(&base, &size, (CUdeviceptr)a) == CUDA_SUCCESS) {
+    CUpointer_attribute which[] = {CU_POINTER_ATTRIBUTE_MEMORY_TYPE, CU_POINTER_ATTRIBUTE_IS_MANAGED,
+                                   CU_POINTER_ATTRIBUTE_DEVICE_ORDINAL, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR,
+                                   CU_POINTER_ATTRIBUTE_RANGE_SIZE};
+    void *values[] = {&type, &managed, &device, &base, &size};
+    const PointerAttributesFn ask = pointer_attributes_fn();
+    if (!ask || ask(5, which, values, (CUdeviceptr)a) != CUDA_SUCCESS) return on_this_device(p);
+    if (!managed && (type != CU_MEMORYTYPE_DEVICE || cudaGetDevice(&current) != cudaSuccess || device != current))
+        return false;
+    if (base && a >= base && a - base < size) {
         last[list] = Range{(uintptr_t)base, (uintptr_t)base + size};
         if (n < MOST) {
             std::copy_backward(at, seen + n, seen + n + 1);
