@@ -13,12 +13,12 @@
 // whose sum overflows or vanishes in fp32 is summed again from values scaled by
 // a power of two, so that any finite input gives its norm.
 //
-// Measured: 48 tensors of 1.0e9 bf16 values, out on other 16-byte offsets than x: 326 us
-// for the norm (2.0 GB, 6.2 TB/s), 665 for the scaling (4.0 GB, 6.1 TB/s); ResNet-50's 161
+// Measured: 48 tensors of 1.0e9 bf16 values, out on other 16-byte offsets than x: 312 us
+// for the norm (2.0 GB, 6.5 TB/s), 651 for the scaling (4.0 GB, 6.2 TB/s); ResNet-50's 161
 // fp32 tensors with metric and weight step: 45 us (204 MB, 4.5 TB/s) and 49 us (307 MB,
 // 6.2 TB/s), the norm bound by the latency of the many runs that its first tiles hold.
-// 256 threads, three CTAs to an SM: with 512 x 2 the scaling takes 700 us, with 256 x 4
-// 771, with 1024 x 2 924 (fewer streams open at once suit the memory better).
+// 256 threads, three CTAs to an SM: the scaling took 663 us so, 700 by 512 x 2, 771 by
+// 256 x 4, 924 by 1024 x 2 (fewer streams open at once suit the memory better).
 #include <algorithm>
 #include <cmath>
 #include <memory>
@@ -236,7 +236,7 @@ __device__ __noinline__ Wide outer_products(const ClipJob &j, long long lo, long
 // This thread's sum of x y over octets lo .. hi - 1 of a tensor, added to `sum`.
 // A short run, and a long one's ends, are one warp's, the n-th of them the
 // n-th warp's, so that many small tensors go on side by side.  (100 tensors of 11 M
-// fp16 values, with metric steps, take 44 us; with SHORT_RUN = 48 47, with 1024 83.)
+// fp16 values, with their metric, took 44 us; with SHORT_RUN = 48 47, with 1024 83.)
 template <int DT, int YT>
 __device__ __forceinline__ void products(const ClipJob &j, int n, long long lo, long long hi, Wide &sum) {
     const int lane = threadIdx.x % 32;
