@@ -515,8 +515,10 @@ def kfac_bn_diag_fisher(items: Sequence[BnItem], gamma: float, xi: float = 0.0, 
 def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
     """The caller's workspace, or a new one that may be dropped while a call on
     `stream` (an own stream, or None) still uses it."""
+    if workspace is None and stream is None:
+        return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=device)
     ws = _workspace(nbytes, device, workspace)
-    if workspace is None and stream is not None:
+    if workspace is None:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(_stream(stream), device=device)
         ws.record_stream(stream)
@@ -536,27 +538,30 @@ def _rowvec(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.float32) -
 
 def _logits_args(logits: torch.Tensor, target: torch.Tensor, temperature: float):
     """The descriptor fields from dtype to temperature, the same for every call on logits."""
-    if logits.dtype not in _DTYPES:
+    dtype, tdtype = _DTYPES.get(logits.dtype), target.dtype
+    if dtype is None:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
-    if target.dtype is not torch.int64 and target.dtype is not torch.int32:
-        raise TypeError(f"target must be int64 or int32, got {target.dtype}")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if tdtype is not torch.int64 and tdtype is not torch.int32:
+        raise TypeError(f"target must be int64 or int32, got {tdtype}")
+    shape, stride = logits.shape, logits.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("logits must be [rows, vocab] with unit column stride")
-    rows, vocab = logits.shape
+    rows, vocab = shape
     if target.numel() != rows or not target.is_contiguous():
         raise ValueError(f"target must be {rows} dense values, got shape {tuple(target.shape)}")
-    return (_DTYPES[logits.dtype], logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, rows, vocab,
-            target.data_ptr(), int(target.dtype is torch.int32), temperature)
+    return (dtype, logits.data_ptr(), stride[0] if rows > 1 else vocab, rows, vocab,
+            target.data_ptr(), tdtype is torch.int32, temperature)
 
 
 def _dlogits_args(logits: torch.Tensor, dlogits: Optional[torch.Tensor]):
     if dlogits is None:
         return None, 0
-    if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
+    shape, stride = dlogits.shape, dlogits.stride()
+    if dlogits.dtype is not logits.dtype or shape != logits.shape:
         raise TypeError("dlogits must have the logits' shape and dtype")
-    if dlogits.shape[1] > 1 and dlogits.stride(1) != 1:
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError("dlogits must have unit column stride")
-    return dlogits.data_ptr(), dlogits.stride(0) if dlogits.shape[0] > 1 else dlogits.shape[1]
+    return dlogits.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
 @dataclass
@@ -655,8 +660,7 @@ def kfac_policy_loss(item: PolicyLoss, workspace: Optional[torch.Tensor] = None,
     d = _policy_desc(item)
     p = ctypes.byref(d)
     ws = _scratch(lib.kfac_policy_loss_workspace_size(p), item.logits.device, workspace, stream)
-    _check(lib.kfac_policy_loss(p, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
-           "kfac_policy_loss")
+    _check(lib.kfac_policy_loss(p, ws.data_ptr(), ws.nbytes, _stream(stream)), "kfac_policy_loss")
     return ws
 
 
@@ -713,8 +717,7 @@ def kfac_preference_loss(item: PreferenceLoss, workspace: Optional[torch.Tensor]
     d = _preference_desc(item)
     p = ctypes.byref(d)
     ws = _scratch(lib.kfac_preference_loss_workspace_size(p), item.logits.device, workspace, stream)
-    _check(lib.kfac_preference_loss(p, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)),
-           "kfac_preference_loss")
+    _check(lib.kfac_preference_loss(p, ws.data_ptr(), ws.nbytes, _stream(stream)), "kfac_preference_loss")
     return ws
 
 
@@ -781,6 +784,6 @@ def kfac_clip_norm(tensors, max_norm: float, norm: Optional[torch.Tensor] = None
     c = tensors if isinstance(tensors, ClipList) else ClipList(tensors)
     ws = _scratch(c.need, c.device, workspace, stream)
     _check(load().kfac_clip_norm(c.descs, len(c.tensors), max_norm, eta, _rowvec(norm, 1, "norm"),
-                                 _rowvec(scale, 1, "scale"), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                 _stream(stream)), "kfac_clip_norm")
+                                 _rowvec(scale, 1, "scale"), ws.data_ptr(), ws.nbytes, _stream(stream)),
+           "kfac_clip_norm")
     return ws
