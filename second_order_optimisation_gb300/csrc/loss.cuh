@@ -527,7 +527,8 @@ __device__ __forceinline__ void store_part(const float4 *local, int rank, float4
 // lanes share a row's fixed work, about 600 instructions, among more rows.  A call for
 // the log-probabilities of 16000 x 2100 bf16 (67 MB) takes 22 us (26 by 32 lanes always,
 // 55 by a CTA to a row), the policy loss of 16000 x 2040 57 us (131 MB) and of 8000 x 4096
-// 47: bound by the latency of the two passes over a row and of their reductions.
+// 47: bound by the latency of the two passes over a row and of their reductions.  CTAs of
+// 128 threads take the same, of 64 threads 6 to 10 us more with the gradient.
 constexpr int WARP_GROUPS = 1024, WARP_GRAD_GROUPS = 512, WARP_SHORT = 64, WARP_THREADS = 256, WARP_PER_SM = 4;
 template <int DT, bool ENT, int L>
 __global__ void __launch_bounds__(WARP_THREADS, WARP_PER_SM) warp_rows_kernel(const __grid_constant__ RowParams P) {

@@ -146,6 +146,25 @@ def test_more_tensors_than_one_launch_takes():
     check(ts, 1.5)
 
 
+def test_many_allocations_and_memory_elsewhere():
+    """Tensors in more allocations than a call remembers, in no order; host memory among them is refused."""
+    g = torch.Generator().manual_seed(12)
+    room = [torch.empty(2_700_000, device=DEV) for _ in range(290)]
+    ts = []
+    for k in torch.randperm(290, generator=g).tolist():
+        x = room[k][k % 5:k % 5 + 90 + k]
+        x.copy_(torch.randn(90 + k, generator=g))
+        ts.append(kfac.ClipTensor(x, room[(k * 7) % 290][5000:5090 + k]))
+    check(ts, 2.0)
+    for at in (0, 150, 289):
+        bad = list(ts)
+        bad[at] = kfac.ClipTensor(torch.zeros(50), torch.zeros(50))
+        norm = torch.full((1,), 7.0, device=DEV)
+        with pytest.raises(kfac.KfacError):
+            kfac.kfac_clip_norm(bad, 2.0, norm)
+        assert float(norm) == 7.0
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-24, 1e-10, 1e10, 1e25, 1e36])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("metric", [False, True])

@@ -231,6 +231,13 @@ def test_policy_weights_and_terms(rows, vocab, mode, kl, ent):
     _policy("bf16", rows, vocab, kl=kl, ent=ent, mode=mode, outputs=mode != "token", seed=3)
 
 
+@pytest.mark.parametrize("rows,vocab,dtype", [(20001, 18, "f32"), (4703, 5003, "bf16")])
+@pytest.mark.parametrize("mode", ["token", "weight", "seq_token", "seq_mean"])
+def test_policy_many_rows(rows, vocab, dtype, mode):
+    """More rows than one pass over their table takes, in order (the second) and not."""
+    _policy(dtype, rows, vocab, mode=mode, seed=5)
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("vocab", [5, 31, 1000, 33000, 50001])
 @pytest.mark.parametrize("pad,shift,same", [(3, 1, True), (0, 0, False), (8, 4, True), (1, 3, False)])
