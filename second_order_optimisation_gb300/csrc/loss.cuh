@@ -628,10 +628,10 @@ __device__ __forceinline__ Part join_parts(const float4 *parts, int n, float k) 
 
 // Statistics only: one row to a CTA or, where there are few rows, to a cluster
 // of cs CTAs, each with a run of the row's groups.  Small CTAs, eight to an SM: the
-// time from a row's first load to its last sum, about 4 us beside the loads, is then
-// some other row's loading time.  12000 x 128000 bf16 (2.15 GB live) takes 328 us, 6.6 TB/s;
+// time between a row's last load and the next one's first is then some other row's
+// loading time.  12000 x 128000 bf16 (2.15 GB live) takes 328 us, 6.6 TB/s;
 // 4099 x 50001 fp16 (410 MB) 73 us, 5.6 TB/s.  256 threads, six to an SM, take 8% more at
-// 6000 x 32000 and the same elsewhere within 3%; four to an SM up to 6% more, batches of two
+// 6000 x 32000 and the same elsewhere within 3%; four to an SM up to 10% more, batches of two
 // groups up to 15% more.  The rows through a shared-memory ring took 104 us in place of 73.
 constexpr int STREAM_THREADS = 128, STREAM_PER_SM = 8, BATCH = 4;
 template <int DT, bool ENT>
@@ -1002,7 +1002,7 @@ struct GradParams {
 // The gradient from saved statistics: one read of the logits, one write, no reduction
 // and no barrier.  T threads of a block of THREADS to a row: all of them, or fewer where
 // rows are short.  Rows are taken from the last: the statistics' launch has left the last
-// of the logits in the L2 cache (of 5.2 GB that is little, of 384 MB about a third).
+// of the logits in the L2 cache (126 MB at most).
 // 12000 x 128000 bf16 (5.2 GB, 30% of the rows zeros) takes 770 us, 6.8 TB/s; 6000 x 32000
 // with an entropy's gradient (730 MB) 110 us, 6.6 TB/s.
 template <int DT, bool ENT, int T>
