@@ -26,6 +26,7 @@
 #include <cmath>
 
 #include "logits.cuh"
+#include "ring.h"
 
 namespace kfac {
 namespace loss {
@@ -784,21 +785,26 @@ __device__ __noinline__ Sums<DT, ENT> stage_sums_slow(const uint4 *stage, int t,
     return stage_sums<DT, ENT, false, TEAM>(stage, t, G, h);
 }
 
-// Waits for the stage that holds the cluster's row n.  The stage's last use may
-// have been the other team's, its copy still under way; the barrier's parity tells
-// one use from the next only once the stage has been given to row n.
+// A stage as a thread of a team waits for it (wait_stage).  The row's number is
+// released by the thread that has given the stage to it and acquired here, so that
+// the barrier's state that is looked at next is no older.
 template <class Shared>
-__device__ __forceinline__ bool wait_stage(Shared &sh, int st, long long n, int parity) {
-    const volatile long long *given = &sh.given[st];
-    if (!mbar_wait(&sh.full[st], parity)) return false;
-    if (*given != n) {
-        const uint64_t t0 = global_timer_ns();
-        while (*given != n)
-            if (global_timer_ns() - t0 > 2000000000ull) return false;
-        if (!mbar_wait(&sh.full[st], parity)) return false;
+struct StageWait {
+    Shared &sh;
+    int st;
+    uint64_t t0;
+    __device__ __forceinline__ long long given() const {
+        long long n;
+        asm volatile("ld.acquire.cta.shared::cta.b64 %0, [%1];" : "=l"(n) : "r"(smem_u32(&sh.given[st])) : "memory");
+        return n;
     }
-    return true;
-}
+    __device__ __forceinline__ void give(long long n) const {
+        asm volatile("st.release.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&sh.given[st])), "l"(n) : "memory");
+    }
+    __device__ __forceinline__ void start() { t0 = global_timer_ns(); }
+    __device__ __forceinline__ bool late() const { return global_timer_ns() - t0 > 2000000000ull; }
+    __device__ __forceinline__ bool wait_full(int parity) const { return mbar_wait(&sh.full[st], parity); }
+};
 
 template <int DT, bool ENT, int TEAMS>
 __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid_constant__ RowParams P, int cs, int stages,
@@ -878,7 +884,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                         bulk_load(ring + (size_t)st * stage_bytes, r.base + (size_t)c0 * 16, (uint32_t)(g1 - c0) * 16,
                                   &sh.full[st]);
                     sh.row[st] = mine;
-                    *(volatile long long *)&sh.given[st] = n;
+                    StageWait<RingShared<TEAMS>>{sh, st, 0}.give(n);
                     if (loads) mbar_arrive_expect_tx(&sh.full[st], (uint32_t)(g1 - c0) * 16);
                     else mbar_arrive(&sh.full[st]);
                 }
@@ -895,7 +901,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         for (long long n = team; n < count; n += TEAMS) {
             const int st = (int)(n % stages);
             // A wait that runs out is noted, and the team leaves after its next barrier.
-            if (!wait_stage(sh, st, n, (int)(n / stages & 1))) {
+            StageWait<RingShared<TEAMS>> wait{sh, st, 0};
+            if (!wait_stage(wait, n, stages)) {
                 if (t % 32 == 0) atomicOr(P.err, ERR_TIMEOUT_FULL);
                 *(volatile int *)&sh.dead = 1;
             }
