@@ -722,11 +722,13 @@ __global__ void __launch_bounds__(STREAM_THREADS, STREAM_PER_SM) stream_rows_ker
 constexpr int TEAM_THREADS = 512, RING_THREADS = TEAM_THREADS + 32, MAX_STAGES = 16;
 constexpr int RING_BYTES = 221184;  // of shared memory for the stages: three of 4608 groups
 
-struct __align__(16) StageRow {
+struct __align__(16) StageInputs {
     PolicyRow q;
-    uint4 edge[2];  // the groups before and behind the whole ones (of the cluster's first CTA)
     int row;
     float ref, z_t;
+};
+struct StageRow : StageInputs {
+    uint4 edge[2];  // the groups before and behind the whole ones (of the cluster's first CTA)
 };
 template <int TEAMS>
 struct RingShared {
@@ -804,6 +806,8 @@ struct StageWait {
     __device__ __forceinline__ void start() { t0 = global_timer_ns(); }
     __device__ __forceinline__ bool late() const { return global_timer_ns() - t0 > 2000000000ull; }
     __device__ __forceinline__ bool wait_full(int parity) const { return mbar_wait(&sh.full[st], parity); }
+    __device__ __forceinline__ bool all(bool ok) const { return __all_sync(ALL_LANES, ok); }
+    __device__ __forceinline__ StageInputs row() const { return sh.row[st]; }
 };
 
 template <int DT, bool ENT, int TEAMS>
@@ -900,16 +904,20 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         int turn = 0;  // counts the team's rows that are not ignored
         for (long long n = team; n < count; n += TEAMS) {
             const int st = (int)(n % stages);
-            // A wait that runs out is noted, and the team leaves after its next barrier.
+            // A wait that runs out is noted, and the warp goes to the team's next barrier, after
+            // which the whole team leaves.
             StageWait<RingShared<TEAMS>> wait{sh, st, 0};
-            if (!wait_stage(wait, n, stages)) {
+            StageInputs in;
+            if (!take_row(wait, n, stages, in)) {
                 if (t % 32 == 0) atomicOr(P.err, ERR_TIMEOUT_FULL);
                 *(volatile int *)&sh.dead = 1;
+                team_any<TEAM>(team, true);
+                break;
             }
             const StageRow &at_stage = sh.row[st];
-            const PolicyRow q = at_stage.q;
-            const float ref = at_stage.ref, z_t = at_stage.z_t;
-            const long long row = at_stage.row;
+            const PolicyRow q = in.q;
+            const float ref = in.ref, z_t = in.z_t;
+            const long long row = in.row;
             char *out = P.dlogits + row * P.ld_d_bytes;
             const char *z = P.in.logits + row * P.in.ld_bytes;
             if (q.target < 0) {
@@ -944,16 +952,17 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                           make_float4(mine.m, mine.s, mine.t, 0.f));
             if (t < 32) {
                 if (t == 0) mbar_arrive_expect_tx(&sh.joined[team][b], cs * TEAM_WARPS * 16);
-                if (!mbar_wait(&sh.joined[team][b], turn >> 1 & 1)) {
+                if (__all_sync(ALL_LANES, mbar_wait(&sh.joined[team][b], turn >> 1 & 1))) {
+                    const Part all = join_parts<ENT>(sh.parts[team][b], cs * TEAM_WARPS, k);
+                    Terms terms{};
+                    const Coef c = finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && t == 0, terms);
+                    if (t == 0) {
+                        sh.coef[team][b] = c;
+                        sh.sums[team].add(terms);
+                    }
+                } else {  // (the parts are not all there)
                     if (t == 0) atomicOr(P.err, ERR_TIMEOUT_ACC);
                     *(volatile int *)&sh.dead = 1;
-                }
-                const Part all = join_parts<ENT>(sh.parts[team][b], cs * TEAM_WARPS, k);
-                Terms terms{};
-                const Coef c = finish_row<ENT>(P, row, q, ref, all, z_t, rank == 0 && t == 0, terms);
-                if (t == 0) {
-                    sh.coef[team][b] = c;
-                    sh.sums[team].add(terms);
                 }
             }
             ++turn;

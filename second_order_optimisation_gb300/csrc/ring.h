@@ -36,5 +36,16 @@ KFAC_RING_FN bool wait_stage(Stage &s, long long n, int stages) {
     return s.wait_full(stage_parity(n, stages));
 }
 
+// Row n's inputs besides its logits, into `row`, once the stage holds it.  False when
+// the wait ran out for any thread of the warp: `row` is then as it was, and nothing of
+// the stage (whose row may be another one, or none yet) may be used, so that no address
+// is ever made from it.
+template <class Stage, class Row>
+KFAC_RING_FN bool take_row(Stage &s, long long n, int stages, Row &row) {
+    if (!s.all(wait_stage(s, n, stages))) return false;
+    row = s.row();
+    return true;
+}
+
 }  // namespace loss
 }  // namespace kfac

@@ -57,6 +57,14 @@ struct Stage {
         ++event;
         return false;
     }
+    // the warp's other threads: `others` says whether their waits ended
+    bool others = true;
+    int reads = 0;
+    bool all(bool ok) const { return ok && others; }
+    long long row() {
+        ++reads;
+        return event >= GIVEN ? n : -1000;  // (what stands there before is another row's, or nothing's)
+    }
 };
 
 int failures = 0;
@@ -80,6 +88,17 @@ int main() {
                         const bool held = kfac::loss::wait_stage(s, n, stages);
                         check(!held || s.event >= LANDED, "returned before the row had landed", n, stages, begin, last);
                         check(held || last < LANDED, "gave up although the row landed", n, stages, begin, last);
+                        ++paths;
+                    } while (c.next());
+                    c = Choices{};
+                    do {
+                        c.at = 0;
+                        Stage s{c, n, stages, begin, last};
+                        s.others = c.pick(2) == 0;
+                        long long row = -7;
+                        const bool held = kfac::loss::take_row(s, n, stages, row);
+                        check(held || (s.reads == 0 && row == -7), "used a stage whose wait ran out", n, stages, begin, last);
+                        check(!held || (row == n && s.others), "went on without the row", n, stages, begin, last);
                         ++paths;
                     } while (c.next());
                 }
