@@ -794,7 +794,7 @@ template <class Shared>
 struct StageWait {
     Shared &sh;
     int st;
-    uint64_t t0;
+    uint64_t limit_ns = 2000000000ull, t0 = 0;
     __device__ __forceinline__ long long given() const {
         long long n;
         asm volatile("ld.acquire.cta.shared::cta.b64 %0, [%1];" : "=l"(n) : "r"(smem_u32(&sh.given[st])) : "memory");
@@ -804,8 +804,8 @@ struct StageWait {
         asm volatile("st.release.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&sh.given[st])), "l"(n) : "memory");
     }
     __device__ __forceinline__ void start() { t0 = global_timer_ns(); }
-    __device__ __forceinline__ bool late() const { return global_timer_ns() - t0 > 2000000000ull; }
-    __device__ __forceinline__ bool wait_full(int parity) const { return mbar_wait(&sh.full[st], parity); }
+    __device__ __forceinline__ bool late() const { return global_timer_ns() - t0 > limit_ns; }
+    __device__ __forceinline__ bool wait_full(int parity) const { return mbar_wait(&sh.full[st], parity, limit_ns); }
     __device__ __forceinline__ bool all(bool ok) const { return __all_sync(ALL_LANES, ok); }
     __device__ __forceinline__ StageInputs row() const { return sh.row[st]; }
 };
@@ -888,7 +888,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
                         bulk_load(ring + (size_t)st * stage_bytes, r.base + (size_t)c0 * 16, (uint32_t)(g1 - c0) * 16,
                                   &sh.full[st]);
                     sh.row[st] = mine;
-                    StageWait<RingShared<TEAMS>>{sh, st, 0}.give(n);
+                    StageWait<RingShared<TEAMS>>{sh, st}.give(n);
                     if (loads) mbar_arrive_expect_tx(&sh.full[st], (uint32_t)(g1 - c0) * 16);
                     else mbar_arrive(&sh.full[st]);
                 }
@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             const int st = (int)(n % stages);
             // A wait that runs out is noted, and the warp goes to the team's next barrier, after
             // which the whole team leaves.
-            StageWait<RingShared<TEAMS>> wait{sh, st, 0};
+            StageWait<RingShared<TEAMS>> wait{sh, st};
             StageInputs in;
             if (!take_row(wait, n, stages, in)) {
                 if (t % 32 == 0) atomicOr(P.err, ERR_TIMEOUT_FULL);
@@ -990,11 +990,18 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
         }
     }
     __syncthreads();
-    if (sh.dead && tid == 0)  // copies in flight land before the CTA leaves
-        for (int i = 0; i < stages; ++i)
-            if (!mbar_wait(&sh.full[i], 0, 100000000ull)) mbar_wait(&sh.full[i], 1, 100000000ull);
+    const bool dead = sh.dead != 0;
+    if (dead && tid == 0)  // copies in flight land before the CTA leaves
+        for (int i = 0; i < stages; ++i) {
+            StageWait<RingShared<TEAMS>> wait{sh, i, 100000000ull};
+            drain_stage(wait, stages);
+        }
     // no CTA leaves while others may still write into its shared memory
     cluster_sync();
+    if (dead && tid == 0) {  // (parts that were sent here and that no wait has seen: far less than 1 ms)
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {}
+    }
     if (rank != 0) return;
     TermSums sums = sh.sums[0];
     for (int i = 1; i < TEAMS; ++i) sums.add(sh.sums[i]);

@@ -47,5 +47,14 @@ KFAC_RING_FN bool take_row(Stage &s, long long n, int stages, Row &row) {
     return true;
 }
 
+// Waits until nothing is on its way into the stage any more: the phase of the row that
+// it was given to last is complete.  (A wait on the other parity passes at once while
+// that row's bytes are still coming.)
+template <class Stage>
+KFAC_RING_FN bool drain_stage(Stage &s, int stages) {
+    const long long n = s.given();
+    return n < 0 || s.wait_full(stage_parity(n, stages));
+}
+
 }  // namespace loss
 }  // namespace kfac

@@ -102,6 +102,19 @@ int main() {
                         ++paths;
                     } while (c.next());
                 }
+    // The end of a run, after which no row is given to the stage: row n, or none, was the last.
+    for (int stages = 2; stages <= 4; ++stages)
+        for (long long n = 0; n < 4 * stages; ++n)
+            for (int begin : {(int)CONSUMED, (int)GIVEN, (int)LANDED}) {
+                Choices c;
+                do {
+                    c.at = 0;
+                    Stage s{c, n, stages, begin, begin == CONSUMED ? CONSUMED : LANDED};
+                    const bool drained = kfac::loss::drain_stage(s, stages);
+                    check(drained && s.event == s.last, "left with bytes on their way", n, stages, begin, s.last);
+                    ++paths;
+                } while (c.next());
+            }
     std::printf("%lld orders, %d failures\n", paths, failures);
     return failures != 0;
 }
