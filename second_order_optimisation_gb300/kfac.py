@@ -230,10 +230,7 @@ def timing_read_launches(n: int = 65536) -> list:
     sm = (ctypes.c_ulonglong * n)()
     cnt = lib.kfac_timing_read_launches(st, du, kd, sm, n)
     if cnt < 0:
-        raise KfacError(KFAC_ERR_CUDA, "kfac_timing_read_launches",
-           "kfac_token_logprob", "kfac_token_logprob_grad", "kfac_policy_loss_workspace_size", "kfac_policy_loss",
-           "kfac_preference_loss_workspace_size", "kfac_preference_loss", "kfac_clip_norm_workspace_size",
-           "kfac_clip_norm")
+        raise KfacError(KFAC_ERR_CUDA, "kfac_timing_read_launches")
     ids = {}
     return [(st[i], du[i], lib.kfac_timing_kind_name(kd[i]).decode(), ids.setdefault(sm[i], len(ids)))
             for i in range(min(cnt, n))]
