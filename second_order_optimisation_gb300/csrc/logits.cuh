@@ -129,10 +129,10 @@ struct Elem<KFAC_F32> {
         return fmaxf(a.x, a.y);
     }
     static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
-        asm("max.NaN.f32 %0, %0, 0fF0000000;" : "+r"(v));  // -1.6e29
+        asm("max.NaN.f32 %0, %0, 0fF0000000;" : "+r"(v));  // BOUND
         return v;
     }
-    static constexpr float M_MIN = -F32_MAX;
+    static constexpr float BOUND = -0x1p97f;  // -1.6e29
     static __device__ __forceinline__ uint4 bounded(uint4 u) {
         return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
     }
@@ -156,10 +156,10 @@ struct Elem<KFAC_BF16> {
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xff7fff7fu); }
     static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
-        const two b = __hmax2_nan(as_two(v), as_two(0xf000f000u));  // -1.6e29
+        const two b = __hmax2_nan(as_two(v), as_two(0xf000f000u));  // BOUND
         return *reinterpret_cast<const uint32_t *>(&b);
     }
-    static constexpr float M_MIN = -F32_MAX;
+    static constexpr float BOUND = -0x1p97f;  // -1.6e29
     static __device__ __forceinline__ uint4 bounded(uint4 u) {
         return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
     }
@@ -193,10 +193,10 @@ struct Elem<KFAC_F16> {
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xfbfffbffu); }
     static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
-        const two b = __hmax2_nan(as_two(v), as_two(0xfbfffbffu));  // the lowest finite value
+        const two b = __hmax2_nan(as_two(v), as_two(0xfbfffbffu));  // BOUND
         return *reinterpret_cast<const uint32_t *>(&b);
     }
-    static constexpr float M_MIN = -32768.f;  // the bound is far below a larger maximum
+    static constexpr float BOUND = -65504.f;  // the lowest finite value
     static __device__ __forceinline__ uint4 bounded(uint4 u) {
         return make_uint4(bounded1(u.x), bounded1(u.y), bounded1(u.z), bounded1(u.w));
     }
@@ -350,12 +350,12 @@ __device__ __forceinline__ void unpack_pairs(uint4 u, f2 *v) {
 // result's own rounding, and for delta = m k - c, which is the same for the whole
 // row and is put back into the sums (2^y (z) = 2^-delta 2^(z k - c)).  `ok` is false
 // where m k is so large that c or delta would be (rows at the type's lowest value):
-// then the difference is formed before the product.  (m_min: Elem::M_MIN.)
+// then the difference is formed before the product.
 struct Shift {
     float m, k, c, delta;
     bool ok;
-    __device__ __forceinline__ Shift(float m_, float k_, float m_min) : m(m_), k(k_), c(m_ * k_) {
-        ok = fabsf(c) < 1048576.f && m >= m_min;
+    __device__ __forceinline__ Shift(float m_, float k_, bool allowed) : m(m_), k(k_), c(m_ * k_) {
+        ok = allowed && fabsf(c) < 1048576.f;
         delta = ok ? fmaf(m, k, -c) : 0.f;
     }
     template <bool FAST>
@@ -364,13 +364,24 @@ struct Shift {
     }
 };
 
+// With an entropy the fast form multiplies 2^y with y (and, in a gradient, with a factor
+// b), and logits of -inf are raised to Elem::BOUND first, so that 0 is not multiplied with
+// -inf.  That needs 2^y = 0 at the bound (y below -150: not so where the temperature, or
+// the row's maximum, is near the bound's size) and a finite b y there (not so for a very
+// small temperature); elsewhere the other form bounds y itself.
+template <int DT, bool ENT>
+__device__ __forceinline__ Shift shift_of(float m, float k, float b = 0.f) {
+    const float far = (m - Elem<DT>::BOUND) * k;
+    return Shift(m, k, !ENT || (far > 200.f && far * fmaxf(1.f, fabsf(b)) < 1e37f));
+}
+
 // Sums over groups whose maximum is at most the shift's.  A thread adds few
 // groups, each summed as a tree first; a long run of groups takes Sum2's way.
 template <int DT, bool ENT>
 struct Sums {
     f2 s, t;
     __device__ __forceinline__ Sums() : s(pair(0.f, 0.f)), t(s) {}
-    // (a logit below the bound has 2^y = 0 in the FAST form, where |m k| is small; its y must stay finite)
+    // (in the FAST form a logit at the bound or below has 2^y = 0, and its y must stay finite: shift_of)
     template <bool FAST>
     __device__ __forceinline__ f2 group(uint4 u, const Shift &h) {
         constexpr int H = Elem<DT>::N / 2;
@@ -425,7 +436,7 @@ struct Running {
         for (int i = 0; i < VPT; ++i)
             if (i < count) best = Elem<DT>::raise(best, u[i]);
         raise(Elem<DT>::largest(best));
-        const Shift h(m, k, Elem<DT>::M_MIN);
+        const Shift h = shift_of<DT, ENT>(m, k);
         Sums<DT, ENT> batch;
         if (h.ok) {
 #pragma unroll

@@ -185,7 +185,7 @@ __device__ __noinline__ void grad_groups_slow(const char *z, char *out, int n, i
 template <int DT, bool ENT>
 __device__ __forceinline__ void grad_row(const char *z, char *out, int n, int tgt, float z_t, const Coef &c, float k,
                                          int tid, int nt) {
-    const Shift h(c.m, k, Elem<DT>::M_MIN);
+    const Shift h = shift_of<DT, ENT>(c.m, k, c.b);
     const float d_t = grad_target<ENT>(z_t, c, k);
     if (h.ok && (((uintptr_t)out ^ (uintptr_t)z) & 15) == 0)
         grad_groups<DT, ENT, true, false>(z, out, n, tgt, shifted(c, h), d_t, h, tid, nt);
@@ -461,7 +461,7 @@ __device__ __forceinline__ void write_gradient(const Kept<DT, VPT> &kept, const 
         zero_row<DT>(out, r.n, tid, nt);
         return;
     }
-    const Shift h(c.m, k, Elem<DT>::M_MIN);
+    const Shift h = shift_of<DT, ENT>(c.m, k, c.b);
     if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
         grad_row<DT, ENT>(z, out, r.n, target, z_t, c, k, tid, nt);
         return;
@@ -507,7 +507,7 @@ __device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, boo
     kept.load(r, r.begin() + lane, L, live ? r.end() : 0, most,
               !live ? -1 : lane == 0 && r.has_front() ? 0 : lane == 1 && r.has_back() ? r.end() : -1);
     const float z_t = live ? logit_at<DT>(z, q.target) : 0.f, ref = live && P.ref_logp ? P.ref_logp[row] : 0.f;
-    const Shift h(lanes_max(kept.largest(r, most), L), P.in.k, Elem<DT>::M_MIN);
+    const Shift h = shift_of<DT, ENT>(lanes_max(kept.largest(r, most), L), P.in.k);
     const Part p = kept.template sums<ENT>(r, h, most, true).part(h, L);
     char *out = P.dlogits ? P.dlogits + (in ? row : 0) * P.ld_d_bytes : nullptr;
     Terms terms{};
@@ -947,7 +947,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             auto best = Elem<DT>::raise(Elem<DT>::lowest(), edge);
 #pragma unroll 4
             for (int g = t; g < G; g += TEAM) best = Elem<DT>::raise(best, stage[g]);
-            const Shift hw(lanes_max(Elem<DT>::largest(best), 32), k, Elem<DT>::M_MIN);
+            const Shift hw = shift_of<DT, ENT>(lanes_max(Elem<DT>::largest(best), 32), k);
             Sums<DT, ENT> sums = hw.ok ? stage_sums<DT, ENT, true, TEAM>(stage, t, G, hw)
                                             : stage_sums_slow<DT, ENT, TEAM>(stage, t, G, hw);
             if (at >= 0) {
@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) ring_rows_kernel(const __grid
             ++turn;
             if (team_any<TEAM>(team, *(volatile int *)&sh.dead != 0)) break;
             const Coef c = sh.coef[team][b];
-            const Shift h(c.m, k, Elem<DT>::M_MIN);
+            const Shift h = shift_of<DT, ENT>(c.m, k, c.b);
             if (c.none) {
                 zero_row<DT>(out, P.in.vocab, rank * TEAM + t, cs * TEAM);
             } else if (!h.ok || (((uintptr_t)out ^ (uintptr_t)z) & 15) != 0) {
