@@ -375,7 +375,8 @@ kfac_status kfac_bn_diag_fisher(const kfac_bn_desc *descs, int count, int n_samp
  *   - dlogits must not overlap logits.  Every element [row][j < vocab] is
  *     written; elements past the vocabulary are neither read nor written.
  *   - vocab is at most 2^24 and rows at most 2^31 - 1 (UNSUPPORTED beyond).
- *   - tau must be positive and finite.
+ *   - tau must be positive and finite, and so must log2(e) / tau in fp32 (tau at
+ *     least 4.3e-39).
  * Results are bitwise reproducible run to run.
  * ==================================================================== */
 

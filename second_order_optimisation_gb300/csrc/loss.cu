@@ -127,7 +127,8 @@ kfac_status check_logits(int dtype, const void *logits, long long ld, long long 
     if (dtype != KFAC_BF16 && dtype != KFAC_F16 && dtype != KFAC_F32) return KFAC_ERR_INVALID;
     if (rows < 0 || vocab < 1 || ld < vocab || (rows > 0 && (!logits || !target))) return KFAC_ERR_INVALID;
     if ((uintptr_t)logits % elem_size(dtype)) return KFAC_ERR_INVALID;
-    if (!(tau > 0.f) || !std::isfinite(tau)) return KFAC_ERR_INVALID;
+    // (below about 4.2e-39 the factor of the exponents is infinite)
+    if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(LOG2E / tau)) return KFAC_ERR_INVALID;
     if (vocab > (1 << 24) || rows > 0x7fffffffLL) return KFAC_ERR_UNSUPPORTED;
     return KFAC_OK;
 }
