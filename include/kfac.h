@@ -447,8 +447,9 @@ kfac_status kfac_token_logprob_grad(const kfac_logprob_grad_desc *desc, void *st
  *   - logp, kl, entropy: [rows], optional.  dlogits NULL: the loss only.
  * Error word (first int32 of the workspace): KFAC_ERRW_TARGET, and
  * KFAC_ERRW_NONFINITE when a counted row's logp, loss term or gradient
- * coefficient, or the loss, is NaN or infinite (a gradient that overflows
- * fp16 as it is rounded does not set it).
+ * coefficient (with grad_scale / tau, where dlogits is given), or the loss, is
+ * NaN or infinite (a gradient that overflows fp16 as it is rounded does not set
+ * it).
  * Errors: INVALID for null logits/target/advantage/old_logp/stats, rows < 0, vocab < 1,
  *   ld or ld_d < vocab, clip_low or clip_high negative or NaN, a coefficient that is not
  *   finite, seqs < 1 with seq_offsets, seq_mean without seq_offsets or with weight,
@@ -491,7 +492,9 @@ kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *workspace, size
  *   - ref_logp [2 pairs], may be NULL (0: no reference).
  *   - loss [1]; pair_loss [pairs] (f), seq_logp [2 pairs] (l) and
  *     token_logp [rows] are optional.  dlogits NULL: the loss only.
- * Error word: as kfac_policy_loss (logp of a counted row, l, f, the loss).
+ * Error word: as kfac_policy_loss (logp of a counted row, l, f, the loss, and
+ * where dlogits is given the gradient coefficients of sequences with counted
+ * rows).
  * Errors: INVALID for null logits/target/seq_offsets/loss, rows < 0, pairs < 1,
  *   vocab < 1, ld or ld_d < vocab, an unknown kind, beta not positive and
  *   finite, label_smoothing outside [0, 1) or with another kind, a grad_scale

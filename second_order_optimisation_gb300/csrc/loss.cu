@@ -296,7 +296,7 @@ extern "C" kfac_status kfac_policy_loss(const kfac_policy_desc *desc, void *work
     PolicyRows R{in, d.rows, d.weight, d.advantage, d.old_logp, d.seq_offsets, d.seqs, d.seq_mean, p.meta,
                  p.order, p.done, p.err};
     const bool kept = rows_kept(d), ent = d.entropy_coef != 0.f || d.entropy;
-    const float scale = d.grad_scale / d.temperature;
+    const float scale = d.dlogits ? d.grad_scale / d.temperature : 1.f;
     RowParams P{};
     P.in = in;
     P.rows = d.rows;
@@ -364,7 +364,7 @@ extern "C" kfac_status kfac_preference_loss(const kfac_preference_desc *desc, vo
     P.scale = d.grad_scale / d.temperature;
     P.ld_d_bytes = d.ld_d * (long long)elem_size(d.dtype);
     PrefPairs Q{d.target, d.target_i32, d.vocab, d.rows, d.seq_offsets, d.pairs, d.ref_logp, d.pair_weight, d.kind,
-                d.average, d.beta, d.label_smoothing, logp, p.ms, p.row_g, p.terms, p.bad, d.pair_loss, d.seq_logp};
+                d.average, d.beta, d.label_smoothing, d.dlogits ? P.scale : 0.f, logp, p.ms, p.row_g, p.terms, p.bad, d.pair_loss, d.seq_logp};
     PrefSum U{p.terms, p.bad, d.pairs, d.loss, p.err, p.done};
     // (a warp goes over a pair's rows and, in turn, over few pairs)
     const int L = d.rows == 0 ? 8 : d.pairs <= SMALL_CLUSTER * ROWS_THREADS ? small_lanes(d.dtype, d.vocab, d.rows) : 0;

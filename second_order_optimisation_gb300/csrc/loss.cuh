@@ -316,7 +316,7 @@ struct RowParams {
     int *err;
     unsigned *zero;            // a counter and a vector of the calls after this one: set to 0 here (rows that
     float *zero_g;             // are ignored), both may be null
-    float scale;               // the call's scale / tau
+    float scale;               // the call's scale / tau (1 for a call without gradient)
     char *dlogits;             // may be null
     long long ld_d_bytes;
 };
@@ -382,7 +382,7 @@ __device__ __forceinline__ Coef finish_row(const RowParams &P, long long row, co
         clipped = open ? 0.f : w;
         g = w * dlp;
         gh = -w * P.entropy_coef;
-        bad = finite(r.logp) && finite(t.x) && finite(g) ? 0.f : 1.f;
+        bad = finite(r.logp) && finite(t.x) && finite(g * P.scale) && (!ENT || finite(gh * P.scale)) ? 0.f : 1.f;
     }
     o.t = t;
     o.f = make_float2(clipped, bad);
@@ -1158,6 +1158,7 @@ struct PrefPairs {
     const float *ref, *pair_weight;
     int kind, average;
     float beta, smooth;
+    float scale;         // the call's scale / tau (0 for a call without gradient)
     const float *logp;   // of every row (0 where ignored)
     const float2 *ms;
     float *row_g;        // gradient of every row's logp
@@ -1258,6 +1259,7 @@ __device__ __forceinline__ void pref_pair(const PrefPairs &P, int b) {
         if (P.pair_loss) P.pair_loss[b] = f;
         for (int q = 0; q < 2; ++q) {
             slope[q] = v == 0.f ? 0.f : v * d * (q ? -1.f : 1.f) / (P.average && n[q] > 0 ? (float)n[q] : 1.f);
+            if (P.scale != 0.f && n[q] > 0 && !finite(slope[q] * P.scale)) bad |= ERR_NONFINITE;
             if (T > 32) shared_slope[q] = slope[q];
         }
     }
