@@ -511,14 +511,18 @@ def kfac_bn_diag_fisher(items: Sequence[BnItem], gamma: float, xi: float = 0.0, 
 
 def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
     """The caller's workspace, or a new one that may be dropped while a call on
-    `stream` (an own stream, or None) still uses it."""
-    if workspace is None and stream is None:
+    `stream` (an own stream, or None) still uses it.  It is that stream's memory: a
+    block of the current stream's may still be in use there by earlier work."""
+    if workspace is not None:
+        return _workspace(nbytes, device, workspace)
+    if stream is None:
         return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=device)
-    ws = _workspace(nbytes, device, workspace)
-    if workspace is None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_stream(stream), device=device)
-        ws.record_stream(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # (0 is the default stream, which has no external handle)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        ws = _workspace(nbytes, device, None)
+    ws.record_stream(torch.cuda.current_stream(device))  # the error word may be read there
     return ws
 
 
