@@ -23,7 +23,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= F32_MAX; }
 
-
 // Two fp32 values in one 64-bit register pair: one instruction for both.
 struct f2 {
     unsigned long long v;
@@ -276,7 +275,6 @@ struct Row {
     }
     __device__ __forceinline__ int groups() const { return (phase + n + E::N - 1) / E::N; }
     __device__ __forceinline__ int first(int g) const { return g * E::N - phase; }
-    __device__ __forceinline__ bool whole(int g) const { return first(g) >= 0 && first(g) + E::N <= n; }
     // Whole groups are begin() .. end() - 1; the elements of group 0 before them
     // (where phase > 0) and those of group end() behind them are the edges.
     __device__ __forceinline__ int begin() const { return phase > 0; }
@@ -315,7 +313,6 @@ struct Row {
         for (int i = 0; i < E::N; ++i)
             if (e0 + i >= 0 && e0 + i < n) ((bits *)out)[e0 + i] = (bits)(E::N == 4 ? w[i] : w[i / 2] >> (i & 1) * 16);
     }
-    __device__ __forceinline__ uint4 load(int g) const { return whole(g) ? load_whole(g) : load_edge(g); }
 };
 
 // Statistics of a part of a row: m its maximum (at least the lowest finite
