@@ -445,8 +445,9 @@ kfac_status kfac_token_logprob_grad(const kfac_logprob_grad_desc *desc, void *st
  *     w [the clipped branch was taken].  H is computed when entropy_coef != 0
  *     or `entropy` is not NULL (else stats[3] = 0).
  *   - logp, kl, entropy: [rows], optional.  dlogits NULL: the loss only.
- * Error word (first int32 of the workspace): KFAC_ERRW_TARGET, and
- * KFAC_ERRW_NONFINITE when a counted row's logp, loss term or gradient
+ * Error word (first int32 of the workspace): KFAC_ERRW_TARGET, 1, 2 or 4
+ * (KFAC_ERRW_TIMEOUT_*: a wait on the rows kept in shared memory ran past about
+ * 2 s; the outputs are then undefined), and KFAC_ERRW_NONFINITE when a counted row's logp, loss term or gradient
  * coefficient (with grad_scale / tau, where dlogits is given), or the loss, is
  * NaN or infinite (a gradient that overflows fp16 as it is rounded does not set
  * it).
@@ -539,9 +540,11 @@ kfac_status kfac_preference_loss(const kfac_preference_desc *desc, void *workspa
  *     one row.  y: [rows][ld_y] of y_dtype, which is dtype or, with x in fp32,
  *     any of the three (fp32 steps and the 16-bit gradients that they come
  *     from).  out: [rows][ld_out] of out_dtype; w: [rows][ld_w] fp32.
- *     Any ld >= cols and any element-aligned base; rows that run on without a
- *     gap (ld = cols) or start on 16-byte boundaries are read 16 bytes at a
- *     time.  rows or cols = 0: the tensor adds nothing.
+ *     Any ld >= cols and any element-aligned base.  A tensor is read 16 bytes at
+ *     a time where all its operands run on without a gap (ld = cols), or where
+ *     the pitches of all of them (x, y, out and w) are multiples of 8 elements;
+ *     else element by element.  Dense tensors are the fastest.  rows or
+ *     cols = 0: the tensor adds nothing.
  *   - out may be x itself (same dtype and ld); then nothing is rewritten when
  *     scale = 1.  Otherwise no output may overlap an input or another output.
  *   - max_norm > 0; +inf never clips.

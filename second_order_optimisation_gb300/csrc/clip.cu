@@ -8,10 +8,11 @@
 // step.  The tensors are cut into octets of eight elements, numbered through all
 // tensors, and every CTA takes an equal run of them in both passes; the second
 // pass walks its run from the end, so that what the first has read last is still
-// in the L2 cache.  A thread adds up to 32 products in fp32 and those sums in
-// two fp32 words; the CTAs' sums are added in fp64 in a fixed order.  A run
-// whose sum overflows or vanishes in fp32 is summed again from values scaled by
-// a power of two, so that any finite input gives its norm.
+// in the L2 cache.  A thread adds up to 64 products in fp32 (16-bit x without y; 32
+// otherwise) and those sums in two fp32 words; the CTAs' sums are added in fp64 in a
+// fixed order.  A run whose sum overflows or vanishes in fp32 is summed again from values
+// scaled by a power of two, so that any finite input gives its norm.  (So is a run of
+// zeros: eight 4096 x 4096 fp32 tensors of zeros take 540 us for the norm, 97 otherwise.)
 //
 // Measured: 48 tensors of 1.0e9 bf16 values, out on other 16-byte offsets than x: 312 us
 // for the norm (2.0 GB, 6.5 TB/s), 651 for the scaling (4.0 GB, 6.2 TB/s); ResNet-50's 161
@@ -19,6 +20,11 @@
 // 6.2 TB/s), the norm bound by the latency of the many runs that its first tiles hold.
 // 256 threads, three CTAs to an SM: the scaling took 663 us so, 700 by 512 x 2, 771 by
 // 256 x 4, 924 by 1024 x 2 (fewer streams open at once suit the memory better).
+// Tensors with gaps between their rows go octet by octet through a division, and element
+// by element where a pitch of any of their operands is not a multiple of eight elements:
+// ResNet-50's layers as KfacStep keeps them (fp32 steps and bf16 gradients on pitches of 64
+// elements, dense weights) take 59 and 124 us, 357 MB with a floor of 53; four layers of
+// 4096 x 4097 159 and 403 us, floor 139.
 #include <algorithm>
 #include <cmath>
 #include <memory>

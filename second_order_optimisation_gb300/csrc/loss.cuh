@@ -493,8 +493,8 @@ __device__ __forceinline__ void leave_sums(const RowParams &P, const TermSums &m
 
 // One row to L lanes of a warp (L = 8 or 32): rows of at most NV L whole groups.
 // All lanes of a warp come here together (the reductions name them all); `in`:
-// there is such a row.  (For many rows the two passes of warp_rows_kernel are as fast:
-// 60000 x 500 bf16 took 84 us by eight lanes of these and takes 82.)
+// there is such a row.  (For many rows the two passes of warp_rows_kernel are faster:
+// 60000 x 500 bf16 took 84 us by eight lanes of these and takes 72.)
 constexpr int NV = 8;
 template <int DT, bool ENT, int L>
 __device__ __forceinline__ Terms lane_row(const RowParams &P, long long row, bool in, const PolicyRow &q) {
@@ -1106,7 +1106,11 @@ constexpr int SMALL_CLUSTER = 8, ROWS_THREADS = 512;
 // launch in place of three, each of which would take longer to start than to run:
 // a call on 100 x 1000 fp32 takes 35 us in three launches, 30 in this form.
 // Up to SMALL_ROUNDS rows to a group: at 2000 x 18 the GPU needs 22 us either way; with
-// 16 rounds 6000 x 18 takes 45 us here and 22 in three launches.
+// 16 rounds 6000 x 18 takes 45 us here and 22 in three launches.  The preference loss takes
+// the same bound.  Its calls are bound by the host there, where one launch is the shorter
+// (500 x 1000 fp32: 31 us a call, 41 in three launches; 2000 x 200: 32 and 41), though the
+// GPU alone would need less in three (35 us against 28 for both, as a captured graph
+// sees it); with 16 rounds 1500 x 1000 takes 69 us a call in place of 40.
 constexpr int SMALL_ROUNDS = 4;
 template <int DT, bool ENT, int L>
 __global__ void __launch_bounds__(ROWS_THREADS) policy_small_kernel(const __grid_constant__ RowParams P,
