@@ -22,6 +22,11 @@
  *   kfac_policy_loss     clipped policy loss with a KL term, and its gradient
  *   kfac_preference_loss loss over pairs of sequences, and its gradient
  *   kfac_clip_norm       norm over many tensors, clipping, weight step
+ *   kfac_verify_draft    drafted tokens accepted or replaced under the policy's
+ *                        probabilities
+ *   kfac_checkpoint_store, kfac_checkpoint_load, kfac_weight_grad
+ *                        layer inputs kept in 8 bits, and the weight gradient
+ *                        from them (kfac_factor_update takes them too)
  *
  * Conventions shared by every entry point:
  *   - Every buffer pointer inside a descriptor is a DEVICE pointer on the
@@ -68,8 +73,9 @@
  *         without trapping; 8 is set when that drain wait ran out too.  The
  *         call's outputs are then undefined.
  *     A word of 0 means no kernel of the call saw either condition.
- *     kfac_policy_loss, kfac_preference_loss and kfac_clip_norm write the
- *     word too (with the bits that their sections name).
+ *     kfac_policy_loss, kfac_preference_loss, kfac_clip_norm,
+ *     kfac_verify_draft and kfac_weight_grad write the word too (with the
+ *     bits that their sections name).
  */
 #ifndef KFAC_GB300_H
 #define KFAC_GB300_H
@@ -90,7 +96,12 @@ typedef enum {
     KFAC_ERR_WORKSPACE = 5     /* workspace missing, misaligned or too small      */
 } kfac_status;
 
-typedef enum { KFAC_BF16 = 0, KFAC_F32 = 1, KFAC_F16 = 2 } kfac_dtype;
+typedef enum {
+    KFAC_BF16 = 0,
+    KFAC_F32 = 1,
+    KFAC_F16 = 2,
+    KFAC_E4M3 = 3   /* a checkpoint (kfac_checkpoint_store): sources of kfac_factor_update only */
+} kfac_dtype;
 
 /* Storage of a symmetric fp32 factor (only its upper triangle is stored or
  * read):
@@ -167,15 +178,22 @@ int kfac_timing_read_launches(double *start_ms, double *dur_ms, int *kind, unsig
  *
  * Fields:
  *   dtype   KFAC_BF16 or KFAC_F16 (tensor cores, fp32 accumulation; the
- *           paper computes in half precision) or KFAC_F32 (fp32 CUDA cores)
+ *           paper computes in half precision), KFAC_F32 (fp32 CUDA cores), or
+ *           KFAC_E4M3: a checkpoint of n rows, c columns (its column of ones
+ *           included) of a fully connected source, x its elements with the
+ *           pitch ldx and `scales` its exponents (tensor cores, the exact values
+ *           that the checkpoint stands for, fp32 accumulation)
  *   x       device, dense NHWC [n][h][w][c] of dtype (channel stride 1)
  *   F, ldf  device fp32 factor in `layout`: KFAC_LAYOUT_FULL [d][ldf] with
  *           ldf >= d, or KFAC_LAYOUT_PACKED_UPPER (d(d+1)/2 floats, ldf
  *           ignored); its upper triangle is updated
  *   layout  kfac_layout of F (a trailing field: zero-initialised = FULL)
  * Errors: INVALID for null x/F, n,h,w,c,kh,kw,stride < 1, pad < 0, Ho/Wo < 1,
- *   ldf < d (full layout), an unknown dtype or layout; UNSUPPORTED for
- *   d > 65536 or more than 2^31 rows.
+ *   ldf < d (full layout), an unknown dtype or layout; for a checkpoint also
+ *   null scales and ldx < c; UNSUPPORTED for
+ *   d > 65536 or more than 2^31 rows; for a checkpoint also for anything but
+ *   h = w = kh = kw = stride = 1, pad = 0, append_one = 0, and for x, scales
+ *   or ldx that are not multiples of 16 bytes.
  * Workspace: kfac_factor_update_workspace_size(descs, count) bytes.
  * ==================================================================== */
 typedef struct {
@@ -188,6 +206,8 @@ typedef struct {
     int64_t ldf;
     float alpha, beta;
     int32_t layout;
+    const uint8_t *scales;   /* KFAC_E4M3: the checkpoint's exponents (else ignored) */
+    int64_t ldx;             /* KFAC_E4M3: its elements' pitch (else ignored) */
 } kfac_factor_desc;
 
 size_t kfac_factor_update_workspace_size(const kfac_factor_desc *descs, int count);
@@ -572,6 +592,151 @@ typedef struct {
 size_t kfac_clip_norm_workspace_size(const kfac_clip_desc *descs, int count);
 kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, float max_norm, float eta, float *norm,
                            float *scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ======================================================================
+ * Checkpoints: matrices kept in 8 bits until the backward pass.
+ *
+ * A layer's input a [rows][cols] is needed again for its weight gradient and for
+ * its factor A.  Kept as a checkpoint it takes 1.03 bytes a value:
+ *   - elements q [rows][ldq], e4m3 (1 sign, 4 exponent, 3 mantissa bits);
+ *   - one exponent for every block of 32 consecutive rows of one column (rows
+ *     32 t .. 32 t + 31; the last block may be shorter), a byte holding e + 127.
+ *   A value is q 2^e, with e the smallest integer >= -127 for which the block's
+ *   largest finite magnitude is at most 448 2^e (-127 for a block of zeros), and
+ *   q = x 2^-e rounded to the nearest e4m3 (ties to even; where e = 120, at
+ *   most 240).  So a value is off by at most 2^-4 of itself or 2^(e - 10),
+ *   whichever is more.  An infinity or NaN is kept as NaN in its own place.
+ *   - Blocks run along the rows because every use sums over rows: a block is one
+ *     step of the tensor cores' block-scaled product, which takes the values
+ *     exactly as they are kept.
+ *   - append_one != 0: the checkpoint has one more column, all ones (exactly
+ *     kept): the input [a, 1] of a layer with a bias.  Its width is then
+ *     cols + 1.
+ *   - scales: kfac_checkpoint_scale_bytes(rows, width) bytes.  The exponent of
+ *     block t of column c is byte
+ *         ((c / 128) ceil(rows / 128) + t / 4) 512 + (c mod 32) 16
+ *             + (c mod 128) / 32 * 4 + t mod 4;
+ *     bytes of no block are 0.
+ *   - q and scales start on 16-byte boundaries and ldq is a multiple of 16;
+ *     elements of q past the width are neither read nor written.
+ * ==================================================================== */
+
+/* kfac_checkpoint_store -- checkpoints of x (KFAC_BF16, KFAC_F16 or KFAC_F32),
+ * any ld >= cols and any element-aligned base.
+ * kfac_checkpoint_load -- the values of checkpoints, rounded to x's type (fp32 and
+ * in general bf16 hold them exactly; fp16 rounds below 2^-14 and overflows above
+ * 65504).
+ * One launch for each 64 matrices.  rows = 0: nothing to do.  No workspace, no
+ * error word.
+ * Errors: INVALID for count < 0, rows < 0, cols < 1, ld < cols, ldq < width,
+ *   null x, q or scales of a matrix with rows, a base of x that is not
+ *   element-aligned, a bad dtype; UNSUPPORTED for q, scales or ldq that are
+ *   not multiples of 16 bytes, width > 65536, more than 2^31 - 1 rows or
+ *   tiles of 128 x 128. */
+typedef struct {
+    int32_t dtype;
+    void *x; int64_t ld;          /* store: read; load: written */
+    int64_t rows; int32_t cols;
+    int32_t append_one;
+    uint8_t *q; int64_t ldq;
+    uint8_t *scales;
+} kfac_checkpoint_desc;
+
+size_t kfac_checkpoint_scale_bytes(int64_t rows, int32_t width);
+kfac_status kfac_checkpoint_store(const kfac_checkpoint_desc *descs, int count, void *stream);
+kfac_status kfac_checkpoint_load(const kfac_checkpoint_desc *descs, int count, void *stream);
+
+/* kfac_weight_grad -- weight gradients of fully connected layers from checkpoints
+ * of their inputs a [rows][dA] and of their output gradients g [rows][dG]:
+ *     out[i][j] <- beta out[i][j] + alpha sum_m g[m][i] a[m][j]
+ * with the values that the checkpoints stand for (their products are exact), fp32
+ * accumulation, one rounding to out's type (KFAC_F32, KFAC_BF16 or KFAC_F16).
+ * out is read only where beta != 0; rows = 0 leaves beta out.  Results are
+ * bitwise reproducible run to run.
+ * Error word (first int32 of the workspace): KFAC_ERRW_NONFINITE when a value of
+ * out (before its rounding) is NaN or infinite, 1, 2, 4, 8 (KFAC_ERRW_TIMEOUT_*).
+ * Errors: INVALID for count < 0, rows < 0, dA or dG < 1, ld < dA, ldq_a < dA,
+ *   ldq_g < dG, null buffers (those of a and g where rows > 0), a base of out
+ *   that is not element-aligned, a bad out_dtype, alpha or beta not finite;
+ *   UNSUPPORTED as kfac_checkpoint_store.
+ * Workspace: kfac_weight_grad_workspace_size(descs, count) bytes. */
+typedef struct {
+    const uint8_t *q_a; int64_t ldq_a; const uint8_t *scales_a;
+    const uint8_t *q_g; int64_t ldq_g; const uint8_t *scales_g;
+    int64_t rows; int32_t dA, dG;
+    void *out; int64_t ld;        /* [dG][ld] */
+    int32_t out_dtype;
+    float alpha, beta;
+} kfac_weight_grad_desc;
+
+size_t kfac_weight_grad_workspace_size(const kfac_weight_grad_desc *descs, int count);
+kfac_status kfac_weight_grad(const kfac_weight_grad_desc *descs, int count, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* ======================================================================
+ * kfac_verify_draft -- drafted tokens accepted or replaced, so that what comes out
+ * is distributed as if every token had been drawn from the policy.
+ *
+ * Sequence b holds rows seq_offsets[b] .. seq_offsets[b + 1] - 1 of `logits`, the
+ * policy's scores at the position of each drafted token and, in the last row, at
+ * the position behind them (so n rows verify n - 1 drafted tokens).  With p =
+ * softmax(z / tau) of a row of logits and q = softmax(zd / tau_d) of the same row
+ * of `draft`, the scores that the drafted token x was drawn from:
+ *   - x is accepted if u q(x) < p(x), u = uniform[row];
+ *   - at the first row whose token is not accepted, or at the last row, the
+ *     sequence gets a new token, argmax_j r_j / E_j, with r = max(p - q, 0) at a
+ *     token that was not accepted (p itself where that leaves nothing), r = p
+ *     at the last row, and E = noise[b][j].  With E drawn from the exponential
+ *     distribution that is a draw from r.  Equal quotients: the lowest j.
+ * draft NULL: the token was not drawn but looked up (q is 1 at x).
+ * greedy != 0: x is accepted if it is the lowest j that maximises z, and the new
+ * token is that j; draft, uniform and noise are not read.
+ *   - accepted [seqs] receives the number of accepted tokens, out_tokens [rows] (the
+ *     type of tokens) the accepted tokens and the new one, and -1 in the rows
+ *     behind it; logp [rows] (may be NULL) ln p of the token, 0 behind it.  As
+ *     target and old_logp these serve kfac_policy_loss.  out_tokens may be tokens.
+ *   - A sequence without rows accepts 0 tokens and writes nothing else.  Rows of
+ *     no sequence are left as they were.  Offsets outside 0 .. rows are read as
+ *     the nearest of the two; sequences must not share rows.
+ *   - tokens int64 or (token_i32 != 0) int32; the one of a last row is not read. A
+ *     token outside 0 .. vocab - 1 is not accepted, and replaced by a draw from
+ *     p; one >= vocab sets KFAC_ERRW_TARGET.
+ *   - Logits of -inf have probability 0.  A row of the policy with NaN, +inf or
+ *     nothing but -inf has no distribution: its token is -1, its logp NaN, the sequence ends
+ *     there, and KFAC_ERRW_NONFINITE is set.  A row of the draft that has none:
+ *     its token is replaced by a draw from p, and the bit is set too.
+ *   - draft_saved [rows][2] (may be NULL): the maximum and the sum of
+ *     exp((z - m) / tau_d) of the draft's rows, as kfac_token_logprob's `saved`
+ *     gives them; then the draft's rows are read only where a token is replaced.
+ *   - noise [seqs][ld_noise]: positive; what is not (NaN, too) is read as 2^-126.  u is in [0, 1).
+ *   - Rows of logits and draft may start at any element boundary, any ld.
+ * Error word (first int32 of the workspace): the two bits named above.
+ * Errors: INVALID for null logits/tokens/seq_offsets/accepted/out_tokens, and
+ *   unless greedy null uniform/noise; rows < 0, seqs < 1, vocab < 1, ld, ld_draft or
+ *   ld_noise < vocab, draft_saved without draft or not on an 8-byte boundary, a bad
+ *   dtype, tau or tau_d; UNSUPPORTED for vocab > 2^24, rows > 2^31 - 1,
+ *   seqs > 2^20.
+ * Workspace: kfac_verify_draft_workspace_size(desc) bytes. */
+typedef struct {
+    int32_t dtype;
+    const void *logits; int64_t ld;
+    int64_t rows; int32_t vocab;
+    const void *tokens; int32_t token_i32;
+    float temperature;
+    const int32_t *seq_offsets; int32_t seqs;    /* [seqs + 1] */
+    const void *draft; int64_t ld_draft;         /* dtype; may be NULL */
+    const float *draft_saved;                    /* [rows][2], may be NULL */
+    float draft_temperature;
+    const float *uniform;                        /* [rows] */
+    const float *noise; int64_t ld_noise;
+    int32_t greedy;
+    int32_t *accepted;                           /* [seqs] */
+    void *out_tokens;                            /* [rows] */
+    float *logp;                                 /* [rows], may be NULL */
+} kfac_verify_desc;
+
+size_t kfac_verify_draft_workspace_size(const kfac_verify_desc *desc);
+kfac_status kfac_verify_draft(const kfac_verify_desc *desc, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -208,7 +208,7 @@ bool geom_of(const kfac_factor_desc &d, FactorGeom &g) {
     g.M = (long long)d.n * g.ho * g.wo;
     g.dcore = d.kh * d.kw * d.c;
     g.d = g.dcore + (d.append_one ? 1 : 0);
-    g.direct = d.dtype != KFAC_F32 && d.kh == 1 && d.kw == 1 && d.stride_h == 1 &&
+    g.direct = d.dtype != KFAC_F32 && d.dtype != KFAC_E4M3 && d.kh == 1 && d.kw == 1 && d.stride_h == 1 &&
                d.stride_w == 1 && d.pad_h == 0 && d.pad_w == 0 && d.c % 8 == 0 &&
                ((uintptr_t)d.x % 16) == 0;
     return true;
@@ -220,14 +220,24 @@ kfac_status validate_factor(const kfac_factor_desc *descs, int count, std::vecto
     for (int i = 0; i < count; ++i) {
         const kfac_factor_desc &d = descs[i];
         if (!d.x || !d.F) return KFAC_ERR_INVALID;
-        if (d.dtype != KFAC_BF16 && d.dtype != KFAC_F32 && d.dtype != KFAC_F16) return KFAC_ERR_INVALID;
+        if (d.dtype != KFAC_BF16 && d.dtype != KFAC_F32 && d.dtype != KFAC_F16 && d.dtype != KFAC_E4M3)
+            return KFAC_ERR_INVALID;
         if (d.layout != KFAC_LAYOUT_FULL && d.layout != KFAC_LAYOUT_PACKED_UPPER) return KFAC_ERR_INVALID;
         if (d.n < 1 || d.h < 1 || d.w < 1 || d.c < 1 || d.kh < 1 || d.kw < 1 || d.stride_h < 1 ||
             d.stride_w < 1 || d.pad_h < 0 || d.pad_w < 0)
             return KFAC_ERR_INVALID;
         if (!std::isfinite(d.alpha) || !std::isfinite(d.beta)) return KFAC_ERR_INVALID;
+        // a checkpoint: rows of a fully connected source, its ones among the columns
+        if (d.dtype == KFAC_E4M3 && (d.h != 1 || d.w != 1 || d.kh != 1 || d.kw != 1 || d.stride_h != 1 ||
+                                     d.stride_w != 1 || d.pad_h || d.pad_w || d.append_one))
+            return KFAC_ERR_UNSUPPORTED;
         if (!geom_of(d, geo[i])) return KFAC_ERR_INVALID;
         if (d.layout == KFAC_LAYOUT_FULL && d.ldf < geo[i].d) return KFAC_ERR_INVALID;
+        if (d.dtype == KFAC_E4M3) {
+            const kfac_status s = check_checkpoint(d.x, d.ldx, d.scales, d.n, d.c);
+            if (s != KFAC_OK) return s;
+            continue;
+        }
         if (geo[i].d > 65536 || geo[i].M >= (1LL << 31)) return KFAC_ERR_UNSUPPORTED;
         // a materialised patch matrix is indexed with 32-bit element counts
         if (!geo[i].direct && geo[i].M * (long long)(geo[i].d + 8) >= (1LL << 31)) return KFAC_ERR_UNSUPPORTED;
@@ -241,6 +251,9 @@ struct FactorPlan {
     std::vector<TcJob> tc;
     std::vector<SgJob> sg;
     std::vector<ColsumJob> cs;
+    std::vector<MxJob> mx;
+    char *mx_ws = nullptr;
+    size_t mx_bytes = 0;
     float *cs_partial = nullptr;
     int *err = nullptr;
     char *tc_ws = nullptr;
@@ -256,13 +269,19 @@ kfac_status plan_factor(const kfac_factor_desc *descs, int count, const std::vec
                         Arena &ws, FactorPlan &p, bool encode) {
     p.err = ws.take<int>(64);
     int n16 = 0;
-    for (int i = 0; i < count; ++i) n16 += descs[i].dtype != KFAC_F32;
+    for (int i = 0; i < count; ++i) n16 += descs[i].dtype != KFAC_F32 && descs[i].dtype != KFAC_E4M3;
     p.dev_maps = ws.take<CUtensorMap>(std::max(n16, 1));
     for (int i = 0; i < count; ++i) {
         const kfac_factor_desc &d = descs[i];
         const FactorGeom &g = geo[i];
         const bool packed = d.layout == KFAC_LAYOUT_PACKED_UPPER;
         const bool f16 = d.dtype == KFAC_F16;
+        if (d.dtype == KFAC_E4M3) {
+            const uint8_t *q = (const uint8_t *)d.x;
+            p.mx.push_back(MxJob{q, d.ldx, d.scales, q, d.ldx, d.scales, d.n, d.c, d.c, 1, packed, d.F, d.ldf, KFAC_F32,
+                                 d.alpha, d.beta});
+            continue;
+        }
         if (d.dtype == KFAC_F32) {
             // fp32 path: explicit patches (with the ones column) + CUDA-core SYRK
             const long long ldp = g.d;
@@ -338,6 +357,8 @@ kfac_status plan_factor(const kfac_factor_desc *descs, int count, const std::vec
     p.cs_partial = ws.take<float>(std::max<size_t>(colsum_partial_floats(p.cs.data(), (int)p.cs.size()), 1));
     p.tc_bytes = tc_workspace_bytes(p.tc.data(), (int)p.tc.size(), TC_KIND_BF16);
     p.tc_ws = ws.take<char>(p.tc_bytes);
+    p.mx_bytes = mx_workspace_bytes(p.mx.data(), (int)p.mx.size());
+    p.mx_ws = ws.take<char>(p.mx_bytes);
     return KFAC_OK;
 }
 
@@ -373,7 +394,7 @@ extern "C" const char *kfac_timing_kind_name(int k) {
     static const char *names[KK_COUNT] = {"tc_gemm_bf16", "tc_gemm_tf32x3", "inv_diag", "inv_prep",
                                           "damping", "im2col", "colsum", "sgemm_f32", "bn_fisher",
                                           "map_copy", "loss_rows", "loss_grad", "loss_small", "clip_norm",
-                                          "clip_apply"};
+                                          "clip_apply", "checkpoint", "mx_gemm", "verify_draft"};
     return (k >= 0 && k < KK_COUNT) ? names[k] : "";
 }
 
@@ -444,7 +465,9 @@ extern "C" kfac_status kfac_factor_update(const kfac_factor_desc *descs, int cou
     if ((s = plan_factor(descs, count, geo, ws, p, false)) != KFAC_OK) return s;
     if (!ws.fits()) return KFAC_ERR_WORKSPACE;
     for (int i = 0; i < count; ++i)
-        if (!all_on_this_device({descs[i].x, descs[i].F})) return KFAC_ERR_INVALID;
+        if (!all_on_this_device({descs[i].x, descs[i].F}) ||
+            (descs[i].dtype == KFAC_E4M3 && !on_this_device(descs[i].scales)))
+            return KFAC_ERR_INVALID;
     ws = Arena(workspace, workspace_bytes);
     p = FactorPlan();
     if ((s = plan_factor(descs, count, geo, ws, p, true)) != KFAC_OK) return s;
@@ -462,6 +485,10 @@ extern "C" kfac_status kfac_factor_update(const kfac_factor_desc *descs, int cou
         if ((s = tc_upload_maps(p.maps.data(), (int)p.maps.size(), p.dev_maps, st)) != KFAC_OK) return s;
         if ((s = tc_run(p.tc.data(), (int)p.tc.size(), TC_KIND_BF16, p.dev_maps, tail, p.err, st)) != KFAC_OK)
             return s;
+    }
+    if (!p.mx.empty()) {
+        Arena scratch(p.mx_ws, p.mx_bytes);
+        if ((s = mx_run(p.mx.data(), (int)p.mx.size(), scratch, p.err, st)) != KFAC_OK) return s;
     }
     if (!p.sg.empty() && (s = sg_run(p.sg.data(), (int)p.sg.size(), p.err, st)) != KFAC_OK) return s;
     if (!p.cs.empty() && (s = colsum_run(p.cs.data(), (int)p.cs.size(), p.cs_partial, st)) != KFAC_OK) return s;

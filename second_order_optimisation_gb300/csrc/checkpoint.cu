@@ -1,0 +1,390 @@
+// checkpoint.cu -- matrices kept in 8 bits (kfac_checkpoint_store) and restored
+// (kfac_checkpoint_load).
+//
+// A block is 32 consecutive rows of one column: every later use sums over rows (the
+// weight gradient, the Kronecker factor), so a block is one K block of a block-scaled
+// tensor-core product, which applies the block's power of two itself.  With a the
+// block's largest finite magnitude, the exponent is the smallest e >= -127 with
+// a <= 448 2^e (448 the largest e4m3 value), and an element is x 2^-e rounded to e4m3:
+// the scaling is exact, so an element has the one rounding of e4m3.
+//
+// Bound by memory.  A CTA takes a tile of 128 rows: each of its four warps 32 rows,
+// half a warp to a row's 16-byte groups, 16 rows to a thread, so that a thread has 16
+// loads in flight, the maximum over a block is one exchange between two lanes, and the
+// tile's exponents leave as one piece of 512 bytes.
+#include <algorithm>
+#include <cstring>
+
+#include "internal.h"
+#include "logits.cuh"
+
+namespace kfac {
+namespace {
+
+constexpr int TILE = 128;  // rows and columns of a tile of exponents
+constexpr int THREADS = 128;
+constexpr int MAX_ITEMS = 64;
+
+struct Item {
+    char *x;  // source, or where the values go
+    long long ld_bytes;
+    uint8_t *q;
+    long long ldq;
+    uint8_t *scales;
+    long long rows;
+    long long tile_begin;
+    int cols, width;  // of x, of the checkpoint (a column of ones more, or not)
+    int chunks;       // tiles along the rows
+    int dtype;
+    int wide;         // 16-byte accesses to x (8-byte, or 4-byte for 32-bit values, to q)
+};
+struct Params {
+    Item item[MAX_ITEMS];
+    int n;
+};
+
+__device__ __forceinline__ const Item &item_of(const Params &P, long long tile) {
+    int lo = 0, hi = P.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (P.item[mid].tile_begin <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    return P.item[lo];
+}
+
+// Largest magnitudes, as bits (of finite values the larger bits are the larger value,
+// and those of infinities and NaN are larger still).
+template <int DT>
+struct Mag;
+template <>
+struct Mag<KFAC_F32> {
+    static constexpr uint32_t TOP = 0x7f800000u;
+    static __device__ __forceinline__ uint32_t raise(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+    static __device__ __forceinline__ uint32_t finite(uint32_t w) { return (w & 0x7fffffffu) >= TOP ? 0u : w; }
+    static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return max(a, b); }
+    static __device__ __forceinline__ uint32_t bits(const uint32_t *m, int i) { return m[i]; }
+    static __device__ __forceinline__ float value(uint32_t b) { return __uint_as_float(b); }
+};
+template <int DT>
+struct Mag16 {
+    static constexpr uint32_t TOP = DT == KFAC_BF16 ? 0x7f80u : 0x7c00u;
+    static __device__ __forceinline__ uint32_t raise(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+    static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+        return w & ~__vcmpgeu2(w & 0x7fff7fffu, TOP | TOP << 16);
+    }
+    static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+    static __device__ __forceinline__ uint32_t bits(const uint32_t *m, int i) { return m[i / 2] >> (i & 1) * 16 & 0xffffu; }
+    static __device__ __forceinline__ float value(uint32_t b) { return Elem<DT>::value((uint16_t)b); }
+};
+template <>
+struct Mag<KFAC_BF16> : Mag16<KFAC_BF16> {};
+template <>
+struct Mag<KFAC_F16> : Mag16<KFAC_F16> {};
+
+// The biased exponent (e + 127) of a block whose largest finite magnitude is a.
+// 448 = 1.75 2^8: a mantissa above 1.75 takes the next power of two.
+__device__ __forceinline__ uint32_t exponent_of(float a) {
+    const int k = (int)((__float_as_uint(a) + 0x1fffffu) >> 23);
+    return (uint32_t)max(k - 8, 0);
+}
+// 2^-e from e + 127 (0 .. 247).
+__device__ __forceinline__ float inverse_of(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+// 2^e (2^-127 is below fp32's normal numbers).
+__device__ __forceinline__ float power_of(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x400000u); }
+// Past this exponent 256 2^e is infinite in fp32: a value may be rounded up to 240 2^e at most.
+constexpr uint32_t LAST_EXPONENT = 247;
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t b) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)b));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// Values that the fast way does not take: an infinity is kept as NaN, and in the last
+// exponent a value does not pass 240.
+__device__ __forceinline__ float bounded(float y, uint32_t b) {
+    if (!(fabsf(y) <= F32_MAX)) return __uint_as_float(0x7fffffffu);
+    return b == LAST_EXPONENT ? fminf(fmaxf(y, -240.f), 240.f) : y;
+}
+
+template <int DT>
+__device__ __forceinline__ void store_tile(const Item &it, long long tile, uint8_t (*exps)[4]) {
+    using M = Mag<DT>;
+    constexpr int N = Elem<DT>::N, ROWS = 16, COLS = 16 * N;
+    using bits = typename Elem<DT>::bits;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const long long ct = tile / it.chunks, rt = tile % it.chunks;
+    const long long r0 = rt * TILE + warp * 32 + lane / 16;  // rows r0, r0 + 2, ...
+#pragma unroll 1
+    for (int part = 0; part < TILE; part += COLS) {
+        const int c0 = (int)ct * TILE + part + lane % 16 * N;
+        const int n = min(N, it.cols - c0);  // values here (may be negative)
+        uint4 u[ROWS];
+        const char *src = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
+        if (it.wide && n == N) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (r0 + 2 * i < it.rows) u[i] = ld16(src + 2 * i * it.ld_bytes);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (r0 + 2 * i < it.rows) {
+                    const bits *p = (const bits *)(src + 2 * i * it.ld_bytes);
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (j < n) w[j * 4 / N] |= (uint32_t)p[j] << (N == 8 ? (j & 1) * 16 : 0);
+                }
+                u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            m[0] = M::raise(m[0], u[i].x); m[1] = M::raise(m[1], u[i].y);
+            m[2] = M::raise(m[2], u[i].z); m[3] = M::raise(m[3], u[i].w);
+        }
+        bool odd = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) m[w] = M::join(m[w], __shfl_xor_sync(ALL_LANES, m[w], 16));
+#pragma unroll
+        for (int j = 0; j < N; ++j) odd |= M::bits(m, j) >= M::TOP;
+        if (__any_sync(ALL_LANES, odd)) {  // infinities or NaN: the largest of the finite ones
+            m[0] = m[1] = m[2] = m[3] = 0;
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                m[0] = M::raise(m[0], M::finite(u[i].x)); m[1] = M::raise(m[1], M::finite(u[i].y));
+                m[2] = M::raise(m[2], M::finite(u[i].z)); m[3] = M::raise(m[3], M::finite(u[i].w));
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) m[w] = M::join(m[w], __shfl_xor_sync(ALL_LANES, m[w], 16));
+        }
+        uint32_t e[N];
+        float inv[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            e[j] = exponent_of(M::value(M::bits(m, j)));
+            odd |= e[j] == LAST_EXPONENT;
+            inv[j] = inverse_of(e[j]);
+        }
+        odd = __any_sync(ALL_LANES, odd);
+        uint8_t *dst = it.q + r0 * it.ldq + c0;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (r0 + 2 * i >= it.rows) continue;
+            float v[N];
+            Elem<DT>::unpack(u[i], v);
+            uint32_t b[N / 4];
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] *= inv[j];
+            if (odd) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] = bounded(v[j], e[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j)
+                b[j] = e4m3x2(v[4 * j], v[4 * j + 1]) | e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
+            uint8_t *d = dst + 2 * i * it.ldq;
+            if (n == N) {  // (q's rows start on 16-byte boundaries, and c0 is a multiple of N)
+                if constexpr (N == 8) *(uint2 *)d = make_uint2(b[0], b[1]);
+                else *(uint32_t *)d = b[0];
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j < n) d[j] = (uint8_t)(b[j / 4] >> j % 4 * 8);
+            }
+            if (c0 <= it.cols && it.cols < c0 + N && it.cols < it.width) d[it.cols - c0] = 0x78;  // 256 = 1 2^8
+        }
+        if (lane < 16) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int c = c0 + j, at = c % 32 * 4 + c % TILE / 32;  // (16 bytes to a column modulo 32, 4 to each of 4)
+                uint32_t b = r0 >= it.rows ? 0u : c < it.cols ? e[j] : c < it.width ? 119u : 0u;  // 1 = 256 2^-8
+                exps[at][warp] = (uint8_t)b;
+            }
+        }
+    }
+    __syncthreads();
+    ((uint32_t *)(it.scales + tile * 512))[threadIdx.x] = ((const uint32_t *)exps)[threadIdx.x];
+}
+
+__global__ void __launch_bounds__(THREADS) store_kernel(const __grid_constant__ Params P) {
+    __shared__ __align__(16) uint8_t exps[TILE][4];
+    pdl_wait();
+    pdl_trigger();
+    const Item &it = item_of(P, blockIdx.x);
+    const long long tile = blockIdx.x - it.tile_begin;
+    if (it.dtype == KFAC_BF16) store_tile<KFAC_BF16>(it, tile, exps);
+    else if (it.dtype == KFAC_F16) store_tile<KFAC_F16>(it, tile, exps);
+    else store_tile<KFAC_F32>(it, tile, exps);
+}
+
+// Values of a tile: x_ij = q_ij 2^e, rounded to x's type.
+template <int DT>
+__device__ __forceinline__ void load_tile(const Item &it, long long tile, const uint8_t (*exps)[4]) {
+    constexpr int N = Elem<DT>::N, ROWS = 16, COLS = 16 * N;
+    using bits = typename Elem<DT>::bits;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const long long ct = tile / it.chunks, rt = tile % it.chunks;
+    const long long r0 = rt * TILE + warp * 32 + lane / 16;
+#pragma unroll 1
+    for (int part = 0; part < TILE; part += COLS) {
+        const int c0 = (int)ct * TILE + part + lane % 16 * N;
+        const int n = min(N, it.cols - c0);
+        if (n <= 0) continue;
+        const uint8_t *src = it.q + r0 * it.ldq + c0;
+        uint32_t b[ROWS][N / 4];
+        if (n == N) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                b[i][0] = b[i][N / 4 - 1] = 0;
+                if (r0 + 2 * i >= it.rows) continue;
+                if constexpr (N == 8) {
+                    const uint2 u = *(const uint2 *)(src + 2 * i * it.ldq);
+                    b[i][0] = u.x;
+                    b[i][1] = u.y;
+                } else {
+                    b[i][0] = *(const uint32_t *)(src + 2 * i * it.ldq);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                b[i][0] = b[i][N / 4 - 1] = 0;
+                if (r0 + 2 * i >= it.rows) continue;
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j < n) b[i][j / 4] |= (uint32_t)src[2 * i * it.ldq + j] << j % 4 * 8;
+            }
+        }
+        float p[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = power_of(exps[(c0 + j) % 32 * 4 + (c0 + j) % TILE / 32][warp]);
+        char *dst = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            if (r0 + 2 * i >= it.rows) continue;
+            float v[N];
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const float2 f = from_e4m3x2(b[i][j / 4] >> j % 4 * 8 & 0xffffu);
+                v[j] = f.x * p[j];
+                v[j + 1] = f.y * p[j + 1];
+            }
+            char *d = dst + 2 * i * it.ld_bytes;
+            if (it.wide && n == N) {
+                *(uint4 *)d = Elem<DT>::pack(v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (j < n) ((bits *)d)[j] = Elem<DT>::round(v[j]);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(THREADS) load_kernel(const __grid_constant__ Params P) {
+    __shared__ __align__(16) uint8_t exps[TILE][4];
+    pdl_wait();
+    pdl_trigger();
+    const Item &it = item_of(P, blockIdx.x);
+    const long long tile = blockIdx.x - it.tile_begin;
+    ((uint32_t *)exps)[threadIdx.x] = ((const uint32_t *)(it.scales + tile * 512))[threadIdx.x];
+    __syncthreads();
+    if (it.dtype == KFAC_BF16) load_tile<KFAC_BF16>(it, tile, exps);
+    else if (it.dtype == KFAC_F16) load_tile<KFAC_F16>(it, tile, exps);
+    else load_tile<KFAC_F32>(it, tile, exps);
+}
+
+size_t elem_size(int dtype) { return dtype == KFAC_F32 ? 4 : 2; }
+
+kfac_status check(const kfac_checkpoint_desc *descs, int count) {
+    if (count < 0 || (count > 0 && !descs)) return KFAC_ERR_INVALID;
+    for (int i = 0; i < count; ++i) {
+        const kfac_checkpoint_desc &d = descs[i];
+        if (d.dtype != KFAC_BF16 && d.dtype != KFAC_F16 && d.dtype != KFAC_F32) return KFAC_ERR_INVALID;
+        if (d.rows < 0 || d.cols < 1 || d.ld < d.cols || (uintptr_t)d.x % elem_size(d.dtype)) return KFAC_ERR_INVALID;
+        const kfac_status s =
+            check_checkpoint(d.q, d.ldq, d.scales, d.rows, (long long)d.cols + (d.append_one ? 1 : 0));
+        if (s != KFAC_OK) return s;
+        if (d.rows > 0 && !d.x) return KFAC_ERR_INVALID;
+    }
+    return KFAC_OK;
+}
+
+kfac_status run(const kfac_checkpoint_desc *descs, int count, bool store, void *stream) {
+    kfac_status s = check(descs, count);
+    if (s != KFAC_OK) return s;
+    for (int i = 0; i < count; ++i)
+        if (descs[i].rows > 0 && !all_on_this_device({descs[i].x, descs[i].q, descs[i].scales})) return KFAC_ERR_INVALID;
+    cudaStream_t st = (cudaStream_t)stream;
+    for (int at = 0; at < count;) {
+        Params P;
+        P.n = 0;
+        long long tiles = 0;
+        while (at < count && P.n < MAX_ITEMS) {
+            const kfac_checkpoint_desc &d = descs[at];
+            const long long chunks = ceil_div(d.rows, TILE), width = d.cols + (d.append_one ? 1 : 0);
+            // (what is only restored may leave the ones' tile out; it is kept, so that a tile's number is its place)
+            const long long here = chunks * ceil_div(width, TILE);
+            if (here == 0) {
+                ++at;
+                continue;
+            }
+            if (tiles + here > 0x7fffffffLL) break;  // (one item alone stays below: check_checkpoint)
+            Item &it = P.item[P.n++];
+            it.x = (char *)d.x;
+            it.ld_bytes = d.ld * (long long)elem_size(d.dtype);
+            it.q = d.q;
+            it.ldq = d.ldq;
+            it.scales = d.scales;
+            it.rows = d.rows;
+            it.tile_begin = tiles;
+            it.cols = d.cols;
+            it.width = (int)width;
+            it.chunks = (int)chunks;
+            it.dtype = d.dtype;
+            it.wide = (uintptr_t)d.x % 16 == 0 && (it.ld_bytes % 16 == 0 || d.rows == 1);
+            tiles += here;
+            ++at;
+        }
+        if (P.n == 0) break;
+        if (store) KFAC_LAUNCH(KK_CHECKPOINT, st, store_kernel, (unsigned)tiles, THREADS, 0, P);
+        else KFAC_LAUNCH(KK_CHECKPOINT, st, load_kernel, (unsigned)tiles, THREADS, 0, P);
+    }
+    return KFAC_OK;
+}
+
+}  // namespace
+
+// What every call that takes a checkpoint checks of it: elements on 16-byte rows, whole
+// tiles of exponents.
+kfac_status check_checkpoint(const void *q, long long ldq, const void *scales, long long rows, long long width) {
+    if (rows < 0 || width < 1 || (rows > 0 && (!q || !scales || ldq < width))) return KFAC_ERR_INVALID;
+    if (rows > 0x7fffffffLL || width > 65536 || ceil_div(rows, TILE) * ceil_div(width, TILE) > 0x7fffffffLL)
+        return KFAC_ERR_UNSUPPORTED;
+    if (rows > 0 && (ldq % 16 || (uintptr_t)q % 16 || (uintptr_t)scales % 16)) return KFAC_ERR_UNSUPPORTED;
+    return KFAC_OK;
+}
+
+}  // namespace kfac
+
+extern "C" size_t kfac_checkpoint_scale_bytes(int64_t rows, int32_t width) {
+    if (rows < 0 || width < 1) return 0;
+    return (size_t)kfac::ceil_div(rows, 128) * (size_t)kfac::ceil_div(width, 128) * 512;
+}
+
+extern "C" kfac_status kfac_checkpoint_store(const kfac_checkpoint_desc *descs, int count, void *stream) {
+    return kfac::run(descs, count, true, stream);
+}
+
+extern "C" kfac_status kfac_checkpoint_load(const kfac_checkpoint_desc *descs, int count, void *stream) {
+    return kfac::run(descs, count, false, stream);
+}

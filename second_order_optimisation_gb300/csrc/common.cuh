@@ -35,7 +35,7 @@ void count_launch();
 enum KernelKind : int {
     KK_TC_BF16 = 0, KK_TC_TF32X3, KK_DIAG, KK_PREP, KK_DAMPING, KK_IM2COL, KK_COLSUM,
     KK_SGEMM, KK_BN, KK_MAPCOPY, KK_LOSS_ROWS, KK_LOSS_GRAD, KK_LOSS_SMALL, KK_CLIP_NORM,
-    KK_CLIP_APPLY, KK_COUNT
+    KK_CLIP_APPLY, KK_CHECKPOINT, KK_MX, KK_VERIFY, KK_COUNT
 };
 // Returns a slot (>= 0) after recording a start event on `st` when timing is
 // enabled, -1 otherwise; timing_end records the matching end event.

@@ -211,4 +211,30 @@ kfac_status inv_run(const InvMatrix *mats, int nmats, const float *damp_dev, int
 kfac_status damping_run(const InvMatrix *mats, int nlayers, float gamma, int pi_split,
                         float *damp_dev, cudaStream_t st);
 
+// ----------------------------------------------------- 8-bit checkpoints
+// INVALID / UNSUPPORTED as kfac.h has it for a checkpoint's buffers.
+kfac_status check_checkpoint(const void *q, long long ldq, const void *scales, long long rows, long long width);
+
+// A product of two checkpoints over their rows on block-scaled tensor cores:
+// C[M x N] = beta C + alpha sum_k A[k][i] B[k][j], A [K][M] and B [K][N].
+//   sym: B is A; only i <= j is read and written (packed: C is a packed upper triangle).
+//   c_dtype: KFAC_F32, or KFAC_BF16 / KFAC_F16 (not sym).
+struct MxJob {
+    const uint8_t *a;
+    long long lda;
+    const uint8_t *sa;
+    const uint8_t *b;
+    long long ldb;
+    const uint8_t *sb;
+    long long K;
+    int M, N;
+    int sym, packed;
+    void *C;
+    long long ldc;
+    int c_dtype;
+    float alpha, beta;
+};
+size_t mx_workspace_bytes(const MxJob *jobs, int njobs);
+kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream_t st);
+
 }  // namespace kfac

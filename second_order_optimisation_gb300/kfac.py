@@ -14,6 +14,9 @@ and, next to the step, the losses that make a policy's or language model's
 output gradients and the bound on the step over all tensors:
   kfac_token_logprob, kfac_token_logprob_grad, kfac_policy_loss,
   kfac_preference_loss, kfac_clip_norm
+and what a policy's tokens are drawn with and a layer's input is kept in until the
+backward pass:
+  kfac_verify_draft, kfac_checkpoint_store, kfac_checkpoint_load, kfac_weight_grad
 """
 from __future__ import annotations
 
@@ -28,7 +31,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkfac_gb300.so")
 
 KFAC_OK, KFAC_ERR_INVALID, KFAC_ERR_UNSUPPORTED, KFAC_ERR_NOT_PD, KFAC_ERR_CUDA, KFAC_ERR_WORKSPACE = range(6)
-KFAC_BF16, KFAC_F32, KFAC_F16 = 0, 1, 2
+KFAC_BF16, KFAC_F32, KFAC_F16, KFAC_E4M3 = 0, 1, 2, 3
 KFAC_LAYOUT_FULL, KFAC_LAYOUT_PACKED_UPPER = 0, 1
 # bits of the device error word (the first int32 of a call's workspace)
 ERRW_TIMEOUT_OPERAND, ERRW_TIMEOUT_STAGE, ERRW_TIMEOUT_ACCUM, ERRW_TIMEOUT_DRAIN, ERRW_NONFINITE = 1, 2, 4, 8, 16
@@ -42,7 +45,9 @@ EXPORTS = ("kfac_status_string", "kfac_version", "kfac_launch_count", "kfac_timi
            "kfac_noalloc_scratch_bytes", "kfac_precondition_noalloc", "kfac_timing_read_launches",
            "kfac_token_logprob", "kfac_token_logprob_grad", "kfac_policy_loss_workspace_size", "kfac_policy_loss",
            "kfac_preference_loss_workspace_size", "kfac_preference_loss", "kfac_clip_norm_workspace_size",
-           "kfac_clip_norm")
+           "kfac_clip_norm", "kfac_checkpoint_scale_bytes", "kfac_checkpoint_store", "kfac_checkpoint_load",
+           "kfac_weight_grad_workspace_size", "kfac_weight_grad", "kfac_verify_draft_workspace_size",
+           "kfac_verify_draft")
 
 
 class KfacError(RuntimeError):
@@ -60,7 +65,7 @@ class FactorDesc(ctypes.Structure):
                 ("append_one", ctypes.c_int32),
                 ("F", ctypes.c_void_p), ("ldf", ctypes.c_int64),
                 ("alpha", ctypes.c_float), ("beta", ctypes.c_float),
-                ("layout", ctypes.c_int32)]
+                ("layout", ctypes.c_int32), ("scales", ctypes.c_void_p), ("ldx", ctypes.c_int64)]
 
 
 class InvertDesc(ctypes.Structure):
@@ -137,6 +142,31 @@ class ClipDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
+class CheckpointDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("x", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("append_one", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("scales", ctypes.c_void_p)]
+
+
+class WeightGradDesc(ctypes.Structure):
+    _fields_ = [("q_a", ctypes.c_void_p), ("ldq_a", ctypes.c_int64), ("scales_a", ctypes.c_void_p),
+                ("q_g", ctypes.c_void_p), ("ldq_g", ctypes.c_int64), ("scales_g", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("dA", ctypes.c_int32), ("dG", ctypes.c_int32),
+                ("out", ctypes.c_void_p), ("ld", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float)]
+
+
+class VerifyDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("tokens", ctypes.c_void_p), ("token_i32", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("seq_offsets", ctypes.c_void_p), ("seqs", ctypes.c_int32),
+                ("draft", ctypes.c_void_p), ("ld_draft", ctypes.c_int64), ("draft_saved", ctypes.c_void_p),
+                ("draft_temperature", ctypes.c_float), ("uniform", ctypes.c_void_p),
+                ("noise", ctypes.c_void_p), ("ld_noise", ctypes.c_int64), ("greedy", ctypes.c_int32),
+                ("accepted", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p), ("logp", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -186,9 +216,20 @@ def load() -> ctypes.CDLL:
         lib.kfac_clip_norm_workspace_size.argtypes = [vp, i32]
         lib.kfac_clip_norm_workspace_size.restype = sz
         lib.kfac_clip_norm.argtypes = [vp, i32, f32, f32, vp, vp, vp, sz, vp]
+        lib.kfac_checkpoint_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32]
+        lib.kfac_checkpoint_scale_bytes.restype = sz
+        lib.kfac_checkpoint_store.argtypes = [vp, i32, vp]
+        lib.kfac_checkpoint_load.argtypes = [vp, i32, vp]
+        lib.kfac_weight_grad_workspace_size.argtypes = [vp, i32]
+        lib.kfac_weight_grad_workspace_size.restype = sz
+        lib.kfac_weight_grad.argtypes = [vp, i32, vp, sz, vp]
+        lib.kfac_verify_draft_workspace_size.argtypes = [vp]
+        lib.kfac_verify_draft_workspace_size.restype = sz
+        lib.kfac_verify_draft.argtypes = [vp, vp, sz, vp]
         for f in ("kfac_factor_update", "kfac_damp_invert", "kfac_precondition", "kfac_bn_diag_fisher",
                   "kfac_precondition_noalloc", "kfac_token_logprob", "kfac_token_logprob_grad", "kfac_policy_loss",
-                  "kfac_preference_loss", "kfac_clip_norm"):
+                  "kfac_preference_loss", "kfac_clip_norm", "kfac_checkpoint_store", "kfac_checkpoint_load",
+                  "kfac_weight_grad", "kfac_verify_draft"):
             getattr(lib, f).restype = i32
         _lib = lib
     return _lib
@@ -268,13 +309,131 @@ def _ld(t: torch.Tensor) -> int:
     return t.stride(0)
 
 
+# ------------------------------------------------------------ checkpoints
+
+@dataclass
+class Checkpoint:
+    """A matrix [rows, width] kept in 8 bits (format in kfac.h): q uint8 with at least
+    that shape, unit column stride and a row pitch of a multiple of 16, scales the
+    dense uint8 exponents.  Checkpoint.empty makes the buffers."""
+    q: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    width: int
+
+    @property
+    def device(self) -> torch.device:
+        return self.q.device
+
+    @staticmethod
+    def empty(rows: int, cols: int, append_one: bool = False, device="cuda") -> "Checkpoint":
+        width = cols + bool(append_one)
+        return Checkpoint(torch.empty(rows, (width + 15) // 16 * 16, dtype=torch.uint8, device=device),
+                          torch.empty(checkpoint_scale_bytes(rows, width), dtype=torch.uint8, device=device), rows, width)
+
+
+def checkpoint_scale_bytes(rows: int, width: int) -> int:
+    """Bytes of a checkpoint's exponents: 512 for each 128 x 128 values, begun ones whole."""
+    return (rows + 127) // 128 * ((width + 127) // 128) * 512
+
+
+def _checkpoint_args(c: Checkpoint):
+    """A checkpoint's elements, pitch and exponents."""
+    q, sc = c.q, c.scales
+    if q.dtype is not torch.uint8 or sc.dtype is not torch.uint8:
+        raise TypeError("a checkpoint's q and scales must be uint8")
+    if q.dim() != 2 or q.shape[0] < c.rows or q.shape[1] < c.width or (q.stride(1) != 1 and q.shape[1] > 1 and c.rows > 0):
+        raise ValueError(f"q must be at least [{c.rows}, {c.width}] with unit column stride, got {tuple(q.shape)}")
+    if not sc.is_contiguous() or sc.numel() < checkpoint_scale_bytes(c.rows, c.width):
+        raise ValueError(f"scales must be {checkpoint_scale_bytes(c.rows, c.width)} dense bytes, got {tuple(sc.shape)}")
+    ld = q.stride(0) if q.shape[0] > 1 else (c.width + 15) // 16 * 16  # (one row has no pitch)
+    return q.data_ptr(), ld, sc.data_ptr()
+
+
+@dataclass
+class CheckpointItem:
+    """A matrix x [rows, cols] (bf16, fp16 or fp32, unit column stride, any pitch) and the
+    checkpoint that keeps it; with append_one the checkpoint has a column of ones more."""
+    x: torch.Tensor
+    checkpoint: Checkpoint
+    append_one: bool = False
+
+
+def _checkpoint_descs(items: Sequence[CheckpointItem]):
+    arr = (CheckpointDesc * max(len(items), 1))()
+    for i, it in enumerate(items):
+        x, c = it.x, it.checkpoint
+        if x.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {x.dtype}")
+        if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1 and x.shape[0] > 0):
+            raise ValueError("x must be [rows, cols] with unit column stride")
+        rows, cols = x.shape
+        if c.rows != rows or c.width != cols + bool(it.append_one):
+            raise ValueError(f"the checkpoint is [{c.rows}, {c.width}], x is {tuple(x.shape)}, append_one {it.append_one}")
+        q, ldq, scales = _checkpoint_args(c)
+        arr[i] = CheckpointDesc(_DTYPES[x.dtype], x.data_ptr(), x.stride(0) if rows > 1 else cols, rows, cols,
+                                int(bool(it.append_one)), q, ldq, scales)
+    return arr
+
+
+def kfac_checkpoint_store(items: Sequence[CheckpointItem], stream=None) -> None:
+    """Keep every x in its checkpoint."""
+    _check(load().kfac_checkpoint_store(_checkpoint_descs(items), len(items), _stream(stream)), "kfac_checkpoint_store")
+
+
+def kfac_checkpoint_load(items: Sequence[CheckpointItem], stream=None) -> None:
+    """Write every checkpoint's values to its x (a column of ones is left out)."""
+    _check(load().kfac_checkpoint_load(_checkpoint_descs(items), len(items), _stream(stream)), "kfac_checkpoint_load")
+
+
+@dataclass
+class WeightGrad:
+    """out [dG, dA] (fp32, bf16 or fp16) <- beta out + alpha g^T a, from the checkpoints of
+    a layer's input a [rows, dA] and of its output gradients g [rows, dG]."""
+    a: Checkpoint
+    g: Checkpoint
+    out: torch.Tensor
+    alpha: float = 1.0
+    beta: float = 0.0
+
+
+def _weight_grad_descs(items: Sequence[WeightGrad]):
+    arr = (WeightGradDesc * max(len(items), 1))()
+    for i, it in enumerate(items):
+        a, g, out = it.a, it.g, it.out
+        if out.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {out.dtype}")
+        if a.rows != g.rows:
+            raise ValueError(f"a has {a.rows} rows, g {g.rows}")
+        if out.shape != (g.width, a.width) or (out.stride(1) != 1 and a.width > 1):
+            raise ValueError(f"out must be [{g.width}, {a.width}] with unit column stride, got {tuple(out.shape)}")
+        arr[i] = WeightGradDesc(*_checkpoint_args(a), *_checkpoint_args(g), a.rows, a.width, g.width, out.data_ptr(),
+                                out.stride(0) if g.width > 1 else a.width, _DTYPES[out.dtype], it.alpha, it.beta)
+    return arr
+
+
+def kfac_weight_grad_workspace_size(items: Sequence[WeightGrad]) -> int:
+    return int(load().kfac_weight_grad_workspace_size(_weight_grad_descs(items), len(items)))
+
+
+def kfac_weight_grad(items: Sequence[WeightGrad], workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue the weight gradients; returns the workspace used (its first int32 is the
+    device error word: ERRW_NONFINITE, ERRW_TIMEOUT_*)."""
+    lib = load()
+    arr = _weight_grad_descs(items)
+    n = len(items)
+    ws = _scratch(lib.kfac_weight_grad_workspace_size(arr, n), items[0].out.device if n else "cuda", workspace, stream)
+    _check(lib.kfac_weight_grad(arr, n, ws.data_ptr(), ws.nbytes, _stream(stream)), "kfac_weight_grad")
+    return ws
+
+
 # ------------------------------------------------------------ factor update
 
 @dataclass
 class FactorSource:
     """One factor update: F[:d, :d] (upper) <- beta F + alpha P^T P, P the patch
     matrix of x.  x: NHWC [n, h, w, c] (conv) or [rows, c] (FC / output grads),
-    bf16, fp16 or fp32.  With packed, F is the packed upper triangle (a 1-D
+    bf16, fp16 or fp32, or a Checkpoint of [rows, c].  With packed, F is the packed upper triangle (a 1-D
     tensor of d(d+1)/2 floats, see pack_upper)."""
     x: torch.Tensor
     F: torch.Tensor
@@ -323,6 +482,14 @@ def _factor_descs(sources: Sequence[FactorSource]):
     arr = (FactorDesc * max(len(sources), 1))()
     for i, s in enumerate(sources):
         x = s.x
+        if isinstance(x, Checkpoint):
+            assert s.F.dtype == torch.float32
+            q, ldq, scales = _checkpoint_args(x)
+            arr[i] = FactorDesc(KFAC_E4M3, q, x.rows, 1, 1, x.width, s.kh, s.kw, s.stride[0], s.stride[1],
+                                s.pad[0], s.pad[1], int(bool(s.append_one)), s.F.data_ptr(), _fld(s.F, s.packed),
+                                float(s.alpha), float(s.beta),
+                                KFAC_LAYOUT_PACKED_UPPER if s.packed else KFAC_LAYOUT_FULL, scales, ldq)
+            continue
         assert x.is_contiguous(), "x must be dense"
         if x.dim() == 2:
             n, h, w, c = x.shape[0], 1, 1, x.shape[1]
@@ -554,14 +721,14 @@ def _logits_args(logits: torch.Tensor, target: torch.Tensor, temperature: float)
             target.data_ptr(), tdtype is torch.int32, temperature)
 
 
-def _dlogits_args(logits: torch.Tensor, dlogits: Optional[torch.Tensor]):
+def _dlogits_args(logits: torch.Tensor, dlogits: Optional[torch.Tensor], name: str = "dlogits"):
     if dlogits is None:
         return None, 0
     shape, stride = dlogits.shape, dlogits.stride()
     if dlogits.dtype is not logits.dtype or shape != logits.shape:
-        raise TypeError("dlogits must have the logits' shape and dtype")
+        raise TypeError(f"{name} must have the logits' shape and dtype")
     if stride[1] != 1 and shape[1] > 1:
-        raise ValueError("dlogits must have unit column stride")
+        raise ValueError(f"{name} must have unit column stride")
     return dlogits.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
@@ -722,6 +889,66 @@ def kfac_preference_loss(item: PreferenceLoss, workspace: Optional[torch.Tensor]
     return ws
 
 
+# ------------------------------------------------------------ drafted tokens
+
+@dataclass
+class VerifyDraft:
+    """Drafted tokens [rows] (int64 or int32) verified under the policy's logits [rows,
+    vocab] (rules in kfac.h).  Sequence b of seq_offsets (int32 [seqs + 1]) holds its
+    drafted tokens' rows and one more.  accepted int32 [seqs]; out_tokens [rows] of tokens'
+    dtype (may be tokens): the tokens and -1 behind them; logp fp32 [rows].  draft: the scores
+    [rows, vocab] of the logits' dtype that the tokens were drawn from (None: looked up),
+    draft_saved their fp32 [rows, 2] from TokenLogprob.saved; uniform fp32 [rows], noise fp32
+    [seqs, vocab].  greedy takes none of these."""
+    logits: torch.Tensor
+    tokens: torch.Tensor
+    seq_offsets: torch.Tensor
+    accepted: torch.Tensor
+    out_tokens: torch.Tensor
+    logp: Optional[torch.Tensor] = None
+    draft: Optional[torch.Tensor] = None
+    draft_saved: Optional[torch.Tensor] = None
+    uniform: Optional[torch.Tensor] = None
+    noise: Optional[torch.Tensor] = None
+    greedy: bool = False
+    temperature: float = 1.0
+    draft_temperature: float = 1.0
+
+
+def _verify_desc(t: VerifyDraft) -> VerifyDesc:
+    n, seqs = t.logits.shape[0], t.seq_offsets.numel() - 1
+    dtype, logits, ld, rows, vocab, tokens, i32, tau = _logits_args(t.logits, t.tokens, t.temperature)
+    draft, ld_draft = _dlogits_args(t.logits, t.draft, "draft")
+    noise, ld_noise = None, 0
+    if t.noise is not None:
+        if t.noise.dtype is not torch.float32:
+            raise TypeError(f"noise must be fp32, got {t.noise.dtype}")
+        if t.noise.shape != (seqs, vocab) or (t.noise.stride(1) != 1 and vocab > 1):
+            raise ValueError(f"noise must be [{seqs}, {vocab}] with unit column stride, got {tuple(t.noise.shape)}")
+        noise, ld_noise = t.noise.data_ptr(), t.noise.stride(0) if seqs > 1 else vocab
+    return VerifyDesc(dtype, logits, ld, rows, vocab, tokens, i32, tau,
+                      _rowvec(t.seq_offsets, seqs + 1, "seq_offsets", torch.int32), seqs, draft, ld_draft,
+                      _rowvec(t.draft_saved, 2 * n, "draft_saved"), t.draft_temperature,
+                      _rowvec(t.uniform, n, "uniform"), noise, ld_noise, bool(t.greedy),
+                      _rowvec(t.accepted, seqs, "accepted", torch.int32),
+                      _rowvec(t.out_tokens, n, "out_tokens", t.tokens.dtype), _rowvec(t.logp, n, "logp"))
+
+
+def kfac_verify_draft_workspace_size(item: VerifyDraft) -> int:
+    return int(load().kfac_verify_draft_workspace_size(ctypes.byref(_verify_desc(item))))
+
+
+def kfac_verify_draft(item: VerifyDraft, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Enqueue the verification; returns the workspace used (its first int32 is the device
+    error word: ERRW_TARGET, ERRW_NONFINITE)."""
+    lib = load()
+    d = _verify_desc(item)
+    p = ctypes.byref(d)
+    ws = _scratch(lib.kfac_verify_draft_workspace_size(p), item.logits.device, workspace, stream)
+    _check(lib.kfac_verify_draft(p, ws.data_ptr(), ws.nbytes, _stream(stream)), "kfac_verify_draft")
+    return ws
+
+
 # ------------------------------------------------------------ norm, clipping, weight step
 
 @dataclass
@@ -786,5 +1013,7 @@ def kfac_clip_norm(tensors, max_norm: float, norm: Optional[torch.Tensor] = None
     ws = _scratch(c.need, c.device, workspace, stream)
     _check(load().kfac_clip_norm(c.descs, len(c.tensors), max_norm, eta, _rowvec(norm, 1, "norm"),
                                  _rowvec(scale, 1, "scale"), ws.data_ptr(), ws.nbytes, _stream(stream)),
-           "kfac_clip_norm")
+           "kfac_clip_norm", "kfac_checkpoint_scale_bytes", "kfac_checkpoint_store", "kfac_checkpoint_load",
+           "kfac_weight_grad_workspace_size", "kfac_weight_grad", "kfac_verify_draft_workspace_size",
+           "kfac_verify_draft")
     return ws
