@@ -9,7 +9,7 @@
 //
 // Bound by memory: every row of logits is read once, and one row of each sequence again.
 // Each quotient is formed from fp32 probabilities (relative error about 1e-6); what
-// accepts a token is compared in fp64.
+// accepts a token is compared in fp64 where fp32 could err.
 #include <algorithm>
 #include <cmath>
 
@@ -40,7 +40,7 @@ struct Params {
     float *logp;
     // scratch
     float4 *parts;  // [units][splits]: maximum, sum, its index (greedy)
-    float4 *best;   // [seqs][pick_splits]: quotient of r, its index, of p, its index
+    float2 *best;   // [seqs][pick_splits]: the largest quotient, its index
     unsigned *done; // [seqs]
     int *err;
     int splits, pick_splits;
@@ -188,11 +188,26 @@ template <int DT>
 __device__ __forceinline__ float score(const Scores &S, long long row, int j) {
     return Elem<DT>::value(((const typename Elem<DT>::bits *)(S.z + row * S.ld_bytes))[j]);
 }
-// ln of a score's probability.
-__device__ __forceinline__ double log_prob(float z, float m, float s, float tau) {
-    return ((double)z - (double)m) / (double)tau - log((double)s);
-}
 __device__ __forceinline__ bool distribution(float s) { return s > 0.f && s <= F32_MAX; }
+__device__ __forceinline__ float log_prob(float z, const Stat &s, float tau) {
+    return (z - s.m) / tau - LN2 * log2f(s.s);
+}
+// Whether u < p / q.  In fp32 where the two are further apart than its error, else in fp64.
+__device__ __noinline__ bool below_exact(float u, float zp, Stat p, float taup, float zq, Stat q, float tauq) {
+    const double lp = ((double)zp - (double)p.m) / (double)taup - log((double)p.s);
+    const double lq = q.s > 0.f ? ((double)zq - (double)q.m) / (double)tauq - log((double)q.s) : 0.;
+    return (double)u < exp(lp - lq);  // (q = 0: infinite where p > 0; both 0: NaN, not below)
+}
+// q.s = 0: a token that was not drawn, q = 1.
+__device__ __forceinline__ bool below_ratio(float u, float zp, const Stat &p, const Scores &P, float zq, const Stat &q,
+                                            const Scores &Q) {
+    const float yp = (zp - p.m) * P.k, yq = q.s > 0.f ? (zq - q.m) * Q.k : 0.f;
+    const float ratio = exp2f((yp - log2f(p.s)) - (q.s > 0.f ? yq - log2f(q.s) : 0.f));
+    const float off = 1e-5f + 4e-7f * (fabsf(yp) + fabsf(yq));
+    if (u < ratio * (1.f - off)) return true;
+    if (u > ratio * (1.f + off)) return false;
+    return below_exact(u, zp, p, P.tau, zq, q, Q.tau);
+}
 
 // What became of a row: its token accepted; replaced by a draw from r, or from p; or no
 // distribution to draw from.
@@ -208,176 +223,248 @@ struct Best {
         }
     }
 };
+__device__ __forceinline__ Best best_of_warp(Best b) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float k = __shfl_xor_sync(ALL_LANES, b.key, o);
+        const int j = __shfl_xor_sync(ALL_LANES, b.at, o);
+        b.take(k, j);
+    }
+    return b;
+}
+// On every thread of warp 0.
+__device__ __forceinline__ Best best_of_block(Best b, Best *shared) {
+    b = best_of_warp(b);
+    if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = b;
+    __syncthreads();
+    return best_of_warp(threadIdx.x % 32 < PICK_WARPS ? shared[threadIdx.x % 32] : Best{0.f, NONE});
+}
+
+// A row's probabilities, of which one is drawn: p, or r = max(p - q, 0).
+struct Row2 {
+    Stat p, q;
+    float lp, lq;  // log2 of the sums
+    float kp, kq;
+    long long x;   // FROM_R of a token that was not drawn: the token (q = 1 there)
+    bool drafted;
+    __device__ __forceinline__ float value(float zp, float zq) const {
+        const float a = ex2(fmaf(zp - p.m, kp, -lp));
+        return drafted ? a - ex2(fmaf(zq - q.m, kq, -lq)) : a;
+    }
+    __device__ __forceinline__ void take(Best &b, float v, float e, int j) const {
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaxf(e, 1.17549435e-38f)));
+        const float key = v * inv;
+        if (key > b.key && j != x) {
+            b.key = key;
+            b.at = j;
+        }
+    }
+};
+
+// The part of a row from a group on, with its noise: 16-byte groups of the policy's scores, the
+// draft's at the same alignment, the noise at any.
+template <int DT, bool ANY, bool DRAFTED>
+__device__ __forceinline__ void race_groups(const Row2 &R, const Row<DT> &zp, const char *zq, const float *E, int g0, int g1,
+                                            Best &best) {
+    constexpr int N = Elem<DT>::N, STEP = PICK_THREADS, PER = 2;
+    const int off = (int)((uintptr_t)(E + zp.first(g0)) & 15);
+#pragma unroll 1
+    for (int g = g0 + threadIdx.x; g < g1; g += PER * STEP) {
+        uint4 u[PER], w[PER];
+        Pieces<N / 4, ANY> e[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int h = min(g + i * STEP, g1 - 1);  // (the last group again where there is none)
+            u[i] = zp.load_whole(h);
+            if (DRAFTED) w[i] = ld16(zq + (size_t)h * 16);
+            e[i].load((const char *)(E + zp.first(h)), off);
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int h = min(g + i * STEP, g1 - 1);
+            float a[N], b[N];
+            uint4 f[N / 4];
+            Elem<DT>::unpack(u[i], a);
+            if (DRAFTED) Elem<DT>::unpack(w[i], b);
+            e[i].take(off, f);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t bits[4] = {f[j / 4].x, f[j / 4].y, f[j / 4].z, f[j / 4].w};
+                R.take(best, R.value(a[j], DRAFTED ? b[j] : 0.f), __uint_as_float(bits[j % 4]), zp.first(h) + j);
+            }
+        }
+    }
+}
+// The race over elements j0 .. j1 - 1 of a row; on every thread its own best.  By 16-byte groups
+// where policy and draft lie alike (rows of one pitch do), else element by element: 256 rows
+// of 131072 bf16 took 361 us element by element.
+template <int DT>
+__device__ __forceinline__ Best race(const Params &P, const Row2 &R, long long row, int seq, int j0, int j1) {
+    using bits = typename Elem<DT>::bits;
+    const char *p = P.target.z + row * P.target.ld_bytes, *q = P.draft.z + row * P.draft.ld_bytes;
+    const float *E = P.noise + seq * P.ld_noise;
+    Best b{0.f, NONE};
+    auto one = [&](int j) {
+        R.take(b, R.value(Elem<DT>::value(((const bits *)p)[j]), R.drafted ? Elem<DT>::value(((const bits *)q)[j]) : 0.f), E[j], j);
+    };
+    if (R.drafted && (((uintptr_t)p ^ (uintptr_t)q) & 15) != 0) {
+#pragma unroll 4
+        for (int j = j0 + threadIdx.x; j < j1; j += PICK_THREADS) one(j);
+        return b;
+    }
+    // the groups that start in the part, and the row's edges
+    const Row<DT> r(p, P.vocab);
+    constexpr int N = Elem<DT>::N;
+    const int g0 = max(r.begin(), (j0 + r.phase + N - 1) / N), g1 = min(r.end(), (j1 + r.phase + N - 1) / N);
+    const int front = r.begin() * N - r.phase, back = r.end() * N - r.phase;  // first elements of the whole groups, and behind them
+    if (j0 == 0 && (int)threadIdx.x < front && (int)threadIdx.x < P.vocab) one(threadIdx.x);
+    if (g0 < g1) {
+        const char *qb = R.drafted ? q - r.phase * (int)sizeof(bits) : nullptr;
+        const bool any = ((uintptr_t)(E + r.first(g0)) & 15) != 0;
+        if (R.drafted && any) race_groups<DT, true, true>(R, r, qb, E, g0, g1, b);
+        else if (R.drafted) race_groups<DT, false, true>(R, r, qb, E, g0, g1, b);
+        else if (any) race_groups<DT, true, false>(R, r, qb, E, g0, g1, b);
+        else race_groups<DT, false, false>(R, r, qb, E, g0, g1, b);
+    }
+    if (j1 == P.vocab && back + (int)threadIdx.x < P.vocab && back >= front) one(back + threadIdx.x);
+    return b;
+}
 
 template <int DT>
 __global__ void __launch_bounds__(PICK_THREADS) verify_pick_kernel(const __grid_constant__ Params P) {
     __shared__ Stat pol[PICK_WARPS], dra[PICK_WARPS];
-    __shared__ int fate_of, at_of;
-    __shared__ Best rs[PICK_WARPS], ps[PICK_WARPS];
+    __shared__ int fates[PICK_WARPS], flags[PICK_WARPS], new_token;
+    __shared__ Best bests[PICK_WARPS];
     __shared__ bool last;
-    pdl_wait();
-    pdl_trigger();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int seq = blockIdx.x / P.pick_splits, split = blockIdx.x % P.pick_splits;
+    const int per = (P.vocab + P.pick_splits - 1) / P.pick_splits;
+    const int j0 = min(P.vocab, split * per), j1 = min(P.vocab, j0 + per);
+    if (!P.greedy && tid == 0 && j1 > j0) {  // this part of the noise on its way to L2 while the sums are made
+        const uintptr_t a = (uintptr_t)(P.noise + seq * P.ld_noise + j0) & ~(uintptr_t)15;
+        const uintptr_t b = (uintptr_t)(P.noise + seq * P.ld_noise + j1) & ~(uintptr_t)15;
+        if (b > a) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)(b - a)) : "memory");
+    }
+    pdl_wait();
+    pdl_trigger();
     const long long r0 = row_at(P, seq), r1 = row_at(P, seq + 1);
     if (r1 <= r0) {
         if (split == 0 && tid == 0) P.accepted[seq] = 0;
         return;
     }
     const bool drafted = P.draft.z && !P.greedy;
-    // the walk, eight rows at a time
-    Stat p{}, q{};
+    // the walk, a row to a warp, eight at a time
     long long row = r0;
-    int fate = ACCEPTED;
-    for (; fate == ACCEPTED; row += PICK_WARPS) {
-        if (row + warp < r1) {
-            const long long i = row + warp;
+    int fate = ACCEPTED, at = 0;
+    for (;; row += PICK_WARPS) {
+        const long long i = row + warp;
+        if (i < r1) {
+            const bool bonus = i + 1 == r1;
+            const long long x = bonus ? -1 : token_at(P, i);
+            const bool is = x >= 0 && x < P.vocab;
+            float zp = 0.f, zq = 0.f, u = 0.f;
+            if (is) {
+                zp = score<DT>(P.target, i, (int)x);
+                if (drafted) zq = score<DT>(P.draft, i, (int)x);
+                if (!P.greedy) u = P.uniform[i];
+            }
             const Stat s = join(P.parts + i * P.splits, P.splits, P.target.k, lane);
-            if (lane == 0) pol[warp] = s;
-            if (drafted && i + 1 < r1) {
-                Stat d;
+            Stat d{0.f, 0.f, NONE};
+            if (drafted && !bonus) {
                 if (P.saved) d = Stat{P.saved[i].x, P.saved[i].y, NONE};
                 else d = join(P.parts + (P.rows + i) * P.splits, P.splits, P.draft.k, lane);
-                if (lane == 0) dra[warp] = d;
+            }
+            int f = ACCEPTED, bits = !bonus && x >= P.vocab ? ERR_TARGET : 0;
+            if (!distribution(s.s)) {
+                f = NOTHING;
+                bits = ERR_NONFINITE;
+            } else if (P.greedy) {
+                if (bonus || x != s.index) f = FROM_P;
+            } else if (!is) {
+                f = FROM_P;
+            } else if (drafted && !distribution(d.s)) {
+                f = FROM_P;
+                bits = ERR_NONFINITE;
+            } else if (!below_ratio(u, zp, s, P.target, zq, d, P.draft)) {
+                f = FROM_R;
+            }
+            if (lane == 0) {
+                pol[warp] = s;
+                dra[warp] = d;
+                fates[warp] = f;
+                flags[warp] = bits;
             }
         }
         __syncthreads();
-        if (warp == 0) {
-            const long long i = row + lane;
-            const bool in = lane < PICK_WARPS && i < r1;
-            int f = ACCEPTED, bits = 0;
-            long long x = -1;
-            double lp = 0.;
-            if (in) {
-                const Stat s = pol[lane];
-                if (!distribution(s.s)) {
-                    f = NOTHING;
-                    bits = ERR_NONFINITE;
-                } else if (i + 1 == r1) {
-                    f = FROM_P;
-                } else {
-                    x = token_at(P, i);
-                    const bool is = x >= 0 && x < P.vocab;
-                    if (x >= P.vocab) bits = ERR_TARGET;
-                    if (is) lp = log_prob(score<DT>(P.target, i, (int)x), s.m, s.s, P.target.tau);
-                    if (P.greedy) {
-                        if (x != s.index) f = FROM_P;
-                    } else if (!is) {
-                        f = FROM_P;
-                    } else {
-                        double ratio = exp(lp);
-                        if (drafted) {
-                            const Stat d = dra[lane];
-                            if (!distribution(d.s)) {
-                                f = FROM_P;
-                                bits = ERR_NONFINITE;
-                            } else {
-                                // (q = 0 and p > 0: infinite; both 0: NaN, and not accepted)
-                                ratio = exp(lp - log_prob(score<DT>(P.draft, i, (int)x), d.m, d.s, P.draft.tau));
-                            }
-                        }
-                        if (f == ACCEPTED && !((double)P.uniform[i] < ratio)) f = FROM_R;
-                    }
-                }
+        const int n = (int)min((long long)PICK_WARPS, r1 - row);
+        for (at = 0; at < n && fates[at] == ACCEPTED;) ++at;
+        if (split == 0) {
+            if (i < r1 && warp < at && lane == 0) {  // accepted (the token is what it was where out is tokens)
+                const int x = (int)token_at(P, i);
+                put_token(P, i, x);
+                if (P.logp) P.logp[i] = log_prob(score<DT>(P.target, i, x), pol[warp], P.target.tau);
             }
-            const unsigned stops = __ballot_sync(ALL_LANES, in && f != ACCEPTED);
-            const int at = stops ? __ffs(stops) - 1 : 32;
-            if (split == 0 && in && lane < at) {  // (the token is what it was where out is tokens)
-                put_token(P, i, (int)x);
-                if (P.logp) P.logp[i] = (float)lp;
-            }
-            if (lane > at) bits = 0;
-            bits = __reduce_or_sync(ALL_LANES, bits);
-            if (stops ? lane == at : lane == 0) {
-                fate_of = stops ? f : ACCEPTED;
-                at_of = at;
-                if (split == 0 && bits) atomicOr(P.err, bits);
-            }
+            if (tid <= at && tid < n && flags[tid]) atomicOr(P.err, flags[tid]);
         }
-        __syncthreads();
-        fate = fate_of;
-        if (fate != ACCEPTED) {
-            p = pol[at_of];
-            q = dra[at_of];
-            row += at_of - PICK_WARPS;  // (the loop's step)
-        }
+        if (at < n) break;
         __syncthreads();
     }
-    if (!P.greedy) {
-        // this CTA's part of the new token's row
-        Best br{0.f, NONE}, bp{0.f, NONE};
-        if (fate == FROM_R || fate == FROM_P) {
-            const int per = (P.vocab + P.pick_splits - 1) / P.pick_splits;
-            const int j0 = split * per, j1 = min(P.vocab, j0 + per);
-            using bits = typename Elem<DT>::bits;
-            const bits *zp = (const bits *)(P.target.z + row * P.target.ld_bytes);
-            const bits *zq = (const bits *)(P.draft.z + row * P.draft.ld_bytes);
-            const float *E = P.noise + seq * P.ld_noise;
-            const float ip = 1.f / p.s, iq = 1.f / q.s;
-            const bool residual = fate == FROM_R;
-            const long long x = residual && !drafted ? token_at(P, row) : -1;
-            for (int j = j0 + tid; j < j1; j += PICK_THREADS) {
-                const float e = fmaxf(E[j], 1.17549435e-38f);
-                const float a = ex2((Elem<DT>::value(zp[j]) - p.m) * P.target.k) * ip;
-                if (a > 0.f) bp.take(a / e, j);
-                if (residual) {
-                    const float b = drafted ? ex2((Elem<DT>::value(zq[j]) - q.m) * P.draft.k) * iq : j == x ? a : 0.f;
-                    if (a > b) br.take((a - b) / e, j);
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float kr = __shfl_xor_sync(ALL_LANES, br.key, o), kp = __shfl_xor_sync(ALL_LANES, bp.key, o);
-            const int jr = __shfl_xor_sync(ALL_LANES, br.at, o), jp = __shfl_xor_sync(ALL_LANES, bp.at, o);
-            br.take(kr, jr);
-            bp.take(kp, jp);
-        }
-        if (lane == 0) {
-            rs[warp] = br;
-            ps[warp] = bp;
-        }
-        __syncthreads();
+    fate = fates[at];
+    row += at;
+    Row2 R;
+    R.p = pol[at];
+    R.q = dra[at];
+    R.lp = log2f(R.p.s);
+    R.kp = P.target.k;
+    R.kq = P.draft.k;
+    R.drafted = fate == FROM_R && drafted;
+    R.lq = R.drafted ? log2f(R.q.s) : 0.f;
+    R.x = fate == FROM_R && !drafted ? token_at(P, row) : -1;
+    int token = -1;
+    if (P.greedy) {
+        if (fate != NOTHING) token = R.p.index;
+    } else {
+        // this CTA's part of the new token's row; the last CTA joins the parts
+        Best b{0.f, NONE};
+        if (fate != NOTHING) b = race<DT>(P, R, row, seq, j0, j1);
+        b = best_of_block(b, bests);
         if (tid == 0) {
-            for (int w = 1; w < PICK_WARPS; ++w) {
-                br.take(rs[w].key, rs[w].at);
-                bp.take(ps[w].key, ps[w].at);
-            }
-            P.best[blockIdx.x] = make_float4(br.key, __int_as_float(br.at), bp.key, __int_as_float(bp.at));
+            P.best[blockIdx.x] = make_float2(b.key, __int_as_float(b.at));
             __threadfence();
             last = atomicAdd(&P.done[seq], 1u) == P.pick_splits - 1;
             __threadfence();
         }
         __syncthreads();
         if (!last) return;
-    }
-    if (warp == 0) {
-        int token = -1;
-        if (P.greedy) {
-            if (fate != NOTHING) token = p.index;
-        } else if (fate != NOTHING) {
-            Best br{0.f, NONE}, bp{0.f, NONE};
+        if (warp == 0) {
+            Best all{0.f, NONE};
             for (int i = lane; i < P.pick_splits; i += 32) {
-                const float4 b = __ldcg(P.best + (long long)seq * P.pick_splits + i);
-                br.take(b.x, __float_as_int(b.y));
-                bp.take(b.z, __float_as_int(b.w));
+                const float2 c = __ldcg(P.best + (long long)seq * P.pick_splits + i);
+                all.take(c.x, __float_as_int(c.y));
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float kr = __shfl_xor_sync(ALL_LANES, br.key, o), kp = __shfl_xor_sync(ALL_LANES, bp.key, o);
-                const int jr = __shfl_xor_sync(ALL_LANES, br.at, o), jp = __shfl_xor_sync(ALL_LANES, bp.at, o);
-                br.take(kr, jr);
-                bp.take(kp, jp);
-            }
-            token = br.at != NONE ? br.at : bp.at;
+            all = best_of_warp(all);
+            if (lane == 0) new_token = all.at;
         }
-        if (lane == 0) {
-            P.accepted[seq] = (int)(row - r0);
-            put_token(P, row, token);
-            if (P.logp)
-                P.logp[row] = token < 0 ? __int_as_float(0x7fc00000)
-                                        : (float)log_prob(score<DT>(P.target, row, token), p.m, p.s, P.target.tau);
+        __syncthreads();
+        token = new_token;
+        if (token == NONE && fate == FROM_R) {  // r is nothing (p and q are equal): from p, by this CTA alone
+            R.drafted = false;
+            R.x = -1;
+            b = race<DT>(P, R, row, seq, 0, P.vocab);
+            __syncthreads();
+            b = best_of_block(b, bests);
+            if (tid == 0) new_token = b.at;
+            __syncthreads();
+            token = new_token;
         }
+        if (token == NONE) token = -1;
+    }
+    if (tid == 0) {
+        P.accepted[seq] = (int)(row - r0);
+        put_token(P, row, token);
+        if (P.logp)
+            P.logp[row] = token < 0 ? __int_as_float(0x7fc00000) : log_prob(score<DT>(P.target, row, token), R.p, P.target.tau);
     }
     for (long long i = row + 1 + tid; i < r1; i += PICK_THREADS) {
         put_token(P, i, -1);
@@ -427,7 +514,7 @@ void plan(const kfac_verify_desc &d, Arena &ws, Params &P) {
     P.pick_splits = s.pick;
     P.err = ws.take<int>(64);
     P.parts = ws.take<float4>((size_t)s.units * s.stats);
-    P.best = ws.take<float4>((size_t)d.seqs * s.pick);
+    P.best = ws.take<float2>((size_t)d.seqs * s.pick);
     P.done = ws.take<unsigned>((size_t)d.seqs);
 }
 
