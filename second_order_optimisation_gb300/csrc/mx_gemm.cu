@@ -8,14 +8,20 @@
 // CHUNK tokens are added up in registers with fp32's own rounding, because a long sum in
 // one tensor-core accumulator loses bits.
 //
-// A persistent kernel of ten warps: one brings operand tiles by TMA, one thread issues the
-// products, and eight take the accumulator out of tensor memory into registers at once,
-// so that the next tile's products start before this one's stores.
+// A persistent kernel, a pair of CTAs (two SMs) to a tile of 256 x 256: each brings half of
+// both operands, and the pair's products (cta_group::2) read both halves, so that a byte
+// brought to an SM serves 128 products (a tile of 128 x 128 on one SM: 64, and the
+// operands' way to the SMs held it at 1.46 PFLOP/s).  In each CTA one warp brings operand tiles
+// by TMA and eight take the accumulator out of tensor memory into registers at once, so that
+// the next tile's products start before this one's stores; one thread of the first CTA issues
+// the products of both.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <memory>
 #include <mutex>
+#include <type_traits>
 #include <vector>
 
 #include "internal.h"
@@ -23,15 +29,22 @@
 namespace kfac {
 namespace {
 
-constexpr int BM = 128, BN = 128, BK = 128;  // a CTA's tile: features x features, tokens a stage
+constexpr int HALF = 128, TILE = 2 * HALF, BK = 128;  // a CTA's rows, the pair's tile, tokens a stage
 constexpr int STAGES = 5;
 constexpr int TILE_BYTES = 128 * 128, SF_BYTES = 512;
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-constexpr int SF_STAGE = 2 * SF_BYTES;
-constexpr int EPI_WARPS = 8, NUM_THREADS = 64 + 32 * EPI_WARPS;
-constexpr int COLS = BN / 2;  // accumulator columns of an epilogue warp
-constexpr int LD = 33;        // pitch of its staging chunk
-constexpr int SF_COL = 256, SF_SLOT = 16;  // tensor memory: exponents, a slot for each stage
+constexpr int SF_STAGE = 3 * SF_BYTES;  // a stage's exponents: of the CTA's rows, and of all columns
+// Four warps (two of them idle) and eight with the accumulator in registers: the register
+// file is split 56 : 224 : 224 a thread among the three groups of four (504 = 3 * 168 at launch).
+constexpr int EPI_WARPS = 8, FIRST_EPI = 4, NUM_THREADS = 32 * (FIRST_EPI + EPI_WARPS);
+constexpr int FEW_REGS = 56, MANY_REGS = 224;
+constexpr int COLS = TILE / 2;  // accumulator columns of an epilogue warp
+constexpr int LD = 36;        // pitch of its staging chunk
+// Tensor memory: the accumulator at column 0 and, of every other chunk, at column 192, so that
+// a chunk's products may start when the 64 columns that both have are taken out of the one
+// before; and the exponents, a slot for each stage.
+constexpr int ACC_SHIFT = 192, SF_COL = 448, SF_SLOT = 12;
+static_assert(SF_COL + STAGES * SF_SLOT <= 512 && ACC_SHIFT + TILE <= SF_COL && TILE - ACC_SHIFT == 64, "tensor memory");
 constexpr int TMEM_COLS = 512;
 constexpr int MAX_PROBS = 48, GROUP = 8;
 constexpr int CHUNK = 16;  // stages (2048 tokens) in one accumulator
@@ -46,7 +59,7 @@ struct Prob {
     long long ldc;
     int M, N, k_tiles, tiles_m, tiles_n, ksplit, work_begin;
     float alpha, beta;
-    uint8_t sym, packed, c_dtype;
+    uint8_t sym, packed, c_dtype, vec;
 };
 struct Params {
     Prob prob[MAX_PROBS];
@@ -116,9 +129,10 @@ __device__ __forceinline__ uint64_t operand(uint32_t tile, int slice) {
 __device__ __forceinline__ uint64_t exponents(uint32_t at) {
     return (uint64_t)((at & 0x3FFFF) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
 }
-// Copies them to four columns of tensor memory, the same for each quarter of the lanes.
+// Copies them to four columns of tensor memory, the same for each quarter of the lanes; in
+// both CTAs, each its own.
 __device__ __forceinline__ void copy_exponents(uint32_t tmem, uint32_t smem) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(exponents(smem)) : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(exponents(smem)) : "memory");
 }
 // Instruction descriptor: e4m3 operands, both MN-major, fp32 accumulator, exponents as
 // powers of two; `slice` is the byte of a column of exponents.
@@ -131,52 +145,170 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 
-__device__ __forceinline__ float old_value(const Prob &q, long long at) {
-    if (q.c_dtype == KFAC_F32) return ((const float *)q.C)[at];
-    const uint16_t b = ((const uint16_t *)q.C)[at];
-    return q.c_dtype == KFAC_F16 ? __half2float(__ushort_as_half(b)) : bf16_bits_to_f32(b);
+// Arrives on `bar` of both CTAs when every product issued so far is done.
+__device__ __forceinline__ void commit_both(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// The address of the first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t of_first(const void *p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(0));
+    return a;
+}
+// A tile into this CTA's shared memory, its bytes counted on the first CTA's barrier.
+__device__ __forceinline__ void load_pair(void *dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t at) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(TMEM_COLS) : "memory");
 }
 
-// Stores 32 rows x 32 columns at (i0, j0): v is a row to a lane; through the warp's
-// stage, so that a lane then has a column and every access of a warp is one run of a row, at
-// any pitch or packing.  Returns whether a value was NaN or infinite.
-__device__ __forceinline__ bool store_chunk(const Prob &q, int i0, int j0, const float *v, float *stage, int lane) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) stage[lane * LD + c] = v[c];
-    __syncwarp();
-    const int rows = min(32, q.M - i0), j = j0 + lane;
-    bool bad = false;
-    if (j0 < q.N && (!q.sym || j0 + 31 >= i0)) {
-        const bool in = j < q.N;
+__device__ __forceinline__ float from_16(uint32_t b, bool f16) {
+    return f16 ? __half2float(__ushort_as_half((uint16_t)b)) : bf16_bits_to_f32((uint16_t)b);
+}
+
+
+// The part inside the result (on and above the diagonal of a symmetric one) of 32 rows x 32
+// columns at (i0, j0): a column to a lane, a row to an instruction, at any pitch or packing.
+// Short loops: what it takes is mostly the fetching of its code (a chunk 6.5 us with
+// the types told apart at every row and 16 rows unrolled).
+template <int DT>
+__device__ __forceinline__ bool store_edge(const Prob &q, int i0, int j0, float *stage, int lane) {
+    using T = std::conditional_t<DT == KFAC_F32, float, uint16_t>;
+    const int j = j0 + lane, rows = min(32, q.M - i0);
+    const int n = j >= q.N ? 0 : q.sym ? min(rows, j - i0 + 1) : rows;  // rows of this lane's column
+    // a packed triangle's row i starts (j counted from 0) at i N - i (i + 1) / 2
+    const int shorter = q.packed ? 1 : 0;
+    const long long first = (shorter ? (long long)i0 * q.N - (long long)i0 * (i0 + 1) / 2 : (long long)i0 * q.ldc) + j;
+    const long long pitch = shorter ? q.N - 1 - i0 : q.ldc;  // to the next row, one less each time in a triangle
+    T *C = (T *)q.C;
+    float scale = q.alpha;
+    if (const float beta = q.beta; beta != 0.f) {
+        long long at = first, to = pitch;
 #pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-            float old[8];
-            long long at[8];
-            bool is[8];
+        for (int r0 = 0; r0 < 32; r0 += 16) {
+            T old[16];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int i = i0 + r0 + r;
-                is[r] = in && r0 + r < rows && (!q.sym || j >= i);
-                at[r] = (q.packed ? (long long)i * q.N - (long long)i * (i + 1) / 2 : (long long)i * q.ldc) + j;
-                old[r] = q.beta != 0.f && is[r] ? old_value(q, at[r]) : 0.f;
+            for (int r = 0; r < 16; ++r) {
+                old[r] = T(0);
+                if (r0 + r < n) old[r] = C[at];
+                at += to;
+                to -= shorter;
             }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                if (!is[r]) continue;
-                const float x = fmaf(q.beta, old[r], q.alpha * stage[(r0 + r) * LD + lane]);
-                bad |= !(fabsf(x) <= 3.402823466e38f);
-                if (q.c_dtype == KFAC_F32) ((float *)q.C)[at[r]] = x;
-                else ((uint16_t *)q.C)[at[r]] = f32_to_16_bits(x, q.c_dtype == KFAC_F16);
+            for (int r = 0; r < 16; ++r) {
+                float &v = stage[(r0 + r) * LD + lane];
+                if constexpr (DT == KFAC_F32) v = fmaf(beta, old[r], scale * v);
+                else v = fmaf(beta, from_16(old[r], DT == KFAC_F16), scale * v);
             }
         }
+        scale = 1.f;
     }
-    __syncwarp();
+    bool bad = false;
+    long long at = first, to = pitch;
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r) {
+        const float v = scale * stage[r * LD + lane];
+        if (r < n) {
+            bad |= !(fabsf(v) <= 3.402823466e38f);
+            if constexpr (DT == KFAC_F32) C[at] = v;
+            else C[at] = f32_to_16_bits(v, DT == KFAC_F16);
+        }
+        at += to;
+        to -= shorter;
+    }
     return bad;
+}
+
+// Stores the 32 rows x 32 columns at (i0, j0) that a warp has in its stage (pitch LD).
+// Returns whether a value was NaN or infinite.  Chunks inside the result whose rows start on
+// 16-byte boundaries (8-byte ones of 16-bit values) go four values to a lane, four rows to an
+// instruction; others go through store_edge.
+__device__ __forceinline__ bool store_chunk(const Prob &q, int i0, int j0, float *stage, int lane) {
+    bool bad = false;
+    if (j0 >= q.N || i0 >= q.M || (q.sym && j0 + 31 < i0)) return false;
+    const float alpha = q.alpha, beta = q.beta;
+    if (q.vec && i0 + 32 <= q.M && j0 + 32 <= q.N && (!q.sym || j0 >= i0 + 32)) {
+        const int r = lane >> 3, c = 4 * (lane & 7);
+        const long long ldc = q.ldc, at = (long long)(i0 + r) * ldc + j0 + c, step = 4 * ldc;
+        if (q.c_dtype == KFAC_F32) {
+            float *dst = (float *)q.C + at;
+            float4 old[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                old[k] = beta != 0.f ? *(const float4 *)(dst + k * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 v = *(const float4 *)(stage + (4 * k + r) * LD + c);
+                const float4 o = make_float4(fmaf(beta, old[k].x, alpha * v.x), fmaf(beta, old[k].y, alpha * v.y),
+                                             fmaf(beta, old[k].z, alpha * v.z), fmaf(beta, old[k].w, alpha * v.w));
+                bad |= !finite4(o);
+                *(float4 *)(dst + k * step) = o;
+            }
+        } else {
+            uint16_t *dst = (uint16_t *)q.C + at;
+            const bool h = q.c_dtype == KFAC_F16;
+            uint2 old[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) old[k] = beta != 0.f ? *(const uint2 *)(dst + k * step) : make_uint2(0, 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float4 v = *(const float4 *)(stage + (4 * k + r) * LD + c);
+                const float4 o =
+                    make_float4(fmaf(beta, from_16(old[k].x, h), alpha * v.x), fmaf(beta, from_16(old[k].x >> 16, h), alpha * v.y),
+                                fmaf(beta, from_16(old[k].y, h), alpha * v.z), fmaf(beta, from_16(old[k].y >> 16, h), alpha * v.w));
+                bad |= !finite4(o);
+                *(uint2 *)(dst + k * step) =
+                    make_uint2(f32_to_16_bits(o.x, h) | (uint32_t)f32_to_16_bits(o.y, h) << 16,
+                               f32_to_16_bits(o.z, h) | (uint32_t)f32_to_16_bits(o.w, h) << 16);
+            }
+        }
+        return bad;
+    }
+    if (q.c_dtype == KFAC_F32) return store_edge<KFAC_F32>(q, i0, j0, stage, lane);
+    if (q.c_dtype == KFAC_F16) return store_edge<KFAC_F16>(q, i0, j0, stage, lane);
+    return store_edge<KFAC_BF16>(q, i0, j0, stage, lane);
+}
+
+__device__ __forceinline__ bool all_of(bool ok) { return __all_sync(0xffffffffu, ok); }
+// True on one lane of a warp that is here as a whole.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// The warp has read what the next chunk's accumulator overlaps.
+__device__ __forceinline__ void released_by(uint32_t bar, int lane) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_at(bar);
+}
+template <int AT>
+__device__ __forceinline__ void add_columns(float (&v)[COLS], const float (&t)[32], const Work &k) {
+    if (k.kt0 >= k.kt1) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[AT + i] += t[i];
 }
 
 __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constant__ Params P) {
@@ -191,117 +323,149 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     volatile int *last_flag = abort_flag + 1;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = blockIdx.x & 1;
+    const int first_work = blockIdx.x >> 1, step = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(accf, 1);
-        mbar_init(acce, EPI_WARPS);
+        mbar_init(acce, 2 * EPI_WARPS);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(tmem_slot, TMEM_COLS);
+    if (warp == 1) tmem_alloc_pair(tmem_slot);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_trigger();
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < FIRST_EPI) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW_REGS));
+        // The whole of a warp runs its loop and one of its threads issues: what copies and products
+        // take (addresses, descriptors) is then the same for all lanes to the compiler, too.  Issued from
+        // a thread's own branch a stage's products took 0.45 us, more than the tensor cores do.
+        if (warp == 0) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
-            for (int w = blockIdx.x; w < P.total_work && !*abort_flag; w += gridDim.x) {
+            bool ok = true;
+            for (int w = first_work; w < P.total_work && ok; w += step) {
                 const Work k = decode(P, w);
                 const Prob &q = P.prob[k.p];
                 const bool same = q.sym && k.tm == k.tn;
-                for (int kt = k.kt0; kt < k.kt1 && !*abort_flag; ++kt) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1)) {
-                        atomicOr(P.err, ERR_TIMEOUT_EMPTY);
+                const uint32_t bytes = 2 * ((same ? 1 : 2) * TILE_BYTES + SF_STAGE);
+                const int i0 = k.tm * TILE + rank * HALF, j0 = k.tn * TILE + rank * HALF, k_tiles = q.k_tiles;
+                const int ta = (2 * k.tm + rank) * k_tiles, tb = 2 * k.tn * k_tiles;
+                for (int kt = k.kt0; kt < k.kt1; ++kt) {
+                    ok = all_of(mbar_wait(&empty[stage], phase ^ 1) && !*abort_flag);
+                    if (!ok) {
+                        if (lane == 0) atomicOr(P.err, ERR_TIMEOUT_EMPTY);
                         *abort_flag = 1;
                         break;
                     }
-                    mbar_arrive_expect_tx(&full[stage], (same ? 1 : 2) * (TILE_BYTES + SF_BYTES));
+                    const uint32_t bar = of_first(&full[stage]);
                     uint8_t *s = smem + stage * STAGE_BYTES, *f = sf + stage * SF_STAGE;
-                    tma_load_2d(s, &q.a, k.tm * BM, kt * BK, &full[stage]);
-                    tma_load_2d(f, &q.sa, 0, k.tm * q.k_tiles + kt, &full[stage]);
-                    if (!same) {
-                        tma_load_2d(s + TILE_BYTES, &q.b, k.tn * BN, kt * BK, &full[stage]);
-                        tma_load_2d(f + SF_BYTES, &q.sb, 0, k.tn * q.k_tiles + kt, &full[stage]);
+                    if (elect_one()) {
+                        // (both CTAs' bytes; the other's may be counted before they are expected)
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+                        load_pair(s, &q.a, i0, kt * BK, bar);
+                        if (!same) load_pair(s + TILE_BYTES, &q.b, j0, kt * BK, bar);
+                        load_pair(f, &q.sa, 0, ta + kt, bar);
+                        load_pair(f + SF_BYTES, &q.sb, 0, tb + kt, bar);
+                        load_pair(f + 2 * SF_BYTES, &q.sb, 0, tb + k_tiles + kt, bar);
                     }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                     ++issued;
                 }
             }
-            if (*abort_flag) {  // cut short: the copies that are on their way land before the CTA leaves
+            // cut short: the copies that are on their way land before the CTAs leave (both wait for each other)
+            if (!ok && rank == 0) {
                 for (int n = 0; n < min(issued, STAGES); ++n) {
                     if (stage == 0) { stage = STAGES - 1; phase ^= 1; } else { --stage; }
-                    if (!mbar_wait(&full[stage], phase)) atomicOr(P.err, ERR_TIMEOUT_DRAIN);
+                    if (!mbar_wait(&full[stage], phase) && lane == 0) atomicOr(P.err, ERR_TIMEOUT_DRAIN);
                 }
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
+        if (warp == 1 && rank == 0) {
             int stage = 0;
             uint32_t phase = 0, use = 0;
             bool ok = true;
-            for (int w = blockIdx.x; w < P.total_work && ok && !*abort_flag; w += gridDim.x) {
+            const uint32_t s0 = smem_u32(smem), f0 = smem_u32(sf);
+            for (int w = first_work; w < P.total_work && ok; w += step) {
                 const Work k = decode(P, w);
                 const Prob &q = P.prob[k.p];
                 const bool same = q.sym && k.tm == k.tn;
                 for (int c0 = k.kt0; ok; c0 += CHUNK) {
                     const int c1 = min(k.kt1, c0 + CHUNK);
-                    if (!mbar_wait(acce, (use & 1) ^ 1)) {
-                        atomicOr(P.err, ERR_TIMEOUT_ACC);
-                        *abort_flag = 1;
-                        ok = false;
+                    ok = all_of(mbar_wait(acce, (use & 1) ^ 1));
+                    if (!ok) {
+                        if (lane == 0) atomicOr(P.err, ERR_TIMEOUT_ACC);
                         break;
                     }
-                    ++use;
                     tc_fence_after();
+                    const uint32_t d = tmem + (use & 1) * ACC_SHIFT;
+                    ++use;
                     for (int kt = c0; kt < c1; ++kt) {
-                        if (!mbar_wait(&full[stage], phase)) {
-                            atomicOr(P.err, ERR_TIMEOUT_FULL);
-                            *abort_flag = 1;
-                            ok = false;
+                        ok = all_of(mbar_wait(&full[stage], phase));
+                        if (!ok) {
+                            if (lane == 0) atomicOr(P.err, ERR_TIMEOUT_FULL);
                             break;
                         }
                         tc_fence_after();
-                        const uint32_t a = smem_u32(smem + stage * STAGE_BYTES), b = same ? a : a + TILE_BYTES;
-                        const uint32_t f = smem_u32(sf + stage * SF_STAGE);
+                        const uint32_t a = s0 + stage * STAGE_BYTES, b = same ? a : a + TILE_BYTES, f = f0 + stage * SF_STAGE;
                         const uint32_t ta = tmem + SF_COL + stage * SF_SLOT, tb = ta + 4;
-                        // (a slot of exponents is written again when its stage's products are done)
-                        copy_exponents(ta, f);
-                        copy_exponents(tb, same ? f : f + SF_BYTES);
+                        if (elect_one()) {
+                            // (a slot of exponents is written again when its stage's products are done)
+                            copy_exponents(ta, f);
+                            copy_exponents(tb, f + SF_BYTES);
+                            copy_exponents(tb + 4, f + 2 * SF_BYTES);
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            mma(tmem, operand(a, s), operand(b, s), idesc(BM, BN, s), ta, tb, kt > c0 || s > 0);
-                        tc_commit(&empty[stage]);
+                            for (int s = 0; s < 4; ++s)
+                                mma(d, operand(a, s), operand(b, s), idesc(TILE, TILE, s), ta, tb, kt > c0 || s > 0);
+                            commit_both(&empty[stage]);
+                        }
+                        __syncwarp();
                         if (++stage == STAGES) { stage = 0; phase ^= 1; }
                     }
                     if (!ok) break;
-                    tc_commit(accf);
+                    if (elect_one()) commit_both(accf);
+                    __syncwarp();
                     if (c1 >= k.kt1) break;
                 }
             }
-            if (*abort_flag) {
-                tc_commit(drain);
-                if (!mbar_wait(drain, 0)) atomicOr(P.err, ERR_TIMEOUT_DRAIN);
+            if (!ok) {
+                *abort_flag = 1;
+                if (elect_one()) commit_both(drain);
+                __syncwarp();
+                if (!mbar_wait(drain, 0) && lane == 0) atomicOr(P.err, ERR_TIMEOUT_DRAIN);
             }
         }
     } else {
-        const int e = warp - 2, quarter = warp & 3, half = e >> 2;
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + half * COLS;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MANY_REGS));
+        const int e = warp - FIRST_EPI, quarter = warp & 3, half = e >> 2;
+        // this warp's columns: 32 of each 64 of the tile, v[32 m ..] those of 64 m + 32 half
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * 32;
         float *stage = stages + e * 32 * LD;
+        const uint32_t released = of_first(acce);
         uint32_t use = 0;
         bool bad = false;
-        for (int w = blockIdx.x; w < P.total_work && !*abort_flag; w += gridDim.x) {
+        for (int w = first_work; w < P.total_work && !*abort_flag; w += step) {
             const Work k = decode(P, w);
             const Prob &q = P.prob[k.p];
+            const int i0 = k.tm * TILE + rank * HALF + quarter * 32, j0 = k.tn * TILE + half * 32;
+            if (q.beta != 0.f && !q.packed && i0 + lane < q.M) {  // the old values on their way to L2 while the products run
+                const int size = q.c_dtype == KFAC_F32 ? 4 : 2;
+                const char *row = (const char *)q.C + ((long long)(i0 + lane) * q.ldc + j0) * size;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 32)
+                    if (j0 + 2 * c < q.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 2 * c * size));
+            }
             float v[COLS];
             bool ok = true;
             for (int c0 = k.kt0;; c0 += CHUNK) {
@@ -309,20 +473,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
                     ok = false;
                     break;
                 }
-                ++use;
                 tc_fence_after();
                 // (without a token nothing was multiplied: the accumulator holds another tile's values)
-                const bool first = c0 == k.kt0, none = k.kt0 >= k.kt1;
+                if (c0 == k.kt0) {
 #pragma unroll
-                for (int c = 0; c < COLS; c += 32) {
-                    float t[32];
-                    tmem_ld_32x32b_x32(at + c, t);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[c + i] = none ? 0.f : first ? t[i] : v[c + i] + t[i];
+                    for (int i = 0; i < COLS; ++i) v[i] = 0.f;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acce);
+                // first what the next chunk's accumulator overlaps: the last 64 columns of one at column 0, the
+                // first of one at column 192
+                float t[32], u[32];
+                if (use & 1) {
+                    tmem_ld_32x32b_x32(lanes + ACC_SHIFT, t);
+                    released_by(released, lane);
+                    add_columns<0>(v, t, k);
+                    tmem_ld_pair_32x32b_x32(lanes + ACC_SHIFT + 64, t, lanes + ACC_SHIFT + 128, u);
+                    add_columns<32>(v, t, k);
+                    add_columns<64>(v, u, k);
+                    tmem_ld_32x32b_x32(lanes + ACC_SHIFT + 192, t);
+                    add_columns<96>(v, t, k);
+                } else {
+                    tmem_ld_32x32b_x32(lanes + 192, t);
+                    released_by(released, lane);
+                    add_columns<96>(v, t, k);
+                    tmem_ld_pair_32x32b_x32(lanes + 64, t, lanes + 128, u);
+                    add_columns<32>(v, t, k);
+                    add_columns<64>(v, u, k);
+                    tmem_ld_32x32b_x32(lanes, t);
+                    add_columns<0>(v, t, k);
+                }
+                ++use;
                 if (c0 + CHUNK >= k.kt1) break;
             }
             if (!ok) {
@@ -330,37 +509,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
                 *abort_flag = 1;
                 break;
             }
-            const int i0 = k.tm * BM + quarter * 32, j0 = k.tn * BN + half * COLS;
             if (q.ksplit > 1) {
-                const long long span = (long long)BM * BN;
-                float *mine = q.partial + ((long long)k.tile * q.ksplit + k.split) * span + e * (32 * COLS) + lane;
+                const long long span = (long long)TILE * TILE;
+                const long long part = (long long)rank * HALF * TILE + e * (32 * COLS) + lane;
+                float *mine = q.partial + ((long long)k.tile * q.ksplit + k.split) * span + part;
 #pragma unroll
                 for (int c = 0; c < COLS; ++c) mine[c * 32] = v[c];
                 __threadfence();
                 named_barrier_sync(1, 32 * EPI_WARPS);
-                if (threadIdx.x == 64) *last_flag = atomicAdd(&q.counters[k.tile], 1) == q.ksplit - 1;
+                if (threadIdx.x == 32 * FIRST_EPI) *last_flag = atomicAdd(&q.counters[2 * k.tile + rank], 1) == q.ksplit - 1;
                 named_barrier_sync(1, 32 * EPI_WARPS);
                 const bool last = *last_flag != 0;
                 named_barrier_sync(1, 32 * EPI_WARPS);
                 if (!last) continue;
                 __threadfence();
-                const float *all = q.partial + (long long)k.tile * q.ksplit * span + e * (32 * COLS) + lane;
+                const float *all = q.partial + (long long)k.tile * q.ksplit * span + part;
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) v[c] = __ldcg(all + c * 32);
-                for (int s = 1; s < q.ksplit; ++s) {
+                for (int c = 0; c < COLS; c += 32) {
 #pragma unroll
-                    for (int c = 0; c < COLS; ++c) v[c] += __ldcg(all + s * span + c * 32);
+                    for (int i = 0; i < 32; ++i) v[c + i] = 0.f;
+#pragma unroll 1
+                    for (int s = 0; s < q.ksplit; ++s) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[c + i] += __ldcg(all + s * span + (c + i) * 32);
+                    }
                 }
             }
+            // (one copy of the stores' code for all chunks: what it costs is mostly fetching it)
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 32) {
 #pragma unroll
-            for (int c = 0; c < COLS; c += 32) bad |= store_chunk(q, i0, j0 + c, v + c, stage, lane);
+                for (int i = 0; i < 32; i += 4)
+                    *(float4 *)(stage + lane * LD + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                __syncwarp();
+                bad |= store_chunk(q, i0, j0 + 2 * c, stage, lane);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i + 32 < COLS; ++i) v[i] = v[i + 32];
+            }
         }
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(P.err, ERR_NONFINITE);
     }
     __syncthreads();
+    cluster_sync();  // nothing of either CTA is used by the other any more
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, TMEM_COLS);
+        tmem_dealloc_pair(tmem);
     }
 }
 
@@ -386,6 +580,32 @@ bool exponent_map(CUtensorMap *m, const void *s, long long tiles) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pairs of CTAs that run at the same time on the current device.
+int pairs() {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * device_sm_count());
+        cfg.blockDim = dim3(NUM_THREADS);
+        cfg.dynamicSmemBytes = SMEM_BYTES;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, mx_kernel, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = std::max(1, device_sm_count() / 2);
+        }
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 struct Plan {
     std::vector<int> tiles, ksplit, k_tiles;
     std::vector<float *> partial;
@@ -395,7 +615,7 @@ struct Plan {
 };
 
 int tiles_of(const MxJob &j) {
-    const int tm = (int)ceil_div(j.M, BM), tn = (int)ceil_div(j.N, BN);
+    const int tm = (int)ceil_div(j.M, TILE), tn = (int)ceil_div(j.N, TILE);
     return j.sym ? tm * (tm + 1) / 2 : tm * tn;
 }
 
@@ -408,20 +628,20 @@ Plan make_plan(const MxJob *jobs, int n, Arena &ws) {
         total += (double)p.tiles[i] * p.k_tiles[i];
     }
     // a tile's tokens are split where it would be the critical path: no item of more than
-    // about half of an SM's share, none of fewer than 8 stages
-    const double target = std::max(8.0, total / (2.0 * device_sm_count()));
+    // about half of a pair's share, none of fewer than 8 stages
+    const double target = std::max(8.0, total / (2.0 * (device_sm_count() / 2)));
     for (int i = 0; i < n; ++i) {
         const int ks = (int)std::min(64.0, std::ceil(p.k_tiles[i] / target));
         p.ksplit.push_back(std::max(1, ks));
-        if (p.ksplit[i] > 1) p.ncounters += p.tiles[i];
+        if (p.ksplit[i] > 1) p.ncounters += 2 * p.tiles[i];
     }
     p.counter_base = ws.take<int>(std::max<size_t>(p.ncounters, 1));
     size_t at = 0;
     for (int i = 0; i < n; ++i) {
         const bool split = p.ksplit[i] > 1;
-        p.partial.push_back(split ? ws.take<float>((size_t)p.tiles[i] * p.ksplit[i] * BM * BN) : nullptr);
+        p.partial.push_back(split ? ws.take<float>((size_t)p.tiles[i] * p.ksplit[i] * TILE * TILE) : nullptr);
         p.counters.push_back(split && p.counter_base ? p.counter_base + at : nullptr);
-        if (split) at += p.tiles[i];
+        if (split) at += 2 * p.tiles[i];
     }
     return p;
 }
@@ -461,16 +681,17 @@ kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream
             Prob &q = P->prob[P->nprob++];
             std::memset(&q, 0, sizeof(q));
             q.k_tiles = p.k_tiles[i];
-            q.tiles_m = (int)ceil_div(j.M, BM);
-            q.tiles_n = (int)ceil_div(j.N, BN);
+            q.tiles_m = (int)ceil_div(j.M, TILE);
+            q.tiles_n = (int)ceil_div(j.N, TILE);
+            const long long sa_tiles = ceil_div(j.M, HALF) * q.k_tiles, sb_tiles = ceil_div(j.N, HALF) * q.k_tiles;
             if (j.K > 0) {  // (without rows nothing is loaded)
-                if (!element_map(&q.a, j.a, j.lda, j.K, j.M) || !exponent_map(&q.sa, j.sa, (long long)q.tiles_m * q.k_tiles))
+                if (!element_map(&q.a, j.a, j.lda, j.K, j.M) || !exponent_map(&q.sa, j.sa, sa_tiles))
                     return KFAC_ERR_CUDA;
                 if (j.sym) {
                     q.b = q.a;
                     q.sb = q.sa;
                 } else if (!element_map(&q.b, j.b, j.ldb, j.K, j.N) ||
-                           !exponent_map(&q.sb, j.sb, (long long)q.tiles_n * q.k_tiles)) {
+                           !exponent_map(&q.sb, j.sb, sb_tiles)) {
                     return KFAC_ERR_CUDA;
                 }
             }
@@ -487,11 +708,12 @@ kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream
             q.sym = j.sym != 0;
             q.packed = j.packed != 0;
             q.c_dtype = (uint8_t)j.c_dtype;
+            q.vec = !j.packed && j.ldc % 4 == 0 && (uintptr_t)j.C % (j.c_dtype == KFAC_F32 ? 16 : 8) == 0;
             P->total_work += p.tiles[i] * p.ksplit[i];
         }
         P->err = err;
-        const int grid = std::max(1, std::min(P->total_work, device_sm_count()));
-        KFAC_LAUNCH(KK_MX, st, mx_kernel, grid, NUM_THREADS, SMEM_BYTES, *P);
+        const int grid = 2 * std::max(1, std::min(P->total_work, pairs()));
+        KFAC_LAUNCH_CLUSTERS(KK_MX, st, mx_kernel, 2, grid, NUM_THREADS, SMEM_BYTES, *P);
     }
     return KFAC_OK;
 }
