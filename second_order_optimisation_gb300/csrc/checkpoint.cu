@@ -11,7 +11,8 @@
 // Bound by memory.  A CTA takes a tile of 128 rows: each of its four warps 32 rows,
 // half a warp to a row's 16-byte groups, 16 rows to a thread, so that a thread has 16
 // loads in flight, the maximum over a block is one exchange between two lanes, and the
-// tile's exponents leave as one piece of 512 bytes.
+// tile's exponents leave as one piece of 512 bytes.  CTAs next to one another take tiles next
+// to one another in the same rows, so that memory is met in long runs.
 #include <algorithm>
 #include <cstring>
 
@@ -34,7 +35,7 @@ struct Item {
     long long rows;
     long long tile_begin;
     int cols, width;  // of x, of the checkpoint (a column of ones more, or not)
-    int chunks;       // tiles along the rows
+    int chunks, wides;  // tiles along the rows and the columns
     int dtype;
     int wide;         // 16-byte accesses to x (8-byte, or 4-byte for 32-bit values, to q)
 };
@@ -112,37 +113,74 @@ __device__ __forceinline__ float bounded(float y, uint32_t b) {
     return b == LAST_EXPONENT ? fminf(fmaxf(y, -240.f), 240.f) : y;
 }
 
+// 16 bytes from byte k (0 .. 15) of 32.
+__device__ __forceinline__ uint4 from_byte(uint4 lo, uint4 hi, int k) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = k & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = k & 4 ? w[i + 1] : w[i];
+    const int s = (k & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+
 template <int DT>
 __device__ __forceinline__ void store_tile(const Item &it, long long tile, uint8_t (*exps)[4]) {
     using M = Mag<DT>;
     constexpr int N = Elem<DT>::N, ROWS = 16, COLS = 16 * N;
     using bits = typename Elem<DT>::bits;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const long long ct = tile / it.chunks, rt = tile % it.chunks;
+    const int ct = (int)(tile % it.wides);
+    const long long rt = tile / it.wides;
     const long long r0 = rt * TILE + warp * 32 + lane / 16;  // rows r0, r0 + 2, ...
 #pragma unroll 1
     for (int part = 0; part < TILE; part += COLS) {
-        const int c0 = (int)ct * TILE + part + lane % 16 * N;
+        const int c0 = ct * TILE + part + lane % 16 * N;
         const int n = min(N, it.cols - c0);  // values here (may be negative)
         uint4 u[ROWS];
         const char *src = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
-        if (it.wide && n == N) {
+        if (it.wide && it.cols % N == 0) {
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 u[i] = make_uint4(0, 0, 0, 0);
-                if (r0 + 2 * i < it.rows) u[i] = ld16(src + 2 * i * it.ld_bytes);
+                if (r0 + 2 * i < it.rows && n > 0) u[i] = ld16(src + 2 * i * it.ld_bytes);
             }
         } else {
+            // At other alignments a lane loads the aligned 16 bytes that its group begins in, and has the rest
+            // of it from the next lane, which loads them where its own group is not whole, too; the last
+            // lane of a row's part loads them itself.  A group that is not whole goes value by value.
+            const bool full = n == N;
+            const unsigned whole = __ballot_sync(ALL_LANES, full);
+            const bool after = lane % 16 > 0 && (whole >> (lane - 1) & 1);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                uint32_t w[4] = {0, 0, 0, 0};
-                if (r0 + 2 * i < it.rows) {
-                    const bits *p = (const bits *)(src + 2 * i * it.ld_bytes);
+                const char *p = src + 2 * i * it.ld_bytes;
+                const int off = (int)((uintptr_t)p & 15);
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (r0 + 2 * i < it.rows && (full || (after && off))) u[i] = ld16(p - off);
+            }
 #pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (j < n) w[j * 4 / N] |= (uint32_t)p[j] << (N == 8 ? (j & 1) * 16 : 0);
+            for (int i = 0; i < ROWS; ++i) {
+                const char *p = src + 2 * i * it.ld_bytes;
+                const int off = (int)((uintptr_t)p & 15);
+                uint4 next = make_uint4(__shfl_down_sync(ALL_LANES, u[i].x, 1, 16), __shfl_down_sync(ALL_LANES, u[i].y, 1, 16),
+                                        __shfl_down_sync(ALL_LANES, u[i].z, 1, 16), __shfl_down_sync(ALL_LANES, u[i].w, 1, 16));
+                if (r0 + 2 * i < it.rows && full && lane % 16 == 15 && off) next = ld16(p - off + 16);
+                u[i] = from_byte(u[i], next, off);
+            }
+            if (!full) {
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) {
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    if (r0 + 2 * i < it.rows) {
+                        const bits *p = (const bits *)(src + 2 * i * it.ld_bytes);
+#pragma unroll
+                        for (int j = 0; j < N - 1; ++j)
+                            if (j < n) w[j * 4 / N] |= (uint32_t)p[j] << (N == 8 ? (j & 1) * 16 : 0);
+                    }
+                    u[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                u[i] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
         uint32_t m[4] = {0, 0, 0, 0};
@@ -212,10 +250,12 @@ __device__ __forceinline__ void store_tile(const Item &it, long long tile, uint8
         }
     }
     __syncthreads();
-    ((uint32_t *)(it.scales + tile * 512))[threadIdx.x] = ((const uint32_t *)exps)[threadIdx.x];
+    ((uint32_t *)(it.scales + (ct * (long long)it.chunks + rt) * 512))[threadIdx.x] = ((const uint32_t *)exps)[threadIdx.x];
 }
 
-__global__ void __launch_bounds__(THREADS) store_kernel(const __grid_constant__ Params P) {
+// 32768 x 8192 bf16 (814 MB) takes 140 us, 5.8 TB/s; three CTAs to an SM 173 us, six 147. 20000 x 5001
+// bf16 (rows on every alignment) 108 us; with two loads a group in place of the exchange 160.
+__global__ void __launch_bounds__(THREADS, 5) store_kernel(const __grid_constant__ Params P) {
     __shared__ __align__(16) uint8_t exps[TILE][4];
     pdl_wait();
     pdl_trigger();
@@ -226,19 +266,30 @@ __global__ void __launch_bounds__(THREADS) store_kernel(const __grid_constant__ 
     else store_tile<KFAC_F32>(it, tile, exps);
 }
 
+// Elements j0 .. j1 - 1 of a group.
+template <int DT>
+__device__ __forceinline__ void store_some(char *d, uint4 u, int j0, int j1) {
+    using bits = typename Elem<DT>::bits;
+    constexpr int N = Elem<DT>::N;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        if (j >= j0 && j < j1) ((bits *)d)[j] = (bits)(N == 4 ? w[j] : w[j / 2] >> (j & 1) * 16);
+}
+
 // Values of a tile: x_ij = q_ij 2^e, rounded to x's type.
 template <int DT>
 __device__ __forceinline__ void load_tile(const Item &it, long long tile, const uint8_t (*exps)[4]) {
     constexpr int N = Elem<DT>::N, ROWS = 16, COLS = 16 * N;
     using bits = typename Elem<DT>::bits;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const long long ct = tile / it.chunks, rt = tile % it.chunks;
+    const int ct = (int)(tile % it.wides);
+    const long long rt = tile / it.wides;
     const long long r0 = rt * TILE + warp * 32 + lane / 16;
 #pragma unroll 1
     for (int part = 0; part < TILE; part += COLS) {
-        const int c0 = (int)ct * TILE + part + lane % 16 * N;
-        const int n = min(N, it.cols - c0);
-        if (n <= 0) continue;
+        const int c0 = ct * TILE + part + lane % 16 * N;
+        const int n = max(0, min(N, it.cols - c0));
         const uint8_t *src = it.q + r0 * it.ldq + c0;
         uint32_t b[ROWS][N / 4];
         if (n == N) {
@@ -268,9 +319,15 @@ __device__ __forceinline__ void load_tile(const Item &it, long long tile, const 
 #pragma unroll
         for (int j = 0; j < N; ++j) p[j] = power_of(exps[(c0 + j) % 32 * 4 + (c0 + j) % TILE / 32][warp]);
         char *dst = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
+        // At other alignments a lane stores the aligned 16 bytes that its group begins in, with the last
+        // bytes of the group of the lane before it, where both groups are whole; the ends of such a
+        // run, and groups that are not whole, go value by value.
+        const bool full = n == N;
+        const unsigned whole = __ballot_sync(ALL_LANES, full);  // (all lanes vote: which groups are whole)
+        const bool joined = full && lane % 16 > 0 && (whole >> (lane - 1) & 1);
+        const bool tail = full && !(lane % 16 < 15 && (whole >> (lane + 1) & 1));
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            if (r0 + 2 * i >= it.rows) continue;
             float v[N];
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
@@ -279,24 +336,33 @@ __device__ __forceinline__ void load_tile(const Item &it, long long tile, const 
                 v[j + 1] = f.y * p[j + 1];
             }
             char *d = dst + 2 * i * it.ld_bytes;
-            if (it.wide && n == N) {
-                *(uint4 *)d = Elem<DT>::pack(v);
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j < n) ((bits *)d)[j] = Elem<DT>::round(v[j]);
+            const uint4 u = Elem<DT>::pack(v);
+            const bool in = r0 + 2 * i < it.rows;
+            if (it.wide) {
+                if (in && full) *(uint4 *)d = u;
+                else if (in) store_some<DT>(d, u, 0, n);
+                continue;
             }
+            const int off = (int)((uintptr_t)d & 15), cut = N - off / (int)sizeof(bits);
+            const uint4 before = make_uint4(__shfl_up_sync(ALL_LANES, u.x, 1, 16), __shfl_up_sync(ALL_LANES, u.y, 1, 16),
+                                            __shfl_up_sync(ALL_LANES, u.z, 1, 16), __shfl_up_sync(ALL_LANES, u.w, 1, 16));
+            if (!in) continue;
+            if (off == 0 && full) *(uint4 *)d = u;
+            else if (joined) *(uint4 *)(d - off) = from_byte(before, u, 16 - off);
+            if (off == 0 ? !full : !joined || tail) store_some<DT>(d, u, joined ? cut : 0, off == 0 || tail || !full ? n : cut);
         }
     }
 }
 
-__global__ void __launch_bounds__(THREADS) load_kernel(const __grid_constant__ Params P) {
+// 32768 x 8192 bf16 takes 130 us, 6.3 TB/s; four CTAs to an SM 138 us, eight 141.
+__global__ void __launch_bounds__(THREADS, 6) load_kernel(const __grid_constant__ Params P) {
     __shared__ __align__(16) uint8_t exps[TILE][4];
     pdl_wait();
     pdl_trigger();
     const Item &it = item_of(P, blockIdx.x);
     const long long tile = blockIdx.x - it.tile_begin;
-    ((uint32_t *)exps)[threadIdx.x] = ((const uint32_t *)(it.scales + tile * 512))[threadIdx.x];
+    const long long at = tile % it.wides * it.chunks + tile / it.wides;
+    ((uint32_t *)exps)[threadIdx.x] = ((const uint32_t *)(it.scales + at * 512))[threadIdx.x];
     __syncthreads();
     if (it.dtype == KFAC_BF16) load_tile<KFAC_BF16>(it, tile, exps);
     else if (it.dtype == KFAC_F16) load_tile<KFAC_F16>(it, tile, exps);
@@ -350,6 +416,7 @@ kfac_status run(const kfac_checkpoint_desc *descs, int count, bool store, void *
             it.cols = d.cols;
             it.width = (int)width;
             it.chunks = (int)chunks;
+            it.wides = (int)ceil_div(width, TILE);
             it.dtype = d.dtype;
             it.wide = (uintptr_t)d.x % 16 == 0 && (it.ld_bytes % 16 == 0 || d.rows == 1);
             tiles += here;
