@@ -474,7 +474,8 @@ extern "C" kfac_status kfac_factor_update(const kfac_factor_desc *descs, int cou
     if (!ws.fits()) return KFAC_ERR_WORKSPACE;
     Arena tail(p.tc_ws, p.tc_bytes);
     cudaStream_t st = (cudaStream_t)stream;
-    KFAC_CUDA_TRY(cudaMemsetAsync(p.err, 0, sizeof(int), st));
+    const bool only_mx = (int)p.mx.size() == count;  // (its launches then begin with the error word)
+    if (!only_mx) KFAC_CUDA_TRY(cudaMemsetAsync(p.err, 0, sizeof(int), st));
     if (!p.im16.empty() && (s = im2col_run(p.im16.data(), (int)p.im16.size(), KFAC_BF16, st)) != KFAC_OK)
         return s;
     if (!p.imh.empty() && (s = im2col_run(p.imh.data(), (int)p.imh.size(), KFAC_F16, st)) != KFAC_OK)
@@ -488,7 +489,7 @@ extern "C" kfac_status kfac_factor_update(const kfac_factor_desc *descs, int cou
     }
     if (!p.mx.empty()) {
         Arena scratch(p.mx_ws, p.mx_bytes);
-        if ((s = mx_run(p.mx.data(), (int)p.mx.size(), scratch, p.err, st)) != KFAC_OK) return s;
+        if ((s = mx_run(p.mx.data(), (int)p.mx.size(), scratch, p.err, only_mx, st)) != KFAC_OK) return s;
     }
     if (!p.sg.empty() && (s = sg_run(p.sg.data(), (int)p.sg.size(), p.err, st)) != KFAC_OK) return s;
     if (!p.cs.empty() && (s = colsum_run(p.cs.data(), (int)p.cs.size(), p.cs_partial, st)) != KFAC_OK) return s;

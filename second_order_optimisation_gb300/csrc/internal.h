@@ -235,6 +235,7 @@ struct MxJob {
     float alpha, beta;
 };
 size_t mx_workspace_bytes(const MxJob *jobs, int njobs);
-kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream_t st);
+// `err`: the call's error word; zero_err: it is to be set to 0 first.
+kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, bool zero_err, cudaStream_t st);
 
 }  // namespace kfac

@@ -25,11 +25,13 @@
 #include <vector>
 
 #include "internal.h"
+#include "mx_plan.h"
 
 namespace kfac {
 namespace {
 
 constexpr int HALF = 128, TILE = 2 * HALF, BK = 128;  // a CTA's rows, the pair's tile, tokens a stage
+using namespace mx;  // how the tiles are dealt out to the pairs
 constexpr int STAGES = 5;
 constexpr int TILE_BYTES = 128 * 128, SF_BYTES = 512;
 constexpr int STAGE_BYTES = 2 * TILE_BYTES;
@@ -46,79 +48,27 @@ constexpr int LD = 36;        // pitch of its staging chunk
 constexpr int ACC_SHIFT = 192, SF_COL = 448, SF_SLOT = 12;
 static_assert(SF_COL + STAGES * SF_SLOT <= 512 && ACC_SHIFT + TILE <= SF_COL && TILE - ACC_SHIFT == 64, "tensor memory");
 constexpr int TMEM_COLS = 512;
-constexpr int MAX_PROBS = 48, GROUP = 8;
 constexpr int CHUNK = 16;  // stages (2048 tokens) in one accumulator
 constexpr size_t SMEM_BYTES =
     1024 + STAGES * (STAGE_BYTES + SF_STAGE) + EPI_WARPS * 32 * LD * sizeof(float) + 256;
 
-struct Prob {
-    CUtensorMap a, b, sa, sb;
-    void *C;
-    float *partial;
-    int *counters;
-    long long ldc;
-    int M, N, k_tiles, tiles_m, tiles_n, ksplit, work_begin;
-    float alpha, beta;
-    uint8_t sym, packed, c_dtype, vec;
+struct Maps {
+    CUtensorMap a, b, sa, sb;  // elements and exponents
 };
-struct Params {
+struct Prob : Maps, Tiles {
+    void *C;
+    long long ldc;
+    int M, N;
+    float alpha, beta;
+    uint8_t packed, c_dtype, vec;
+};
+struct Params : Deal {
     Prob prob[MAX_PROBS];
-    int nprob, total_work;
+    float *partial;  // [2 pairs][TILE][TILE] pieces of tiles: 2 p begins inside a tile, 2 p + 1 ends inside one
+    int *counters;   // [pairs][2] pieces that are there of the tile that the pair's share ends in, by CTA
     int *err;
 };
 static_assert(sizeof(Params) <= 32000, "kernel parameters");
-
-struct Work {
-    int p, tm, tn, tile, split, kt0, kt1;
-};
-
-__device__ __forceinline__ Work decode(const Params &P, int w) {
-    int lo = 0, hi = P.nprob - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (P.prob[mid].work_begin <= w) lo = mid;
-        else hi = mid - 1;
-    }
-    const Prob &q = P.prob[lo];
-    Work k;
-    k.p = lo;
-    const int local = w - q.work_begin;
-    k.tile = local / q.ksplit;
-    k.split = local - k.tile * q.ksplit;
-    // bands of GROUP rows of tiles, column by column, so that the CTAs at work together
-    // share panels of both operands in L2; of a symmetric result the upper tiles
-    const int T = q.tiles_n;
-    int u = k.tile;
-    if (q.sym) {
-        int b0 = 0, gb;
-        for (;;) {
-            gb = min(GROUP, T - b0);
-            const int size = gb * (T - b0) - gb * (gb - 1) / 2;
-            if (u < size) break;
-            u -= size;
-            b0 += gb;
-        }
-        const int stair = gb * (gb + 1) / 2;
-        if (u < stair) {
-            int c = 0;
-            while (u > c) u -= ++c;
-            k.tn = b0 + c;
-            k.tm = b0 + u;
-        } else {
-            u -= stair;
-            k.tn = b0 + gb + u / gb;
-            k.tm = b0 + u % gb;
-        }
-    } else {
-        const int band = u / (GROUP * T), b0 = band * GROUP, gb = min(GROUP, q.tiles_m - b0);
-        u -= b0 * T;
-        k.tn = u / gb;
-        k.tm = b0 + u % gb;
-    }
-    k.kt0 = (int)((long long)k.split * q.k_tiles / q.ksplit);
-    k.kt1 = (int)((long long)(k.split + 1) * q.k_tiles / q.ksplit);
-    return k;
-}
 
 // Shared-memory descriptor of a slice of 32 tokens: groups of 8 rows of 128 features,
 // 128-byte swizzle, 1024 bytes apart.
@@ -305,7 +255,7 @@ __device__ __forceinline__ void released_by(uint32_t bar, int lane) {
     if (lane == 0) arrive_at(bar);
 }
 template <int AT>
-__device__ __forceinline__ void add_columns(float (&v)[COLS], const float (&t)[32], const Work &k) {
+__device__ __forceinline__ void add_columns(float (&v)[COLS], const float (&t)[32], const Item &k) {
     if (k.kt0 >= k.kt1) return;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[AT + i] += t[i];
@@ -324,7 +274,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
     volatile int *last_flag = abort_flag + 1;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = blockIdx.x & 1;
-    const int first_work = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -337,6 +287,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot);
+    if (warp == 2 && lane < 4) tma_prefetch_desc(&P.prob[0].a + lane);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are there
@@ -354,8 +305,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int w = first_work; w < P.total_work && ok; w += step) {
-                const Work k = decode(P, w);
+            Walk walk(P, pair, pairs);
+            for (Item k; ok && walk.next(P, k);) {
                 const Prob &q = P.prob[k.p];
                 const bool same = q.sym && k.tm == k.tn;
                 const uint32_t bytes = 2 * ((same ? 1 : 2) * TILE_BYTES + SF_STAGE);
@@ -397,8 +348,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
             uint32_t phase = 0, use = 0;
             bool ok = true;
             const uint32_t s0 = smem_u32(smem), f0 = smem_u32(sf);
-            for (int w = first_work; w < P.total_work && ok; w += step) {
-                const Work k = decode(P, w);
+            Walk walk(P, pair, pairs);
+            for (Item k; ok && walk.next(P, k);) {
                 const Prob &q = P.prob[k.p];
                 const bool same = q.sym && k.tm == k.tn;
                 for (int c0 = k.kt0; ok; c0 += CHUNK) {
@@ -455,8 +406,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
         const uint32_t released = of_first(acce);
         uint32_t use = 0;
         bool bad = false;
-        for (int w = first_work; w < P.total_work && !*abort_flag; w += step) {
-            const Work k = decode(P, w);
+        Walk walk(P, pair, pairs);
+        for (Item k; !*abort_flag && walk.next(P, k);) {
             const Prob &q = P.prob[k.p];
             const int i0 = k.tm * TILE + rank * HALF + quarter * 32, j0 = k.tn * TILE + half * 32;
             if (q.beta != 0.f && !q.packed && i0 + lane < q.M) {  // the old values on their way to L2 while the products run
@@ -509,29 +460,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
                 *abort_flag = 1;
                 break;
             }
-            if (q.ksplit > 1) {
-                const long long span = (long long)TILE * TILE;
-                const long long part = (long long)rank * HALF * TILE + e * (32 * COLS) + lane;
-                float *mine = q.partial + ((long long)k.tile * q.ksplit + k.split) * span + part;
+            if (k.piece) {
+                // The piece to memory; whoever brings a tile's last piece adds them up in their order.
+                const long long slot = (long long)TILE * TILE;
+                const long long part = (long long)rank * HALF * TILE + e * (32 * COLS) + lane * 4;
+                float *mine = P.partial + (2 * pair + (k.kt0 == 0)) * slot + part;
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) mine[c * 32] = v[c];
+                for (int c = 0; c < COLS; c += 4)
+                    *(float4 *)(mine + c * 32) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                 __threadfence();
+                const Pieces pieces = pieces_of(P, k.begin, q.k_tiles, pair);
+                const int first = pieces.first, last = pieces.last;
                 named_barrier_sync(1, 32 * EPI_WARPS);
-                if (threadIdx.x == 32 * FIRST_EPI) *last_flag = atomicAdd(&q.counters[2 * k.tile + rank], 1) == q.ksplit - 1;
+                if (threadIdx.x == 32 * FIRST_EPI) *last_flag = atomicAdd(&P.counters[2 * first + rank], 1) == pieces.count - 1;
                 named_barrier_sync(1, 32 * EPI_WARPS);
-                const bool last = *last_flag != 0;
+                const bool all_there = *last_flag != 0;
                 named_barrier_sync(1, 32 * EPI_WARPS);
-                if (!last) continue;
+                if (!all_there) continue;
                 __threadfence();
-                const float *all = q.partial + (long long)k.tile * q.ksplit * span + part;
 #pragma unroll
-                for (int c = 0; c < COLS; c += 32) {
+                for (int c = 0; c < COLS; c += 64) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[c + i] = 0.f;
+                    for (int i = 0; i < 64; ++i) v[c + i] = 0.f;
 #pragma unroll 1
-                    for (int s = 0; s < q.ksplit; ++s) {
+                    for (int s = first; s <= last; ++s) {
+                        if (s > first && P.share[s] == P.share[s - 1]) continue;  // (an empty share)
+                        const float *from = P.partial + (2 * s + (s == first)) * slot + part + c * 32;
+                        float4 f[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[c + i] += __ldcg(all + s * span + (c + i) * 32);
+                        for (int i = 0; i < 16; ++i) f[i] = __ldcg((const float4 *)(from + i * 128));
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v[c + 4 * i] += f[i].x;
+                            v[c + 4 * i + 1] += f[i].y;
+                            v[c + 4 * i + 2] += f[i].z;
+                            v[c + 4 * i + 3] += f[i].w;
+                        }
                     }
                 }
             }
@@ -556,6 +520,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
         tc_fence_after();
         tmem_dealloc_pair(tmem);
     }
+}
+
+// The error word and the counters of a call.  A kernel, not a memset: the next kernel's start
+// overlaps it.
+__global__ void zero_kernel(int *err, int *counters, int n) {
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0 && err) *err = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
 }
 
 // ------------------------------------------------------------------ host
@@ -606,43 +579,37 @@ int pairs() {
     return n;
 }
 
+Tiles tiles_of(const MxJob &j) {
+    return Tiles{(int)ceil_div(j.M, TILE), (int)ceil_div(j.N, TILE), (int)ceil_div(j.K, BK), j.sym != 0, 0, 0};
+}
+
+// The launches of a call, and the scratch that they share (they follow one another).
 struct Plan {
-    std::vector<int> tiles, ksplit, k_tiles;
-    std::vector<float *> partial;
-    std::vector<int *> counters;
-    int *counter_base = nullptr;
+    std::vector<int> order;
+    std::vector<Launch> launches;
+    float *partial = nullptr;
+    int *counters = nullptr;
     size_t ncounters = 0;
 };
 
-int tiles_of(const MxJob &j) {
-    const int tm = (int)ceil_div(j.M, TILE), tn = (int)ceil_div(j.N, TILE);
-    return j.sym ? tm * (tm + 1) / 2 : tm * tn;
-}
-
 Plan make_plan(const MxJob *jobs, int n, Arena &ws) {
     Plan p;
-    double total = 0;
-    for (int i = 0; i < n; ++i) {
-        p.tiles.push_back(tiles_of(jobs[i]));
-        p.k_tiles.push_back((int)ceil_div(jobs[i].K, BK));
-        total += (double)p.tiles[i] * p.k_tiles[i];
+    p.order.resize(n);
+    for (int i = 0; i < n; ++i) p.order[i] = i;
+    std::stable_sort(p.order.begin(), p.order.end(), [&](int x, int y) { return jobs[x].K > jobs[y].K; });
+    std::vector<Tiles> tiles(n);
+    for (int i = 0; i < n; ++i) tiles[i] = tiles_of(jobs[p.order[i]]);
+    const int most = std::min(pairs(), MAX_PAIRS);
+    int slots = 0;
+    for (int at = 0; at < n; at = p.launches.back().to) {
+        p.launches.push_back(make_launch(tiles, at, most));
+        if (const Launch &l = p.launches.back(); l.span > 0) {
+            slots = std::max(slots, 2 * l.pairs);
+            p.ncounters += 2 * l.pairs;
+        }
     }
-    // a tile's tokens are split where it would be the critical path: no item of more than
-    // about half of a pair's share, none of fewer than 8 stages
-    const double target = std::max(8.0, total / (2.0 * (device_sm_count() / 2)));
-    for (int i = 0; i < n; ++i) {
-        const int ks = (int)std::min(64.0, std::ceil(p.k_tiles[i] / target));
-        p.ksplit.push_back(std::max(1, ks));
-        if (p.ksplit[i] > 1) p.ncounters += 2 * p.tiles[i];
-    }
-    p.counter_base = ws.take<int>(std::max<size_t>(p.ncounters, 1));
-    size_t at = 0;
-    for (int i = 0; i < n; ++i) {
-        const bool split = p.ksplit[i] > 1;
-        p.partial.push_back(split ? ws.take<float>((size_t)p.tiles[i] * p.ksplit[i] * TILE * TILE) : nullptr);
-        p.counters.push_back(split && p.counter_base ? p.counter_base + at : nullptr);
-        if (split) at += 2 * p.tiles[i];
-    }
+    p.counters = ws.take<int>(std::max<size_t>(p.ncounters, 1));
+    p.partial = ws.take<float>((size_t)slots * TILE * TILE);
     return p;
 }
 
@@ -655,7 +622,7 @@ size_t mx_workspace_bytes(const MxJob *jobs, int njobs) {
     return a.used;
 }
 
-kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream_t st) {
+kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, bool zero_err, cudaStream_t st) {
     if (njobs <= 0) return KFAC_OK;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
@@ -665,24 +632,20 @@ kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream
     if (attr != cudaSuccess) return KFAC_ERR_CUDA;
     const Plan p = make_plan(jobs, njobs, ws);
     if (!ws.fits()) return KFAC_ERR_WORKSPACE;
-    if (p.ncounters) KFAC_CUDA_TRY(cudaMemsetAsync(p.counter_base, 0, p.ncounters * sizeof(int), st));
-    std::vector<int> order(njobs);  // long items first
-    for (int i = 0; i < njobs; ++i) order[i] = i;
-    std::stable_sort(order.begin(), order.end(), [&](int x, int y) {
-        return (long long)p.k_tiles[x] * p.ksplit[y] > (long long)p.k_tiles[y] * p.ksplit[x];
-    });
-    std::unique_ptr<Params> P(new Params);
-    for (int at = 0; at < njobs;) {
-        P->nprob = P->total_work = 0;
-        for (; at < njobs && P->nprob < MAX_PROBS; ++at) {
-            const MxJob &j = jobs[order[at]];
-            const int i = order[at];
-            if ((long long)P->total_work + (long long)p.tiles[i] * p.ksplit[i] > 0x7fffffffLL) break;
-            Prob &q = P->prob[P->nprob++];
-            std::memset(&q, 0, sizeof(q));
-            q.k_tiles = p.k_tiles[i];
-            q.tiles_m = (int)ceil_div(j.M, TILE);
-            q.tiles_n = (int)ceil_div(j.N, TILE);
+    if (zero_err || p.ncounters)
+        KFAC_LAUNCH(KK_MX, st, zero_kernel, 1, 256, 0, zero_err ? err : nullptr, p.counters, (int)p.ncounters);
+    std::unique_ptr<Params> P(new Params());
+    int *counters = p.counters;
+    for (const Launch &l : p.launches) {
+        static_cast<Deal &>(*P) = l.deal;
+        P->partial = p.partial;
+        P->counters = counters;
+        if (l.span > 0) counters += 2 * l.pairs;
+        P->err = err;
+        for (int i = 0; i < P->nprob; ++i) {
+            const MxJob &j = jobs[p.order[l.from + i]];
+            Prob &q = P->prob[i];
+            static_cast<Tiles &>(q) = l.tiles[i];
             const long long sa_tiles = ceil_div(j.M, HALF) * q.k_tiles, sb_tiles = ceil_div(j.N, HALF) * q.k_tiles;
             if (j.K > 0) {  // (without rows nothing is loaded)
                 if (!element_map(&q.a, j.a, j.lda, j.K, j.M) || !exponent_map(&q.sa, j.sa, sa_tiles))
@@ -690,30 +653,21 @@ kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, cudaStream
                 if (j.sym) {
                     q.b = q.a;
                     q.sb = q.sa;
-                } else if (!element_map(&q.b, j.b, j.ldb, j.K, j.N) ||
-                           !exponent_map(&q.sb, j.sb, sb_tiles)) {
+                } else if (!element_map(&q.b, j.b, j.ldb, j.K, j.N) || !exponent_map(&q.sb, j.sb, sb_tiles)) {
                     return KFAC_ERR_CUDA;
                 }
             }
             q.C = j.C;
             q.ldc = j.ldc;
-            q.partial = p.partial[i];
-            q.counters = p.counters[i];
             q.M = j.M;
             q.N = j.N;
-            q.ksplit = p.ksplit[i];
-            q.work_begin = P->total_work;
             q.alpha = j.alpha;
             q.beta = j.beta;
-            q.sym = j.sym != 0;
             q.packed = j.packed != 0;
             q.c_dtype = (uint8_t)j.c_dtype;
             q.vec = !j.packed && j.ldc % 4 == 0 && (uintptr_t)j.C % (j.c_dtype == KFAC_F32 ? 16 : 8) == 0;
-            P->total_work += p.tiles[i] * p.ksplit[i];
         }
-        P->err = err;
-        const int grid = 2 * std::max(1, std::min(P->total_work, pairs()));
-        KFAC_LAUNCH_CLUSTERS(KK_MX, st, mx_kernel, 2, grid, NUM_THREADS, SMEM_BYTES, *P);
+        KFAC_LAUNCH_CLUSTERS(KK_MX, st, mx_kernel, 2, 2 * l.pairs, NUM_THREADS, SMEM_BYTES, *P);
     }
     return KFAC_OK;
 }
@@ -767,6 +721,5 @@ extern "C" kfac_status kfac_weight_grad(const kfac_weight_grad_desc *descs, int 
             return KFAC_ERR_INVALID;
     int *err = ws.take<int>(64);
     cudaStream_t st = (cudaStream_t)stream;
-    KFAC_CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(int), st));
-    return mx_run(jobs.data(), count, ws, err, st);
+    return mx_run(jobs.data(), count, ws, err, true, st);
 }

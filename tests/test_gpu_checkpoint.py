@@ -314,3 +314,22 @@ def test_host_memory_is_refused():
     with pytest.raises(kfac.KfacError):
         kfac.kfac_factor_update([kfac.FactorSource(kfac.Checkpoint(c.q, host.scales, 40, 100), torch.eye(100, device="cuda"))],
                                 workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("rows,dA,dG", [(3100, 900, 1500), (7000, 300, 200), (6200, 2500, 2300)])
+def test_weight_grad_of_tiles_in_pieces(rows, dA, dG):
+    """Few tiles of many stages, and a last round that would leave most pairs idle: tiles in several pieces."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, dA, device="cuda", generator=g)
+    y = torch.randn(rows, dG, device="cuda", generator=g)
+    a, b = kfac.Checkpoint.empty(rows, dA), kfac.Checkpoint.empty(rows, dG)
+    kfac.kfac_checkpoint_store([kfac.CheckpointItem(x, a), kfac.CheckpointItem(y, b)])
+    kfac.kfac_checkpoint_load([kfac.CheckpointItem(x, a), kfac.CheckpointItem(y, b)])
+    old = torch.randn(dG, dA, device="cuda", generator=g)
+    outs = [old.clone() for _ in range(2)]
+    for o in outs:
+        ws = kfac.kfac_weight_grad([kfac.WeightGrad(a, b, o, 0.5, 0.25)])
+    want = 0.25 * old.double() + 0.5 * (y.double().t() @ x.double())
+    size = 0.25 * old.double().abs() + 0.5 * (y.double().abs().t() @ x.double().abs())
+    assert bool(((outs[0].double() - want).abs() <= ref.SUM * size + ref.E * want.abs()).all())
+    assert torch.equal(outs[0], outs[1]) and _err(ws) == 0
