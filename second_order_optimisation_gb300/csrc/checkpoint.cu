@@ -388,8 +388,10 @@ kfac_status check(const kfac_checkpoint_desc *descs, int count) {
 kfac_status run(const kfac_checkpoint_desc *descs, int count, bool store, void *stream) {
     kfac_status s = check(descs, count);
     if (s != KFAC_OK) return s;
+    DeviceMemory memory;
     for (int i = 0; i < count; ++i)
-        if (descs[i].rows > 0 && !all_on_this_device({descs[i].x, descs[i].q, descs[i].scales})) return KFAC_ERR_INVALID;
+        if (descs[i].rows > 0 && !(memory.holds(descs[i].x, 0) && memory.holds(descs[i].q, 1) && memory.holds(descs[i].scales, 2)))
+            return KFAC_ERR_INVALID;
     cudaStream_t st = (cudaStream_t)stream;
     for (int at = 0; at < count;) {
         Params P;

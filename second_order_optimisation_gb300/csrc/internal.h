@@ -188,6 +188,12 @@ class DeviceMemory {
 
 public:
     bool holds(const void *p, int list);
+    // Of pointers that are likely to be parts of few allocations.
+    bool holds_all(std::initializer_list<const void *> ps) {
+        for (const void *p : ps)
+            if (!holds(p, 0)) return false;
+        return true;
+    }
 };
 
 // ----------------------------------------------------- inversion

@@ -20,7 +20,6 @@
 #include <cmath>
 #include <cstring>
 #include <memory>
-#include <mutex>
 #include <type_traits>
 #include <vector>
 
@@ -62,13 +61,17 @@ struct Prob : Maps, Tiles {
     float alpha, beta;
     uint8_t packed, c_dtype, vec;
 };
+// CAP: room for problems.  A kernel's parameters are copied at its launch (30 KB of them for
+// about 3 us), so that few problems have a kernel of their own.
+template <int CAP>
 struct Params : Deal {
-    Prob prob[MAX_PROBS];
+    Prob prob[CAP];
     float *partial;  // [2 pairs][TILE][TILE] pieces of tiles: 2 p begins inside a tile, 2 p + 1 ends inside one
     int *counters;   // [pairs][2] pieces that are there of the tile that the pair's share ends in, by CTA
     int *err;
 };
-static_assert(sizeof(Params) <= 32000, "kernel parameters");
+constexpr int FEW_PROBS = 4;
+static_assert(sizeof(Params<MAX_PROBS>) <= 32000, "kernel parameters");
 
 // Shared-memory descriptor of a slice of 32 tokens: groups of 8 rows of 128 features,
 // 128-byte swizzle, 1024 bytes apart.
@@ -261,7 +264,8 @@ __device__ __forceinline__ void add_columns(float (&v)[COLS], const float (&t)[3
     for (int i = 0; i < 32; ++i) v[AT + i] += t[i];
 }
 
-__global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constant__ Params P) {
+template <int CAP>
+__global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constant__ Params<CAP> P) {
     extern __shared__ uint8_t raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     uint8_t *sf = smem + STAGES * STAGE_BYTES;
@@ -553,13 +557,16 @@ bool exponent_map(CUtensorMap *m, const void *s, long long tiles) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pairs of CTAs that run at the same time on the current device.
+// Pairs of CTAs that run at the same time on the current device.  Asked once for each device, where
+// the kernels' shared memory is allowed first.
 int pairs() {
     static std::atomic<int> cache[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
     int n = cache[dev].load(std::memory_order_relaxed);
     if (n == 0) {
+        cudaFuncSetAttribute(mx_kernel<FEW_PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        cudaFuncSetAttribute(mx_kernel<MAX_PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * device_sm_count());
         cfg.blockDim = dim3(NUM_THREADS);
@@ -570,7 +577,7 @@ int pairs() {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, mx_kernel, &cfg) != cudaSuccess || n < 1) {
+        if (cudaOccupancyMaxActiveClusters(&n, mx_kernel<FEW_PROBS>, &cfg) != cudaSuccess || n < 1) {
             cudaGetLastError();
             n = std::max(1, device_sm_count() / 2);
         }
@@ -622,54 +629,62 @@ size_t mx_workspace_bytes(const MxJob *jobs, int njobs) {
     return a.used;
 }
 
-kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, bool zero_err, cudaStream_t st) {
-    if (njobs <= 0) return KFAC_OK;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-    });
-    if (attr != cudaSuccess) return KFAC_ERR_CUDA;
-    const Plan p = make_plan(jobs, njobs, ws);
-    if (!ws.fits()) return KFAC_ERR_WORKSPACE;
+namespace {
+
+template <int CAP>
+kfac_status launch(const MxJob *jobs, const Plan &p, const Launch &l, int *counters, int *err, cudaStream_t st) {
+    std::unique_ptr<Params<CAP>> P(new Params<CAP>());
+    static_cast<Deal &>(*P) = l.deal;
+    P->partial = p.partial;
+    P->counters = counters;
+    P->err = err;
+    for (int i = 0; i < P->nprob; ++i) {
+        const MxJob &j = jobs[p.order[l.from + i]];
+        Prob &q = P->prob[i];
+        static_cast<Tiles &>(q) = l.tiles[i];
+        const long long sa_tiles = ceil_div(j.M, HALF) * q.k_tiles, sb_tiles = ceil_div(j.N, HALF) * q.k_tiles;
+        if (j.K > 0) {  // (without rows nothing is loaded)
+            if (!element_map(&q.a, j.a, j.lda, j.K, j.M) || !exponent_map(&q.sa, j.sa, sa_tiles)) return KFAC_ERR_CUDA;
+            if (j.sym) {
+                q.b = q.a;
+                q.sb = q.sa;
+            } else if (!element_map(&q.b, j.b, j.ldb, j.K, j.N) || !exponent_map(&q.sb, j.sb, sb_tiles)) {
+                return KFAC_ERR_CUDA;
+            }
+        }
+        q.C = j.C;
+        q.ldc = j.ldc;
+        q.M = j.M;
+        q.N = j.N;
+        q.alpha = j.alpha;
+        q.beta = j.beta;
+        q.packed = j.packed != 0;
+        q.c_dtype = (uint8_t)j.c_dtype;
+        q.vec = !j.packed && j.ldc % 4 == 0 && (uintptr_t)j.C % (j.c_dtype == KFAC_F32 ? 16 : 8) == 0;
+    }
+    KFAC_LAUNCH_CLUSTERS(KK_MX, st, mx_kernel<CAP>, 2, 2 * l.pairs, NUM_THREADS, SMEM_BYTES, *P);
+    return KFAC_OK;
+}
+
+kfac_status run_plan(const MxJob *jobs, const Plan &p, int *err, bool zero_err, cudaStream_t st) {
     if (zero_err || p.ncounters)
         KFAC_LAUNCH(KK_MX, st, zero_kernel, 1, 256, 0, zero_err ? err : nullptr, p.counters, (int)p.ncounters);
-    std::unique_ptr<Params> P(new Params());
     int *counters = p.counters;
     for (const Launch &l : p.launches) {
-        static_cast<Deal &>(*P) = l.deal;
-        P->partial = p.partial;
-        P->counters = counters;
+        const kfac_status s = l.deal.nprob <= FEW_PROBS ? launch<FEW_PROBS>(jobs, p, l, counters, err, st)
+                                                        : launch<MAX_PROBS>(jobs, p, l, counters, err, st);
+        if (s != KFAC_OK) return s;
         if (l.span > 0) counters += 2 * l.pairs;
-        P->err = err;
-        for (int i = 0; i < P->nprob; ++i) {
-            const MxJob &j = jobs[p.order[l.from + i]];
-            Prob &q = P->prob[i];
-            static_cast<Tiles &>(q) = l.tiles[i];
-            const long long sa_tiles = ceil_div(j.M, HALF) * q.k_tiles, sb_tiles = ceil_div(j.N, HALF) * q.k_tiles;
-            if (j.K > 0) {  // (without rows nothing is loaded)
-                if (!element_map(&q.a, j.a, j.lda, j.K, j.M) || !exponent_map(&q.sa, j.sa, sa_tiles))
-                    return KFAC_ERR_CUDA;
-                if (j.sym) {
-                    q.b = q.a;
-                    q.sb = q.sa;
-                } else if (!element_map(&q.b, j.b, j.ldb, j.K, j.N) || !exponent_map(&q.sb, j.sb, sb_tiles)) {
-                    return KFAC_ERR_CUDA;
-                }
-            }
-            q.C = j.C;
-            q.ldc = j.ldc;
-            q.M = j.M;
-            q.N = j.N;
-            q.alpha = j.alpha;
-            q.beta = j.beta;
-            q.packed = j.packed != 0;
-            q.c_dtype = (uint8_t)j.c_dtype;
-            q.vec = !j.packed && j.ldc % 4 == 0 && (uintptr_t)j.C % (j.c_dtype == KFAC_F32 ? 16 : 8) == 0;
-        }
-        KFAC_LAUNCH_CLUSTERS(KK_MX, st, mx_kernel, 2, 2 * l.pairs, NUM_THREADS, SMEM_BYTES, *P);
     }
     return KFAC_OK;
+}
+
+}  // namespace
+
+kfac_status mx_run(const MxJob *jobs, int njobs, Arena &ws, int *err, bool zero_err, cudaStream_t st) {
+    if (njobs <= 0) return KFAC_OK;
+    const Plan p = make_plan(jobs, njobs, ws);
+    return ws.fits() ? run_plan(jobs, p, err, zero_err, st) : KFAC_ERR_WORKSPACE;
 }
 
 namespace {
@@ -711,15 +726,14 @@ extern "C" kfac_status kfac_weight_grad(const kfac_weight_grad_desc *descs, int 
     kfac_status s = check_weight_grad(descs, count, jobs);
     if (s != KFAC_OK || count == 0) return s;
     if (!workspace || ((uintptr_t)workspace % 256) != 0) return KFAC_ERR_WORKSPACE;
-    Arena ws(workspace, workspace_bytes), probe(workspace, workspace_bytes);
-    probe.take<int>(64);
-    make_plan(jobs.data(), count, probe);
-    if (!probe.fits()) return KFAC_ERR_WORKSPACE;
-    for (const kfac_weight_grad_desc *d = descs; d < descs + count; ++d)
-        if (!all_on_this_device({d->out}) ||
-            (d->rows > 0 && !all_on_this_device({d->q_a, d->scales_a, d->q_g, d->scales_g})))
-            return KFAC_ERR_INVALID;
+    Arena ws(workspace, workspace_bytes);
     int *err = ws.take<int>(64);
-    cudaStream_t st = (cudaStream_t)stream;
-    return mx_run(jobs.data(), count, ws, err, true, st);
+    const Plan p = make_plan(jobs.data(), count, ws);
+    if (!ws.fits()) return KFAC_ERR_WORKSPACE;
+    DeviceMemory memory;
+    for (const kfac_weight_grad_desc *d = descs; d < descs + count; ++d)
+        if (!memory.holds(d->out, 0) || (d->rows > 0 && !(memory.holds(d->q_a, 1) && memory.holds(d->scales_a, 2) &&
+                                                          memory.holds(d->q_g, 1) && memory.holds(d->scales_g, 2))))
+            return KFAC_ERR_INVALID;
+    return run_plan(jobs.data(), p, err, true, (cudaStream_t)stream);
 }

@@ -551,8 +551,9 @@ extern "C" kfac_status kfac_verify_draft(const kfac_verify_desc *desc, void *wor
     plan(d, ws, P);
     if (!ws.fits()) return KFAC_ERR_WORKSPACE;
     const bool draws = !d.greedy;
-    if (!all_on_this_device({d.logits, d.tokens, d.seq_offsets, d.accepted, d.out_tokens, d.logp}) ||
-        (draws && !all_on_this_device({d.draft, d.draft_saved, d.uniform, d.noise})))
+    DeviceMemory memory;
+    if (!memory.holds_all({d.logits, d.tokens, d.seq_offsets, d.accepted, d.out_tokens, d.logp}) ||
+        (draws && !memory.holds_all({d.draft, d.draft_saved, d.uniform, d.noise})))
         return KFAC_ERR_INVALID;
     const long long e = (long long)elem_size(d.dtype);
     P.target = Scores{(const char *)d.logits, d.ld * e, LOG2E / d.temperature, d.temperature};
