@@ -1013,7 +1013,5 @@ def kfac_clip_norm(tensors, max_norm: float, norm: Optional[torch.Tensor] = None
     ws = _scratch(c.need, c.device, workspace, stream)
     _check(load().kfac_clip_norm(c.descs, len(c.tensors), max_norm, eta, _rowvec(norm, 1, "norm"),
                                  _rowvec(scale, 1, "scale"), ws.data_ptr(), ws.nbytes, _stream(stream)),
-           "kfac_clip_norm", "kfac_checkpoint_scale_bytes", "kfac_checkpoint_store", "kfac_checkpoint_load",
-           "kfac_weight_grad_workspace_size", "kfac_weight_grad", "kfac_verify_draft_workspace_size",
-           "kfac_verify_draft")
+           "kfac_clip_norm")
     return ws

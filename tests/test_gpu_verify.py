@@ -299,3 +299,95 @@ def test_offsets_past_32_bits():
     want = ref.verify(sub[0].double().numpy(), sub[2].numpy(), [0, 4], sub[3].double().numpy(), sub[4].double().numpy())
     assert got[0].tolist()[1] == want[0][0] and got[1][-4:].tolist() == want[1]
     assert got[0].tolist()[0] == 0 and int(got[1][0]) == 1
+
+
+# ------------------------------------------------------------ many sequences: a cluster to a sequence
+
+def _among_many(off, z, zd, t, u, e, seed=90):
+    """The sequences with 400 more behind them, of one to three rows each."""
+    rng = np.random.default_rng(seed)
+    more = np.cumsum(rng.integers(1, 4, 400)).tolist()
+    z2, zd2, t2, u2, e2 = _inputs([0] + more, z.shape[1], {v: k for k, v in DT.items()}[z.dtype], seed)
+    cat = lambda a, b: None if a is None else torch.cat([a, b.to(a.dtype)])  # noqa: E731
+    return off + [off[-1] + m for m in more], cat(z, z2), cat(zd, zd2), cat(t, t2), cat(u, u2), cat(e, e2)
+
+
+def _np(x):
+    return None if x is None else x.double().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("vocab", [1, 7, 130, 1003])
+@pytest.mark.parametrize("how", ["rows", "saved", "none", "greedy"])
+def test_many_sequences(dtype, vocab, how):
+    off, z, zd, t, u, e = _among_many([0, 0, 5, 5, 6, 19], *_inputs([0, 4, 8, 12, 16, 19], vocab, dtype, 41))
+    kw = dict(temperature=0.9)
+    if how == "greedy":
+        best = torch.from_numpy(np.argmax(_np(z), 1))
+        t = torch.where(torch.arange(len(t)) % 5 != 3, best, t)
+        want = ref.verify(_np(z), t.numpy(), off, greedy=True, tau=0.9)
+        got = _run(z, t, off, greedy=True, **kw)
+    else:
+        saved = None
+        if how == "saved":
+            saved = torch.empty(len(t), 2, device="cuda")
+            kfac.kfac_token_logprob(kfac.TokenLogprob(zd.cuda(), t.cuda(), torch.empty(len(t), device="cuda"), temperature=1.2, saved=saved))
+        zd = None if how == "none" else zd
+        want = ref.verify(_np(z), t.numpy(), off, _np(u), _np(e), _np(zd), tau=0.9, tau_d=1.2)
+        got = _run(z, t, off, u, e, zd, saved, draft_temperature=1.2, **kw)
+    _check(got, want)
+
+
+@pytest.mark.parametrize("dtype,vocab,seqs", [("bf16", 17001, 170), ("f16", 40000, 90), ("f32", 33001, 60), ("bf16", 70003, 50)])
+@pytest.mark.parametrize("how", ["rows", "none", "greedy"])
+def test_many_sequences_over_large_vocabularies(dtype, vocab, seqs, how):
+    rng = np.random.default_rng(5)
+    off = [0] + np.cumsum(rng.integers(1, 4, seqs)).tolist()
+    z, zd, t, u, e = _inputs(off, vocab, dtype, 51)
+    if how == "greedy":
+        best = torch.from_numpy(np.argmax(_np(z), 1))
+        t = torch.where(torch.arange(len(t)) % 5 != 3, best, t)
+        return _check(_run(z, t, off, greedy=True), ref.verify(_np(z), t.numpy(), off, greedy=True))
+    zd = None if how == "none" else zd
+    _check(_run(z, t, off, u, e, zd), ref.verify(_np(z), t.numpy(), off, _np(u), _np(e), _np(zd)))
+
+
+def test_many_sequences_with_special_rows():
+    """Masked, broken and equal rows, tokens outside the vocabulary, in place, rows of no sequence."""
+    off = [2, 4, 6, 8, 10, 13, 16, 19, 22]
+    z, zd, t, u, e = _inputs([0, 3, 6, 9, 12, 15, 18, 20, 22], 50, "f32", 61, near=0.0)
+    u[:] = 0.0
+    z[2, t[2]] = -INF                       # forbidden
+    z[4] = -INF                             # nothing to draw from
+    zd[6] = -INF
+    z[8, 3] = NAN
+    t[10], t[14] = -1, 50
+    z[17] = INF
+    e[6, :] = NAN
+    u[19] = 2.0                             # p = q, not accepted: r is nothing
+    zd[19] = z[19]
+    off, z, zd, t, u, e = _among_many(off, z, zd, t, u, e)
+    want = ref.verify(_np(z), t.numpy(), off, _np(u), _np(e), _np(zd))
+    assert want[4] == kfac.ERRW_NONFINITE | kfac.ERRW_TARGET
+    _check(_run(z, t, off, u, e, zd), want)
+    _check(_run(z, t.clone(), off, u, e, zd, inplace=True), want, before=t)
+
+
+def test_many_sequences_repeated_and_captured():
+    off = np.arange(0, 1201, 3).tolist()
+    z, zd, t, u, e = (x.cuda() for x in _inputs(off, 3000, "bf16", 71))
+    first = _run(z, t, off, u, e, zd)
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    acc, out, logp = torch.empty(400, dtype=torch.int32, device="cuda"), torch.empty_like(t), torch.empty(1200, device="cuda")
+    item = kfac.VerifyDraft(z, t, offsets, acc, out, logp, zd, uniform=u, noise=e)
+    ws = torch.empty(kfac.kfac_verify_draft_workspace_size(item), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        kfac.kfac_verify_draft(item, ws)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(first[:3], (acc.cpu(), out.cpu(), logp.cpu())))
