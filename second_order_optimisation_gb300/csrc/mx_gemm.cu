@@ -47,9 +47,11 @@ constexpr int LD = 36;        // pitch of its staging chunk
 constexpr int ACC_SHIFT = 192, SF_COL = 448, SF_SLOT = 12;
 static_assert(SF_COL + STAGES * SF_SLOT <= 512 && ACC_SHIFT + TILE <= SF_COL && TILE - ACC_SHIFT == 64, "tensor memory");
 constexpr int TMEM_COLS = 512;
-// Stages (1536 tokens) in one accumulator: a sum of 16384 tokens is off by 7e-7 of itself (16 stages: 1.05e-6, 64:
-// 3.2e-6; 8: 4.6e-7), and taking a chunk out costs about 0.8 us (16384 x 4096 x 8192: 360 us at 16 stages).
-constexpr int CHUNK = 12;
+// Stages (1280 tokens) in one accumulator.  Sums of 2048 to 20000 tokens are off by at most 9e-7 of
+// themselves (8 stages 7e-7, 16 stages 1.6e-6, 64 stages 3e-6), and taking a chunk out costs 0.9 us
+// (16384 x 4096 x 8192: 8 stages 426 us, 10 stages 395, 16 stages 354).  Three accumulators of half a
+// tile that are taken out in turn cost more (403 us): the exponents then need another order.
+constexpr int CHUNK = 10;
 constexpr size_t SMEM_BYTES =
     1024 + STAGES * (STAGE_BYTES + SF_STAGE) + EPI_WARPS * 32 * LD * sizeof(float) + 256;
 
