@@ -29,6 +29,10 @@ With `max_norm` the step over all layers is bounded first: kfac_clip_norm takes
 the length sqrt(sum P . grad) of the natural gradient step in the Fisher metric
 (`metric=False`: the Euclidean norm of P), and the weights move by
 eta * min(1, max_norm / length) * P; `norm` and `scale` hold the last step's.
+
+A fully connected layer's x and g may be checkpoints (kfac.Checkpoint: the matrix kept in
+8 bits, x with its column of ones where the layer has a bias).  The factors are then built
+from them, and with grads = None the weight gradients are, too (kfac_weight_grad).
 """
 from __future__ import annotations
 
@@ -104,6 +108,7 @@ class KfacStep:
         self.info = torch.zeros(2 * len(self.layers), dtype=torch.int32, device=self.device)
         self.damp = torch.zeros(2 * len(self.layers), device=self.device)
         self._ws = {}
+        self._grads = None
 
     # ---------------------------------------------------------------- pieces
     def reset_factors(self):
@@ -118,12 +123,17 @@ class KfacStep:
             M = rows_total[i] if rows_total is not None else L.rows(self.batch)
             alpha = (1.0 - self.xi) / M
             beta = self.xi if first else 1.0
-            if L.name == "fc" or (L.hin == 1 and L.k == 1):
-                xa = x.reshape(x.shape[0], -1)
+            if isinstance(x, kfac.Checkpoint):
+                if x.width != L.d_a:
+                    raise ValueError(f"layer {L.name}: a checkpoint of {x.width} columns, {L.d_a} wanted")
+                srcs.append(kfac.FactorSource(x, s.A, alpha=alpha, beta=beta))
             else:
-                xa = x
-            srcs.append(kfac.FactorSource(xa, s.A, L.k, L.k, (L.stride, L.stride), (L.pad, L.pad),
-                                          L.bias, alpha, beta))
+                if L.name == "fc" or (L.hin == 1 and L.k == 1):
+                    xa = x.reshape(x.shape[0], -1)
+                else:
+                    xa = x
+                srcs.append(kfac.FactorSource(xa, s.A, L.k, L.k, (L.stride, L.stride), (L.pad, L.pad),
+                                              L.bias, alpha, beta))
             srcs.append(kfac.FactorSource(g, s.G, alpha=alpha, beta=beta))
         return srcs
 
@@ -174,8 +184,24 @@ class KfacStep:
         ws = self._workspace("clip", tensors.need)
         kfac.kfac_clip_norm(tensors, self.max_norm, self.norm, self.scale, self.eta, ws, stream)
 
-    def run(self, xs, gs, grads, stream=None):
-        """One full step: factors + inverse + preconditioning for all layers."""
+    def weight_grads(self, xs, gs, alphas: Optional[Sequence[float]] = None, stream=None):
+        """The layers' weight gradients alpha g^T x (default: 1 / rows) from checkpoints, in bf16;
+        the buffers are the step's own and are written again by the next call."""
+        if any(not isinstance(t, kfac.Checkpoint) for t in (*xs, *gs)):
+            raise TypeError("weight gradients are made from checkpoints")
+        if self._grads is None:
+            self._grads = [_matrix(L.d_g, L.d_a, self.device, torch.bfloat16) for L in self.layers]
+        alphas = [1.0 / max(x.rows, 1) for x in xs] if alphas is None else alphas
+        items = [kfac.WeightGrad(x, g, out, alpha) for x, g, out, alpha in zip(xs, gs, self._grads, alphas)]
+        ws = self._workspace("weight_grad", kfac.kfac_weight_grad_workspace_size(items))
+        kfac.kfac_weight_grad(items, ws, stream)
+        return self._grads
+
+    def run(self, xs, gs, grads=None, stream=None):
+        """One full step: factors + inverse + preconditioning for all layers.  grads None:
+        made from the checkpoints xs and gs."""
+        if grads is None:
+            grads = self.weight_grads(xs, gs, stream=stream)
         self.factor_update(xs, gs, stream=stream)
         self.damp_invert(stream)
         self.precondition(grads, stream)
@@ -186,9 +212,12 @@ class KfacStep:
         t = self.t if t is None else t
         return t < self.warmup or (t - self.warmup) % self.update_every == 0
 
-    def step(self, xs, gs, grads, stream=None) -> bool:
+    def step(self, xs, gs, grads=None, stream=None) -> bool:
         """Step t of the stale-factor schedule; returns whether it refreshed.
-        xs / gs are only read on refresh steps (None is accepted otherwise)."""
+        xs / gs are only read on refresh steps (None is accepted otherwise), unless grads is
+        None: then the weight gradients are made from them."""
+        if grads is None:
+            grads = self.weight_grads(xs, gs, stream=stream)
         refresh = self.refresh_due()
         if refresh:
             self.factor_update(xs, gs, stream=stream)
