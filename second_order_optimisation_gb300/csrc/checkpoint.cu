@@ -125,137 +125,148 @@ __device__ __forceinline__ uint4 from_byte(uint4 lo, uint4 hi, int k) {
                       __funnelshift_r(w[3], w[4], s));
 }
 
-template <int DT>
-__device__ __forceinline__ void store_tile(const Item &it, long long tile, uint8_t (*exps)[4]) {
+// 16 N columns of a tile, by all its warps.  FULL: all its rows and columns are x's (nothing is
+// looked at row by row then; otherwise 12.8 instructions an element held it at 5.5 TB/s).
+template <int DT, bool FULL>
+__device__ __forceinline__ void store_part(const Item &it, long long rt, int cp, uint8_t (*exps)[4]) {
     using M = Mag<DT>;
-    constexpr int N = Elem<DT>::N, ROWS = 16, COLS = 16 * N;
+    constexpr int N = Elem<DT>::N, ROWS = 16;
     using bits = typename Elem<DT>::bits;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int ct = (int)(tile % it.wides);
-    const long long rt = tile / it.wides;
     const long long r0 = rt * TILE + warp * 32 + lane / 16;  // rows r0, r0 + 2, ...
-#pragma unroll 1
-    for (int part = 0; part < TILE; part += COLS) {
-        const int c0 = ct * TILE + part + lane % 16 * N;
-        const int n = min(N, it.cols - c0);  // values here (may be negative)
-        uint4 u[ROWS];
-        const char *src = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
-        if (it.wide && it.cols % N == 0) {
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (r0 + 2 * i < it.rows && n > 0) u[i] = ld16(src + 2 * i * it.ld_bytes);
-            }
-        } else {
-            // At other alignments a lane loads the aligned 16 bytes that its group begins in, and has the rest
-            // of it from the next lane, which loads them where its own group is not whole, too; the last
-            // lane of a row's part loads them itself.  A group that is not whole goes value by value.
-            const bool full = n == N;
-            const unsigned whole = __ballot_sync(ALL_LANES, full);
-            const bool after = lane % 16 > 0 && (whole >> (lane - 1) & 1);
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const char *p = src + 2 * i * it.ld_bytes;
-                const int off = (int)((uintptr_t)p & 15);
-                u[i] = make_uint4(0, 0, 0, 0);
-                if (r0 + 2 * i < it.rows && (full || (after && off))) u[i] = ld16(p - off);
-            }
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const char *p = src + 2 * i * it.ld_bytes;
-                const int off = (int)((uintptr_t)p & 15);
-                uint4 next = make_uint4(__shfl_down_sync(ALL_LANES, u[i].x, 1, 16), __shfl_down_sync(ALL_LANES, u[i].y, 1, 16),
-                                        __shfl_down_sync(ALL_LANES, u[i].z, 1, 16), __shfl_down_sync(ALL_LANES, u[i].w, 1, 16));
-                if (r0 + 2 * i < it.rows && full && lane % 16 == 15 && off) next = ld16(p - off + 16);
-                u[i] = from_byte(u[i], next, off);
-            }
-            if (!full) {
-#pragma unroll
-                for (int i = 0; i < ROWS; ++i) {
-                    uint32_t w[4] = {0, 0, 0, 0};
-                    if (r0 + 2 * i < it.rows) {
-                        const bits *p = (const bits *)(src + 2 * i * it.ld_bytes);
-#pragma unroll
-                        for (int j = 0; j < N - 1; ++j)
-                            if (j < n) w[j * 4 / N] |= (uint32_t)p[j] << (N == 8 ? (j & 1) * 16 : 0);
-                    }
-                    u[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-        }
-        uint32_t m[4] = {0, 0, 0, 0};
+    const int c0 = cp + lane % 16 * N;
+    const int n = FULL ? N : min(N, it.cols - c0);  // values here (may be negative)
+    uint4 u[ROWS];
+    const char *src = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
+    if (it.wide && (FULL || it.cols % N == 0)) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            m[0] = M::raise(m[0], u[i].x); m[1] = M::raise(m[1], u[i].y);
-            m[2] = M::raise(m[2], u[i].z); m[3] = M::raise(m[3], u[i].w);
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (FULL || (r0 + 2 * i < it.rows && n > 0)) u[i] = ld16(src + 2 * i * it.ld_bytes);
         }
-        bool odd = false;
+    } else {
+        // At other alignments a lane loads the aligned 16 bytes that its group begins in, and has the rest
+        // of it from the next lane, which loads them where its own group is not whole, too; the last
+        // lane of a row's part loads them itself.  A group that is not whole goes value by value.
+        const bool full = FULL || n == N;
+        const unsigned whole = __ballot_sync(ALL_LANES, full);
+        const bool after = lane % 16 > 0 && (whole >> (lane - 1) & 1);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const char *p = src + 2 * i * it.ld_bytes;
+            const int off = (int)((uintptr_t)p & 15);
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (FULL || (r0 + 2 * i < it.rows && (full || (after && off)))) u[i] = ld16(p - off);
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const char *p = src + 2 * i * it.ld_bytes;
+            const int off = (int)((uintptr_t)p & 15);
+            uint4 next = make_uint4(__shfl_down_sync(ALL_LANES, u[i].x, 1, 16), __shfl_down_sync(ALL_LANES, u[i].y, 1, 16),
+                                    __shfl_down_sync(ALL_LANES, u[i].z, 1, 16), __shfl_down_sync(ALL_LANES, u[i].w, 1, 16));
+            if ((FULL || (r0 + 2 * i < it.rows && full)) && lane % 16 == 15 && off) next = ld16(p - off + 16);
+            u[i] = from_byte(u[i], next, off);
+        }
+        if (!FULL && !full) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (r0 + 2 * i < it.rows) {
+                    const bits *p = (const bits *)(src + 2 * i * it.ld_bytes);
+#pragma unroll
+                    for (int j = 0; j < N - 1; ++j)
+                        if (j < n) w[j * 4 / N] |= (uint32_t)p[j] << (N == 8 ? (j & 1) * 16 : 0);
+                }
+                u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        m[0] = M::raise(m[0], u[i].x); m[1] = M::raise(m[1], u[i].y);
+        m[2] = M::raise(m[2], u[i].z); m[3] = M::raise(m[3], u[i].w);
+    }
+    bool odd = false;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m[w] = M::join(m[w], __shfl_xor_sync(ALL_LANES, m[w], 16));
+#pragma unroll
+    for (int j = 0; j < N; ++j) odd |= M::bits(m, j) >= M::TOP;
+    if (__any_sync(ALL_LANES, odd)) {  // infinities or NaN: the largest of the finite ones
+        m[0] = m[1] = m[2] = m[3] = 0;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            m[0] = M::raise(m[0], M::finite(u[i].x)); m[1] = M::raise(m[1], M::finite(u[i].y));
+            m[2] = M::raise(m[2], M::finite(u[i].z)); m[3] = M::raise(m[3], M::finite(u[i].w));
+        }
 #pragma unroll
         for (int w = 0; w < 4; ++w) m[w] = M::join(m[w], __shfl_xor_sync(ALL_LANES, m[w], 16));
+    }
+    uint32_t e[N];
+    float inv[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) odd |= M::bits(m, j) >= M::TOP;
-        if (__any_sync(ALL_LANES, odd)) {  // infinities or NaN: the largest of the finite ones
-            m[0] = m[1] = m[2] = m[3] = 0;
+    for (int j = 0; j < N; ++j) {
+        e[j] = exponent_of(M::value(M::bits(m, j)));
+        odd |= e[j] == LAST_EXPONENT;
+        inv[j] = inverse_of(e[j]);
+    }
+    odd = __any_sync(ALL_LANES, odd);
+    uint8_t *dst = it.q + r0 * it.ldq + c0;
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                m[0] = M::raise(m[0], M::finite(u[i].x)); m[1] = M::raise(m[1], M::finite(u[i].y));
-                m[2] = M::raise(m[2], M::finite(u[i].z)); m[3] = M::raise(m[3], M::finite(u[i].w));
-            }
+    for (int i = 0; i < ROWS; ++i) {
+        if (!FULL && r0 + 2 * i >= it.rows) continue;
+        float v[N];
+        Elem<DT>::unpack(u[i], v);
+        uint32_t b[N / 4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) m[w] = M::join(m[w], __shfl_xor_sync(ALL_LANES, m[w], 16));
+        for (int j = 0; j < N; ++j) v[j] *= inv[j];
+        if (odd) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = bounded(v[j], e[j]);
         }
-        uint32_t e[N];
-        float inv[N];
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+            b[j] = e4m3x2(v[4 * j], v[4 * j + 1]) | e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
+        uint8_t *d = dst + 2 * i * it.ldq;
+        if (FULL || n == N) {  // (q's rows start on 16-byte boundaries, and c0 is a multiple of N)
+            if constexpr (N == 8) *(uint2 *)d = make_uint2(b[0], b[1]);
+            else *(uint32_t *)d = b[0];
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < n) d[j] = (uint8_t)(b[j / 4] >> j % 4 * 8);
+        }
+        if (!FULL && c0 <= it.cols && it.cols < c0 + N && it.cols < it.width) d[it.cols - c0] = 0x78;  // 256 = 1 2^8
+    }
+    if (lane < 16) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            e[j] = exponent_of(M::value(M::bits(m, j)));
-            odd |= e[j] == LAST_EXPONENT;
-            inv[j] = inverse_of(e[j]);
+            const int c = c0 + j, at = c % 32 * 4 + c % TILE / 32;  // (16 bytes to a column modulo 32, 4 to each of 4)
+            const uint32_t b = FULL ? e[j] : r0 >= it.rows ? 0u : c < it.cols ? e[j] : c < it.width ? 119u : 0u;  // 1 = 256 2^-8
+            exps[at][warp] = (uint8_t)b;
         }
-        odd = __any_sync(ALL_LANES, odd);
-        uint8_t *dst = it.q + r0 * it.ldq + c0;
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            if (r0 + 2 * i >= it.rows) continue;
-            float v[N];
-            Elem<DT>::unpack(u[i], v);
-            uint32_t b[N / 4];
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] *= inv[j];
-            if (odd) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) v[j] = bounded(v[j], e[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < N / 4; ++j)
-                b[j] = e4m3x2(v[4 * j], v[4 * j + 1]) | e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
-            uint8_t *d = dst + 2 * i * it.ldq;
-            if (n == N) {  // (q's rows start on 16-byte boundaries, and c0 is a multiple of N)
-                if constexpr (N == 8) *(uint2 *)d = make_uint2(b[0], b[1]);
-                else *(uint32_t *)d = b[0];
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j < n) d[j] = (uint8_t)(b[j / 4] >> j % 4 * 8);
-            }
-            if (c0 <= it.cols && it.cols < c0 + N && it.cols < it.width) d[it.cols - c0] = 0x78;  // 256 = 1 2^8
-        }
-        if (lane < 16) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int c = c0 + j, at = c % 32 * 4 + c % TILE / 32;  // (16 bytes to a column modulo 32, 4 to each of 4)
-                uint32_t b = r0 >= it.rows ? 0u : c < it.cols ? e[j] : c < it.width ? 119u : 0u;  // 1 = 256 2^-8
-                exps[at][warp] = (uint8_t)b;
-            }
-        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store_tile(const Item &it, long long tile, uint8_t (*exps)[4]) {
+    constexpr int COLS = 16 * Elem<DT>::N;
+    const int ct = (int)(tile % it.wides);
+    const long long rt = tile / it.wides;
+    const bool rows = (rt + 1) * TILE <= it.rows;
+#pragma unroll 1
+    for (int cp = ct * TILE; cp < (ct + 1) * TILE; cp += COLS) {
+        if (rows && cp + COLS <= it.cols) store_part<DT, true>(it, rt, cp, exps);
+        else store_part<DT, false>(it, rt, cp, exps);
     }
     __syncthreads();
     ((uint32_t *)(it.scales + (ct * (long long)it.chunks + rt) * 512))[threadIdx.x] = ((const uint32_t *)exps)[threadIdx.x];
 }
 
-// 32768 x 8192 bf16 (814 MB) takes 140 us, 5.8 TB/s; three CTAs to an SM 173 us, six 147. 20000 x 5001
-// bf16 (rows on every alignment) 108 us; with two loads a group in place of the exchange 160.
-__global__ void __launch_bounds__(THREADS, 5) store_kernel(const __grid_constant__ Params P) {
+// 32768 x 8192 bf16 (814 MB) takes 115 us, 7.1 TB/s (a copy: 6.8); 20000 x 5001 bf16 (rows on every
+// alignment) 76 us, 4.0 TB/s, with five CTAs to an SM 84; with two loads a group in place of the exchange
+// between lanes twice as long.
+__global__ void __launch_bounds__(THREADS, 4) store_kernel(const __grid_constant__ Params P) {
     __shared__ __align__(16) uint8_t exps[TILE][4];
     pdl_wait();
     pdl_trigger();
@@ -277,84 +288,92 @@ __device__ __forceinline__ void store_some(char *d, uint4 u, int j0, int j1) {
         if (j >= j0 && j < j1) ((bits *)d)[j] = (bits)(N == 4 ? w[j] : w[j / 2] >> (j & 1) * 16);
 }
 
-// Values of a tile: x_ij = q_ij 2^e, rounded to x's type.
-template <int DT>
-__device__ __forceinline__ void load_tile(const Item &it, long long tile, const uint8_t (*exps)[4]) {
-    constexpr int N = Elem<DT>::N, ROWS = 16, COLS = 16 * N;
+// Values of 16 N columns of a tile, x_ij = q_ij 2^e, rounded to x's type.  FULL as in store_part.
+template <int DT, bool FULL>
+__device__ __forceinline__ void load_part(const Item &it, long long rt, int cp, const uint8_t (*exps)[4]) {
+    constexpr int N = Elem<DT>::N, ROWS = 16;
     using bits = typename Elem<DT>::bits;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int ct = (int)(tile % it.wides);
-    const long long rt = tile / it.wides;
     const long long r0 = rt * TILE + warp * 32 + lane / 16;
-#pragma unroll 1
-    for (int part = 0; part < TILE; part += COLS) {
-        const int c0 = ct * TILE + part + lane % 16 * N;
-        const int n = max(0, min(N, it.cols - c0));
-        const uint8_t *src = it.q + r0 * it.ldq + c0;
-        uint32_t b[ROWS][N / 4];
-        if (n == N) {
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                b[i][0] = b[i][N / 4 - 1] = 0;
-                if (r0 + 2 * i >= it.rows) continue;
-                if constexpr (N == 8) {
-                    const uint2 u = *(const uint2 *)(src + 2 * i * it.ldq);
-                    b[i][0] = u.x;
-                    b[i][1] = u.y;
-                } else {
-                    b[i][0] = *(const uint32_t *)(src + 2 * i * it.ldq);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                b[i][0] = b[i][N / 4 - 1] = 0;
-                if (r0 + 2 * i >= it.rows) continue;
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j < n) b[i][j / 4] |= (uint32_t)src[2 * i * it.ldq + j] << j % 4 * 8;
-            }
-        }
-        float p[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) p[j] = power_of(exps[(c0 + j) % 32 * 4 + (c0 + j) % TILE / 32][warp]);
-        char *dst = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
-        // At other alignments a lane stores the aligned 16 bytes that its group begins in, with the last
-        // bytes of the group of the lane before it, where both groups are whole; the ends of such a
-        // run, and groups that are not whole, go value by value.
-        const bool full = n == N;
-        const unsigned whole = __ballot_sync(ALL_LANES, full);  // (all lanes vote: which groups are whole)
-        const bool joined = full && lane % 16 > 0 && (whole >> (lane - 1) & 1);
-        const bool tail = full && !(lane % 16 < 15 && (whole >> (lane + 1) & 1));
+    const int c0 = cp + lane % 16 * N;
+    const int n = FULL ? N : max(0, min(N, it.cols - c0));
+    const uint8_t *src = it.q + r0 * it.ldq + c0;
+    uint32_t b[ROWS][N / 4];
+    if (FULL || n == N) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            float v[N];
-#pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const float2 f = from_e4m3x2(b[i][j / 4] >> j % 4 * 8 & 0xffffu);
-                v[j] = f.x * p[j];
-                v[j + 1] = f.y * p[j + 1];
+            b[i][0] = b[i][N / 4 - 1] = 0;
+            if (!FULL && r0 + 2 * i >= it.rows) continue;
+            if constexpr (N == 8) {
+                const uint2 u = *(const uint2 *)(src + 2 * i * it.ldq);
+                b[i][0] = u.x;
+                b[i][1] = u.y;
+            } else {
+                b[i][0] = *(const uint32_t *)(src + 2 * i * it.ldq);
             }
-            char *d = dst + 2 * i * it.ld_bytes;
-            const uint4 u = Elem<DT>::pack(v);
-            const bool in = r0 + 2 * i < it.rows;
-            if (it.wide) {
-                if (in && full) *(uint4 *)d = u;
-                else if (in) store_some<DT>(d, u, 0, n);
-                continue;
-            }
-            const int off = (int)((uintptr_t)d & 15), cut = N - off / (int)sizeof(bits);
-            const uint4 before = make_uint4(__shfl_up_sync(ALL_LANES, u.x, 1, 16), __shfl_up_sync(ALL_LANES, u.y, 1, 16),
-                                            __shfl_up_sync(ALL_LANES, u.z, 1, 16), __shfl_up_sync(ALL_LANES, u.w, 1, 16));
-            if (!in) continue;
-            if (off == 0 && full) *(uint4 *)d = u;
-            else if (joined) *(uint4 *)(d - off) = from_byte(before, u, 16 - off);
-            if (off == 0 ? !full : !joined || tail) store_some<DT>(d, u, joined ? cut : 0, off == 0 || tail || !full ? n : cut);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            b[i][0] = b[i][N / 4 - 1] = 0;
+            if (r0 + 2 * i >= it.rows) continue;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (j < n) b[i][j / 4] |= (uint32_t)src[2 * i * it.ldq + j] << j % 4 * 8;
+        }
+    }
+    float p[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] = power_of(exps[(c0 + j) % 32 * 4 + (c0 + j) % TILE / 32][warp]);
+    char *dst = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
+    // At other alignments a lane stores the aligned 16 bytes that its group begins in, with the last
+    // bytes of the group of the lane before it, where both groups are whole; the ends of such a
+    // run, and groups that are not whole, go value by value.
+    const bool full = FULL || n == N;
+    const unsigned whole = __ballot_sync(ALL_LANES, full);  // (all lanes vote: which groups are whole)
+    const bool joined = full && lane % 16 > 0 && (whole >> (lane - 1) & 1);
+    const bool tail = full && !(lane % 16 < 15 && (whole >> (lane + 1) & 1));
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        float v[N];
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            const float2 f = from_e4m3x2(b[i][j / 4] >> j % 4 * 8 & 0xffffu);
+            v[j] = f.x * p[j];
+            v[j + 1] = f.y * p[j + 1];
+        }
+        char *d = dst + 2 * i * it.ld_bytes;
+        const uint4 u = Elem<DT>::pack(v);
+        const bool in = FULL || r0 + 2 * i < it.rows;
+        if (it.wide) {
+            if (in && full) *(uint4 *)d = u;
+            else if (in) store_some<DT>(d, u, 0, n);
+            continue;
+        }
+        const int off = (int)((uintptr_t)d & 15), cut = N - off / (int)sizeof(bits);
+        const uint4 before = make_uint4(__shfl_up_sync(ALL_LANES, u.x, 1, 16), __shfl_up_sync(ALL_LANES, u.y, 1, 16),
+                                        __shfl_up_sync(ALL_LANES, u.z, 1, 16), __shfl_up_sync(ALL_LANES, u.w, 1, 16));
+        if (!in) continue;
+        if (off == 0 && full) *(uint4 *)d = u;
+        else if (joined) *(uint4 *)(d - off) = from_byte(before, u, 16 - off);
+        if (off == 0 ? !full : !joined || tail) store_some<DT>(d, u, joined ? cut : 0, off == 0 || tail || !full ? n : cut);
     }
 }
 
-// 32768 x 8192 bf16 takes 130 us, 6.3 TB/s; four CTAs to an SM 138 us, eight 141.
+template <int DT>
+__device__ __forceinline__ void load_tile(const Item &it, long long tile, const uint8_t (*exps)[4]) {
+    constexpr int COLS = 16 * Elem<DT>::N;
+    const int ct = (int)(tile % it.wides);
+    const long long rt = tile / it.wides;
+    const bool rows = (rt + 1) * TILE <= it.rows;
+#pragma unroll 1
+    for (int cp = ct * TILE; cp < (ct + 1) * TILE; cp += COLS) {
+        if (rows && cp + COLS <= it.cols) load_part<DT, true>(it, rt, cp, exps);
+        else load_part<DT, false>(it, rt, cp, exps);
+    }
+}
+
+// 32768 x 8192 bf16 takes 121 us, 6.8 TB/s (four CTAs to an SM 128); 20000 x 5001 bf16 69 us.
 __global__ void __launch_bounds__(THREADS, 6) load_kernel(const __grid_constant__ Params P) {
     __shared__ __align__(16) uint8_t exps[TILE][4];
     pdl_wait();

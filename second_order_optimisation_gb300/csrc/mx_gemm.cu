@@ -73,6 +73,7 @@ struct Params : Deal {
     float *partial;  // [2 pairs][TILE][TILE] pieces of tiles: 2 p begins inside a tile, 2 p + 1 ends inside one
     int *counters;   // [pairs][2] pieces that are there of the tile that the pair's share ends in, by CTA
     int *err;
+    bool alone;      // one pair, which sets *err to 0 (no one else writes it)
 };
 constexpr int FEW_PROBS = 4;
 static_assert(sizeof(Params<MAX_PROBS>) <= 32000, "kernel parameters");
@@ -356,6 +357,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
             uint32_t phase = 0, use = 0;
             bool ok = true;
             const uint32_t s0 = smem_u32(smem), f0 = smem_u32(sf);
+            if (P.alone && lane == 0) {  // before the first product, and so before anyone reports
+                *P.err = 0;
+                __threadfence();
+            }
+            __syncwarp();
             Walk walk(P, pair, pairs);
             for (Item k; ok && walk.next(P, k);) {
                 const Prob &q = P.prob[k.p];
@@ -636,12 +642,13 @@ size_t mx_workspace_bytes(const MxJob *jobs, int njobs) {
 namespace {
 
 template <int CAP>
-kfac_status launch(const MxJob *jobs, const Plan &p, const Launch &l, int *counters, int *err, cudaStream_t st) {
+kfac_status launch(const MxJob *jobs, const Plan &p, const Launch &l, int *counters, int *err, bool alone, cudaStream_t st) {
     std::unique_ptr<Params<CAP>> P(new Params<CAP>());
     static_cast<Deal &>(*P) = l.deal;
     P->partial = p.partial;
     P->counters = counters;
     P->err = err;
+    P->alone = alone;
     for (int i = 0; i < P->nprob; ++i) {
         const MxJob &j = jobs[p.order[l.from + i]];
         Prob &q = P->prob[i];
@@ -671,12 +678,14 @@ kfac_status launch(const MxJob *jobs, const Plan &p, const Launch &l, int *count
 }
 
 kfac_status run_plan(const MxJob *jobs, const Plan &p, int *err, bool zero_err, cudaStream_t st) {
-    if (zero_err || p.ncounters)
+    // (one pair of CTAs sets the error word to 0 itself)
+    const bool alone = zero_err && p.launches.size() == 1 && p.launches[0].pairs == 1 && !p.ncounters;
+    if (!alone && (zero_err || p.ncounters))
         KFAC_LAUNCH(KK_MX, st, zero_kernel, 1, 256, 0, zero_err ? err : nullptr, p.counters, (int)p.ncounters);
     int *counters = p.counters;
     for (const Launch &l : p.launches) {
-        const kfac_status s = l.deal.nprob <= FEW_PROBS ? launch<FEW_PROBS>(jobs, p, l, counters, err, st)
-                                                        : launch<MAX_PROBS>(jobs, p, l, counters, err, st);
+        const kfac_status s = l.deal.nprob <= FEW_PROBS ? launch<FEW_PROBS>(jobs, p, l, counters, err, alone, st)
+                                                        : launch<MAX_PROBS>(jobs, p, l, counters, err, alone, st);
         if (s != KFAC_OK) return s;
         if (l.span > 0) counters += 2 * l.pairs;
     }

@@ -338,16 +338,21 @@ def checkpoint_scale_bytes(rows: int, width: int) -> int:
 
 
 def _checkpoint_args(c: Checkpoint):
-    """A checkpoint's elements, pitch and exponents."""
-    q, sc = c.q, c.scales
+    """A checkpoint's elements, pitch and exponents.  (Few questions to the tensors: each costs
+    as much as the rest of a field.)"""
+    q, sc, rows, width = c.q, c.scales, c.rows, c.width
     if q.dtype is not torch.uint8 or sc.dtype is not torch.uint8:
         raise TypeError("a checkpoint's q and scales must be uint8")
-    if q.dim() != 2 or q.shape[0] < c.rows or q.shape[1] < c.width or (q.stride(1) != 1 and q.shape[1] > 1 and c.rows > 0):
-        raise ValueError(f"q must be at least [{c.rows}, {c.width}] with unit column stride, got {tuple(q.shape)}")
-    if not sc.is_contiguous() or sc.numel() < checkpoint_scale_bytes(c.rows, c.width):
-        raise ValueError(f"scales must be {checkpoint_scale_bytes(c.rows, c.width)} dense bytes, got {tuple(sc.shape)}")
-    ld = q.stride(0) if q.shape[0] > 1 else (c.width + 15) // 16 * 16  # (one row has no pitch)
-    return q.data_ptr(), ld, sc.data_ptr()
+    shape = q.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] < width:
+        raise ValueError(f"q must be at least [{rows}, {width}], got {tuple(shape)}")
+    ld, unit = q.stride()
+    if unit != 1 and shape[1] > 1 and rows > 0:
+        raise ValueError("q must have unit column stride")
+    if not sc.is_contiguous() or sc.numel() < checkpoint_scale_bytes(rows, width):
+        raise ValueError(f"scales must be {checkpoint_scale_bytes(rows, width)} dense bytes, got {tuple(sc.shape)}")
+    # (one row has no pitch)
+    return q.data_ptr(), ld if shape[0] > 1 else (width + 15) // 16 * 16, sc.data_ptr()
 
 
 @dataclass
@@ -359,21 +364,27 @@ class CheckpointItem:
     append_one: bool = False
 
 
+def _checkpoint_desc(it: CheckpointItem) -> CheckpointDesc:
+    x, c, one = it.x, it.checkpoint, bool(it.append_one)
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [rows, cols], got {tuple(shape)}")
+    rows, cols = shape
+    ld, unit = x.stride()
+    if unit != 1 and cols > 1 and rows > 0:
+        raise ValueError("x must have unit column stride")
+    if c.rows != rows or c.width != cols + one:
+        raise ValueError(f"the checkpoint is [{c.rows}, {c.width}], x is {tuple(shape)}, append_one {one}")
+    return CheckpointDesc(dtype, x.data_ptr(), ld if rows > 1 else cols, rows, cols, one, *_checkpoint_args(c))
+
+
 def _checkpoint_descs(items: Sequence[CheckpointItem]):
-    arr = (CheckpointDesc * max(len(items), 1))()
-    for i, it in enumerate(items):
-        x, c = it.x, it.checkpoint
-        if x.dtype not in _DTYPES:
-            raise TypeError(f"unsupported dtype {x.dtype}")
-        if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1 and x.shape[0] > 0):
-            raise ValueError("x must be [rows, cols] with unit column stride")
-        rows, cols = x.shape
-        if c.rows != rows or c.width != cols + bool(it.append_one):
-            raise ValueError(f"the checkpoint is [{c.rows}, {c.width}], x is {tuple(x.shape)}, append_one {it.append_one}")
-        q, ldq, scales = _checkpoint_args(c)
-        arr[i] = CheckpointDesc(_DTYPES[x.dtype], x.data_ptr(), x.stride(0) if rows > 1 else cols, rows, cols,
-                                int(bool(it.append_one)), q, ldq, scales)
-    return arr
+    if len(items) == 1:
+        return ctypes.byref(_checkpoint_desc(items[0]))
+    return (CheckpointDesc * max(len(items), 1))(*[_checkpoint_desc(it) for it in items])
 
 
 def kfac_checkpoint_store(items: Sequence[CheckpointItem], stream=None) -> None:
@@ -397,19 +408,26 @@ class WeightGrad:
     beta: float = 0.0
 
 
+def _weight_grad_desc(it: WeightGrad) -> WeightGradDesc:
+    a, g, out = it.a, it.g, it.out
+    dtype, dA, dG = _DTYPES.get(out.dtype), a.width, g.width
+    if dtype is None:
+        raise TypeError(f"unsupported dtype {out.dtype}")
+    if a.rows != g.rows:
+        raise ValueError(f"a has {a.rows} rows, g {g.rows}")
+    if out.shape != (dG, dA):
+        raise ValueError(f"out must be [{dG}, {dA}], got {tuple(out.shape)}")
+    ld, unit = out.stride()
+    if unit != 1 and dA > 1:
+        raise ValueError("out must have unit column stride")
+    return WeightGradDesc(*_checkpoint_args(a), *_checkpoint_args(g), a.rows, dA, dG, out.data_ptr(),
+                          ld if dG > 1 else dA, dtype, it.alpha, it.beta)
+
+
 def _weight_grad_descs(items: Sequence[WeightGrad]):
-    arr = (WeightGradDesc * max(len(items), 1))()
-    for i, it in enumerate(items):
-        a, g, out = it.a, it.g, it.out
-        if out.dtype not in _DTYPES:
-            raise TypeError(f"unsupported dtype {out.dtype}")
-        if a.rows != g.rows:
-            raise ValueError(f"a has {a.rows} rows, g {g.rows}")
-        if out.shape != (g.width, a.width) or (out.stride(1) != 1 and a.width > 1):
-            raise ValueError(f"out must be [{g.width}, {a.width}] with unit column stride, got {tuple(out.shape)}")
-        arr[i] = WeightGradDesc(*_checkpoint_args(a), *_checkpoint_args(g), a.rows, a.width, g.width, out.data_ptr(),
-                                out.stride(0) if g.width > 1 else a.width, _DTYPES[out.dtype], it.alpha, it.beta)
-    return arr
+    if len(items) == 1:
+        return ctypes.byref(_weight_grad_desc(items[0]))
+    return (WeightGradDesc * max(len(items), 1))(*[_weight_grad_desc(it) for it in items])
 
 
 def kfac_weight_grad_workspace_size(items: Sequence[WeightGrad]) -> int:
@@ -704,19 +722,19 @@ def _rowvec(t: Optional[torch.Tensor], n: int, name: str, dtype=torch.float32) -
     return t.data_ptr()
 
 
-def _logits_args(logits: torch.Tensor, target: torch.Tensor, temperature: float):
+def _logits_args(logits: torch.Tensor, target: torch.Tensor, temperature: float, name: str = "target"):
     """The descriptor fields from dtype to temperature, the same for every call on logits."""
     dtype, tdtype = _DTYPES.get(logits.dtype), target.dtype
     if dtype is None:
         raise TypeError(f"unsupported logits dtype {logits.dtype}")
     if tdtype is not torch.int64 and tdtype is not torch.int32:
-        raise TypeError(f"target must be int64 or int32, got {tdtype}")
+        raise TypeError(f"{name} must be int64 or int32, got {tdtype}")
     shape, stride = logits.shape, logits.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("logits must be [rows, vocab] with unit column stride")
     rows, vocab = shape
     if target.numel() != rows or not target.is_contiguous():
-        raise ValueError(f"target must be {rows} dense values, got shape {tuple(target.shape)}")
+        raise ValueError(f"{name} must be {rows} dense values, got shape {tuple(target.shape)}")
     return (dtype, logits.data_ptr(), stride[0] if rows > 1 else vocab, rows, vocab,
             target.data_ptr(), tdtype is torch.int32, temperature)
 
@@ -916,20 +934,23 @@ class VerifyDraft:
 
 
 def _verify_desc(t: VerifyDraft) -> VerifyDesc:
-    n, seqs = t.logits.shape[0], t.seq_offsets.numel() - 1
-    dtype, logits, ld, rows, vocab, tokens, i32, tau = _logits_args(t.logits, t.tokens, t.temperature)
+    seqs, saved, noise = t.seq_offsets.numel() - 1, t.draft_saved, t.noise
+    dtype, logits, ld, n, vocab, tokens, i32, tau = _logits_args(t.logits, t.tokens, t.temperature, "tokens")
     draft, ld_draft = _dlogits_args(t.logits, t.draft, "draft")
-    noise, ld_noise = None, 0
-    if t.noise is not None:
-        if t.noise.dtype is not torch.float32:
-            raise TypeError(f"noise must be fp32, got {t.noise.dtype}")
-        if t.noise.shape != (seqs, vocab) or (t.noise.stride(1) != 1 and vocab > 1):
-            raise ValueError(f"noise must be [{seqs}, {vocab}] with unit column stride, got {tuple(t.noise.shape)}")
-        noise, ld_noise = t.noise.data_ptr(), t.noise.stride(0) if seqs > 1 else vocab
-    return VerifyDesc(dtype, logits, ld, rows, vocab, tokens, i32, tau,
+    at, ld_noise = None, 0
+    if noise is not None:
+        if noise.dtype is not torch.float32:
+            raise TypeError(f"noise must be fp32, got {noise.dtype}")
+        if noise.shape != (seqs, vocab):
+            raise ValueError(f"noise must be [{seqs}, {vocab}], got {tuple(noise.shape)}")
+        ld_noise, unit = noise.stride()
+        if unit != 1 and vocab > 1:
+            raise ValueError("noise must have unit column stride")
+        at, ld_noise = noise.data_ptr(), ld_noise if seqs > 1 else vocab
+    return VerifyDesc(dtype, logits, ld, n, vocab, tokens, i32, tau,
                       _rowvec(t.seq_offsets, seqs + 1, "seq_offsets", torch.int32), seqs, draft, ld_draft,
-                      _rowvec(t.draft_saved, 2 * n, "draft_saved"), t.draft_temperature,
-                      _rowvec(t.uniform, n, "uniform"), noise, ld_noise, bool(t.greedy),
+                      _rowvec(saved, 2 * n, "draft_saved"), t.draft_temperature,
+                      _rowvec(t.uniform, n, "uniform"), at, ld_noise, bool(t.greedy),
                       _rowvec(t.accepted, seqs, "accepted", torch.int32),
                       _rowvec(t.out_tokens, n, "out_tokens", t.tokens.dtype), _rowvec(t.logp, n, "logp"))
 
