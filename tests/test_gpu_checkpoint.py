@@ -333,3 +333,95 @@ def test_weight_grad_of_tiles_in_pieces(rows, dA, dG):
     size = 0.25 * old.double().abs() + 0.5 * (y.double().abs().t() @ x.double().abs())
     assert bool(((outs[0].double() - want).abs() <= ref.SUM * size + ref.E * want.abs()).all())
     assert torch.equal(outs[0], outs[1]) and _err(ws) == 0
+
+
+# ------------------------------------------------------------ more tiles than run at once
+
+def _pair(rows, dA, dG, seed, pitch=0):
+    """Checkpoints of random values and these values, on the GPU; nothing behind a row may be read."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    out = []
+    for d in (dA, dG):
+        x = torch.randn(rows, d, device="cuda", generator=g) * torch.exp(torch.randn(d, device="cuda", generator=g))
+        c = kfac.Checkpoint.empty(rows, d)
+        if pitch:
+            c.q = torch.empty(rows, c.q.shape[1] + pitch, dtype=torch.uint8, device="cuda")
+        c.q.fill_(127)  # NaN
+        kfac.kfac_checkpoint_store([kfac.CheckpointItem(x, c)])
+        kfac.kfac_checkpoint_load([kfac.CheckpointItem(x, c)])
+        out += [c, x.double()]
+    return out
+
+
+@pytest.mark.parametrize("rows", [1, 300, 1500])
+@pytest.mark.parametrize("dA,dG,out", [(257, 19400, "f32"), (259, 19300, "bf16"), (260, 19201, "f16")])
+def test_weight_grad_of_a_few_columns_more_than_tiles(rows, dA, dG, out):
+    """76 tiles of 256 x 256, and narrow ones for a few columns more."""
+    a, av, g, gv = _pair(rows, dA, dG, rows, pitch=16 * (rows % 2))
+    old = torch.randn(dG, dA + 3, device="cuda").to(DT[out])
+    outs = [old.clone() for _ in range(3)]
+    for o, beta in zip(outs, (0.0, 0.5, 0.5)):
+        ws = kfac.kfac_weight_grad([kfac.WeightGrad(a, g, o[:, :dA], 0.25, beta)])
+        assert _err(ws) == 0
+    p, size = 0.25 * (gv.t() @ av), 0.25 * (gv.abs().t() @ av.abs())
+    for o, beta in zip(outs, (0.0, 0.5)):
+        want, most = p + beta * old[:, :dA].double(), size + beta * old[:, :dA].double().abs()
+        assert bool(((o[:, :dA].double() - want).abs() <= ref.SUM * most + ref.ROUND[out] * want.abs() + 2.0 ** -25).all())
+        assert torch.equal(o[:, dA:], old[:, dA:])
+    assert torch.equal(outs[1], outs[2])
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("rows,cols", [(70, 2816), (2100, 2819)])
+def test_factor_of_a_few_columns_more_than_tiles(rows, cols, packed):
+    """66 tiles on and above the diagonal, and 78 with the columns that are more."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    d = cols + 1
+    x = torch.randn(rows, cols, device="cuda", generator=gen)
+    c = kfac.Checkpoint.empty(rows, cols, True)
+    kfac.kfac_checkpoint_store([kfac.CheckpointItem(x, c, True)])
+    kfac.kfac_checkpoint_load([kfac.CheckpointItem(x, c, True)])
+    v = torch.cat([x, torch.ones(rows, 1, device="cuda")], 1).double()
+    old = torch.randn(d, d, device="cuda", generator=gen)
+    F = [kfac.pack_upper(old) if packed else old.clone() for _ in range(2)]
+    for f in F:
+        ws = kfac.kfac_factor_update([kfac.FactorSource(c, f, alpha=0.25, beta=0.5, packed=packed)])
+        assert _err(ws) == 0
+    assert torch.equal(F[0], F[1])
+    got = (kfac.unpack_upper(F[0], d) if packed else F[0]).double()
+    want = 0.25 * (v.t() @ v) + 0.5 * old.double()
+    size = 0.25 * (v.abs().t() @ v.abs()) + 0.5 * old.double().abs()
+    up = torch.triu(torch.ones(d, d, dtype=torch.bool, device="cuda"))
+    assert bool(((got - want).abs() <= ref.SUM * size + ref.E * want.abs())[up].all())
+    if not packed:
+        assert torch.equal(F[0][~up], old[~up])
+
+
+def test_weight_grad_of_more_problems_and_tiles_than_a_launch_takes():
+    a, av, g, gv = _pair(200, 514, 500, 3)
+    outs = [torch.empty(500, 514, device="cuda") for _ in range(51)]
+    ws = kfac.kfac_weight_grad([kfac.WeightGrad(a, g, o, 0.5) for o in outs])
+    want, size = 0.5 * (gv.t() @ av), 0.5 * (gv.abs().t() @ av.abs())
+    for o in outs:
+        assert bool(((o.double() - want).abs() <= ref.SUM * size + ref.E * want.abs()).all())
+    assert _err(ws) == 0
+
+
+@pytest.mark.parametrize("a,g", [(1e-36, 1e36), (1e30, 1e-30), (1e-20, 1e-18), (1e30, 1e30)])
+def test_weight_grad_of_extreme_exponents(a, g):
+    """Exponents whose product leaves fp32 on the way, or in the end."""
+    ca, av, cg, gv = _pair(160, 257, 300, 5)
+    for c, v, s in ((ca, av, a), (cg, gv, g)):
+        x = v.float() * s
+        kfac.kfac_checkpoint_store([kfac.CheckpointItem(x, c)])
+        kfac.kfac_checkpoint_load([kfac.CheckpointItem(x, c)])
+        v.copy_(x.double())
+    o = torch.empty(300, 257, device="cuda")
+    ws = kfac.kfac_weight_grad([kfac.WeightGrad(ca, cg, o)])
+    if a * g > 1e40:
+        assert not bool(torch.isfinite(o).any()) and _err(ws) == kfac.ERRW_NONFINITE
+        return
+    want, size = gv.t() @ av, gv.abs().t() @ av.abs()
+    # (products of subnormal sums lose what is below 2^-149, one a block of exponents)
+    assert bool(((o.double() - want).abs() <= ref.SUM * size + ref.E * want.abs() + 160 / 32 * 2.0 ** -149).all())
+    assert _err(ws) == 0
