@@ -628,11 +628,11 @@ kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, float max_nor
  * in general bf16 hold them exactly; fp16 rounds below 2^-14 and overflows above
  * 65504).
  * One launch for each 64 matrices.  rows = 0: nothing to do.  No workspace, no
- * error word.
+ * error word.  What a call writes must not overlap anything else that it reads or writes.
  * Errors: INVALID for count < 0, rows < 0, cols < 1, ld < cols, ldq < width,
  *   null x, q or scales of a matrix with rows, a base of x that is not
  *   element-aligned, a bad dtype; UNSUPPORTED for q, scales or ldq that are
- *   not multiples of 16 bytes, width > 65536, more than 2^31 - 1 rows or
+ *   not multiples of 16 bytes, width > 2^20, more than 2^31 - 1 rows or
  *   tiles of 128 x 128. */
 typedef struct {
     int32_t dtype;
@@ -653,7 +653,8 @@ kfac_status kfac_checkpoint_load(const kfac_checkpoint_desc *descs, int count, v
  * with the values that the checkpoints stand for (their products are exact), fp32
  * accumulation, one rounding to out's type (KFAC_F32, KFAC_BF16 or KFAC_F16).
  * out is read only where beta != 0; rows = 0 leaves beta out.  Results are
- * bitwise reproducible run to run.
+ * bitwise reproducible run to run.  No out may overlap another one of the call (sums over
+ * parts of a batch: one call for each, with beta = 1) or an input.
  * Error word (first int32 of the workspace): KFAC_ERRW_NONFINITE when a value of
  * out (before its rounding) is NaN or infinite, 1, 2, 4, 8 (KFAC_ERRW_TIMEOUT_*).
  * Errors: INVALID for count < 0, rows < 0, dA or dG < 1, ld < dA, ldq_a < dA,

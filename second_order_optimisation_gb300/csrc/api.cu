@@ -236,6 +236,7 @@ kfac_status validate_factor(const kfac_factor_desc *descs, int count, std::vecto
         if (d.dtype == KFAC_E4M3) {
             const kfac_status s = check_checkpoint(d.x, d.ldx, d.scales, d.n, d.c);
             if (s != KFAC_OK) return s;
+            if (d.c > 65536) return KFAC_ERR_UNSUPPORTED;
             continue;
         }
         if (geo[i].d > 65536 || geo[i].M >= (1LL << 31)) return KFAC_ERR_UNSUPPORTED;

@@ -456,7 +456,7 @@ kfac_status run(const kfac_checkpoint_desc *descs, int count, bool store, void *
 // tiles of exponents.
 kfac_status check_checkpoint(const void *q, long long ldq, const void *scales, long long rows, long long width) {
     if (rows < 0 || width < 1 || (rows > 0 && (!q || !scales || ldq < width))) return KFAC_ERR_INVALID;
-    if (rows > 0x7fffffffLL || width > 65536 || ceil_div(rows, TILE) * ceil_div(width, TILE) > 0x7fffffffLL)
+    if (rows > 0x7fffffffLL || width > (1 << 20) || ceil_div(rows, TILE) * ceil_div(width, TILE) > 0x7fffffffLL)
         return KFAC_ERR_UNSUPPORTED;
     if (rows > 0 && (ldq % 16 || (uintptr_t)q % 16 || (uintptr_t)scales % 16)) return KFAC_ERR_UNSUPPORTED;
     return KFAC_OK;

@@ -401,7 +401,8 @@ def kfac_checkpoint_load(items: Sequence[CheckpointItem], stream=None) -> None:
 @dataclass
 class WeightGrad:
     """out [dG, dA] (fp32, bf16 or fp16) <- beta out + alpha g^T a, from the checkpoints of
-    a layer's input a [rows, dA] and of its output gradients g [rows, dG]."""
+    a layer's input a [rows, dA] and of its output gradients g [rows, dG].  The outs of one
+    call must not overlap."""
     a: Checkpoint
     g: Checkpoint
     out: torch.Tensor

@@ -84,7 +84,7 @@ CK_BAD = [(dict(x=None), INVALID), (dict(q=None), INVALID), (dict(scales=None), 
           (dict(cols=0), INVALID), (dict(ld=99), INVALID), (dict(ldq=96), INVALID), (dict(dtype=3), INVALID),
           (dict(dtype=9), INVALID), (dict(x=0x1001), INVALID), (dict(append_one=1, cols=112, ld=112), INVALID),
           (dict(ldq=104), UNSUPPORTED), (dict(q=0x2008), UNSUPPORTED), (dict(scales=0x3008), UNSUPPORTED),
-          (dict(cols=65537, ld=70000, ldq=70016), UNSUPPORTED), (dict(rows=1 << 31), UNSUPPORTED),
+          (dict(cols=1048577, ld=1048577, ldq=1048592), UNSUPPORTED), (dict(rows=1 << 31), UNSUPPORTED),
           (dict(), INVALID)]  # (the last: pointers that are not device memory)
 
 
@@ -142,7 +142,7 @@ def _fd(**kw):
 @pytest.mark.parametrize("bad,status", [(dict(scales=None), INVALID), (dict(ldx=96), INVALID), (dict(ldf=99), INVALID),
                                         (dict(ldx=0), INVALID), (dict(ldx=104), UNSUPPORTED), (dict(x=0x1008), UNSUPPORTED),
                                         (dict(scales=0x3004), UNSUPPORTED), (dict(append_one=1, ldf=101), UNSUPPORTED),
-                                        (dict(h=2), UNSUPPORTED), (dict(kh=3, pad_h=1), UNSUPPORTED)])
+                                        (dict(c=65537, ldf=65537, ldx=65552), UNSUPPORTED), (dict(h=2), UNSUPPORTED), (dict(kh=3, pad_h=1), UNSUPPORTED)])
 def test_factor_update_refuses_checkpoints(lib, bad, status):
     arr = _fd(**bad)
     assert lib.kfac_factor_update_workspace_size(arr, 1) == 0

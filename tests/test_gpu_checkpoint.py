@@ -425,3 +425,23 @@ def test_weight_grad_of_extreme_exponents(a, g):
     # (products of subnormal sums lose what is below 2^-149, one a block of exponents)
     assert bool(((o.double() - want).abs() <= ref.SUM * size + ref.E * want.abs() + 160 / 32 * 2.0 ** -149).all())
     assert _err(ws) == 0
+
+
+def test_an_output_layer_of_a_wide_vocabulary():
+    """More columns than a factor may have: kept, restored, and multiplied."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rows, vocab, dA = 70, 131075, 65
+    y = torch.randn(rows, vocab, device="cuda", generator=gen)
+    x = torch.randn(rows, dA, device="cuda", generator=gen)
+    a, g = kfac.Checkpoint.empty(rows, dA), kfac.Checkpoint.empty(rows, vocab)
+    items = [kfac.CheckpointItem(x, a), kfac.CheckpointItem(y, g)]
+    before = y.clone()
+    kfac.kfac_checkpoint_store(items)
+    kfac.kfac_checkpoint_load(items)
+    assert bool(((y - before).abs() <= 2.0 ** -4 * before.abs() + 2.0 ** -10 * before.abs().max() / 224).all())
+    out = torch.empty(vocab, dA, device="cuda")
+    ws = kfac.kfac_weight_grad([kfac.WeightGrad(a, g, out)])
+    want, size = y.double().t() @ x.double(), y.double().abs().t() @ x.double().abs()
+    assert bool(((out.double() - want).abs() <= ref.SUM * size + ref.E * want.abs()).all()) and _err(ws) == 0
+    with pytest.raises(kfac.KfacError):
+        kfac.kfac_factor_update([kfac.FactorSource(g, torch.empty(16, device="cuda"), alpha=1.0, beta=0.0, packed=True)])
