@@ -8,7 +8,7 @@
 // sequences; the last CTA of a sequence joins them.  Rows behind a token that is not accepted are
 // read too: ways that read only those needed (a cluster that goes through a sequence row by
 // row; rows in three waves with a look at each sequence between them) took 283 and 208 us in place
-// of 225 for 256 x 8 rows of 131072 at 17 of 20 accepted, and more for fewer rows.
+// of 225 for 256 x 8 rows of 131072 of which 7 of 8 tokens are accepted, and more for fewer rows.
 //
 // Bound by memory: every row of logits is read once, and one row of each sequence again.
 // Each quotient is formed from fp32 probabilities (relative error about 1e-6); what
