@@ -335,7 +335,8 @@ __device__ __forceinline__ Best race(const Params &P, const Row2 &R, long long r
 }
 
 template <int DT>
-// 256 rows of 131072 bf16, draft and noise (268 MB, half of it in L2) take 57 us; two CTAs to an SM 67, four 66.
+// 256 rows of 131072 bf16, draft and noise (268 MB, half of it in L2) take 57 us; two CTAs to an SM 67, four 66;
+// the walk in a launch of its own and shorter parts of rows, 8 + 53.
 __global__ void __launch_bounds__(PICK_THREADS, 3) verify_pick_kernel(const __grid_constant__ Params P) {
     __shared__ Stat pol[PICK_WARPS], dra[PICK_WARPS];
     __shared__ int fates[PICK_WARPS], flags[PICK_WARPS], new_token;
