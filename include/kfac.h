@@ -619,7 +619,8 @@ kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, float max_nor
  *     bytes of no block are 0.
  *   - q and scales start on 16-byte boundaries and ldq is a multiple of 16 (of
  *     32 is better: a factor of 8192 x 4097 takes 95 us then, and 102 if not);
- *     elements of q past the width are neither read nor written.
+ *     elements of q past the width are not written, and what they hold does not
+ *     matter.
  * ==================================================================== */
 
 /* kfac_checkpoint_store -- checkpoints of x (KFAC_BF16, KFAC_F16 or KFAC_F32),

@@ -84,6 +84,29 @@ def test_store_and_load_at_any_pitch(dtype, pitch, offset):
     assert (wide == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 5, 130])
+def test_every_width_at_every_alignment(dtype, rows):
+    """Rows that begin and end anywhere: what is beside them stays as it was."""
+    step = 8 if dtype == "bf16" else 4
+    for cols in [*range(1, 2 * step + 3), *range(126, 128 + step + 2), 250, 257]:
+        x, v = _x(rows, cols, dtype, cols)
+        q, ex = ref.store(v, True)
+        want = torch.from_numpy(ref.values(q, ex)[:, :cols]).float().to(DT[dtype]).cuda()
+        for offset in range(step):
+            xd, buf = _pitched(x, cols + offset % 3, offset)
+            c = kfac.Checkpoint.empty(rows, cols, True)
+            c.q.fill_(7)
+            kfac.kfac_checkpoint_store([kfac.CheckpointItem(xd, c, True)])
+            assert np.array_equal(c.q[:, :cols + 1].cpu().numpy(), q) and bool((c.q[:, cols + 1:] == 7).all()), (cols, offset)
+            assert np.array_equal(c.scales.cpu().numpy(), ref.scale_bytes(ex, rows))
+            c.q[:, cols + 1:] = 255
+            buf.fill_(3.0)
+            kfac.kfac_checkpoint_load([kfac.CheckpointItem(xd, c, True)])
+            assert torch.equal(xd, want), (cols, offset)
+            assert int((buf == 3.0).sum()) == buf.numel() - rows * cols + int((want == 3.0).sum()), (cols, offset)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_store_of_special_values(dtype):
     big = torch.finfo(DT[dtype]).max
