@@ -8,11 +8,11 @@
 // a <= 448 2^e (448 the largest e4m3 value), and an element is x 2^-e rounded to e4m3:
 // the scaling is exact, so an element has the one rounding of e4m3.
 //
-// Bound by memory.  A CTA takes a tile of 128 rows: each of its four warps 32 rows,
-// half a warp to a row's 16-byte groups, 16 rows to a thread, so that a thread has 16
-// loads in flight, the maximum over a block is one exchange between two lanes, and the
-// tile's exponents leave as one piece of 512 bytes.  CTAs next to one another take tiles next
-// to one another in the same rows, so that memory is met in long runs.
+// Bound by memory.  A CTA takes a tile of 128 rows: each of its four warps 32 rows.  In whole tiles on
+// 16-byte boundaries half a warp takes a row's 16-byte groups, 16 rows to a thread, so that a thread has 16
+// loads in flight and the maximum over a block is one exchange between two lanes; the tile's
+// exponents leave as one piece of 512 bytes.  CTAs next to one another take tiles next to one another in the
+// same rows, so that memory is met in long runs.
 #include <algorithm>
 #include <cstring>
 
@@ -113,68 +113,24 @@ __device__ __forceinline__ float bounded(float y, uint32_t b) {
     return b == LAST_EXPONENT ? fminf(fmaxf(y, -240.f), 240.f) : y;
 }
 
-// 16 bytes from byte k (0 .. 15) of 32.
-__device__ __forceinline__ uint4 from_byte(uint4 lo, uint4 hi, int k) {
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = k & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = k & 4 ? w[i + 1] : w[i];
-    const int s = (k & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
-                      __funnelshift_r(w[3], w[4], s));
-}
+// The place of column c's exponents in a tile's (16 bytes to a column modulo 32, 4 to each of 4).
+__device__ __forceinline__ int place_of(int c) { return c % 32 * 4 + c % TILE / 32; }
 
-// 16 N columns of a tile, by all its warps.  FULL: all its rows and columns are x's (nothing is
-// looked at row by row then; otherwise 12.8 instructions an element held it at 5.5 TB/s).
-template <int DT, bool FULL>
-__device__ __forceinline__ void store_part(const Item &it, long long rt, int cp, uint8_t (*exps)[4]) {
+// 16 N columns of a tile, by all its warps, where all its rows and columns are x's and x's rows start
+// on 16-byte boundaries: nothing is looked at row by row (otherwise 12.8 instructions an element held it at
+// 5.5 TB/s).
+template <int DT>
+__device__ __forceinline__ void store_whole(const Item &it, long long rt, int cp, uint8_t (*exps)[4]) {
     using M = Mag<DT>;
     constexpr int N = Elem<DT>::N, ROWS = 16;
     using bits = typename Elem<DT>::bits;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const long long r0 = rt * TILE + warp * 32 + lane / 16;  // rows r0, r0 + 2, ...
     const int c0 = cp + lane % 16 * N;
-    const int n = FULL ? N : min(N, it.cols - c0);  // values here (may be negative)
     uint4 u[ROWS];
     const char *src = it.x + r0 * it.ld_bytes + (long long)c0 * (int)sizeof(bits);
-    // Aligned 16 bytes with a value in them are loaded whole; what is not x's is masked.
-    if (it.wide) {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (FULL || (r0 + 2 * i < it.rows && n > 0)) u[i] = ld16(src + 2 * i * it.ld_bytes);
-        }
-    } else {
-        // At other alignments a lane loads the 16 bytes that its group begins in, and has the rest of it
-        // from the next lane; the last lane of a row's part loads them itself.
-        const bool end = lane % 16 == 15 || n < N || c0 + N >= it.cols;
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const char *p = src + 2 * i * it.ld_bytes;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (FULL || (r0 + 2 * i < it.rows && n > 0)) u[i] = ld16(p - ((uintptr_t)p & 15));
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const char *p = src + 2 * i * it.ld_bytes;
-            const int off = (int)((uintptr_t)p & 15);
-            uint4 next = make_uint4(__shfl_down_sync(ALL_LANES, u[i].x, 1, 16), __shfl_down_sync(ALL_LANES, u[i].y, 1, 16),
-                                    __shfl_down_sync(ALL_LANES, u[i].z, 1, 16), __shfl_down_sync(ALL_LANES, u[i].w, 1, 16));
-            if ((FULL || r0 + 2 * i < it.rows) && (FULL ? lane % 16 == 15 : end) && off + n * (int)sizeof(bits) > 16) next = ld16(p - off + 16);
-            u[i] = from_byte(u[i], next, off);
-        }
-    }
-    if (!FULL && n < N) {
-        uint32_t keep[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int here = n - w * N / 4;  // values of this word
-            keep[w] = here <= 0 ? 0u : N == 8 && here == 1 ? 0xffffu : 0xffffffffu;
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) u[i] = make_uint4(u[i].x & keep[0], u[i].y & keep[1], u[i].z & keep[2], u[i].w & keep[3]);
-    }
+    for (int i = 0; i < ROWS; ++i) u[i] = ld16(src + 2 * i * it.ld_bytes);
     uint32_t m[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -208,7 +164,6 @@ __device__ __forceinline__ void store_part(const Item &it, long long rt, int cp,
     uint8_t *dst = it.q + r0 * it.ldq + c0;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        if (!FULL && r0 + 2 * i >= it.rows) continue;
         float v[N];
         Elem<DT>::unpack(u[i], v);
         uint32_t b[N / 4];
@@ -221,36 +176,80 @@ __device__ __forceinline__ void store_part(const Item &it, long long rt, int cp,
 #pragma unroll
         for (int j = 0; j < N / 4; ++j)
             b[j] = e4m3x2(v[4 * j], v[4 * j + 1]) | e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
-        uint8_t *d = dst + 2 * i * it.ldq;
-        if (!FULL && n >= 0 && n < N && it.cols < it.width) {  // a one: 256 2^-8
-            if (n < 4) b[0] |= 0x78u << n % 4 * 8;
-            else b[N / 4 - 1] |= 0x78u << n % 4 * 8;
-        }
-        if (FULL || it.width - c0 >= N) {  // (q's rows start on 16-byte boundaries, and c0 is a multiple of N)
-            if constexpr (N == 8) *(uint2 *)d = make_uint2(b[0], b[1]);
-            else *(uint32_t *)d = b[0];
-        } else if (it.width > c0) {
-            const int some = it.width - c0;
-            uint32_t w = b[0];
-            if (N == 8 && some & 4) {
-                *(uint32_t *)d = w;
-                w = b[N / 4 - 1];
-                d += 4;
-            }
-            if (some & 2) {
-                *(uint16_t *)d = (uint16_t)w;
-                w >>= 16;
-                d += 2;
-            }
-            if (some & 1) *d = (uint8_t)w;
-        }
+        // (q's rows start on 16-byte boundaries, and c0 is a multiple of N)
+        if constexpr (N == 8) *(uint2 *)(dst + 2 * i * it.ldq) = make_uint2(b[0], b[1]);
+        else *(uint32_t *)(dst + 2 * i * it.ldq) = b[0];
     }
     if (lane < 16) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int c = c0 + j, at = c % 32 * 4 + c % TILE / 32;  // (16 bytes to a column modulo 32, 4 to each of 4)
-            const uint32_t b = FULL ? e[j] : r0 >= it.rows ? 0u : c < it.cols ? e[j] : c < it.width ? 119u : 0u;  // 1 = 256 2^-8
-            exps[at][warp] = (uint8_t)b;
+        for (int j = 0; j < N; ++j) exps[place_of(c0 + j)][warp] = (uint8_t)e[j];
+    }
+}
+
+// A value by itself.
+template <int DT>
+__device__ __forceinline__ float value_of(uint32_t b) {
+    if constexpr (DT == KFAC_F32) return __uint_as_float(b);
+    else return Elem<DT>::value((uint16_t)b);
+}
+
+// A whole tile at any alignment, whatever part of it is x's: a column to a lane, 32 rows to a warp, 32 columns
+// at a time (2 groups of them in flight), value by value.  A block is a lane's own then, and an instruction
+// meets 32 values side by side.
+template <int DT>
+__device__ __forceinline__ void store_columns(const Item &it, long long rt, int ct, uint8_t (*exps)[4]) {
+    using bits = typename Elem<DT>::bits;
+    constexpr int GROUPS = 2;
+    constexpr uint32_t SIGN = DT == KFAC_F32 ? 0x80000000u : 0x8000u, TOP = Mag<DT>::TOP;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const long long r0 = rt * TILE + warp * 32;
+    const int rows = (int)max(0LL, min(32LL, it.rows - r0));
+#pragma unroll 1
+    for (int g = 0; g < TILE / 32; g += GROUPS) {
+        uint32_t w[GROUPS][32];
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+            const int c = ct * TILE + (g + k) * 32 + lane;
+            const char *p = it.x + r0 * it.ld_bytes + (long long)c * (int)sizeof(bits);
+            const int here = c < it.cols ? rows : 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                w[k][i] = 0;
+                if (i < here) w[k][i] = *(const bits *)p;
+                p += it.ld_bytes;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < GROUPS; ++k) {
+            const int c = ct * TILE + (g + k) * 32 + lane;
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = max(m, w[k][i] & ~SIGN);
+            bool odd = m >= TOP;
+            if (__any_sync(ALL_LANES, odd)) {  // infinities or NaN: the largest of the finite ones
+                m = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) m = max(m, (w[k][i] & ~SIGN) >= TOP ? 0u : w[k][i] & ~SIGN);
+            }
+            const uint32_t e = exponent_of(value_of<DT>(m));
+            const float inv = inverse_of(e);
+            odd = __any_sync(ALL_LANES, odd || e == LAST_EXPONENT);
+            uint8_t *d = it.q + r0 * it.ldq + c;
+            const int here = c < it.width ? rows : 0;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float v0 = value_of<DT>(w[k][i]) * inv, v1 = value_of<DT>(w[k][i + 1]) * inv;
+                if (odd) {
+                    v0 = bounded(v0, e);
+                    v1 = bounded(v1, e);
+                }
+                const uint32_t b = c == it.cols ? 0x7878u : e4m3x2(v0, v1);  // a one: 256 2^-8
+                if (i < here) *d = (uint8_t)b;
+                d += it.ldq;
+                if (i + 1 < here) *d = (uint8_t)(b >> 8);
+                d += it.ldq;
+            }
+            exps[place_of(c)][warp] = (uint8_t)(here == 0 ? 0u : c < it.cols ? e : 119u);  // 1 = 256 2^-8
         }
     }
 }
@@ -260,20 +259,20 @@ __device__ __forceinline__ void store_tile(const Item &it, long long tile, uint8
     constexpr int COLS = 16 * Elem<DT>::N;
     const int ct = (int)(tile % it.wides);
     const long long rt = tile / it.wides;
-    const bool rows = (rt + 1) * TILE <= it.rows;
+    if (it.wide && (rt + 1) * TILE <= it.rows && (ct + 1) * TILE <= it.cols) {
 #pragma unroll 1
-    for (int cp = ct * TILE; cp < (ct + 1) * TILE; cp += COLS) {
-        if (rows && cp + COLS <= it.cols) store_part<DT, true>(it, rt, cp, exps);
-        else store_part<DT, false>(it, rt, cp, exps);
+        for (int cp = ct * TILE; cp < (ct + 1) * TILE; cp += COLS) store_whole<DT>(it, rt, cp, exps);
+    } else {
+        store_columns<DT>(it, rt, ct, exps);
     }
     __syncthreads();
     ((uint32_t *)(it.scales + (ct * (long long)it.chunks + rt) * 512))[threadIdx.x] = ((const uint32_t *)exps)[threadIdx.x];
 }
 
 // 32768 x 8192 16-bit values (814 MB) take 115 us, 7.1 TB/s (a copy: 6.8); 20000 x 5001 (rows on every
-// alignment) 74 us, 4.1 TB/s, with five CTAs to an SM 85; with two loads a group in place of the exchange
-// between lanes twice as long.  Parts that are not whole four rows at a time in short code, as the restore takes
-// them: 1000 x 1000 6.4 us in place of 7.9, but 20000 x 5001 81 (registers).
+// alignment) 77 us, 3.9 TB/s, 16384 x 4097 fp32 63, 5.3 TB/s, 1000 x 1001 4.4.  With five CTAs to an SM or one group
+// in flight 106 and 138, 97 and 100, 7 and 9; by 16 bytes with the rest of a group from the next lane
+// 74, 76 and 11.
 __global__ void __launch_bounds__(THREADS, 4) store_kernel(const __grid_constant__ Params P) {
     __shared__ __align__(16) uint8_t exps[TILE][4];
     pdl_wait();
@@ -283,6 +282,18 @@ __global__ void __launch_bounds__(THREADS, 4) store_kernel(const __grid_constant
     if (it.dtype == KFAC_BF16) store_tile<KFAC_BF16>(it, tile, exps);
     else if (it.dtype == KFAC_F16) store_tile<KFAC_F16>(it, tile, exps);
     else store_tile<KFAC_F32>(it, tile, exps);
+}
+
+// 16 bytes from byte k (0 .. 15) of 32.
+__device__ __forceinline__ uint4 from_byte(uint4 lo, uint4 hi, int k) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = k & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = k & 4 ? w[i + 1] : w[i];
+    const int s = (k & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
 }
 
 // Elements j0 .. j1 - 1 of a group.  (In pieces of 2, 4 and 8 bytes, fewer but other ones for either end of a
@@ -345,9 +356,10 @@ __device__ __forceinline__ int rows_of(const Item &it, long long rt, int warp) {
     return (int)max(0LL, min(16LL, (it.rows - (rt * TILE + warp * 32) + 1) / 2));
 }
 
-// Values of 16 N columns of a tile, x_ij = q_ij 2^e, rounded to x's type.  FULL as in store_part; other
-// parts go four rows at a time in short code, most of whose time is its fetching (1000 x 1001: 13.5 us
-// with all rows unrolled).
+// Values of 16 N columns of a tile, x_ij = q_ij 2^e, rounded to x's type.  FULL: all rows and columns are
+// x's, and nothing is looked at row by row; other parts go four rows at a time in short code, most of whose
+// time is its fetching (1000 x 1000 4 us, with all rows unrolled 7).  A column to a lane, as in store_columns, takes
+// 2.5 times as long: the pieces of sectors that are written then.
 template <int DT, bool FULL>
 __device__ __forceinline__ void load_part(const Item &it, long long rt, int cp, const uint8_t (*exps)[4]) {
     constexpr int N = Elem<DT>::N, ROWS = FULL ? 16 : 4;
@@ -359,7 +371,7 @@ __device__ __forceinline__ void load_part(const Item &it, long long rt, int cp, 
     const int rows = FULL ? 16 : cp >= it.cols ? 0 : rows_of(it, rt, warp);
     float p[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) p[j] = power_of(exps[(c0 + j) % 32 * 4 + (c0 + j) % TILE / 32][warp]);
+    for (int j = 0; j < N; ++j) p[j] = power_of(exps[place_of(c0 + j)][warp]);
     // At other alignments a lane stores the 16 bytes that its group begins in, with the last elements of the
     // group of the lane before it; the last lane of a row's part stores what is left of its own, too.
     const bool begin = lane % 16 == 0, end = FULL ? lane % 16 == 15 : lane % 16 == 15 || c0 + N >= it.cols;
