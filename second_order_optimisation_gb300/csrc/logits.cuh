@@ -118,6 +118,7 @@ struct Elem<KFAC_F32> {
     static __device__ __forceinline__ float value(bits b) { return __uint_as_float(b); }
     using two = f2;  // running maximum of groups (NaN is passed over)
     static __device__ __forceinline__ two lowest() { return pair(-F32_MAX, -F32_MAX); }
+    static __device__ __forceinline__ two nothing() { return pair(-INFINITY, -INFINITY); }
     static __device__ __forceinline__ two raise(two m, uint4 u) {
         const float2 a = both(m);
         return pair(fmaxf(a.x, fmaxf(__uint_as_float(u.x), __uint_as_float(u.y))),
@@ -154,6 +155,7 @@ struct Elem<KFAC_BF16> {
     using two = __nv_bfloat162;  // running maximum of groups (NaN is passed over)
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xff7fff7fu); }
+    static __device__ __forceinline__ two nothing() { return as_two(NEG_INF); }
     static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
         const two b = __hmax2_nan(as_two(v), as_two(0xf000f000u));  // BOUND
         return *reinterpret_cast<const uint32_t *>(&b);
@@ -191,6 +193,7 @@ struct Elem<KFAC_F16> {
     using two = __half2;  // running maximum of groups (NaN is passed over)
     static __device__ __forceinline__ two as_two(uint32_t w) { return *reinterpret_cast<two *>(&w); }
     static __device__ __forceinline__ two lowest() { return as_two(0xfbfffbffu); }
+    static __device__ __forceinline__ two nothing() { return as_two(NEG_INF); }
     static __device__ __forceinline__ uint32_t bounded1(uint32_t v) {
         const two b = __hmax2_nan(as_two(v), as_two(0xfbfffbffu));  // BOUND
         return *reinterpret_cast<const uint32_t *>(&b);

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(STAT_THREADS) verify_stats_kernel(const __grid
                 }
             run.template add<BATCH>(u, most, skip);
             if (P.greedy) {
-                auto m = Elem<DT>::lowest();
+                auto m = Elem<DT>::nothing();  // (not the lowest finite value: a batch of masked scores does not hold it)
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i)
                     if (i < most) m = Elem<DT>::raise(m, u[i]);
@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(PICK_THREADS, 3) verify_pick_kernel(const __gr
             __syncthreads();
             token = new_token;
         }
-        if (token == NONE) token = -1;
     }
+    if (token == NONE) token = -1;
     if (tid == 0) {
         P.accepted[seq] = (int)(row - r0);
         put_token(P, row, token);
