@@ -696,6 +696,15 @@ def kfac_bn_diag_fisher(items: Sequence[BnItem], gamma: float, xi: float = 0.0, 
 
 # ------------------------------------------------------------ losses on logits
 
+def memory_of(stream, device):
+    """A context in which new tensors are the memory of `stream` (a torch stream, a raw handle, or
+    None: the current one), and what fills them is enqueued there."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # (0 is the default stream, which has no external handle)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
     """The caller's workspace, or a new one that may be dropped while a call on
     `stream` (an own stream, or None) still uses it.  It is that stream's memory: a
@@ -704,10 +713,7 @@ def _scratch(nbytes: int, device, workspace: Optional[torch.Tensor], stream) -> 
         return _workspace(nbytes, device, workspace)
     if stream is None:
         return torch.empty(nbytes if nbytes > 256 else 256, dtype=torch.uint8, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)  # (0 is the default stream, which has no external handle)
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    with memory_of(stream, device):
         ws = _workspace(nbytes, device, None)
     ws.record_stream(torch.cuda.current_stream(device))  # the error word may be read there
     return ws

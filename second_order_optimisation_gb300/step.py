@@ -147,27 +147,28 @@ class KfacStep:
                                  w=w, eta=self.eta)
                 for s, gr, w in zip(self.state, grads, ws)]
 
-    def _workspace(self, key, nbytes):
+    def _workspace(self, key, nbytes, stream=None):
         w = self._ws.get(key)
         if w is None or w.numel() < nbytes:
-            w = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            with kfac.memory_of(stream, self.device):
+                w = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[key] = w
         return w
 
     # ---------------------------------------------------------------- phases
     def factor_update(self, xs, gs, rows_total=None, first=True, stream=None):
         srcs = self.factor_sources(xs, gs, rows_total, first)
-        ws = self._workspace("factor", kfac.kfac_factor_update_workspace_size(srcs))
+        ws = self._workspace("factor", kfac.kfac_factor_update_workspace_size(srcs), stream)
         kfac.kfac_factor_update(srcs, ws, stream)
 
     def damp_invert(self, stream=None):
         pairs = self.invert_pairs()
-        ws = self._workspace("invert", kfac.kfac_damp_invert_workspace_size(pairs))
+        ws = self._workspace("invert", kfac.kfac_damp_invert_workspace_size(pairs), stream)
         kfac.kfac_damp_invert(pairs, self.gamma, True, self.info, self.damp, ws, stream)
 
     def precondition(self, grads, stream=None):
         items = self.precond_items(grads)
-        ws = self._workspace("precond", kfac.kfac_precondition_workspace_size(items))
+        ws = self._workspace("precond", kfac.kfac_precondition_workspace_size(items), stream)
         kfac.kfac_precondition(items, ws, stream)
         if self.max_norm is not None:
             self.clip(grads, stream)
@@ -181,7 +182,7 @@ class KfacStep:
         """Bound the preconditioned gradients by max_norm and take the step on the
         weights (without weights: scale the preconditioned gradients)."""
         tensors = kfac.ClipList(self.clip_tensors(grads))
-        ws = self._workspace("clip", tensors.need)
+        ws = self._workspace("clip", tensors.need, stream)
         kfac.kfac_clip_norm(tensors, self.max_norm, self.norm, self.scale, self.eta, ws, stream)
 
     def weight_grads(self, xs, gs, alphas: Optional[Sequence[float]] = None, stream=None):
@@ -190,10 +191,14 @@ class KfacStep:
         if any(not isinstance(t, kfac.Checkpoint) for t in (*xs, *gs)):
             raise TypeError("weight gradients are made from checkpoints")
         if self._grads is None:
-            self._grads = [_matrix(L.d_g, L.d_a, self.device, torch.bfloat16) for L in self.layers]
+            with kfac.memory_of(stream, self.device):  # (their zeros come before the product, on the same stream)
+                self._grads = [_matrix(L.d_g, L.d_a, self.device, torch.bfloat16) for L in self.layers]
+            if stream is not None:
+                for t in self._grads:
+                    t.record_stream(torch.cuda.current_stream(self.device))  # (they may be read there)
         alphas = [1.0 / max(x.rows, 1) for x in xs] if alphas is None else alphas
         items = [kfac.WeightGrad(x, g, out, alpha) for x, g, out, alpha in zip(xs, gs, self._grads, alphas)]
-        ws = self._workspace("weight_grad", kfac.kfac_weight_grad_workspace_size(items))
+        ws = self._workspace("weight_grad", kfac.kfac_weight_grad_workspace_size(items), stream)
         kfac.kfac_weight_grad(items, ws, stream)
         return self._grads
 
