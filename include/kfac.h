@@ -714,9 +714,9 @@ kfac_status kfac_weight_grad(const kfac_weight_grad_desc *descs, int count, void
  *   - noise [seqs][ld_noise]: positive; what is not (NaN, too) is read as 2^-126.  u is in [0, 1).
  *   - Rows of logits and draft may start at any element boundary, any ld.
  * Error word (first int32 of the workspace): the two bits named above.
- * Errors: INVALID for null logits/tokens/seq_offsets/accepted/out_tokens, and
- *   unless greedy null uniform/noise; rows < 0, seqs < 1, vocab < 1, ld, ld_draft or
- *   ld_noise < vocab, draft_saved without draft or not on an 8-byte boundary, a bad
+ * Errors: INVALID for null seq_offsets/accepted, with rows also for null logits/tokens/
+ *   out_tokens and unless greedy null uniform/noise and ld_noise < vocab (rows = 0: none
+ *   of these is read); rows < 0, seqs < 1, vocab < 1, ld or ld_draft < vocab, draft_saved without draft or not on an 8-byte boundary, a bad
  *   dtype, tau or tau_d; UNSUPPORTED for vocab > 2^24, rows > 2^31 - 1,
  *   seqs > 2^20.
  * Workspace: kfac_verify_draft_workspace_size(desc) bytes. */

@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(PICK_THREADS, 3) verify_pick_kernel(const __gr
     const int seq = blockIdx.x / P.pick_splits, split = blockIdx.x % P.pick_splits;
     const int per = (P.vocab + P.pick_splits - 1) / P.pick_splits;
     const int j0 = min(P.vocab, split * per), j1 = min(P.vocab, j0 + per);
-    if (!P.greedy && tid == 0 && j1 > j0) {  // this part of the noise on its way to L2 while the sums are made
+    // this part of the noise on its way to L2 while the sums are made (without rows there may be no noise)
+    if (!P.greedy && P.rows > 0 && tid == 0 && j1 > j0) {
         const uintptr_t a = (uintptr_t)(P.noise + seq * P.ld_noise + j0) & ~(uintptr_t)15;
         const uintptr_t b = (uintptr_t)(P.noise + seq * P.ld_noise + j1) & ~(uintptr_t)15;
         if (b > a) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"((uint32_t)(b - a)) : "memory");
