@@ -505,6 +505,8 @@ def _factor_descs(sources: Sequence[FactorSource]):
         if isinstance(x, Checkpoint):
             assert s.F.dtype == torch.float32
             q, ldq, scales = _checkpoint_args(x)
+            if s.F.numel() < packed_size(x.width) if s.packed else min(s.F.shape) < x.width:
+                raise KfacError(KFAC_ERR_INVALID, f"F is {tuple(s.F.shape)}, the checkpoint has {x.width} columns")
             arr[i] = FactorDesc(KFAC_E4M3, q, x.rows, 1, 1, x.width, s.kh, s.kw, s.stride[0], s.stride[1],
                                 s.pad[0], s.pad[1], int(bool(s.append_one)), s.F.data_ptr(), _fld(s.F, s.packed),
                                 float(s.alpha), float(s.beta),

@@ -73,6 +73,11 @@ class LayerState:
     out: torch.Tensor          # preconditioned gradient [dG, dA] fp32
 
 
+def _check_width(layer: Layer, c: kfac.Checkpoint, d: int) -> None:
+    if c.width != d:
+        raise ValueError(f"layer {layer.name}: a checkpoint of {c.width} columns, {d} wanted")
+
+
 class KfacStep:
     def __init__(self, layers: Sequence[Layer], batch: int, xi: float = 0.95, gamma: float = 1e-3,
                  device="cuda", update_every: int = 1, warmup: int = 0,
@@ -124,8 +129,7 @@ class KfacStep:
             alpha = (1.0 - self.xi) / M
             beta = self.xi if first else 1.0
             if isinstance(x, kfac.Checkpoint):
-                if x.width != L.d_a:
-                    raise ValueError(f"layer {L.name}: a checkpoint of {x.width} columns, {L.d_a} wanted")
+                _check_width(L, x, L.d_a)
                 srcs.append(kfac.FactorSource(x, s.A, alpha=alpha, beta=beta))
             else:
                 if L.name == "fc" or (L.hin == 1 and L.k == 1):
@@ -134,6 +138,8 @@ class KfacStep:
                     xa = x
                 srcs.append(kfac.FactorSource(xa, s.A, L.k, L.k, (L.stride, L.stride), (L.pad, L.pad),
                                               L.bias, alpha, beta))
+            if isinstance(g, kfac.Checkpoint):
+                _check_width(L, g, L.d_g)
             srcs.append(kfac.FactorSource(g, s.G, alpha=alpha, beta=beta))
         return srcs
 
