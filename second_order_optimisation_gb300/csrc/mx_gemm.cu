@@ -72,7 +72,7 @@ template <int CAP>
 struct Params : Deal {
     Prob prob[CAP];
     float *partial;  // [2 pairs][TILE][TILE] pieces of tiles: 2 p begins inside a tile, 2 p + 1 ends inside one
-    int *counters;   // [pairs][2] pieces that are there of the tile that the pair's share ends in, by CTA
+    int *counters;   // [pairs][2][EPI_WARPS] pieces that are there of the tile that the pair's share ends in, by CTA and warp
     int *err;
     bool alone;      // one pair, which sets *err to 0 (no one else writes it)
 };
@@ -281,7 +281,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
     uint64_t *accf = empty + STAGES, *acce = accf + 1, *drain = acce + 1;
     uint32_t *tmem_slot = (uint32_t *)(drain + 1);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
-    volatile int *last_flag = abort_flag + 1;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -476,7 +475,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
                 break;
             }
             if (k.piece) {
-                // The piece to memory; whoever brings a tile's last piece adds them up in their order.
+                // The piece to memory; whoever brings the last piece of this warp's part of a tile adds them up in
+                // their order.  (Part by part: no warp waits for another one, which may have given up.)
                 const long long slot = (long long)TILE * TILE;
                 const long long part = (long long)rank * HALF * TILE + e * (32 * COLS) + lane * 4;
                 float *mine = P.partial + (2 * pair + (k.kt0 == 0)) * slot + part;
@@ -486,12 +486,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
                 __threadfence();
                 const Pieces pieces = pieces_of(P, k.begin, q.k_tiles, pair);
                 const int first = pieces.first, last = pieces.last;
-                named_barrier_sync(1, 32 * EPI_WARPS);
-                if (threadIdx.x == 32 * FIRST_EPI) *last_flag = atomicAdd(&P.counters[2 * first + rank], 1) == pieces.count - 1;
-                named_barrier_sync(1, 32 * EPI_WARPS);
-                const bool all_there = *last_flag != 0;
-                named_barrier_sync(1, 32 * EPI_WARPS);
-                if (!all_there) continue;
+                __syncwarp();
+                int there = 0;
+                if (lane == 0) there = atomicAdd(&P.counters[(2 * first + rank) * EPI_WARPS + e], 1) + 1;
+                if (__shfl_sync(0xffffffffu, there, 0) != pieces.count) continue;
+                __syncwarp();
                 __threadfence();
 #pragma unroll
                 for (int c = 0; c < COLS; c += 64) {
@@ -610,6 +609,8 @@ struct Plan {
     size_t ncounters = 0;
 };
 
+size_t counters_of(const Launch &l) { return (size_t)l.pairs * 2 * EPI_WARPS; }
+
 Plan make_plan(const MxJob *jobs, int n, Arena &ws) {
     Plan p;
     p.order.resize(n);
@@ -623,7 +624,7 @@ Plan make_plan(const MxJob *jobs, int n, Arena &ws) {
         p.launches.push_back(make_launch(tiles, at, most));
         if (const Launch &l = p.launches.back(); l.span > 0) {
             slots = std::max(slots, 2 * l.pairs);
-            p.ncounters += 2 * l.pairs;
+            p.ncounters += counters_of(l);
         }
     }
     p.counters = ws.take<int>(std::max<size_t>(p.ncounters, 1));
@@ -688,7 +689,7 @@ kfac_status run_plan(const MxJob *jobs, const Plan &p, int *err, bool zero_err, 
         const kfac_status s = l.deal.nprob <= FEW_PROBS ? launch<FEW_PROBS>(jobs, p, l, counters, err, alone, st)
                                                         : launch<MAX_PROBS>(jobs, p, l, counters, err, alone, st);
         if (s != KFAC_OK) return s;
-        if (l.span > 0) counters += 2 * l.pairs;
+        if (l.span > 0) counters += counters_of(l);
     }
     return KFAC_OK;
 }
