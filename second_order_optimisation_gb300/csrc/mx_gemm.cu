@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
         uint32_t use = 0;
         bool bad = false;
         Walk walk(P, pair, pairs);
-        for (Item k; !*abort_flag && walk.next(P, k);) {
+        for (Item k; all_of(!*abort_flag) && walk.next(P, k);) {
             const Prob &q = P.prob[k.p];
             const int i0 = k.tm * TILE + rank * HALF + quarter * 32, j0 = k.tn * TILE + half * 32;
             if (q.beta != 0.f && !q.packed && i0 + lane < q.M) {  // the old values on their way to L2 while the products run
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
             float v[COLS];
             bool ok = true;
             for (int c0 = k.kt0;; c0 += CHUNK) {
-                if (!mbar_wait(accf, use & 1)) {
+                if (!all_of(mbar_wait(accf, use & 1))) {  // (the loads from tensor memory want the whole warp)
                     ok = false;
                     break;
                 }
