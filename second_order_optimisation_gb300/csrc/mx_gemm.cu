@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) mx_kernel(const __grid_constan
         fence_barrier_init();
     }
     if (warp == 1) tmem_alloc_pair(tmem_slot);
-    if (warp == 2 && lane < 4) tma_prefetch_desc(&P.prob[0].a + lane);
+    if (warp == 2 && lane < 4 && P.prob[0].k_tiles > 0) tma_prefetch_desc(&P.prob[0].a + lane);  // (without rows there are none)
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are there
