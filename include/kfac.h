@@ -716,8 +716,9 @@ kfac_status kfac_weight_grad(const kfac_weight_grad_desc *descs, int count, void
  * Error word (first int32 of the workspace): the two bits named above.
  * Errors: INVALID for null seq_offsets/accepted, with rows also for null logits/tokens/
  *   out_tokens and unless greedy null uniform/noise and ld_noise < vocab (rows = 0: none
- *   of these is read); rows < 0, seqs < 1, vocab < 1, ld or ld_draft < vocab, draft_saved without draft or not on an 8-byte boundary, a bad
- *   dtype, tau or tau_d; UNSUPPORTED for vocab > 2^24, rows > 2^31 - 1,
+ *   of these is read); rows < 0, seqs < 1, vocab < 1, ld or ld_draft < vocab, a pointer
+ *   that is not on its elements' boundary, draft_saved without draft or not on an 8-byte
+ *   boundary, a bad dtype, tau or tau_d; UNSUPPORTED for vocab > 2^24, rows > 2^31 - 1,
  *   seqs > 2^20.
  * Workspace: kfac_verify_draft_workspace_size(desc) bytes. */
 typedef struct {

@@ -488,8 +488,12 @@ kfac_status check(const kfac_verify_desc *d) {
     if (d->rows < 0 || d->seqs < 1 || d->vocab < 1 || d->ld < d->vocab || bad_tau(d->temperature)) return KFAC_ERR_INVALID;
     if (!d->seq_offsets || !d->accepted || (uintptr_t)d->logits % elem_size(d->dtype)) return KFAC_ERR_INVALID;
     if (d->rows > 0 && (!d->logits || !d->tokens || !d->out_tokens)) return KFAC_ERR_INVALID;
+    if (((uintptr_t)d->tokens | (uintptr_t)d->out_tokens) % (d->token_i32 ? 4 : 8) ||
+        ((uintptr_t)d->seq_offsets | (uintptr_t)d->accepted | (uintptr_t)d->logp) % 4)
+        return KFAC_ERR_INVALID;
     if (!d->greedy) {
         if (d->rows > 0 && (!d->uniform || !d->noise || d->ld_noise < d->vocab)) return KFAC_ERR_INVALID;
+        if (((uintptr_t)d->uniform | (uintptr_t)d->noise) % 4) return KFAC_ERR_INVALID;
         if (d->draft && (d->ld_draft < d->vocab || (uintptr_t)d->draft % elem_size(d->dtype) || bad_tau(d->draft_temperature)))
             return KFAC_ERR_INVALID;
         if (d->draft_saved && (!d->draft || (uintptr_t)d->draft_saved % 8)) return KFAC_ERR_INVALID;
