@@ -127,7 +127,11 @@ enum {
 /* Human-readable name of a status code (static string, never NULL). */
 const char *kfac_status_string(int status);
 
-/* Library version as major*10000 + minor*100 + patch. */
+/* Library version as major*10000 + minor*100 + patch: KFAC_VERSION of the header that the
+ * library was built with.  Where a caller's KFAC_VERSION has another minor or major number
+ * its descriptors may have another size (an array of them another stride): it must not call.
+ *   300: kfac_factor_desc ends with scales and ldx. */
+#define KFAC_VERSION 300
 int kfac_version(void);
 
 /* Number of kernel launches this library has enqueued in this process so far

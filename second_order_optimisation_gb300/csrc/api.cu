@@ -380,7 +380,7 @@ extern "C" const char *kfac_status_string(int status) {
     }
 }
 
-extern "C" int kfac_version(void) { return 200; }
+extern "C" int kfac_version(void) { return KFAC_VERSION; }
 
 extern "C" long long kfac_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
