@@ -630,8 +630,9 @@ kfac_status kfac_clip_norm(const kfac_clip_desc *descs, int count, float max_nor
 /* kfac_checkpoint_store -- checkpoints of x (KFAC_BF16, KFAC_F16 or KFAC_F32),
  * any ld >= cols and any element-aligned base.
  * kfac_checkpoint_load -- the values of checkpoints, rounded to x's type (fp32 and
- * in general bf16 hold them exactly; fp16 rounds below 2^-14 and overflows above
- * 65504).
+ * in general bf16 hold them exactly; fp16 rounds below 2^-14, and a value above 65504 becomes
+ * infinite there.  Finite fp16 values from 63488 on have such a value, 65536: a matrix that may
+ * hold them is restored to bf16 or fp32).
  * One launch for each 64 matrices.  rows = 0: nothing to do.  No workspace, no
  * error word.  What a call writes must not overlap anything else that it reads or writes.
  * Errors: INVALID for count < 0, rows < 0, cols < 1, ld < cols, ldq < width,
@@ -708,6 +709,8 @@ kfac_status kfac_weight_grad(const kfac_weight_grad_desc *descs, int count, void
  *   - tokens int64 or (token_i32 != 0) int32; the one of a last row is not read. A
  *     token outside 0 .. vocab - 1 is not accepted, and replaced by a draw from
  *     p; one >= vocab sets KFAC_ERRW_TARGET.
+ *   - p and q are formed in fp32: each is off by about 1e-6 of itself, and r by as much of the
+ *     larger of the two.
  *   - Logits of -inf have probability 0.  A row of the policy with NaN, +inf or
  *     nothing but -inf has no distribution: its token is -1, its logp NaN, the sequence ends
  *     there, and KFAC_ERRW_NONFINITE is set.  A row of the draft that has none:

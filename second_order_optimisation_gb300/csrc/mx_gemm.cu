@@ -48,7 +48,7 @@ constexpr int ACC_SHIFT = 192, SF_COL = 448, SF_SLOT = 12;
 static_assert(SF_COL + STAGES * SF_SLOT <= 512 && ACC_SHIFT + TILE <= SF_COL && TILE - ACC_SHIFT == 64, "tensor memory");
 constexpr int TMEM_COLS = 512;
 // Stages (1280 tokens) in one accumulator.  Sums of 2048 to 20000 tokens are off by at most 9e-7 of
-// themselves (8 stages 7e-7, 16 stages 1.6e-6, 64 stages 3e-6), and taking a chunk out costs 0.9 us
+// themselves (8 stages 7e-7, 16 stages 1.6e-6, 64 stages 3e-6 to 7e-6), and taking a chunk out costs 0.9 us
 // (16384 x 4096 x 8192: 8 stages 426 us, 10 stages 395, 16 stages 354).  Three accumulators of half a
 // tile that are taken out in turn wait less, but their products of 128 columns read A twice from shared
 // memory (391 us; 2048 x 4096 x 4096 48 in place of 41).

@@ -8,11 +8,13 @@
 // sequences; the last CTA of a sequence joins them.  Rows behind a token that is not accepted are
 // read too: ways that read only those needed (a cluster that goes through a sequence row by
 // row; rows in three waves with a look at each sequence between them) took 283 and 208 us in place
-// of 225 for 256 x 8 rows of 131072 of which 7 of 8 tokens are accepted, and more for fewer rows.
+// of 225 for 256 x 8 rows of 131072 of whose tokens 86% are accepted, and more for fewer rows.
 //
 // Bound by memory: every row of logits is read once, and one row of each sequence again.
-// Each quotient is formed from fp32 probabilities (relative error about 1e-6); what
-// accepts a token is compared in fp64 where fp32 could err.
+// p and q are fp32 (relative error about 1e-6), so r = p - q is off by as much of the larger of
+// the two: where policy and draft nearly agree, few of its bits are right.  What accepts a token is
+// compared in fp64 where fp32's arithmetic on scores and sums could err; the sums themselves are
+// fp32 (off by 1e-7 to 1e-6, the more the further a row's weight lies below its maximum).
 #include <algorithm>
 #include <cmath>
 
@@ -195,7 +197,8 @@ __device__ __forceinline__ bool distribution(float s) { return s > 0.f && s <= F
 __device__ __forceinline__ float log_prob(float z, const Stat &s, float tau) {
     return (z - s.m) / tau - LN2 * log2f(s.s);
 }
-// Whether u < p / q.  In fp32 where the two are further apart than its error, else in fp64.
+// Whether u < p / q.  In fp32 where the two are further apart than its error, else in fp64 from the same
+// sums: then as right as these are.
 __device__ __noinline__ bool below_exact(float u, float zp, Stat p, float taup, float zq, Stat q, float tauq) {
     const double lp = ((double)zp - (double)p.m) / (double)taup - log((double)p.s);
     const double lq = q.s > 0.f ? ((double)zq - (double)q.m) / (double)tauq - log((double)q.s) : 0.;
